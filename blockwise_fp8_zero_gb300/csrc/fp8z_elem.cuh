@@ -1,0 +1,74 @@
+// fp8z_elem.cuh -- 16-byte vectors of FP32, BF16 and FP16 elements, widened to
+// and rounded from FP32 (round to nearest even), for the kernels around the
+// optimizer step.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "fp8z.h"
+
+namespace fp8z {
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+    static constexpr int kCode = FP8Z_F32;
+    static __device__ __forceinline__ float widen(float x) { return x; }
+    static __device__ __forceinline__ float narrow(float x) { return x; }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr int kCode = FP8Z_BF16;
+    static __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ __nv_bfloat16 narrow(float x) { return __float2bfloat16_rn(x); }
+};
+template <>
+struct Elem<__half> {
+    static constexpr int kCode = FP8Z_F16;
+    static __device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+    static __device__ __forceinline__ __half narrow(float x) { return __float2half_rn(x); }
+};
+
+// N consecutive elements from an address aligned to min(16, N * sizeof(T)):
+// read once, through the non-coherent path.
+template <typename T, int N>
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
+    T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> ld_nc(const T* p) {
+    static_assert(sizeof(T) * N % 16 == 0, "whole 16-byte vectors");
+    Pack<T, N> r;
+    uint4* u = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) * N / 16); ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    return r;
+}
+
+// The same for memory that this kernel also writes (accumulation in place).
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> ld_plain(const T* p) {
+    Pack<T, N> r;
+    uint4* u = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) * N / 16); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    return r;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void st_vec(T* p, const Pack<T, N>& r) {
+    const uint4* u = reinterpret_cast<const uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) * N / 16); ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+}
+
+inline bool dtype_ok(int32_t d) { return d == FP8Z_F32 || d == FP8Z_BF16 || d == FP8Z_F16; }
+inline int dtype_bytes(int32_t d) { return d == FP8Z_F32 ? 4 : 2; }
+
+}  // namespace fp8z

@@ -25,6 +25,8 @@ FP8Z_ECUDA, FP8Z_ETIMEOUT, FP8Z_EUNSUPPORTED = -4, -5, -6
 FP8Z_SPLIT_BLOCKWISE, FP8Z_SPLIT_PARAMWISE = 0, 1
 FP8Z_SCALE_EXACT, FP8Z_SCALE_POW2 = 0, 1
 FP8Z_DECAY_PRE, FP8Z_DECAY_POST = 0, 1
+FP8Z_F32, FP8Z_BF16, FP8Z_F16, FP8Z_I32, FP8Z_I64 = 0, 1, 2, 3, 4
+GRAD_NORM_WORKSPACE = 32768  # FP8Z_GRAD_NORM_WORKSPACE
 
 # numpy views of the ABI structs (include/fp8z.h)
 param_shape_dtype = np.dtype([("e", "<i8"), ("rows", "<i8"), ("cols", "<i8")])
@@ -42,13 +44,21 @@ plan_summary_dtype = np.dtype([
     ("real_elems", "<i8"), ("total_blocks", "<i8"), ("fold_pad_elems", "<i8"),
     ("shard_pad_elems", "<i8"), ("capacity_blocks", "<i8"), ("naive_straddled_blocks", "<i8"),
 ])
+tensor_entry_dtype = np.dtype([
+    ("src", "<u8"), ("dst", "<u8"), ("numel", "<i8"), ("first_chunk", "<i8"),
+    ("src_dtype", "<i4"), ("dst_dtype", "<i4"),
+])
+assert tensor_entry_dtype.itemsize == 40
 assert param_entry_dtype.itemsize == 64 and block_desc_dtype.itemsize == 20
 
 EXPORTED = ("fp8z_plan_shards", "fp8z_adamw_requant_step", "fp8z_adamw_requant_step_rowmajor",
             "fp8z_adamw_requant_step_mx", "fp8z_adamw_requant_step_rowmajor_static",
             "fp8z_encode_grad_maps", "fp8z_dequant",
             "fp8z_transpose_fp8", "fp8z_fold", "fp8z_unfold", "fp8z_quantize_rowwise",
-            "fp8z_transpose_rowwise", "fp8z_dequant_rowwise", "fp8z_e4m3_encode_bits",
+            "fp8z_transpose_rowwise", "fp8z_dequant_rowwise",
+            "fp8z_encode_tensor_list", "fp8z_grad_norm", "fp8z_grad_clip",
+            "fp8z_embedding", "fp8z_embedding_grad", "fp8z_embedding_grad_workspace",
+            "fp8z_e4m3_encode_bits",
             "fp8z_watchdog_selftest", "fp8z_set_wait_limit_ns", "fp8z_get_wait_limit_ns",
             "fp8z_status_string")
 
@@ -110,6 +120,14 @@ def lib():
         L.fp8z_quantize_rowwise.argtypes = [P, i64, i64, i32, P, P, P]
         L.fp8z_transpose_rowwise.argtypes = [P, P, i64, i64, P, P, P]
         L.fp8z_dequant_rowwise.argtypes = [P, P, i64, i64, i32, P, P]
+        f32 = ctypes.c_float
+        L.fp8z_encode_tensor_list.argtypes = [P, P, P, P, P, i32, P, P]
+        L.fp8z_grad_norm.argtypes = [P, i32, i64, f32, P, P, P]
+        L.fp8z_grad_clip.argtypes = [P, i32, i64, f32, f32, f32, P, P, P]
+        L.fp8z_embedding.argtypes = [P, i32, i64, P, i32, i64, i64, i64, P, i32, i64, f32, P, P]
+        L.fp8z_embedding_grad_workspace.argtypes = [i64, i64, i64]
+        L.fp8z_embedding_grad.argtypes = [P, i32, i64, P, i32, i64, P, i32, i64, i64, i64, f32, i64, i32,
+                                          P, i64, P, P]
         L.fp8z_e4m3_encode_bits.argtypes = [ctypes.c_uint32, i64, P, P]
         L.fp8z_watchdog_selftest.argtypes = [P, i64, P]
         L.fp8z_set_wait_limit_ns.argtypes = [i64]
@@ -120,6 +138,7 @@ def lib():
             if name != "fp8z_status_string":
                 getattr(L, name).restype = ctypes.c_int
         L.fp8z_get_wait_limit_ns.restype = i64
+        L.fp8z_embedding_grad_workspace.restype = i64
         _lib = L
     return _lib
 
@@ -449,6 +468,135 @@ def fp8z_dequant_rowwise(q, s, out, transpose=False, stream=None):
                                     int(bool(transpose)), _dptr(out, torch.float32, "out"),
                                     _stream_handle(stream))
     _check("fp8z_dequant_rowwise", rc)
+
+
+# ------------------------------------- operators around the optimizer step
+def _dtype_code(t, name, allowed=(FP8Z_F32, FP8Z_BF16, FP8Z_F16)):
+    import torch
+    code = {torch.float32: FP8Z_F32, torch.bfloat16: FP8Z_BF16, torch.float16: FP8Z_F16,
+            torch.int32: FP8Z_I32, torch.int64: FP8Z_I64}.get(t.dtype)
+    if code not in allowed:
+        raise ValueError(f"{name} must not be {t.dtype}")
+    return code
+
+
+def _matrix(t, name):
+    """(pointer, rows, cols, row stride in elements) of a 2-D CUDA tensor on the
+    current device whose rows are contiguous and do not overlap."""
+    import torch
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr(), rows, cols, ld
+
+
+class TensorList:
+    """The device table of a list of tensors (fp8z_encode_tensor_list), the
+    number of its chunks, and the tensors it points to, which it keeps alive."""
+
+    def __init__(self, table, n, chunks, tensors):
+        self.table, self.n, self.chunks, self.tensors = table, n, chunks, tensors
+
+
+def fp8z_encode_tensor_list(srcs, dsts=None, device="cuda"):
+    """Table over srcs (contiguous CUDA tensors, float32 / bfloat16 / float16 in
+    any mixture) for fp8z_grad_norm and fp8z_grad_clip.  dsts: tensors of the
+    same sizes that the clipped values go to (None: in place).  The table holds
+    addresses: make a new one when a tensor moves."""
+    import torch
+    srcs = list(srcs)
+    dsts = srcs if dsts is None else list(dsts)
+    if len(dsts) != len(srcs):
+        raise ValueError("one dst per src")
+    n = len(srcs)
+    rows = np.zeros((5, max(n, 1)), np.int64)
+    for i, (s, d) in enumerate(zip(srcs, dsts)):
+        if s.numel() != d.numel():
+            raise ValueError(f"dst {i} holds {d.numel()} elements, src {s.numel()}")
+        rows[:, i] = (_dptr(s, None, f"src {i}"), _dptr(d, None, f"dst {i}"), s.numel(),
+                      _dtype_code(s, f"src {i}"), _dtype_code(d, f"dst {i}"))
+    kinds = rows[3:].astype(np.int32)
+    out = np.zeros(max(n, 1), tensor_entry_dtype)
+    chunks = ctypes.c_int64(0)
+    rc = lib().fp8z_encode_tensor_list(rows[0].ctypes.data, rows[1].ctypes.data, rows[2].ctypes.data,
+                                       kinds[0].ctypes.data, kinds[1].ctypes.data, n, out.ctypes.data,
+                                       ctypes.byref(chunks))
+    _check("fp8z_encode_tensor_list", rc)
+    return TensorList(table_to_device(out, device), n, int(chunks.value), (srcs, dsts))
+
+
+def fp8z_grad_norm_workspace():
+    """Bytes of the norm's workspace: zero it once, before the first call."""
+    return GRAD_NORM_WORKSPACE
+
+
+def _norm_args(tensors, norm, workspace):
+    import torch
+    if norm.numel() < 2:
+        raise ValueError("norm must hold two float32 values: the norm and the coefficient")
+    if workspace.numel() * workspace.element_size() < GRAD_NORM_WORKSPACE:
+        raise ValueError(f"workspace must hold {GRAD_NORM_WORKSPACE} bytes")
+    return (_dptr(tensors.table, None, "table"), tensors.n, tensors.chunks, _dptr(norm, torch.float32, "norm"),
+            _dptr(workspace, None, "workspace"))
+
+
+def fp8z_grad_norm(tensors, norm, workspace, grad_scale=1.0, stream=None):
+    """norm[0] = |grad_scale| * sqrt(sum of squares over the whole list), norm[1] = 1."""
+    table, n, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
+    _check("fp8z_grad_norm", lib().fp8z_grad_norm(table, n, chunks, grad_scale, nptr, ws, _stream_handle(stream)))
+
+
+def fp8z_grad_clip(tensors, max_norm, norm, workspace, grad_scale=1.0, eps=1e-6, stream=None):
+    """The norm, then dst = grad_scale * min(1, max_norm / (norm + eps)) * src for
+    every tensor; norm (float32 [2], CUDA) gets the norm and the coefficient."""
+    table, n, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
+    _check("fp8z_grad_clip", lib().fp8z_grad_clip(table, n, chunks, grad_scale, max_norm, eps, nptr, ws,
+                                                  _stream_handle(stream)))
+
+
+def fp8z_embedding(ids, table, out, scale=1.0, dev_status=None, stream=None):
+    """out[t] = scale * table[ids[t]].  ids: int64 or int32, any shape, contiguous;
+    table [vocab, hidden], out [tokens, hidden]: float32 / bfloat16 / float16,
+    rows may be strided."""
+    import torch
+    tp, vocab, hidden, t_ld = _matrix(table, "table")
+    op, tokens, cols, o_ld = _matrix(out, "out")
+    if ids.numel() != tokens or cols != hidden:
+        raise ValueError(f"out must be [{ids.numel()}, {hidden}], got {list(out.shape)}")
+    rc = lib().fp8z_embedding(_dptr(ids, None, "ids"), _dtype_code(ids, "ids", (FP8Z_I32, FP8Z_I64)), tokens, tp,
+                              _dtype_code(table, "table"), vocab, hidden, t_ld, op, _dtype_code(out, "out"), o_ld,
+                              scale, _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
+    _check("fp8z_embedding", rc)
+
+
+def fp8z_embedding_grad_workspace(tokens, vocab, hidden):
+    """Bytes of workspace fp8z_embedding_grad needs for these sizes."""
+    size = int(lib().fp8z_embedding_grad_workspace(int(tokens), int(vocab), int(hidden)))
+    if size < 0:
+        raise Fp8zError("fp8z_embedding_grad_workspace", size)
+    return size
+
+
+def fp8z_embedding_grad(ids, d_out, d_table, workspace, scale=1.0, padding_idx=-1, accumulate=False,
+                        dev_status=None, stream=None):
+    """d_table[v] = scale * sum of d_out[t] over ids[t] == v (zeros elsewhere), or
+    that sum added to d_table (accumulate).  Deterministic."""
+    import torch
+    dp, tokens, hidden, d_ld = _matrix(d_out, "d_out")
+    tp, vocab, cols, t_ld = _matrix(d_table, "d_table")
+    if ids.numel() != tokens or cols != hidden:
+        raise ValueError(f"d_out must be [{ids.numel()}, {cols}], got {list(d_out.shape)}")
+    rc = lib().fp8z_embedding_grad(_dptr(ids, None, "ids"), _dtype_code(ids, "ids", (FP8Z_I32, FP8Z_I64)), tokens, dp,
+                                   _dtype_code(d_out, "d_out"), d_ld, tp, _dtype_code(d_table, "d_table"), vocab,
+                                   hidden, t_ld, scale, int(padding_idx), int(bool(accumulate)),
+                                   _dptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
+                                   _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
+    _check("fp8z_embedding_grad", rc)
 
 
 def fp8z_e4m3_encode_bits(first_bits, n, out, stream=None):

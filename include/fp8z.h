@@ -406,6 +406,98 @@ FP8Z_API int fp8z_transpose_rowwise(const uint8_t *q, const float *s, int64_t ro
 FP8Z_API int fp8z_dequant_rowwise(const uint8_t *q, const float *s, int64_t rows, int64_t cols,
                                   int32_t transpose, float *out, void *stream);
 
+/* Element types of the entry points below. */
+typedef enum { FP8Z_F32 = 0, FP8Z_BF16 = 1, FP8Z_F16 = 2, FP8Z_I32 = 3, FP8Z_I64 = 4 } fp8z_dtype;
+
+/*
+ * The entry points from here to fp8z_linear_xent_grad are the operators of a
+ * language model's training step that stand around the optimizer step: the two
+ * ends of the model whose FP32 gradients are the largest the step takes, and
+ * the norm and clipping between them and the step.  Their formulas are given
+ * here; the pages cited above have no counterpart.  Row strides (`_ld`) are in
+ * elements and at least the row length; a buffer has to be aligned to its
+ * element, and rows that all start on 16-byte boundaries take the vector paths.
+ * A workspace is 16-byte aligned (256 for fp8z_linear_xent), belongs to the
+ * calls of one stream at a time, and holds nothing between calls that a caller
+ * may rely on.  Tensors of one call do not overlap except where a comment says
+ * so.
+ */
+
+/* One tensor of a list: numel contiguous elements at src, scaled into dst. */
+typedef struct {
+    const void *src;
+    void *dst;               /* src itself, or another buffer of dst_dtype          */
+    int64_t numel;
+    int64_t first_chunk;     /* written by fp8z_encode_tensor_list                   */
+    int32_t src_dtype, dst_dtype;
+} fp8z_tensor_entry;         /* 40 bytes */
+
+#define FP8Z_TENSOR_CHUNK 4096             /* elements of one chunk of a list          */
+#define FP8Z_GRAD_NORM_WORKSPACE 32768     /* bytes; zeroed by the caller once, before the
+                                              first call                              */
+
+/*
+ * fp8z_encode_tensor_list -- host only: the table fp8z_grad_norm and
+ * fp8z_grad_clip read the tensors through.  srcs, numels, src_dtypes (FP8Z_F32,
+ * FP8Z_BF16 or FP8Z_F16): host arrays of n; dsts and dst_dtypes: host arrays of
+ * n, or both NULL for scaling in place.  out: host array of n entries, which the
+ * caller copies to device memory; *chunks_out: the number of chunks, passed to
+ * the calls.  A tensor may be empty.  In place (dst == src) needs equal types.
+ */
+FP8Z_API int fp8z_encode_tensor_list(const void *const *srcs, void *const *dsts, const int64_t *numels,
+                                     const int32_t *src_dtypes, const int32_t *dst_dtypes, int32_t n,
+                                     fp8z_tensor_entry *out, int64_t *chunks_out);
+
+/*
+ * fp8z_grad_norm -- norm[0] = |grad_scale| * sqrt(sum of g^2 over every element
+ * of every src of the list), norm[1] = 1.  Squares are FP32 (an element beyond
+ * 1.8e19 makes the norm infinite), sums FP64 in a fixed order: the same list
+ * gives the same bits.  An empty list has norm 0.  list: device,
+ * fp8z_tensor_entry[n]; norm: device f32[2]; workspace: device,
+ * FP8Z_GRAD_NORM_WORKSPACE bytes.
+ *
+ * fp8z_grad_clip -- the same, then norm[1] = coef = min(1, max_norm /
+ * (norm[0] + eps)) (1 when max_norm is infinite) and
+ * dst = (grad_scale * coef) * g for every element, rounded once to dst's type.
+ * Everything stays on the device: an infinite norm gives coef 0 and a NaN gives
+ * NaN everywhere, so the caller can tell from norm[0] that a step is lost.  In
+ * place with grad_scale * coef == 1, nothing is written.
+ * Returns FP8Z_OK / EINVAL / EALIGN / EUNSUPPORTED / ECUDA.
+ */
+FP8Z_API int fp8z_grad_norm(const fp8z_tensor_entry *list, int32_t n, int64_t chunks, float grad_scale, float *norm,
+                            void *workspace, void *stream);
+FP8Z_API int fp8z_grad_clip(const fp8z_tensor_entry *list, int32_t n, int64_t chunks, float grad_scale,
+                            float max_norm, float eps, float *norm, void *workspace, void *stream);
+
+/*
+ * fp8z_embedding -- out[t][:] = scale * table[ids[t]][:], the product in FP32,
+ * rounded once.  ids: device, FP8Z_I32 or FP8Z_I64; table [vocab, hidden] and
+ * out [tokens, hidden]: device, FP8Z_F32, FP8Z_BF16 or FP8Z_F16 each.  An id
+ * outside [0, vocab) gives a row of zeros and FP8Z_EINVAL in *dev_status.
+ */
+FP8Z_API int fp8z_embedding(const void *ids, int32_t ids_dtype, int64_t tokens, const void *table,
+                            int32_t table_dtype, int64_t vocab, int64_t hidden, int64_t table_ld, void *out,
+                            int32_t out_dtype, int64_t out_ld, float scale, int32_t *dev_status, void *stream);
+
+/*
+ * fp8z_embedding_grad -- d_table[v][:] = scale * (sum of d_out[t][:] over the
+ * tokens t with ids[t] == v), in FP32 and in token order, rounded once; rows
+ * without a token are written as zeros.  With accumulate = 1 the sum is added
+ * to d_table instead and rows without a token are not touched.  Tokens whose id
+ * is padding_idx give no gradient (-1: no padding), and tokens whose id is
+ * outside [0, vocab) none either, with FP8Z_EINVAL in *dev_status.  The tokens
+ * are sorted by id, and runs of equal ids are summed piece by piece: no
+ * floating-point atomics, the same bits every time.  workspace: device,
+ * fp8z_embedding_grad_workspace(tokens, vocab, hidden) bytes, no
+ * initialisation.  tokens, vocab <= 2^30, hidden <= 2^23.
+ */
+FP8Z_API int64_t fp8z_embedding_grad_workspace(int64_t tokens, int64_t vocab, int64_t hidden);
+FP8Z_API int fp8z_embedding_grad(const void *ids, int32_t ids_dtype, int64_t tokens, const void *d_out,
+                                 int32_t d_dtype, int64_t d_ld, void *d_table, int32_t table_dtype, int64_t vocab,
+                                 int64_t hidden, int64_t table_ld, float scale, int64_t padding_idx,
+                                 int32_t accumulate, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
+                                 void *stream);
+
 /*
  * fp8z_e4m3_encode_bits -- out[i] = E4M3 code (round to nearest even,
  * saturating, as in the step) of the float whose bit pattern is
