@@ -26,6 +26,7 @@ FP8Z_SPLIT_BLOCKWISE, FP8Z_SPLIT_PARAMWISE = 0, 1
 FP8Z_SCALE_EXACT, FP8Z_SCALE_POW2 = 0, 1
 FP8Z_DECAY_PRE, FP8Z_DECAY_POST = 0, 1
 FP8Z_F32, FP8Z_BF16, FP8Z_F16, FP8Z_I32, FP8Z_I64 = 0, 1, 2, 3, 4
+FP8Z_MEAN, FP8Z_SUM = 0, 1
 GRAD_NORM_WORKSPACE = 32768  # FP8Z_GRAD_NORM_WORKSPACE
 
 # numpy views of the ABI structs (include/fp8z.h)
@@ -58,6 +59,7 @@ EXPORTED = ("fp8z_plan_shards", "fp8z_adamw_requant_step", "fp8z_adamw_requant_s
             "fp8z_transpose_rowwise", "fp8z_dequant_rowwise",
             "fp8z_encode_tensor_list", "fp8z_grad_norm", "fp8z_grad_clip",
             "fp8z_embedding", "fp8z_embedding_grad", "fp8z_embedding_grad_workspace",
+            "fp8z_linear_xent", "fp8z_linear_xent_grad", "fp8z_linear_xent_workspace",
             "fp8z_e4m3_encode_bits",
             "fp8z_watchdog_selftest", "fp8z_set_wait_limit_ns", "fp8z_get_wait_limit_ns",
             "fp8z_status_string")
@@ -73,6 +75,19 @@ class fp8z_adamw_hparams(ctypes.Structure):
 
 
 assert ctypes.sizeof(fp8z_adamw_hparams) == 48
+
+
+class fp8z_xent_args(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("vocab", ctypes.c_int64),
+        ("x_ld", ctypes.c_int64), ("w_ld", ctypes.c_int64), ("dx_ld", ctypes.c_int64), ("dw_ld", ctypes.c_int64),
+        ("ignore_index", ctypes.c_int64), ("dtype", ctypes.c_int32), ("targets_dtype", ctypes.c_int32),
+        ("dw_dtype", ctypes.c_int32), ("accumulate_dw", ctypes.c_int32), ("reduction", ctypes.c_int32),
+        ("grad_scale", ctypes.c_float),
+    ]
+
+
+assert ctypes.sizeof(fp8z_xent_args) == 88
 
 
 def hparams(lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=1,
@@ -128,6 +143,10 @@ def lib():
         L.fp8z_embedding_grad_workspace.argtypes = [i64, i64, i64]
         L.fp8z_embedding_grad.argtypes = [P, i32, i64, P, i32, i64, P, i32, i64, i64, i64, f32, i64, i32,
                                           P, i64, P, P]
+        XA = ctypes.POINTER(fp8z_xent_args)
+        L.fp8z_linear_xent_workspace.argtypes = [P, P, XA, i32, i64]
+        L.fp8z_linear_xent.argtypes = [P, P, P, XA, P, P, P, P, i64, P, P]
+        L.fp8z_linear_xent_grad.argtypes = [P, P, P, XA, P, P, P, P, P, P, i64, P, P]
         L.fp8z_e4m3_encode_bits.argtypes = [ctypes.c_uint32, i64, P, P]
         L.fp8z_watchdog_selftest.argtypes = [P, i64, P]
         L.fp8z_set_wait_limit_ns.argtypes = [i64]
@@ -139,6 +158,7 @@ def lib():
                 getattr(L, name).restype = ctypes.c_int
         L.fp8z_get_wait_limit_ns.restype = i64
         L.fp8z_embedding_grad_workspace.restype = i64
+        L.fp8z_linear_xent_workspace.restype = i64
         _lib = L
     return _lib
 
@@ -597,6 +617,83 @@ def fp8z_embedding_grad(ids, d_out, d_table, workspace, scale=1.0, padding_idx=-
                                    _dptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
                                    _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
     _check("fp8z_embedding_grad", rc)
+
+
+_REDUCTIONS = {"mean": FP8Z_MEAN, "sum": FP8Z_SUM}
+
+
+def _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accumulate_dw):
+    """(x pointer, w pointer, filled fp8z_xent_args)."""
+    xp, tokens, hidden, x_ld = _matrix(x, "x")
+    wp, vocab, cols, w_ld = _matrix(w, "w")
+    dtype = _dtype_code(x, "x", (FP8Z_BF16, FP8Z_F16))
+    if cols != hidden or w.dtype != x.dtype:
+        raise ValueError(f"w must be [vocab, {hidden}] of {x.dtype}, got {list(w.shape)} of {w.dtype}")
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be 'mean' or 'sum', got {reduction!r}")
+    a = fp8z_xent_args(tokens, hidden, vocab, x_ld, w_ld, hidden, hidden, ignore_index, dtype, FP8Z_I64,
+                       FP8Z_F32, int(bool(accumulate_dw)), _REDUCTIONS[reduction], grad_scale)
+    if targets is not None:
+        if targets.numel() != tokens:
+            raise ValueError(f"targets must hold {tokens} words, got {targets.numel()}")
+        a.targets_dtype = _dtype_code(targets, "targets", (FP8Z_I32, FP8Z_I64))
+    if dx is not None:
+        _, rows, cols, a.dx_ld = _matrix(dx, "dx")
+        if (rows, cols) != (tokens, hidden) or dx.dtype != x.dtype:
+            raise ValueError(f"dx must be [{tokens}, {hidden}] of {x.dtype}, got {list(dx.shape)} of {dx.dtype}")
+    if dw is not None:
+        _, rows, cols, a.dw_ld = _matrix(dw, "dw")
+        if (rows, cols) != (vocab, hidden):
+            raise ValueError(f"dw must be [{vocab}, {hidden}], got {list(dw.shape)}")
+        a.dw_dtype = _dtype_code(dw, "dw", (FP8Z_F32, dtype))
+    return xp, wp, a
+
+
+def fp8z_linear_xent_workspace(x, w, dw=None, piece_words=0):
+    """Bytes of workspace for fp8z_linear_xent(x, w, ..) or, with dw, for
+    fp8z_linear_xent_grad(x, w, .., dw=dw): P is kept for pieces of at most
+    piece_words words (0: at most 1 GiB)."""
+    xp, wp, a = _xent_args(x, w, None, None, dw, -100, "mean", 1.0, False)
+    size = int(lib().fp8z_linear_xent_workspace(xp, wp, ctypes.byref(a), int(dw is not None), int(piece_words)))
+    if size < 0:
+        raise Fp8zError("fp8z_linear_xent_workspace", size)
+    return size
+
+
+def _xent_outputs(tokens, loss, lse, total):
+    import torch
+    if loss.numel() < tokens or (lse is not None and lse.numel() < tokens) or total.numel() < 2:
+        raise ValueError("loss and lse must hold one value per token, total two")
+    return _dptr(loss, torch.float32, "loss"), _dptr(lse, torch.float32, "lse"), _dptr(total, torch.float32, "total")
+
+
+def fp8z_linear_xent(x, w, targets, loss, total, workspace, ignore_index=-100, reduction="mean", lse=None,
+                     dev_status=None, stream=None):
+    """Cross entropy of softmax(x w^T) against targets: loss float32 [tokens], total
+    float32 [2] (mean or sum of the kept tokens' losses, their number), lse
+    optional.  x [tokens, hidden], w [vocab, hidden]: bfloat16 or float16, rows
+    may be strided; targets int64 or int32."""
+    import torch
+    xp, wp, a = _xent_args(x, w, targets, None, None, ignore_index, reduction, 1.0, False)
+    rc = lib().fp8z_linear_xent(xp, wp, _dptr(targets, None, "targets"), ctypes.byref(a),
+                                *_xent_outputs(a.tokens, loss, lse, total), _dptr(workspace, None, "workspace"),
+                                workspace.numel() * workspace.element_size(),
+                                _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
+    _check("fp8z_linear_xent", rc)
+
+
+def fp8z_linear_xent_grad(x, w, targets, loss, total, dx, dw, workspace, ignore_index=-100, reduction="mean",
+                          grad_scale=1.0, accumulate_dw=False, lse=None, dev_status=None, stream=None):
+    """fp8z_linear_xent and the gradients of grad_scale * total[0]: dx of x's type,
+    dw of x's type or float32 (overwritten, or added to with accumulate_dw)."""
+    import torch
+    xp, wp, a = _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accumulate_dw)
+    rc = lib().fp8z_linear_xent_grad(xp, wp, _dptr(targets, None, "targets"), ctypes.byref(a),
+                                     *_xent_outputs(a.tokens, loss, lse, total), dx.data_ptr(), dw.data_ptr(),
+                                     _dptr(workspace, None, "workspace"),
+                                     workspace.numel() * workspace.element_size(),
+                                     _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
+    _check("fp8z_linear_xent_grad", rc)
 
 
 def fp8z_e4m3_encode_bits(first_bits, n, out, stream=None):

@@ -498,6 +498,58 @@ FP8Z_API int fp8z_embedding_grad(const void *ids, int32_t ids_dtype, int64_t tok
                                  int32_t accumulate, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
                                  void *stream);
 
+typedef enum { FP8Z_MEAN = 0, FP8Z_SUM = 1 } fp8z_reduction;
+
+/* Shapes and options of fp8z_linear_xent and fp8z_linear_xent_grad. */
+typedef struct {
+    int64_t tokens, hidden, vocab;
+    int64_t x_ld, w_ld, dx_ld, dw_ld;   /* row strides in elements (dx_ld, dw_ld: gradient only) */
+    int64_t ignore_index;               /* targets of this value take no part                    */
+    int32_t dtype;                      /* of x, w and dx: FP8Z_BF16 or FP8Z_F16                   */
+    int32_t targets_dtype;              /* FP8Z_I32 or FP8Z_I64                                    */
+    int32_t dw_dtype;                   /* FP8Z_F32, or dtype                                      */
+    int32_t accumulate_dw;              /* 1: the gradient is added to dw, 0: dw is overwritten    */
+    int32_t reduction;                  /* fp8z_reduction                                          */
+    float grad_scale;                   /* factor on dx and dw (a loss scale), finite              */
+} fp8z_xent_args;                       /* 88 bytes */
+
+/*
+ * fp8z_linear_xent -- softmax cross entropy of a vocabulary projection:
+ *   l[t][v] = sum_h x[t][h] * w[v][h],  lse[t] = log sum_v exp(l[t][v]),
+ *   loss[t] = lse[t] - l[t][targets[t]],
+ *   total[0] = sum of loss / max(1, kept tokens) (FP8Z_MEAN) or the sum
+ *   (FP8Z_SUM), total[1] = number of kept tokens.
+ * A target equal to ignore_index, or outside [0, vocab) (reported as
+ * FP8Z_EINVAL in *dev_status), has loss 0, takes no part in the total and gives
+ * no gradient.  x [tokens, hidden], w [vocab, hidden], targets [tokens],
+ * loss f32 [tokens], lse f32 [tokens] or NULL, total f32 [2]: device.
+ *
+ * fp8z_linear_xent_grad -- the same, and the gradients of grad_scale * total[0]:
+ *   P[t][v] = (exp(l[t][v] - lse[t]) - [v == targets[t]]) for kept tokens,
+ *   dx = a * P w (of dtype),  dw = a * P^T x (of dw_dtype, or added to dw),
+ *   a = grad_scale / max(1, kept tokens) (FP8Z_MEAN) or grad_scale.
+ * Products run on the tensor cores in FP32; P enters them in dtype (11 or 8
+ * significant bits), as two summands of dtype where dw is FP32 (16 bits or
+ * more).  The logits are never stored: the gradient goes through the vocabulary
+ * in pieces, computes a piece's logits again and keeps P for that piece alone.
+ *
+ * fp8z_linear_xent_workspace -- bytes of workspace (device, 256-byte aligned, no
+ * initialisation) for these arguments, with pieces of at most piece_words words
+ * (0: the default, at most 1 GiB of P).  x and w count by their alignment: rows
+ * that do not all start on 16-byte boundaries, or a hidden size that is not a
+ * multiple of 8, are copied into the workspace first.  The gradient takes the
+ * largest piece that fits the workspace it is given, up to the default.
+ * tokens <= 2^24, hidden <= 2^20, vocab <= 2^28.
+ */
+FP8Z_API int64_t fp8z_linear_xent_workspace(const void *x, const void *w, const fp8z_xent_args *args,
+                                            int32_t with_grad, int64_t piece_words);
+FP8Z_API int fp8z_linear_xent(const void *x, const void *w, const void *targets, const fp8z_xent_args *args,
+                              float *loss, float *lse, float *total, void *workspace, int64_t workspace_bytes,
+                              int32_t *dev_status, void *stream);
+FP8Z_API int fp8z_linear_xent_grad(const void *x, const void *w, const void *targets, const fp8z_xent_args *args,
+                                   float *loss, float *lse, float *total, void *dx, void *dw, void *workspace,
+                                   int64_t workspace_bytes, int32_t *dev_status, void *stream);
+
 /*
  * fp8z_e4m3_encode_bits -- out[i] = E4M3 code (round to nearest even,
  * saturating, as in the step) of the float whose bit pattern is
