@@ -7,11 +7,13 @@
 //   dx = a * P w,   dw = a * P^T x,   a = grad_scale / (number of kept tokens, or 1)
 //
 // The loss needs one product whose epilogue turns each 256 columns of logits
-// into a running maximum and a sum of exponentials per token.  The gradient
-// goes through the vocabulary in pieces: the logits of a piece are computed
-// again, turned into P in the epilogue and written in 16 bits; two products
-// read it.  What is kept is one piece of P, never the logits.
-#include <cfloat>
+// into a maximum and a sum of exponentials per token.  The gradient goes through
+// the vocabulary in pieces: P of a piece, in 16 bits, is what the two other
+// products read.  The buffer that holds one piece of P holds the logits of one
+// piece just as well, so the first pass leaves the last piece's logits there
+// and they become P in place; the pieces before it are multiplied again.  What
+// is kept is one piece, never all the logits of a long batch.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -34,8 +36,11 @@ constexpr int kStages = 4;
 constexpr int kBytesA = kTM * kBK * 2, kBytesB = kTN * kBK * 2, kStageBytes = kBytesA + kBytesB;
 constexpr int kThreads = 256;                          // warp 0 loads, warp 1 multiplies, warps 4-7 read the sums
 constexpr int kTmemCols = 512;                         // two accumulators of 256 columns
+constexpr int kSlab = 32 * 128;                        // staged results of one warp: 32 rows of 128 bytes
+constexpr int kStaging = 4 * 2 * kSlab;
 constexpr int kNumBars = 2 * kStages + 5;
-constexpr int kSmem = kStages * kStageBytes + kNumBars * 8 + 16 + 1024;
+constexpr int kSmem = kStages * kStageBytes + kStaging + kNumBars * 8 + 16 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum Epilogue { kStats, kProb, kSum, kWeight };
@@ -49,20 +54,24 @@ struct MmaArgs {
     int bf16;
     int64_t timeout_ns;
     int32_t* dev_status;
-    // kStats, kProb: rows are tokens, columns words v0 + n of this piece
+    // kStats, kProb: rows are tokens, columns words v0 + n of this launch
     int v0;
-    const int32_t* target;    // -1: takes no part in the loss
+    const void* targets;      // as the caller gave them
+    int targets_wide;
+    int64_t ignore, vocab;
+    const int32_t* target;    // -1: takes no part in the loss (written by rows_kernel)
     float2* part;             // [tile][rows_pad] maximum and sum
     float* target_logit;
     const float* lse;
-    void *p_hi, *p_lo;        // [rows_pad][p_ld]
-    int64_t p_ld;
-    int rows_pad;
+    int keep_from;            // words from here on leave their logits in the piece's buffer
+    uint32_t* ticket;         // of rows_kernel, set to zero here
+    int split_p;              // P in two parts
     float p_scale;
-    // kSum: FP32 [splits][rows_pad][out_ld];  kWeight: out + v0 rows
+    int rows_pad;
+    // kSum: FP32 [splits][rows_pad];  kWeight: rows v0 + m of dw
     void* out;
     int64_t out_ld;
-    int out_dtype, accumulate, vec;
+    int out_dtype, accumulate, staged;
     const float* alpha;
 };
 
@@ -97,26 +106,75 @@ __device__ __forceinline__ float2 unpack16(uint32_t u, int bf16) {
     return __half22float2(h);
 }
 
-// Running maximum and sum of exponentials of one row over the tile's columns.
-__device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const TileAt& t, uint32_t acc, int row) {
-    const int n_valid = min(kTN, A.n - t.n * kTN);
-    const int target = row < A.m ? A.target[row] - (A.v0 + t.n * kTN) : -1;
+__device__ __forceinline__ int load_target(const void* targets, int wide, int64_t ignore, int64_t vocab, int row) {
+    const int64_t y = wide ? static_cast<const int64_t*>(targets)[row] : int64_t(static_cast<const int32_t*>(targets)[row]);
+    return y == ignore || y < 0 || y >= vocab ? -1 : int(y);
+}
+
+// A warp's way out: 32 rows of 128 bytes go to one of two slabs in the layout
+// of a 128-byte-swizzled tensor map, and from there to global memory as one
+// tile, clipped at the tensor's edges.  Rows of 16 bytes per thread would leave
+// half-written 32-byte sectors all over the result.
+struct Stager {
+    uint32_t slab;
+    int which, lane;
+    __device__ __forceinline__ uint32_t begin() {
+        if (lane == 0) bulk_wait_read<1>();          // the slab's last tile but one has been read
+        __syncwarp();
+        return slab + which * kSlab;
+    }
+    __device__ __forceinline__ void put(uint32_t s, int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) const {
+        st_shared_v4(s + lane * 128 + ((chunk ^ (lane & 7)) << 4), a, b, c, d);
+    }
+    template <typename F>
+    __device__ __forceinline__ void end(F store) {
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            store(slab + which * kSlab);
+            bulk_commit();
+        }
+        which ^= 1;
+    }
+};
+
+__device__ __forceinline__ void stage32(Stager& sg, const uint32_t (&r)[32]) {
+    const uint32_t s = sg.begin();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sg.put(s, j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+}
+
+// Maximum and sum of exponentials of one row over the tile's columns.
+__device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
+                                               int row, Stager& sg) {
+    const int col0 = t.n * kTN, n_valid = min(kTN, A.n - col0);
+    const int target = row < A.m ? load_target(A.targets, A.targets_wide, A.ignore, A.vocab, row) - col0 : -1;
+    const bool keep = col0 >= A.keep_from;
     float mx = -INFINITY, sum = 0.0f;
     for (int c = 0; c < n_valid; c += 32) {
         uint32_t r[32];
         tmem_ld32(r, acc + c);
         tmem_wait_ld();
+        if (keep) {
+            stage32(sg, r);
+            sg.end([&](uint32_t s) { tma_store_2d(&out, col0 - A.keep_from + c, row - sg.lane, s); });
+        }
+        if (c + 32 > n_valid) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j >= n_valid) r[j] = __float_as_uint(-INFINITY);
+        }
         float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (c + j >= n_valid) r[j] = __float_as_uint(-INFINITY);
-            top = fmaxf(top, __uint_as_float(r[j]));
-        }
+        for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(r[j]));
         const float m2 = fmaxf(mx, top), ref = m2 == -INFINITY ? 0.0f : m2 * kLog2e;
-        float s = 0.0f;
+        float s = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-        sum = fmaf(sum, ex2(fmaf(mx, kLog2e, -ref)), s);
+        for (int j = 0; j < 32; j += 2) {
+            s += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
+            s2 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -ref));
+        }
+        sum = fmaf(sum, ex2(fmaf(mx, kLog2e, -ref)), s + s2);
         mx = m2;
         if (target >= c && target < c + 32) {
             float x = 0.0f;
@@ -126,49 +184,69 @@ __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const TileAt& t
             A.target_logit[row] = x;
         }
     }
-    if (row < A.m) A.part[size_t(A.v0 / kTN + t.n) * A.rows_pad + row] = make_float2(mx, sum);
+    if (row < A.m) A.part[size_t(t.n) * A.rows_pad + row] = make_float2(mx, sum);
 }
 
-// P in 16 bits, and what the rounding left in another 16 where FP32 weight
-// gradients are asked for.  Rows and columns past the end are written as zeros:
-// the products read whole tiles.
-__device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const TileAt& t, uint32_t acc, int row) {
+// P of eight neighbouring words of one row, times p_scale: in 16 bits, and what
+// that rounding left in another 16.  ref = lse * log2(e); target: the row's word
+// relative to the first of the eight; valid: words before the vocabulary's end.
+__device__ __forceinline__ void prob8(const uint32_t* r, float ref, int target, int valid, bool kept, float p_scale,
+                                      int bf16, uint32_t (&h)[4], uint32_t (&l)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float p[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int j = i * 2 + k;
+            float v = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
+            if (target == j) v -= 1.0f;
+            p[k] = kept && j < valid ? v * p_scale : 0.0f;
+        }
+        h[i] = pack16(p[0], p[1], bf16);
+        const float2 w = unpack16(h[i], bf16);
+        l[i] = pack16(p[0] - w.x, p[1] - w.y, bf16);
+    }
+}
+
+// Rows and columns past the end become zeros: the products read whole tiles.
+// The buffer holds, for each row and tile of 256 words, 512 bytes of P and 512
+// bytes of its second part: the room of the tile's FP32 logits.
+__device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
+                                              int row, Stager& sg) {
     const int n_valid = min(kTN, A.n - t.n * kTN);
     const int y = row < A.m ? A.target[row] : -1;
     const int target = y - (A.v0 + t.n * kTN);
     const float ref = y >= 0 ? A.lse[row] * kLog2e : 0.0f;
-    const size_t at = size_t(row) * A.p_ld + size_t(t.n) * kTN;
-    uint4* hi = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.p_hi) + at);
-    uint4* lo = A.p_lo ? reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.p_lo) + at) : nullptr;
-    for (int c = 0; c < kTN; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(r, acc + c);
-        tmem_wait_ld();
+    for (int c = 0; c < kTN; c += 64) {
+        uint32_t h[32], l[32];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t h[4], l[4];
+        for (int half = 0; half < 2; ++half) {
+            uint32_t r[32];
+            tmem_ld32(r, acc + c + half * 32);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float p[2];
+            for (int q = 0; q < 4; ++q) {
+                const int at = c + half * 32 + q * 8;
+                uint32_t hq[4], lq[4];
+                prob8(r + q * 8, ref, target - at, n_valid - at, y >= 0, A.p_scale, A.bf16, hq, lq);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int j = q * 8 + i * 2 + k;
-                    float v = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-                    if (target == c + j) v -= 1.0f;
-                    p[k] = (y >= 0 && c + j < n_valid) ? v * A.p_scale : 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    h[half * 16 + q * 4 + i] = hq[i];
+                    l[half * 16 + q * 4 + i] = lq[i];
                 }
-                h[i] = pack16(p[0], p[1], A.bf16);
-                const float2 w = unpack16(h[i], A.bf16);
-                l[i] = pack16(p[0] - w.x, p[1] - w.y, A.bf16);
             }
-            hi[c / 8 + q] = make_uint4(h[0], h[1], h[2], h[3]);
-            if (lo) lo[c / 8 + q] = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+        stage32(sg, h);
+        sg.end([&](uint32_t s) { tma_store_3d(&out, c, 2 * t.n, row - sg.lane, s); });
+        if (A.split_p) {
+            stage32(sg, l);
+            sg.end([&](uint32_t s) { tma_store_3d(&out, c, 2 * t.n + 1, row - sg.lane, s); });
         }
     }
 }
 
-__device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const TileAt& t, uint32_t acc, int row) {
-    float* out = static_cast<float*>(A.out) + (size_t(t.split) * A.rows_pad + row) * A.out_ld + size_t(t.n) * kTN;
+__device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
+                                             int row, Stager& sg) {
     for (int c = 0; c < kTN && t.n * kTN + c < A.n; c += 32) {
         uint32_t r[32];
         tmem_ld32(r, acc + c);
@@ -176,86 +254,93 @@ __device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const TileAt& t, 
         if (t.k0 == t.k1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = 0;
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            if (t.n * kTN + c + j >= A.n) break;           // out_ld is a multiple of 4
-            float4* p = reinterpret_cast<float4*>(out + c + j);
-            float4 v = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
-                                   __uint_as_float(r[j + 3]));
-            if (A.accumulate) {
-                const float4 o = *p;
-                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-            }
-            *p = v;
-        }
+        stage32(sg, r);
+        const int x = t.n * kTN + c, y = t.split * A.rows_pad + row - sg.lane;
+        if (A.accumulate) sg.end([&](uint32_t s) { tma_add_2d(&out, x, y, s); });
+        else sg.end([&](uint32_t s) { tma_store_2d(&out, x, y, s); });
     }
 }
 
+// A dw whose rows do not all start on 16-byte boundaries, and sums of 16-bit
+// gradients (one rounding of the whole sum), are written by the threads.
 template <typename T>
-__device__ __forceinline__ void weight_chunk(T* p, const uint32_t (&r)[32], int n, float a, const MmaArgs& A) {
-    if (A.vec && n >= 32) {
+__device__ __forceinline__ void weight_chunk(T* p, const uint32_t (&r)[32], int n, float a, bool accumulate) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            Pack<T, 8> y;
-            if (A.accumulate) y = ld_plain<T, 8>(p + j);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = __uint_as_float(r[j + i]) * a;
-                y.v[i] = Elem<T>::narrow(A.accumulate ? Elem<T>::widen(y.v[i]) + v : v);
-            }
-            st_vec<T, 8>(p + j, y);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j < n) {
-                const float v = __uint_as_float(r[j]) * a;
-                p[j] = Elem<T>::narrow(A.accumulate ? Elem<T>::widen(p[j]) + v : v);
-            }
+    for (int j = 0; j < 32; ++j) {
+        if (j < n) {
+            const float v = __uint_as_float(r[j]) * a;
+            p[j] = Elem<T>::narrow(accumulate ? Elem<T>::widen(p[j]) + v : v);
         }
     }
 }
 
-__device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const TileAt& t, uint32_t acc, int row) {
+__device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
+                                                int row, Stager& sg) {
     const float a = *A.alpha;
+    const int y = A.v0 + row - sg.lane;
+    if (A.staged && A.out_dtype != FP8Z_F32) {
+        for (int c = 0; c < kTN && t.n * kTN + c < A.n; c += 64) {
+            uint32_t h[32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t r[32];
+                tmem_ld32(r, acc + c + half * 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    h[half * 16 + j] =
+                        pack16(__uint_as_float(r[2 * j]) * a, __uint_as_float(r[2 * j + 1]) * a, A.bf16);
+            }
+            stage32(sg, h);
+            sg.end([&](uint32_t s) { tma_store_2d(&out, t.n * kTN + c, y, s); });
+        }
+        return;
+    }
     for (int c = 0; c < kTN && t.n * kTN + c < A.n; c += 32) {
         uint32_t r[32];
         tmem_ld32(r, acc + c);
         tmem_wait_ld();
-        if (t.k0 == t.k1)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0;
-        if (row >= A.m) continue;
         const int col = t.n * kTN + c;
-        const size_t at = size_t(A.v0 + row) * A.out_ld + col;
-        const int n = A.n - col;
-        if (A.out_dtype == FP8Z_F32) weight_chunk(static_cast<float*>(A.out) + at, r, n, a, A);
-        else if (A.out_dtype == FP8Z_BF16) weight_chunk(static_cast<__nv_bfloat16*>(A.out) + at, r, n, a, A);
-        else weight_chunk(static_cast<__half*>(A.out) + at, r, n, a, A);
+        if (A.staged) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a);
+            stage32(sg, r);
+            if (A.accumulate) sg.end([&](uint32_t s) { tma_add_2d(&out, col, y, s); });
+            else sg.end([&](uint32_t s) { tma_store_2d(&out, col, y, s); });
+        } else if (row < A.m) {
+            const size_t at = size_t(A.v0 + row) * A.out_ld + col;
+            const int n = A.n - col;
+            if (A.out_dtype == FP8Z_F32) weight_chunk(static_cast<float*>(A.out) + at, r, n, a, A.accumulate);
+            else if (A.out_dtype == FP8Z_BF16) weight_chunk(static_cast<__nv_bfloat16*>(A.out) + at, r, n, a, A.accumulate);
+            else weight_chunk(static_cast<__half*>(A.out) + at, r, n, a, A.accumulate);
+        }
     }
 }
 
 // One block of 128 x 256 results at a time: a warp keeps kStages tiles of
 // operands in flight, one thread issues the products into one of two
 // accumulators in tensor memory while four warps read the other.
-template <bool kAMn, bool kBMn, int kEpi>
+template <int kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
     mma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-               const __grid_constant__ MmaArgs A) {
+               const __grid_constant__ CUtensorMap tc, const __grid_constant__ MmaArgs A) {
+    constexpr bool kAMn = kEpi == kWeight, kBMn = kEpi == kSum || kEpi == kWeight;   // operands along M or N
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_addr(smem_raw));
-    const uint32_t bars = base + kStages * kStageBytes;
+    constexpr int kBarsAt = kStages * kStageBytes + kStaging;
+    const uint32_t bars = base + kBarsAt;
     auto full = [&](int s) { return bars + s * 8; };
     auto empty = [&](int s) { return bars + (kStages + s) * 8; };
     auto tfull = [&](int b) { return bars + (2 * kStages + b) * 8; };
     auto tempty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };
     const uint32_t drain = bars + (2 * kStages + 4) * 8;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kStages * kStageBytes + kNumBars * 8);
-    volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(smem + kStages * kStageBytes + kNumBars * 8 + 8);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBarsAt + kNumBars * 8);
+    volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(smem + kBarsAt + kNumBars * 8 + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+        if (kEpi == kStats && blockIdx.x == 0) *A.ticket = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
@@ -290,13 +375,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kBytesA;
                     mbar_arrive_expect_tx(full(s), kStageBytes);
-                    const int ka = k * kBK, kb = (k >= A.b_wrap ? k - A.b_wrap : k) * kBK + A.b_k0;
-                    if constexpr (kAMn) {
+                    const int kw = k >= A.b_wrap ? k - A.b_wrap : k, kb = kw * kBK + A.b_k0;
+                    if constexpr (kEpi == kWeight) {         // P^T: 128 words, 64 tokens of one part
 #pragma unroll
-                        for (int j = 0; j < kTM / 64; ++j)
-                            tma_load_2d(sa + j * (64 * kBK * 2), &ta, at.m * kTM + j * 64, ka, full(s));
+                        for (int j = 0; j < kTM / 64; ++j) {
+                            const int word = at.m * kTM + j * 64;
+                            tma_load_3d(sa + j * (64 * kBK * 2), &ta, word % kTN, word / kTN * 2 + (k >= A.b_wrap),
+                                        kw * kBK, full(s));
+                        }
+                    } else if constexpr (kEpi == kSum) {     // P: 128 tokens, 64 words of the first part
+                        tma_load_3d(sa, &ta, k * kBK % kTN, k * kBK / kTN * 2, at.m * kTM, full(s));
                     } else {
-                        tma_load_2d(sa, &ta, ka, at.m * kTM, full(s));
+                        tma_load_2d(sa, &ta, k * kBK, at.m * kTM, full(s));
                     }
                     if constexpr (kBMn) {
 #pragma unroll
@@ -354,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 4) {
         const int quarter = warp - 4;
+        Stager sg{base + kStages * kStageBytes + quarter * 2 * kSlab, 0, lane};
         int b = 0, bph = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
             const TileAt at = tile_at(A, t);
@@ -361,16 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t acc = tmem + b * kTN + (uint32_t(quarter * 32) << 16);
             const int row = at.m * kTM + quarter * 32 + lane;
-            if constexpr (kEpi == kStats) epilogue_stats(A, at, acc, row);
-            else if constexpr (kEpi == kProb) epilogue_prob(A, at, acc, row);
-            else if constexpr (kEpi == kSum) epilogue_sum(A, at, acc, row);
-            else epilogue_weight(A, at, acc, row);
+            if constexpr (kEpi == kStats) epilogue_stats(A, tc, at, acc, row, sg);
+            else if constexpr (kEpi == kProb) epilogue_prob(A, tc, at, acc, row, sg);
+            else if constexpr (kEpi == kSum) epilogue_sum(A, tc, at, acc, row, sg);
+            else epilogue_weight(A, tc, at, acc, row, sg);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty(b));
             if (b) bph ^= 1;
             b ^= 1;
         }
+        if (lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -381,17 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ small kernels
-// Targets as int32 (-1: ignored or out of range), once.
-__global__ void target_kernel(const void* __restrict__ targets, int wide, int n, int64_t ignore, int64_t vocab,
-                              int32_t* __restrict__ out, int32_t* dev_status) {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n) return;
-    const int64_t y = wide ? static_cast<const int64_t*>(targets)[i] : static_cast<const int32_t*>(targets)[i];
-    const bool ok = y != ignore && y >= 0 && y < vocab;
-    if (y != ignore && !ok) report_status(dev_status, FP8Z_EINVAL);
-    out[i] = ok ? int32_t(y) : -1;
-}
-
 // 16-bit rows copied to a stride the tensor maps can step over, zeros after the end.
 __global__ void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, int cols_pad,
                                 uint16_t* __restrict__ dst) {
@@ -400,63 +481,139 @@ __global__ void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, in
             dst[r * cols_pad + c] = c < cols ? src[r * ld + c] : uint16_t(0);
 }
 
-// lse and loss of 32 rows from the tiles' maxima and sums, eight threads a row.
-__global__ void __launch_bounds__(256) rows_kernel(const float2* __restrict__ part, int tiles, int n, int rows_pad,
-                                                   const int32_t* __restrict__ target,
-                                                   const float* __restrict__ target_logit, float* __restrict__ lse_ws,
-                                                   float* __restrict__ lse_out, float* __restrict__ loss) {
-    __shared__ float2 sh[8][32];
-    const int r = threadIdx.x & 31, g = threadIdx.x >> 5, row = blockIdx.x * 32 + r;
+// lse and loss of 32 rows from the tiles' maxima and sums, 32 threads a row; the
+// block that finishes last adds up the blocks' sums, in order.
+struct BlockTotal {
+    double loss;
+    int64_t kept;
+};
+
+__global__ void __launch_bounds__(1024) rows_kernel(const float2* __restrict__ part, int tiles, int n, int rows_pad,
+                                                    const void* __restrict__ targets, int wide, int64_t ignore,
+                                                    int64_t vocab, const float* __restrict__ target_logit,
+                                                    int32_t* __restrict__ target, float* __restrict__ lse_ws,
+                                                    float* __restrict__ lse_out, float* __restrict__ loss,
+                                                    BlockTotal* __restrict__ totals, uint32_t* __restrict__ ticket,
+                                                    int mean, float scale, float* __restrict__ total,
+                                                    float* __restrict__ alpha, int32_t* dev_status) {
+    __shared__ float2 sh[32][33];
+    __shared__ bool last;
+    const int r = threadIdx.x & 31, g = threadIdx.x >> 5;
     float m = -INFINITY, s = 0.0f;
     auto add = [&](float2 p) {
         const float m2 = fmaxf(m, p.x), ref = m2 == -INFINITY ? 0.0f : m2;
         s = s * ex2((m - ref) * kLog2e) + p.y * ex2((p.x - ref) * kLog2e);
         m = m2;
     };
-    if (row < n)
-        for (int t = g; t < tiles; t += 8) add(part[size_t(t) * rows_pad + row]);
-    sh[g][r] = make_float2(m, s);
+    {
+        const int row = blockIdx.x * 32 + r;
+        if (row < n) {
+            int t = g;
+            for (; t + 96 < tiles; t += 128) {
+                float2 q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = part[size_t(t + 32 * i) * rows_pad + row];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) add(q[i]);
+            }
+            for (; t < tiles; t += 32) add(part[size_t(t) * rows_pad + row]);
+        }
+    }
+    sh[r][g] = make_float2(m, s);
     __syncthreads();
-    if (g != 0 || row >= n) return;
-    for (int k = 1; k < 8; ++k) add(sh[k][r]);
-    const float lse = m + logf(s);
-    lse_ws[row] = lse;
-    if (lse_out) lse_out[row] = lse;
-    loss[row] = target[row] >= 0 ? lse - target_logit[row] : 0.0f;
+    const int row = blockIdx.x * 32 + g;               // from here a warp a row
+    const float2 mine = sh[g][r];
+    m = mine.x;
+    s = mine.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        add(make_float2(__shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o)));
+    __syncthreads();
+    if (r == 0) {
+        float out = 0.0f;
+        int y = -1;
+        if (row < n) {
+            y = load_target(targets, wide, ignore, vocab, row);
+            if (y < 0) {
+                const int64_t raw = wide ? static_cast<const int64_t*>(targets)[row]
+                                         : int64_t(static_cast<const int32_t*>(targets)[row]);
+                if (raw != ignore) report_status(dev_status, FP8Z_EINVAL);
+            }
+            const float lse = m + logf(s);
+            out = y >= 0 ? lse - target_logit[row] : 0.0f;
+            target[row] = y;
+            lse_ws[row] = lse;
+            if (lse_out) lse_out[row] = lse;
+            loss[row] = out;
+        }
+        sh[0][g] = make_float2(out, y >= 0 ? 1.0f : 0.0f);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        BlockTotal b = {0.0, 0};
+        for (int i = 0; i < 32; ++i) {
+            b.loss += double(sh[0][i].x);
+            b.kept += sh[0][i].y != 0.0f;
+        }
+        totals[blockIdx.x] = b;
+        __threadfence();
+        last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last || g != 0) return;
+    __threadfence();
+    BlockTotal b = {0.0, 0};
+    for (int i = r; i < int(gridDim.x); i += 32) {
+        b.loss += __ldcg(&totals[i].loss);
+        b.kept += __ldcg(reinterpret_cast<const long long*>(&totals[i].kept));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        b.loss += __shfl_down_sync(0xFFFFFFFFu, b.loss, o);
+        b.kept += __shfl_down_sync(0xFFFFFFFFu, b.kept, o);
+    }
+    if (r == 0) {
+        const double by = mean ? double(b.kept > 0 ? b.kept : 1) : 1.0;
+        total[0] = float(b.loss / by);
+        total[1] = float(b.kept);
+        if (alpha) *alpha = float(double(scale) / by);
+    }
 }
 
-__global__ void __launch_bounds__(1024) total_kernel(const float* __restrict__ loss, const int32_t* __restrict__ target,
-                                                     int n, int mean, float scale, float* __restrict__ total,
-                                                     float* __restrict__ alpha) {
-    __shared__ double sh[32];
-    __shared__ int sc[32];
-    double s = 0.0;
-    int c = 0;
-    for (int i = threadIdx.x; i < n; i += 1024) {
-        s += double(loss[i]);
-        c += target[i] >= 0;
+// The kept logits of a piece become P, in place: a warp takes a row's 256 words
+// (1 KB), reads all of it, and writes the two parts over it.
+constexpr int kProbTiles = 4;
+__global__ void __launch_bounds__(256) prob_kernel(uint8_t* __restrict__ p, int64_t row_bytes, int tiles, int words, int n,
+                                                   int v0, const int32_t* __restrict__ target,
+                                                   const float* __restrict__ lse, float p_scale, int bf16, int split_p) {
+    const int row = blockIdx.x, lane = threadIdx.x & 31;
+    const int y = row < n ? target[row] : -1;
+    const float ref = y >= 0 ? lse[row] * kLog2e : 0.0f;
+    const int t0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kProbTiles;
+    uint4 in[kProbTiles][2];
+#pragma unroll
+    for (int i = 0; i < kProbTiles; ++i) {
+        if (t0 + i >= tiles) break;
+        const uint4* q = reinterpret_cast<const uint4*>(p + row * row_bytes + int64_t(t0 + i) * 1024) + lane * 2;
+        in[i][0] = q[0];
+        in[i][1] = q[1];
     }
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_down_sync(0xFFFFFFFFu, s, o);
-        c += __shfl_down_sync(0xFFFFFFFFu, c, o);
+    __syncwarp();                                      // the whole warp has read what it now overwrites
+#pragma unroll
+    for (int i = 0; i < kProbTiles; ++i) {
+        if (t0 + i >= tiles) break;
+        const uint32_t r[8] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w,
+                               in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
+        const int at = (t0 + i) * kTN + lane * 8;
+        uint32_t h[4], l[4];
+        prob8(r, ref, y - v0 - at, words - at, y >= 0, p_scale, bf16, h, l);
+        uint4* q = reinterpret_cast<uint4*>(p + row * row_bytes + int64_t(t0 + i) * 1024);
+        q[lane] = make_uint4(h[0], h[1], h[2], h[3]);
+        if (split_p) q[32 + lane] = make_uint4(l[0], l[1], l[2], l[3]);
     }
-    if ((threadIdx.x & 31) == 0) {
-        sh[threadIdx.x >> 5] = s;
-        sc[threadIdx.x >> 5] = c;
-    }
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    s = 0.0;
-    c = 0;
-    for (int w = 0; w < 32; ++w) {
-        s += sh[w];
-        c += sc[w];
-    }
-    const double by = mean ? double(c > 0 ? c : 1) : 1.0;
-    total[0] = float(s / by);
-    total[1] = float(c);
-    if (alpha) *alpha = float(double(scale) / by);
 }
+
+__global__ void empty_total_kernel(float* total) { total[threadIdx.x] = 0.0f; }
 
 // dx = a * the sum of the K parts.
 template <typename T>
@@ -491,10 +648,10 @@ struct Layout {
     int64_t rows_pad, hidden_pad, vocab_tiles, piece, pieces, parts;
     int splits;
     bool copy_x, copy_w;
-    size_t x, w, target, target_logit, lse, part, alpha, p, sum, total;
+    size_t x, w, target, target_logit, lse, part, totals, alpha, p, sum, total;
 };
 
-constexpr int64_t kPieceBytes = 1LL << 30;        // of P, unless the caller's workspace is smaller
+constexpr int64_t kPieceBytes = 1LL << 30;        // of one piece, see layout()
 constexpr int kSms = 152;                         // the layout's, the same for the size query and the call
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
@@ -520,6 +677,24 @@ bool map_ok(const void* p, int64_t ld, int64_t hidden) {
     return host::aligned(p, 16) && ld % 8 == 0 && hidden % 8 == 0;
 }
 
+// Parts of dx's sum over the vocabulary.  Too few tiles leave SMs idle, and a
+// last wave that is not full leaves them idle too; every part costs a write and
+// a read of FP32 sums.  Times in ns: 135 for a tile's K block of 64 (the tensor
+// cores' rate at 1.9 GHz), 8 bytes of an element at 6.5 TB/s for a part.
+int dx_splits(int64_t tiles, int64_t k_blocks, int64_t elems) {
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 64 && s * 4 <= k_blocks; ++s) {
+        const double waves = double((tiles * s + kSms - 1) / kSms);
+        const double t = waves * double((k_blocks + s - 1) / s) * 135.0 + double(s) * double(elems) * 8.0 / 6500.0;
+        if (s == 1 || t < least) {
+            least = t;
+            best = s;
+        }
+    }
+    return best;
+}
+
 Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int64_t have) {
     Layout L;
     std::memset(&L, 0, sizeof(L));
@@ -539,49 +714,69 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int6
     L.target = take(L.rows_pad * 4);
     L.target_logit = take(L.rows_pad * 4);
     L.lse = take(L.rows_pad * 4);
-    L.alpha = take(4);
+    L.alpha = take(8);
     L.part = take(L.vocab_tiles * L.rows_pad * 8);
+    L.totals = take((L.rows_pad / 32) * sizeof(BlockTotal));
     if (grad) {
         L.parts = a.dw_dtype == FP8Z_F32 ? 2 : 1;
-        const int64_t dx_tiles = L.rows_pad / kTM * ((L.hidden_pad + kTN - 1) / kTN);
-        const int64_t row_bytes = L.rows_pad * 2 * L.parts;          // of one word in P
-        // few rows: the dx product is cut along the vocabulary until every SM has a part
-        int64_t splits = (kSms + dx_tiles - 1) / dx_tiles;
-        const int64_t vocab_blocks = L.vocab_tiles * (kTN / kBK);
-        if (splits > vocab_blocks / 4) splits = vocab_blocks / 4;
-        L.splits = int(splits < 1 ? 1 : splits);
-        L.sum = take(int64_t(L.splits) * L.rows_pad * up(L.hidden_pad, 4) * 4);
-        int64_t room = kPieceBytes;
+        L.splits = dx_splits(L.rows_pad / kTM * ((L.hidden_pad + kTN - 1) / kTN), L.vocab_tiles * (kTN / kBK),
+                             L.rows_pad * L.hidden_pad);
+        L.sum = take(int64_t(L.splits) * L.rows_pad * L.hidden_pad * 4);
+        // One piece takes 4 bytes a word and token.  By default it is at most 1 GiB, or the size of
+        // the FP32 dw where that is more: what the call keeps stays below what the caller keeps.
+        int64_t room = std::max(kPieceBytes, a.vocab * a.hidden * 4);
         if (have >= 0 && have - int64_t(at) < room) room = have - int64_t(at);
-        int64_t tiles = room / (row_bytes * kTN);
-        if (tiles < 1) tiles = 1;
-        if (tiles > L.vocab_tiles) tiles = L.vocab_tiles;
+        const int64_t tile_bytes = L.rows_pad * kTN * 4;
+        const int64_t tiles = std::min(std::max<int64_t>(room / tile_bytes, 1), L.vocab_tiles);
         L.pieces = (L.vocab_tiles + tiles - 1) / tiles;
         L.piece = (L.vocab_tiles + L.pieces - 1) / L.pieces * kTN;       // equal pieces
-        L.p = take(row_bytes * L.piece);
+        L.pieces = (L.vocab_tiles * kTN + L.piece - 1) / L.piece;
+        L.p = take(L.rows_pad * L.piece * 4);
     }
     L.total = at;
     return L;
 }
 
-bool make_map(CUtensorMap* map, const void* p, int64_t inner, int64_t rows, int64_t ld, int box_inner, int box_rows) {
+// Tensor maps with the 128-byte swizzle: a box is 128 bytes wide.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* p, const cuuint64_t* dims,
+              const cuuint64_t* strides, const cuuint32_t* box) {
     const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(host::tensor_map_encoder());
     if (!enc) return false;
     std::memset(map, 0, sizeof(*map));
-    const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(rows)}, strides[1] = {cuuint64_t(ld * 2)};
-    const cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(box_rows)}, estr[2] = {1, 1};
-    // 16-bit elements move as they are, whichever type they hold
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, type, cuuint32_t(rank), const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kAMn, bool kBMn, int kEpi>
-int launch_mma(const CUtensorMap& ta, const CUtensorMap& tb, const MmaArgs& A, int sms, cudaStream_t st) {
-    const auto k = &mma_kernel<kAMn, kBMn, kEpi>;
+// 16-bit elements move as they are, whichever of the two types they hold.
+bool map_16(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(ld * 2)};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box);
+}
+
+bool map_f32(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld) {
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(ld * 4)};
+    const cuuint32_t box[2] = {32, 32};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p, dims, strides, box);
+}
+
+// The piece's buffer as P: 256 words, the two parts of each tile in turn, rows.
+bool map_p(CUtensorMap* map, const void* p, int64_t piece, int64_t rows, int box_rows) {
+    const cuuint64_t dims[3] = {cuuint64_t(kTN), cuuint64_t(piece / kTN * 2), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {kTN * 2, cuuint64_t(piece * 4)};
+    const cuuint32_t box[3] = {64, 1, cuuint32_t(box_rows)};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box);
+}
+
+template <int kEpi>
+int launch_mma(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const MmaArgs& A, int sms,
+               cudaStream_t st) {
+    const auto k = &mma_kernel<kEpi>;
     if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), 12 + kEpi, kSmem)) return rc;
     const int64_t tiles = int64_t(A.mt) * A.nt * A.splits;
-    k<<<unsigned(tiles < sms ? tiles : sms), kThreads, kSmem, st>>>(ta, tb, A);
+    k<<<unsigned(tiles < sms ? tiles : sms), kThreads, kSmem, st>>>(ta, tb, tc, A);
     return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA;
 }
 
@@ -610,16 +805,17 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     auto* lse_ws = reinterpret_cast<float*>(ws + L.lse);
     auto* alpha = reinterpret_cast<float*>(ws + L.alpha);
     auto* part = reinterpret_cast<float2*>(ws + L.part);
+    const auto done = [] { return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA; };
 
     if (n == 0) {
-        total_kernel<<<1, 1024, 0, st>>>(loss, target, 0, a.reduction == FP8Z_MEAN, 1.0f, total, nullptr);
+        empty_total_kernel<<<1, 2, 0, st>>>(total);
         if (grad && !a.accumulate_dw) {
             if (a.dw_dtype == FP8Z_F32)
                 zero_rows_kernel<<<sms * 8, 256, 0, st>>>(static_cast<float*>(dw), a.dw_ld, a.vocab, hidden);
             else
                 zero_rows_kernel<<<sms * 8, 256, 0, st>>>(static_cast<__half*>(dw), a.dw_ld, a.vocab, hidden);
         }
-        return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA;
+        return done();
     }
     const void *xp = x, *wp = w;
     int64_t x_ld = a.x_ld, w_ld = a.w_ld;
@@ -635,11 +831,13 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         wp = ws + L.w;
         w_ld = L.hidden_pad;
     }
-    target_kernel<<<(n + 255) / 256, 256, 0, st>>>(targets, a.targets_dtype == FP8Z_I64, n, a.ignore_index, a.vocab,
-                                                   target, dev_status);
-    CUtensorMap x_k, w_k;
-    if (!make_map(&x_k, xp, L.hidden_pad, n, x_ld, kBK, kTM) || !make_map(&w_k, wp, L.hidden_pad, vocab, w_ld, kBK, kTN))
+    uint8_t* p = ws + L.p;
+    CUtensorMap x_k, w_k, logits;
+    if (!map_16(&x_k, xp, L.hidden_pad, n, x_ld, kTM) || !map_16(&w_k, wp, L.hidden_pad, vocab, w_ld, kTN))
         return FP8Z_ECUDA;
+    if (!grad) logits = w_k;                        // not used
+    else if (!map_f32(&logits, p, L.piece, L.rows_pad, L.piece)) return FP8Z_ECUDA;
+    const int last = grad ? int((L.pieces - 1) * L.piece) : vocab;      // the piece whose logits stay
     MmaArgs A;
     std::memset(&A, 0, sizeof(A));
     A.bf16 = a.dtype == FP8Z_BF16;
@@ -652,51 +850,62 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.nt = int(L.vocab_tiles);
     A.splits = 1;
     A.kb = A.b_wrap = int((L.hidden_pad + kBK - 1) / kBK);
+    A.targets = targets;
+    A.targets_wide = a.targets_dtype == FP8Z_I64;
+    A.ignore = a.ignore_index;
+    A.vocab = a.vocab;
     A.target = target;
     A.part = part;
     A.target_logit = target_logit;
-    if (int rc = launch_mma<false, false, kStats>(x_k, w_k, A, sms, st)) return rc;
-    rows_kernel<<<(n + 31) / 32, 256, 0, st>>>(part, A.nt, n, A.rows_pad, target, target_logit, lse_ws, lse, loss);
+    A.keep_from = last;
+    A.ticket = reinterpret_cast<uint32_t*>(alpha + 1);
+    if (int rc = launch_mma<kStats>(x_k, w_k, logits, A, sms, st)) return rc;
     // FP16 P is kept times 2^12: probabilities down to 2^-36 stay normal numbers or close
     const float p_scale = A.bf16 ? 1.0f : 4096.0f;
-    total_kernel<<<1, 1024, 0, st>>>(loss, target, n, a.reduction == FP8Z_MEAN, grad ? a.grad_scale / p_scale : 1.0f,
-                                     total, grad ? alpha : nullptr);
-    if (!grad) return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA;
+    rows_kernel<<<(n + 31) / 32, 1024, 0, st>>>(part, A.nt, n, A.rows_pad, targets, A.targets_wide, A.ignore, A.vocab,
+                                                target_logit, target, lse_ws, lse, loss,
+                                                reinterpret_cast<BlockTotal*>(ws + L.totals), A.ticket,
+                                                a.reduction == FP8Z_MEAN, grad ? a.grad_scale / p_scale : 1.0f, total,
+                                                grad ? alpha : nullptr, dev_status);
+    if (!grad) return done();
 
-    auto* p_hi = ws + L.p;
-    auto* p_lo = L.parts == 2 ? p_hi + L.rows_pad * L.piece * 2 : nullptr;
     auto* sum = reinterpret_cast<float*>(ws + L.sum);
-    CUtensorMap p_k, w_mn, p_mn, x_mn;
-    if (!make_map(&p_k, p_hi, L.piece, L.rows_pad, L.piece, kBK, kTM) ||
-        !make_map(&w_mn, wp, L.hidden_pad, vocab, w_ld, 64, kBK) ||
-        !make_map(&p_mn, p_hi, L.piece, L.rows_pad * L.parts, L.piece, 64, kBK) ||
-        !make_map(&x_mn, xp, L.hidden_pad, n, x_ld, 64, kBK))
+    const bool dw_rows = host::aligned(dw, 16) && (a.dw_ld * dtype_bytes(a.dw_dtype)) % 16 == 0;
+    CUtensorMap p_k, w_mn, p_mn, x_mn, p_out, sum_out, dw_out = x_k;
+    if (!map_p(&p_k, p, L.piece, L.rows_pad, kTM) || !map_16(&w_mn, wp, L.hidden_pad, vocab, w_ld, kBK) ||
+        !map_p(&p_mn, p, L.piece, L.rows_pad, kBK) || !map_16(&x_mn, xp, L.hidden_pad, n, x_ld, kBK) ||
+        !map_p(&p_out, p, L.piece, L.rows_pad, 32) ||
+        !map_f32(&sum_out, sum, L.hidden_pad, L.rows_pad * L.splits, L.hidden_pad))
         return FP8Z_ECUDA;
-    for (int64_t i = 0; i < L.pieces; ++i) {
+    if (dw_rows && !(a.dw_dtype == FP8Z_F32 ? map_f32(&dw_out, dw, hidden, vocab, a.dw_ld)
+                                            : map_16(&dw_out, dw, hidden, vocab, a.dw_ld, 32)))
+        return FP8Z_ECUDA;
+    for (int64_t i = L.pieces - 1; i >= 0; --i) {
         const int v0 = int(i * L.piece);
-        if (v0 >= vocab) break;
         const int words = int(a.vocab - v0 < L.piece ? a.vocab - v0 : L.piece), tiles = (words + kTN - 1) / kTN;
-        MmaArgs Q = A;                                  // P of the piece
-        Q.n = words;
-        Q.nt = tiles;
-        Q.v0 = v0;
-        Q.b_n0 = v0;
-        Q.lse = lse_ws;
-        Q.p_hi = p_hi;
-        Q.p_lo = p_lo;
-        Q.p_ld = L.piece;
-        Q.p_scale = p_scale;
-        if (int rc = launch_mma<false, false, kProb>(x_k, w_k, Q, sms, st)) return rc;
+        if (v0 == last) {
+            const dim3 grid(unsigned(L.rows_pad), unsigned((tiles + 8 * kProbTiles - 1) / (8 * kProbTiles)));
+            prob_kernel<<<grid, 256, 0, st>>>(p, L.piece * 4, tiles, words, n, v0, target, lse_ws, p_scale, A.bf16,
+                                              L.parts == 2);
+        } else {
+            MmaArgs Q = A;                              // the piece's logits again, as P
+            Q.n = words;
+            Q.nt = tiles;
+            Q.v0 = v0;
+            Q.b_n0 = v0;
+            Q.lse = lse_ws;
+            Q.split_p = L.parts == 2;
+            Q.p_scale = p_scale;
+            if (int rc = launch_mma<kProb>(x_k, w_k, p_out, Q, sms, st)) return rc;
+        }
         MmaArgs D = A;                                  // dx += P w
         D.n = int(L.hidden_pad);
         D.nt = int((L.hidden_pad + kTN - 1) / kTN);
         D.kb = D.b_wrap = tiles * (kTN / kBK);
         D.splits = L.splits;
         D.b_k0 = v0;
-        D.out = sum;
-        D.out_ld = up(L.hidden_pad, 4);
-        D.accumulate = i > 0;
-        if (int rc = launch_mma<false, true, kSum>(p_k, w_mn, D, sms, st)) return rc;
+        D.accumulate = v0 != last;
+        if (int rc = launch_mma<kSum>(p_k, w_mn, sum_out, D, sms, st)) return rc;
         MmaArgs W = A;                                  // dw of the piece's words = P^T x
         W.m = words;
         W.n = hidden;
@@ -709,19 +918,18 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.out_ld = a.dw_ld;
         W.out_dtype = a.dw_dtype;
         W.accumulate = a.accumulate_dw;
-        W.vec = host::aligned(dw, 16) && (a.dw_ld * dtype_bytes(a.dw_dtype)) % 16 == 0;
+        W.staged = dw_rows && (a.dw_dtype == FP8Z_F32 || !a.accumulate_dw);
         W.alpha = alpha;
-        if (int rc = launch_mma<true, true, kWeight>(p_mn, x_mn, W, sms, st)) return rc;
+        if (int rc = launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st)) return rc;
     }
     const dim3 grid(unsigned(n), unsigned((hidden + 1023) / 1024));
-    const int64_t sum_ld = up(L.hidden_pad, 4);
     if (A.bf16)
-        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, L.rows_pad * sum_ld, sum_ld, n, hidden, alpha,
+        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, L.rows_pad * L.hidden_pad, L.hidden_pad, n, hidden, alpha,
                                                static_cast<__nv_bfloat16*>(dx), a.dx_ld);
     else
-        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, L.rows_pad * sum_ld, sum_ld, n, hidden, alpha,
+        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, L.rows_pad * L.hidden_pad, L.hidden_pad, n, hidden, alpha,
                                                static_cast<__half*>(dx), a.dx_ld);
-    return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA;
+    return done();
 }
 
 }  // namespace
@@ -735,7 +943,7 @@ extern "C" int64_t fp8z_linear_xent_workspace(const void* x, const void* w, cons
     Layout L = layout(*args, with_grad != 0, cx, cw, -1);
     if (with_grad && piece_words > 0) {
         const int64_t less = L.piece - up(piece_words, kTN);
-        if (less > 0) return int64_t(L.total) - less * L.rows_pad * 2 * L.parts;
+        if (less > 0) return int64_t(L.total) - less * L.rows_pad * 4;
     }
     return int64_t(L.total);
 }
