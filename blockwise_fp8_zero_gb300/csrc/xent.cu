@@ -31,15 +31,16 @@
 namespace fp8z {
 namespace {
 
-constexpr int kTM = 128, kTN = 256, kBK = 64;          // output tile, K per stage
-constexpr int kStages = 4;
-constexpr int kBytesA = kTM * kBK * 2, kBytesB = kTN * kBK * 2, kStageBytes = kBytesA + kBytesB;
+constexpr int kTM = 256, kTN = 256, kBK = 64;          // output tile of a pair of blocks, K per stage
+constexpr int kHalf = 128;                             // a block's rows of A and of the result, and columns of B
+constexpr int kStages = 6;
+constexpr int kBytesA = kHalf * kBK * 2, kBytesB = kHalf * kBK * 2, kStageBytes = kBytesA + kBytesB;
 constexpr int kThreads = 256;                          // warp 0 loads, warp 1 multiplies, warps 4-7 read the sums
 constexpr int kTmemCols = 512;                         // two accumulators of 256 columns
 constexpr int kSlab = 32 * 128;                        // staged results of one warp: 32 rows of 128 bytes
 constexpr int kStaging = 4 * 2 * kSlab;
 constexpr int kNumBars = 2 * kStages + 5;
-constexpr int kSmem = kStages * kStageBytes + kStaging + kNumBars * 8 + 16 + 1024;
+constexpr int kSmem = kStages * kStageBytes + kStaging + kNumBars * 8 + 24 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -60,15 +61,15 @@ struct MmaArgs {
     int targets_wide;
     int64_t ignore, vocab;
     const int32_t* target;    // -1: takes no part in the loss (written by rows_kernel)
-    float2* part;             // [tile][rows_pad] maximum and sum
+    float2* part;             // [tile][rows] maximum and sum
     float* target_logit;
     const float* lse;
     int keep_from;            // words from here on leave their logits in the piece's buffer
     uint32_t* ticket;         // of rows_kernel, set to zero here
     int split_p;              // P in two parts
     float p_scale;
-    int rows_pad;
-    // kSum: FP32 [splits][rows_pad];  kWeight: rows v0 + m of dw
+    int rows;                 // tokens, rounded up to 32: stride of part
+    // kSum: FP32 [splits][m];  kWeight: rows v0 + m of dw
     void* out;
     int64_t out_ld;
     int out_dtype, accumulate, staged;
@@ -126,6 +127,7 @@ struct Stager {
     __device__ __forceinline__ void put(uint32_t s, int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) const {
         st_shared_v4(s + lane * 128 + ((chunk ^ (lane & 7)) << 4), a, b, c, d);
     }
+    // store(address) is called by lane 0 alone, whose row is the slab's first
     template <typename F>
     __device__ __forceinline__ void end(F store) {
         fence_proxy_async();
@@ -157,7 +159,9 @@ __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorM
         tmem_wait_ld();
         if (keep) {
             stage32(sg, r);
-            sg.end([&](uint32_t s) { tma_store_2d(&out, col0 - A.keep_from + c, row - sg.lane, s); });
+            sg.end([&](uint32_t s) {
+                if (row < A.m) tma_store_2d(&out, col0 - A.keep_from + c, row, s);
+            });
         }
         if (c + 32 > n_valid) {
 #pragma unroll
@@ -184,7 +188,7 @@ __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorM
             A.target_logit[row] = x;
         }
     }
-    if (row < A.m) A.part[size_t(t.n) * A.rows_pad + row] = make_float2(mx, sum);
+    if (row < A.m) A.part[size_t(t.n) * A.rows + row] = make_float2(mx, sum);
 }
 
 // P of eight neighbouring words of one row, times p_scale: in 16 bits, and what
@@ -237,10 +241,10 @@ __device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMa
             }
         }
         stage32(sg, h);
-        sg.end([&](uint32_t s) { tma_store_3d(&out, c, 2 * t.n, row - sg.lane, s); });
+        sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c, 2 * t.n, row, s); });
         if (A.split_p) {
             stage32(sg, l);
-            sg.end([&](uint32_t s) { tma_store_3d(&out, c, 2 * t.n + 1, row - sg.lane, s); });
+            sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c, 2 * t.n + 1, row, s); });
         }
     }
 }
@@ -255,9 +259,11 @@ __device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = 0;
         stage32(sg, r);
-        const int x = t.n * kTN + c, y = t.split * A.rows_pad + row - sg.lane;
-        if (A.accumulate) sg.end([&](uint32_t s) { tma_add_2d(&out, x, y, s); });
-        else sg.end([&](uint32_t s) { tma_store_2d(&out, x, y, s); });
+        sg.end([&](uint32_t s) {
+            if (row >= A.m) return;
+            if (A.accumulate) tma_add_3d(&out, t.n * kTN + c, row, t.split, s);
+            else tma_store_3d(&out, t.n * kTN + c, row, t.split, s);
+        });
     }
 }
 
@@ -277,7 +283,7 @@ __device__ __forceinline__ void weight_chunk(T* p, const uint32_t (&r)[32], int 
 __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
                                                 int row, Stager& sg) {
     const float a = *A.alpha;
-    const int y = A.v0 + row - sg.lane;
+    const int y = A.v0 + row;                        // of lane 0, which issues the stores
     if (A.staged && A.out_dtype != FP8Z_F32) {
         for (int c = 0; c < kTN && t.n * kTN + c < A.n; c += 64) {
             uint32_t h[32];
@@ -292,7 +298,7 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
                         pack16(__uint_as_float(r[2 * j]) * a, __uint_as_float(r[2 * j + 1]) * a, A.bf16);
             }
             stage32(sg, h);
-            sg.end([&](uint32_t s) { tma_store_2d(&out, t.n * kTN + c, y, s); });
+            sg.end([&](uint32_t s) { if (row < A.m) tma_store_2d(&out, t.n * kTN + c, y, s); });
         }
         return;
     }
@@ -305,8 +311,11 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a);
             stage32(sg, r);
-            if (A.accumulate) sg.end([&](uint32_t s) { tma_add_2d(&out, col, y, s); });
-            else sg.end([&](uint32_t s) { tma_store_2d(&out, col, y, s); });
+            sg.end([&](uint32_t s) {
+                if (row >= A.m) return;
+                if (A.accumulate) tma_add_2d(&out, col, y, s);
+                else tma_store_2d(&out, col, y, s);
+            });
         } else if (row < A.m) {
             const size_t at = size_t(A.v0 + row) * A.out_ld + col;
             const int n = A.n - col;
@@ -317,11 +326,14 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
     }
 }
 
-// One block of 128 x 256 results at a time: a warp keeps kStages tiles of
-// operands in flight, one thread issues the products into one of two
-// accumulators in tensor memory while four warps read the other.
+// A pair of blocks takes 256 x 256 results at a time.  Each block loads 128 rows
+// of A and 128 columns of B into a ring of kStages tiles; one thread of the
+// first block issues the products of both, into one of two accumulators in each
+// block's tensor memory, while four warps of each block read the other.  The
+// copies of both blocks count on the first block's barriers, each block arriving
+// for its own.
 template <int kEpi>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                const __grid_constant__ CUtensorMap tc, const __grid_constant__ MmaArgs A) {
     constexpr bool kAMn = kEpi == kWeight, kBMn = kEpi == kSum || kEpi == kWeight;   // operands along M or N
@@ -330,24 +342,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = smem_raw + (base - smem_addr(smem_raw));
     constexpr int kBarsAt = kStages * kStageBytes + kStaging;
     const uint32_t bars = base + kBarsAt;
-    auto full = [&](int s) { return bars + s * 8; };
-    auto empty = [&](int s) { return bars + (kStages + s) * 8; };
+    auto full = [&](int s) { return bars + s * 8; };                       // first block: both blocks' copies are there
+    auto empty = [&](int s) { return bars + (kStages + s) * 8; };          // the products that read them are done
     auto tfull = [&](int b) { return bars + (2 * kStages + b) * 8; };
-    auto tempty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };
+    auto tempty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };  // first block: all eight warps have read it
     const uint32_t drain = bars + (2 * kStages + 4) * 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBarsAt + kNumBars * 8);
     volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(smem + kBarsAt + kNumBars * 8 + 8);
+    volatile uint32_t* issued_by = reinterpret_cast<volatile uint32_t*>(smem + kBarsAt + kNumBars * 8 + 12);   // [2]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = int(cluster_rank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         if (kEpi == kStats && blockIdx.x == 0) *A.ticket = 0;
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full(s), 1);
+            mbar_init(full(s), 2);
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), 4);
+            mbar_init(tempty(b), 8);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -356,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) tmem_alloc(smem_addr(const_cast<uint32_t*>(tmem_at)), kTmemCols);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
     const Watchdog wd{abort_flag, A.dev_status, A.timeout_ns};
@@ -364,36 +379,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             int s = 0, ph = 0;
-            int64_t issued = 0;
+            uint32_t issued = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = pair; t < tiles && ok; t += pairs) {
                 const TileAt at = tile_at(A, t);
+                const int m = at.m * kTM + rank * kHalf, n = A.b_n0 + at.n * kTN + rank * kHalf;
                 for (int k = at.k0; k < at.k1; ++k) {
                     if (!mbar_wait_bounded(empty(s), ph ^ 1, wd)) {
                         ok = false;
                         break;
                     }
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kBytesA;
-                    mbar_arrive_expect_tx(full(s), kStageBytes);
+                    const uint32_t bar = cluster_addr(full(s), 0);
+                    mbar_arrive_expect_tx_cluster(bar, kStageBytes);
                     const int kw = k >= A.b_wrap ? k - A.b_wrap : k, kb = kw * kBK + A.b_k0;
                     if constexpr (kEpi == kWeight) {         // P^T: 128 words, 64 tokens of one part
 #pragma unroll
-                        for (int j = 0; j < kTM / 64; ++j) {
-                            const int word = at.m * kTM + j * 64;
-                            tma_load_3d(sa + j * (64 * kBK * 2), &ta, word % kTN, word / kTN * 2 + (k >= A.b_wrap),
-                                        kw * kBK, full(s));
+                        for (int j = 0; j < kHalf / 64; ++j) {
+                            const int word = m + j * 64;
+                            tma_load_3d_pair(sa + j * (64 * kBK * 2), &ta, word % kTN, word / kTN * 2 + (k >= A.b_wrap),
+                                             kw * kBK, bar);
                         }
                     } else if constexpr (kEpi == kSum) {     // P: 128 tokens, 64 words of the first part
-                        tma_load_3d(sa, &ta, k * kBK % kTN, k * kBK / kTN * 2, at.m * kTM, full(s));
+                        tma_load_3d_pair(sa, &ta, k * kBK % kTN, k * kBK / kTN * 2, m, bar);
                     } else {
-                        tma_load_2d(sa, &ta, k * kBK, at.m * kTM, full(s));
+                        tma_load_2d_pair(sa, &ta, k * kBK, m, bar);
                     }
                     if constexpr (kBMn) {
 #pragma unroll
-                        for (int j = 0; j < kTN / 64; ++j)
-                            tma_load_2d(sb + j * (64 * kBK * 2), &tb, A.b_n0 + at.n * kTN + j * 64, kb, full(s));
+                        for (int j = 0; j < kHalf / 64; ++j)
+                            tma_load_2d_pair(sb + j * (64 * kBK * 2), &tb, n + j * 64, kb, bar);
                     } else {
-                        tma_load_2d(sb, &tb, kb, A.b_n0 + at.n * kTN, full(s));
+                        tma_load_2d_pair(sb, &tb, kb, n, bar);
                     }
                     ++issued;
                     if (++s == kStages) {
@@ -402,16 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // whatever a wait elsewhere gave up on: every copy lands before the block ends
-            for (int i = 0; i < kStages && issued > i; ++i)
-                mbar_wait_drain(full(i), uint32_t(((issued - i + kStages - 1) / kStages - 1) & 1), A.dev_status);
+            st_cluster_u32(cluster_addr(smem_addr(const_cast<uint32_t*>(issued_by + rank)), 0), issued);
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         if (lane == 0) {
             const uint32_t idesc = umma_idesc(A.bf16 != 0, kAMn, kBMn, kTM, kTN);
             int s = 0, ph = 0, b = 0, bph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = pair; t < tiles && ok; t += pairs) {
                 const TileAt at = tile_at(A, t);
                 if (!mbar_wait_bounded(tempty(b), bph ^ 1, wd)) break;
                 tc_fence_after();
@@ -428,37 +443,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < kBK / 16; ++i)      // 16 of K: 32 bytes of a row, or 16 rows of 128 bytes
                         umma_f16(tmem + b * kTN, da + i * (kAMn ? 128 : 2), db + i * (kBMn ? 128 : 2), idesc,
                                  k != at.k0 || i != 0);
-                    umma_commit(empty(s));
+                    umma_commit_pair(empty(s));
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1;
                     }
                 }
                 if (!ok) break;
-                umma_commit(tfull(b));
+                umma_commit_pair(tfull(b));
                 if (b) bph ^= 1;
                 b ^= 1;
             }
-            umma_commit(drain);            // and every product is done before tensor memory is freed
+            umma_commit_pair(drain);       // and every product is done before tensor memory is freed
             mbar_wait_drain(drain, 0, A.dev_status);
         }
     } else if (warp >= 4) {
         const int quarter = warp - 4;
         Stager sg{base + kStages * kStageBytes + quarter * 2 * kSlab, 0, lane};
         int b = 0, bph = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        for (int t = pair; t < tiles; t += pairs) {
             const TileAt at = tile_at(A, t);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull(b), bph, wd))) break;
             tc_fence_after();
             const uint32_t acc = tmem + b * kTN + (uint32_t(quarter * 32) << 16);
-            const int row = at.m * kTM + quarter * 32 + lane;
+            const int row = at.m * kTM + rank * kHalf + quarter * 32 + lane;
             if constexpr (kEpi == kStats) epilogue_stats(A, tc, at, acc, row, sg);
             else if constexpr (kEpi == kProb) epilogue_prob(A, tc, at, acc, row, sg);
             else if constexpr (kEpi == kSum) epilogue_sum(A, tc, at, acc, row, sg);
             else epilogue_weight(A, tc, at, acc, row, sg);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty(b));
+            if (lane == 0) mbar_arrive_remote(tempty(b), 0);
             if (b) bph ^= 1;
             b ^= 1;
         }
@@ -466,6 +481,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
+    // Whatever a wait gave up on, every copy lands before either block ends.  A stage for which
+    // only one of the blocks came to issue its copies lacks the other's arrival: it is made here.
+    if (rank == 0 && threadIdx.x == 0) {
+        const uint32_t a = issued_by[0], b = issued_by[1], most = max(a, b);
+        for (uint32_t i = min(a, b); i < most; ++i) mbar_arrive(full(i % kStages));
+        for (uint32_t i = most > kStages ? most - kStages : 0; i < most; ++i)
+            mbar_wait_drain(full(i % kStages), (i / kStages) & 1, A.dev_status);
+    }
+    if (rank == 1 && threadIdx.x == 0) mbar_wait_drain(drain, 0, A.dev_status);    // the last arrival from the first block
+    cluster_sync();                        // neither block ends, nor frees, while the other may still reach it
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
@@ -488,7 +514,7 @@ struct BlockTotal {
     int64_t kept;
 };
 
-__global__ void __launch_bounds__(1024) rows_kernel(const float2* __restrict__ part, int tiles, int n, int rows_pad,
+__global__ void __launch_bounds__(1024) rows_kernel(const float2* __restrict__ part, int tiles, int n, int rows,
                                                     const void* __restrict__ targets, int wide, int64_t ignore,
                                                     int64_t vocab, const float* __restrict__ target_logit,
                                                     int32_t* __restrict__ target, float* __restrict__ lse_ws,
@@ -512,11 +538,11 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* __restrict__ p
             for (; t + 96 < tiles; t += 128) {
                 float2 q[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = part[size_t(t + 32 * i) * rows_pad + row];
+                for (int i = 0; i < 4; ++i) q[i] = part[size_t(t + 32 * i) * rows + row];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) add(q[i]);
             }
-            for (; t < tiles; t += 32) add(part[size_t(t) * rows_pad + row]);
+            for (; t < tiles; t += 32) add(part[size_t(t) * rows + row]);
         }
     }
     sh[r][g] = make_float2(m, s);
@@ -645,7 +671,7 @@ __global__ void zero_rows_kernel(T* out, int64_t ld, int64_t rows, int cols) {
 
 // ------------------------------------------------------------------ launches
 struct Layout {
-    int64_t rows_pad, hidden_pad, vocab_tiles, piece, pieces, parts;
+    int64_t rows, hidden_pad, vocab_tiles, piece, pieces, parts;
     int splits;
     bool copy_x, copy_w;
     size_t x, w, target, target_logit, lse, part, totals, alpha, p, sum, total;
@@ -685,7 +711,7 @@ int dx_splits(int64_t tiles, int64_t k_blocks, int64_t elems) {
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= 64 && s * 4 <= k_blocks; ++s) {
-        const double waves = double((tiles * s + kSms - 1) / kSms);
+        const double waves = double((tiles * s + kSms / 2 - 1) / (kSms / 2));
         const double t = waves * double((k_blocks + s - 1) / s) * 135.0 + double(s) * double(elems) * 8.0 / 6500.0;
         if (s == 1 || t < least) {
             least = t;
@@ -700,7 +726,7 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int6
     std::memset(&L, 0, sizeof(L));
     L.copy_x = copy_x;
     L.copy_w = copy_w;
-    L.rows_pad = up(a.tokens > 0 ? a.tokens : 1, kTM);
+    L.rows = up(a.tokens > 0 ? a.tokens : 1, 32);
     L.hidden_pad = up(a.hidden, 8);
     L.vocab_tiles = (a.vocab + kTN - 1) / kTN;
     size_t at = 0;
@@ -711,27 +737,27 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int6
     };
     L.x = take(copy_x ? a.tokens * L.hidden_pad * 2 : 0);
     L.w = take(copy_w ? a.vocab * L.hidden_pad * 2 : 0);
-    L.target = take(L.rows_pad * 4);
-    L.target_logit = take(L.rows_pad * 4);
-    L.lse = take(L.rows_pad * 4);
+    L.target = take(L.rows * 4);
+    L.target_logit = take(L.rows * 4);
+    L.lse = take(L.rows * 4);
     L.alpha = take(8);
-    L.part = take(L.vocab_tiles * L.rows_pad * 8);
-    L.totals = take((L.rows_pad / 32) * sizeof(BlockTotal));
+    L.part = take(L.vocab_tiles * L.rows * 8);
+    L.totals = take((L.rows / 32) * sizeof(BlockTotal));
     if (grad) {
         L.parts = a.dw_dtype == FP8Z_F32 ? 2 : 1;
-        L.splits = dx_splits(L.rows_pad / kTM * ((L.hidden_pad + kTN - 1) / kTN), L.vocab_tiles * (kTN / kBK),
-                             L.rows_pad * L.hidden_pad);
-        L.sum = take(int64_t(L.splits) * L.rows_pad * L.hidden_pad * 4);
+        L.splits = dx_splits((L.rows + kTM - 1) / kTM * ((L.hidden_pad + kTN - 1) / kTN), L.vocab_tiles * (kTN / kBK),
+                             a.tokens * L.hidden_pad);
+        L.sum = take(int64_t(L.splits) * a.tokens * L.hidden_pad * 4);
         // One piece takes 4 bytes a word and token.  By default it is at most 1 GiB, or the size of
         // the FP32 dw where that is more: what the call keeps stays below what the caller keeps.
         int64_t room = std::max(kPieceBytes, a.vocab * a.hidden * 4);
         if (have >= 0 && have - int64_t(at) < room) room = have - int64_t(at);
-        const int64_t tile_bytes = L.rows_pad * kTN * 4;
+        const int64_t tile_bytes = std::max<int64_t>(a.tokens, 1) * kTN * 4;
         const int64_t tiles = std::min(std::max<int64_t>(room / tile_bytes, 1), L.vocab_tiles);
         L.pieces = (L.vocab_tiles + tiles - 1) / tiles;
         L.piece = (L.vocab_tiles + L.pieces - 1) / L.pieces * kTN;       // equal pieces
         L.pieces = (L.vocab_tiles * kTN + L.piece - 1) / L.piece;
-        L.p = take(L.rows_pad * L.piece * 4);
+        L.p = take(a.tokens * L.piece * 4);
     }
     L.total = at;
     return L;
@@ -770,13 +796,21 @@ bool map_p(CUtensorMap* map, const void* p, int64_t piece, int64_t rows, int box
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box);
 }
 
+// dx's parts: hidden, tokens, parts.
+bool map_sum(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t parts) {
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(parts)};
+    const cuuint64_t strides[2] = {cuuint64_t(cols * 4), cuuint64_t(cols * rows * 4)};
+    const cuuint32_t box[3] = {32, 32, 1};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box);
+}
+
 template <int kEpi>
 int launch_mma(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const MmaArgs& A, int sms,
                cudaStream_t st) {
     const auto k = &mma_kernel<kEpi>;
     if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), 12 + kEpi, kSmem)) return rc;
     const int64_t tiles = int64_t(A.mt) * A.nt * A.splits;
-    k<<<unsigned(tiles < sms ? tiles : sms), kThreads, kSmem, st>>>(ta, tb, tc, A);
+    k<<<2 * unsigned(tiles < sms / 2 ? tiles : sms / 2), kThreads, kSmem, st>>>(ta, tb, tc, A);
     return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA;
 }
 
@@ -833,10 +867,10 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     }
     uint8_t* p = ws + L.p;
     CUtensorMap x_k, w_k, logits;
-    if (!map_16(&x_k, xp, L.hidden_pad, n, x_ld, kTM) || !map_16(&w_k, wp, L.hidden_pad, vocab, w_ld, kTN))
+    if (!map_16(&x_k, xp, L.hidden_pad, n, x_ld, kHalf) || !map_16(&w_k, wp, L.hidden_pad, vocab, w_ld, kHalf))
         return FP8Z_ECUDA;
     if (!grad) logits = w_k;                        // not used
-    else if (!map_f32(&logits, p, L.piece, L.rows_pad, L.piece)) return FP8Z_ECUDA;
+    else if (!map_f32(&logits, p, L.piece, n, L.piece)) return FP8Z_ECUDA;
     const int last = grad ? int((L.pieces - 1) * L.piece) : vocab;      // the piece whose logits stay
     MmaArgs A;
     std::memset(&A, 0, sizeof(A));
@@ -844,9 +878,9 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.timeout_ns = host::wait_limit_ns();
     A.dev_status = dev_status;
     A.m = n;
-    A.rows_pad = int(L.rows_pad);
+    A.rows = int(L.rows);
     A.n = vocab;
-    A.mt = int(L.rows_pad / kTM);
+    A.mt = (n + kTM - 1) / kTM;
     A.nt = int(L.vocab_tiles);
     A.splits = 1;
     A.kb = A.b_wrap = int((L.hidden_pad + kBK - 1) / kBK);
@@ -862,7 +896,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     if (int rc = launch_mma<kStats>(x_k, w_k, logits, A, sms, st)) return rc;
     // FP16 P is kept times 2^12: probabilities down to 2^-36 stay normal numbers or close
     const float p_scale = A.bf16 ? 1.0f : 4096.0f;
-    rows_kernel<<<(n + 31) / 32, 1024, 0, st>>>(part, A.nt, n, A.rows_pad, targets, A.targets_wide, A.ignore, A.vocab,
+    rows_kernel<<<(n + 31) / 32, 1024, 0, st>>>(part, A.nt, n, A.rows, targets, A.targets_wide, A.ignore, A.vocab,
                                                 target_logit, target, lse_ws, lse, loss,
                                                 reinterpret_cast<BlockTotal*>(ws + L.totals), A.ticket,
                                                 a.reduction == FP8Z_MEAN, grad ? a.grad_scale / p_scale : 1.0f, total,
@@ -872,10 +906,10 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     auto* sum = reinterpret_cast<float*>(ws + L.sum);
     const bool dw_rows = host::aligned(dw, 16) && (a.dw_ld * dtype_bytes(a.dw_dtype)) % 16 == 0;
     CUtensorMap p_k, w_mn, p_mn, x_mn, p_out, sum_out, dw_out = x_k;
-    if (!map_p(&p_k, p, L.piece, L.rows_pad, kTM) || !map_16(&w_mn, wp, L.hidden_pad, vocab, w_ld, kBK) ||
-        !map_p(&p_mn, p, L.piece, L.rows_pad, kBK) || !map_16(&x_mn, xp, L.hidden_pad, n, x_ld, kBK) ||
-        !map_p(&p_out, p, L.piece, L.rows_pad, 32) ||
-        !map_f32(&sum_out, sum, L.hidden_pad, L.rows_pad * L.splits, L.hidden_pad))
+    if (!map_p(&p_k, p, L.piece, n, kHalf) || !map_16(&w_mn, wp, L.hidden_pad, vocab, w_ld, kBK) ||
+        !map_p(&p_mn, p, L.piece, n, kBK) || !map_16(&x_mn, xp, L.hidden_pad, n, x_ld, kBK) ||
+        !map_p(&p_out, p, L.piece, n, 32) ||
+        !map_sum(&sum_out, sum, L.hidden_pad, n, L.splits))
         return FP8Z_ECUDA;
     if (dw_rows && !(a.dw_dtype == FP8Z_F32 ? map_f32(&dw_out, dw, hidden, vocab, a.dw_ld)
                                             : map_16(&dw_out, dw, hidden, vocab, a.dw_ld, 32)))
@@ -884,7 +918,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         const int v0 = int(i * L.piece);
         const int words = int(a.vocab - v0 < L.piece ? a.vocab - v0 : L.piece), tiles = (words + kTN - 1) / kTN;
         if (v0 == last) {
-            const dim3 grid(unsigned(L.rows_pad), unsigned((tiles + 8 * kProbTiles - 1) / (8 * kProbTiles)));
+            const dim3 grid(unsigned(n), unsigned((tiles + 8 * kProbTiles - 1) / (8 * kProbTiles)));
             prob_kernel<<<grid, 256, 0, st>>>(p, L.piece * 4, tiles, words, n, v0, target, lse_ws, p_scale, A.bf16,
                                               L.parts == 2);
         } else {
@@ -911,7 +945,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.n = hidden;
         W.mt = (words + kTM - 1) / kTM;
         W.nt = D.nt;
-        W.b_wrap = int(L.rows_pad / kBK);
+        W.b_wrap = (n + kBK - 1) / kBK;
         W.kb = W.b_wrap * int(L.parts);
         W.v0 = v0;
         W.out = dw;
@@ -924,10 +958,10 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     }
     const dim3 grid(unsigned(n), unsigned((hidden + 1023) / 1024));
     if (A.bf16)
-        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, L.rows_pad * L.hidden_pad, L.hidden_pad, n, hidden, alpha,
+        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, n * L.hidden_pad, L.hidden_pad, n, hidden, alpha,
                                                static_cast<__nv_bfloat16*>(dx), a.dx_ld);
     else
-        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, L.rows_pad * L.hidden_pad, L.hidden_pad, n, hidden, alpha,
+        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, n * L.hidden_pad, L.hidden_pad, n, hidden, alpha,
                                                static_cast<__half*>(dx), a.dx_ld);
     return done();
 }
@@ -943,7 +977,7 @@ extern "C" int64_t fp8z_linear_xent_workspace(const void* x, const void* w, cons
     Layout L = layout(*args, with_grad != 0, cx, cw, -1);
     if (with_grad && piece_words > 0) {
         const int64_t less = L.piece - up(piece_words, kTN);
-        if (less > 0) return int64_t(L.total) - less * L.rows_pad * 4;
+        if (less > 0) return int64_t(L.total) - less * args->tokens * 4;
     }
     return int64_t(L.total);
 }
