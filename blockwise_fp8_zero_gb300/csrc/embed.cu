@@ -5,9 +5,9 @@
 //
 // The gradient sorts the tokens by id (stable, so equal ids keep token order),
 // cuts the sorted list into pieces of equal length, sums each run of equal ids
-// inside a piece in registers, and joins the runs that cross pieces in a second
-// pass.  Every sum runs in FP32 in token order, whatever the schedule, and a
+// inside a piece in registers, and joins the runs that cross pieces.  Every sum runs in FP32 in token order, whatever the schedule, and a
 // word that makes up most of a batch costs no more than many rare ones.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -18,6 +18,7 @@
 #include "fp8z_device.cuh"
 #include "fp8z_elem.cuh"
 #include "fp8z_host.h"
+#include "fp8z_launch.cuh"
 
 namespace fp8z {
 namespace {
@@ -32,11 +33,12 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int wide, int64_t i)
 // One block writes one piece of one row.  VEC: rows of both sides start on
 // 16-byte boundaries, eight elements a thread and step; else one element.
 template <typename S, typename D, bool VEC>
-__global__ void __launch_bounds__(kThreads) lookup_kernel(const void* __restrict__ ids, int wide,
-                                                          const S* __restrict__ table, int64_t table_ld,
-                                                          int64_t vocab, D* __restrict__ out, int64_t out_ld,
+__global__ void __launch_bounds__(kThreads) lookup_kernel(const void* ids, int wide,
+                                                          const S* table, int64_t table_ld,
+                                                          int64_t vocab, D* out, int64_t out_ld,
                                                           int hidden, float scale, int32_t* dev_status) {
     constexpr int V = VEC ? 8 : 1, R = 4;
+    dependent_wait();
     const int64_t t = blockIdx.x;
     const int64_t id = load_id(ids, wide, t);
     const bool ok = id >= 0 && id < vocab;
@@ -110,11 +112,62 @@ struct Ids {
     }
 };
 
-// counts[tile * kBins + digit]; the first pass also marks the rows that occur.
-__global__ void __launch_bounds__(kThreads) count_kernel(Ids ids, const uint32_t* __restrict__ keys, int n, int shift,
-                                                         int digit, uint32_t* __restrict__ counts,
-                                                         uint8_t* __restrict__ used) {
+// Rows that no token names are written as zeros, by blocks that run beside the
+// sort's and the sums' in the same launches: a launch of the sort takes some 8 us
+// on a few SMs, and the rest of the machine writes about kFillBesideSort bytes in
+// that time.  Which rows occur is known from `used`, or, where one block sorts
+// the whole list, from the ids themselves.
+constexpr int kFillRows = 64;           // most rows of one block
+constexpr int64_t kFillBytes = 128 << 10;
+constexpr int64_t kFillBesideSort = 48 << 20;
+struct Fill {
+    void* table;
+    const uint8_t* used;                         // [vocab], or null
+    int64_t ld_bytes, row_bytes, begin, end;     // rows [begin, end) are this launch's
+    int rows, blocks;                            // rows of one block
+};
+
+__device__ __forceinline__ void fill_rows(const Fill& f, const Ids& ids, int n, int64_t block) {
+    __shared__ uint32_t named[kFillRows / 32];
+    const int64_t r0 = f.begin + block * f.rows;
+    const int rows = int(min(int64_t(f.rows), f.end - r0));
+    if (threadIdx.x < kFillRows / 32) named[threadIdx.x] = 0;
+    __syncthreads();
+    if (f.used) {
+        if (int(threadIdx.x) < rows && f.used[r0 + threadIdx.x])
+            atomicOr(&named[threadIdx.x >> 5], 1u << (threadIdx.x & 31));
+    } else {
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            const int64_t r = int64_t(ids.key(i, false)) - r0;
+            if (r >= 0 && r < rows) atomicOr(&named[r >> 5], 1u << (r & 31));
+        }
+    }
+    __syncthreads();
+    const bool wide = ((reinterpret_cast<uintptr_t>(f.table) | f.ld_bytes | f.row_bytes) & 15) == 0;
+    for (int r = 0; r < rows; ++r) {
+        if (named[r >> 5] >> (r & 31) & 1) continue;
+        uint8_t* p = static_cast<uint8_t*>(f.table) + (r0 + r) * f.ld_bytes;
+        if (wide)
+            for (int64_t c = threadIdx.x; c < f.row_bytes / 16; c += blockDim.x)
+                reinterpret_cast<uint4*>(p)[c] = make_uint4(0, 0, 0, 0);
+        else
+            for (int64_t c = threadIdx.x; c < f.row_bytes / 2; c += blockDim.x) reinterpret_cast<uint16_t*>(p)[c] = 0;
+    }
+}
+
+// counts[tile * kBins + digit]; the first pass marks the rows that occur
+__global__ void __launch_bounds__(kThreads) count_kernel(Ids ids, const uint32_t* keys, int n, int shift,
+                                                         int digit, uint32_t* counts, Fill fill,
+                                                         uint32_t* tickets, int ntickets, uint8_t* used) {
     __shared__ uint32_t bins[kBins];
+    dependent_wait();
+    const int tiles = gridDim.x - fill.blocks;
+    if (int(blockIdx.x) >= tiles) {
+        fill_rows(fill, ids, n, blockIdx.x - tiles);
+        return;
+    }
+    if (tickets)
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < ntickets; i += tiles * kThreads) tickets[i] = 0;
     const uint32_t mask = (1u << digit) - 1;
     for (int b = threadIdx.x; b <= int(mask); b += kThreads) bins[b] = 0;
     __syncthreads();
@@ -132,32 +185,24 @@ __global__ void __launch_bounds__(kThreads) count_kernel(Ids ids, const uint32_t
     for (int b = threadIdx.x; b <= int(mask); b += kThreads) counts[size_t(blockIdx.x) * kBins + b] = bins[b];
 }
 
-__global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t* __restrict__ keys,
-                                                         const uint32_t* __restrict__ vals, int n, int shift,
-                                                         int digit, const uint32_t* __restrict__ counts, int tiles,
-                                                         uint32_t* __restrict__ keys_out,
-                                                         uint32_t* __restrict__ vals_out) {
-    __shared__ uint16_t warp_count[kWarps][kBins];      // equal digits in earlier rounds, then in earlier warps
-    __shared__ uint32_t base[kBins];
-    __shared__ uint32_t warp_total[kWarps];
-    const int nb = 1 << digit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t mask = nb - 1;
-    for (int b = threadIdx.x; b < nb; b += kThreads)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) warp_count[w][b] = 0;
-    // base[b] = tokens of smaller digits anywhere + tokens of digit b in earlier tiles
+struct SortShared {
+    uint16_t warp_count[kWarps][kBins];      // equal digits in earlier rounds, then in earlier warps
+    uint32_t base[kBins];
+    uint32_t warp_total[kWarps];
+};
+
+// base[b] = tokens of smaller digits anywhere + tokens of digit b in earlier
+// tiles, from the block's own sums of (earlier tiles, all tiles) for each bin.
+template <typename F>
+__device__ __forceinline__ void digit_bases(SortShared& sh, int nb, F sums) {
     constexpr int B = kBins / kThreads;                 // neighbouring bins of one thread
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t mine[B], total[B], sum = 0;
 #pragma unroll
     for (int j = 0; j < B; ++j) {
         const int b = threadIdx.x * B + j;
         mine[j] = total[j] = 0;
-        if (b < nb)
-            for (int t = 0; t < tiles; ++t) {
-                const uint32_t c = counts[size_t(t) * kBins + b];
-                if (t < int(blockIdx.x)) mine[j] += c;
-                total[j] += c;
-            }
+        if (b < nb) sums(b, mine[j], total[j]);
         sum += total[j];
     }
     uint32_t scan = sum;
@@ -166,17 +211,82 @@ __global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t
         const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, scan, o);
         if (lane >= o) scan += y;
     }
-    if (lane == 31) warp_total[warp] = scan;
+    if (lane == 31) sh.warp_total[warp] = scan;
     __syncthreads();
     uint32_t before = scan - sum;
-    for (int w = 0; w < warp; ++w) before += warp_total[w];
+    for (int w = 0; w < warp; ++w) before += sh.warp_total[w];
 #pragma unroll
     for (int j = 0; j < B; ++j) {
         const int b = threadIdx.x * B + j;
-        if (b < nb) base[b] = before + mine[j];
+        if (b < nb) sh.base[b] = before + mine[j];
         before += total[j];
     }
-    // rank inside the tile: a warp owns 256 consecutive tokens, 32 at a time in order
+}
+
+// Rank of each of the warp's tokens (32 * kItems of them in order, 32 at a time)
+// among equal digits of the tile's earlier tokens.  k: keys; rounds < n in use.
+__device__ __forceinline__ void tile_ranks(SortShared& sh, const uint32_t (&k)[kItems], uint32_t (&rank)[kItems],
+                                           int count, int shift, int nb) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t mask = nb - 1;
+#pragma unroll
+    for (int r = 0; r < kItems; ++r) {
+        const bool in = r * 32 + lane < count;
+        const uint32_t d = (k[r] >> shift) & mask;
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, in ? d : 0xFFFFFFFFu);
+        const int before_me = __popc(peers & ((1u << lane) - 1));
+        uint32_t seen = 0;
+        if (in) seen = sh.warp_count[warp][d];
+        __syncwarp();
+        if (in && before_me == 0) sh.warp_count[warp][d] = uint16_t(seen + __popc(peers));
+        __syncwarp();
+        rank[r] = seen + before_me;
+    }
+}
+
+// Counts of the tile's warps become the counts of the warps before each; returns through total(b, n) the tile's.
+template <typename F>
+__device__ __forceinline__ void warp_bases(SortShared& sh, int nb, F total) {
+    for (int b = threadIdx.x; b < nb; b += kThreads) {
+        uint32_t s = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const uint32_t c = sh.warp_count[w][b];
+            sh.warp_count[w][b] = uint16_t(s);
+            s += c;
+        }
+        total(b, s);
+    }
+}
+
+__device__ __forceinline__ void clear_counts(SortShared& sh, int nb) {
+    for (int i = threadIdx.x; i < nb * kWarps / 2; i += kThreads) {
+        const int w = i / (nb / 2), b = i % (nb / 2);
+        reinterpret_cast<uint32_t*>(sh.warp_count[w])[b] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t* keys,
+                                                         const uint32_t* vals, int n, int shift,
+                                                         int digit, const uint32_t* counts, int tiles,
+                                                         uint32_t* keys_out,
+                                                         uint32_t* vals_out, Fill fill) {
+    __shared__ SortShared sh;
+    dependent_wait();
+    if (int(blockIdx.x) >= tiles) {
+        fill_rows(fill, ids, n, blockIdx.x - tiles);
+        return;
+    }
+    const int nb = 1 << digit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    clear_counts(sh, nb);
+    digit_bases(sh, nb, [&](int b, uint32_t& mine, uint32_t& total) {
+#pragma unroll 4
+        for (int t = 0; t < tiles; ++t) {
+            const uint32_t c = counts[size_t(t) * kBins + b];
+            if (t < int(blockIdx.x)) mine += c;
+            total += c;
+        }
+    });
     const int t0 = blockIdx.x * kTile + warp * (32 * kItems);
     uint32_t k[kItems], v[kItems], rank[kItems];
 #pragma unroll
@@ -186,42 +296,77 @@ __global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t
         k[r] = in ? (keys ? keys[i] : ids.key(i, false)) : 0;
         v[r] = in ? (vals ? vals[i] : uint32_t(i)) : 0;
     }
-#pragma unroll
-    for (int r = 0; r < kItems; ++r) {
-        const bool in = t0 + r * 32 + lane < n;
-        const uint32_t d = (k[r] >> shift) & mask;
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, in ? d : 0xFFFFFFFFu);
-        const int before_me = __popc(peers & ((1u << lane) - 1));
-        uint32_t seen = 0;
-        if (in) seen = warp_count[warp][d];
-        __syncwarp();
-        if (in && before_me == 0) warp_count[warp][d] = uint16_t(seen + __popc(peers));
-        __syncwarp();
-        rank[r] = seen + before_me;
-    }
+    tile_ranks(sh, k, rank, n - t0, shift, nb);
     __syncthreads();
-    for (int b = threadIdx.x; b < nb; b += kThreads) {
-        uint32_t s = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const uint32_t c = warp_count[w][b];
-            warp_count[w][b] = uint16_t(s);
-            s += c;
-        }
-    }
+    warp_bases(sh, nb, [](int, uint32_t) {});
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kItems; ++r) {
         if (t0 + r * 32 + lane < n) {
-            const uint32_t d = (k[r] >> shift) & mask;
-            const uint32_t at = base[d] + warp_count[warp][d] + rank[r];
+            const uint32_t d = (k[r] >> shift) & (nb - 1);
+            const uint32_t at = sh.base[d] + sh.warp_count[warp][d] + rank[r];
             keys_out[at] = k[r];
             vals_out[at] = v[r];
         }
     }
 }
 
+// One tile: all passes in one block, the list in shared memory between them.
+__global__ void __launch_bounds__(kThreads) sort_tile_kernel(Ids ids, int n, int passes, int digit,
+                                                             uint32_t* keys_out,
+                                                             uint32_t* vals_out, Fill fill,
+                                                             uint32_t* tickets, int ntickets) {
+    __shared__ SortShared sh;
+    __shared__ uint32_t list[kTile];                   // token of each place
+    __shared__ uint32_t key_at[kTile];
+    dependent_wait();
+    if (blockIdx.x > 0) {
+        fill_rows(fill, ids, n, blockIdx.x - 1);
+        return;
+    }
+    for (int i = threadIdx.x; i < ntickets; i += kThreads) tickets[i] = 0;
+    const int nb = 1 << digit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = warp * (32 * kItems);
+    uint32_t k[kItems], v[kItems], rank[kItems];
+#pragma unroll
+    for (int r = 0; r < kItems; ++r) {
+        const int i = t0 + r * 32 + lane;
+        k[r] = i < n ? ids.key(i, true) : 0;
+        v[r] = uint32_t(i);
+    }
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * digit;
+        clear_counts(sh, nb);
+        __syncthreads();
+        tile_ranks(sh, k, rank, n - t0, shift, nb);
+        __syncthreads();
+        warp_bases(sh, nb, [&](int b, uint32_t total) { sh.base[b] = total; });
+        __syncthreads();
+        digit_bases(sh, nb, [&](int b, uint32_t&, uint32_t& total) { total = sh.base[b]; });
+        __syncthreads();
+        const bool last = p == passes - 1;
+#pragma unroll
+        for (int r = 0; r < kItems; ++r) {
+            if (t0 + r * 32 + lane < n) {
+                const uint32_t d = (k[r] >> shift) & (nb - 1);
+                const uint32_t at = sh.base[d] + sh.warp_count[warp][d] + rank[r];
+                (last ? keys_out : key_at)[at] = k[r];
+                (last ? vals_out : list)[at] = v[r];
+            }
+        }
+        __syncthreads();
+        if (!last) {
+#pragma unroll
+            for (int r = 0; r < kItems; ++r) {
+                const int i = t0 + r * 32 + lane;
+                k[r] = i < n ? key_at[i] : 0;
+                v[r] = i < n ? list[i] : 0;
+            }
+        }
+    }
+}
+
 // -------------------------------------------------------------------- sums
+constexpr int kMaxPiece = 32;
 // Columns one block takes: V per thread.
 template <bool VEC>
 constexpr int kCols = kThreads * (VEC ? 8 : 1);
@@ -242,110 +387,161 @@ __device__ __forceinline__ void write_row(D* p, const float (&acc)[V], float sca
     else *p = y.v[0];
 }
 
-// Blocks [0, pieces) x slabs sum the runs of one piece of the sorted list;
-// blocks beyond write zeros to the rows that do not occur.  A run inside its
-// piece is finished here.  One that came in from the piece before leaves its
-// part in partial[2 * piece], one that starts here and goes on in
-// partial[2 * piece + 1]; join_kernel adds them.
+// One block sums the runs of one piece of the sorted list, in its columns.  A run
+// inside its piece is finished there.  A longer one leaves a partial sum for each
+// of its pieces (partial[2 * piece] for one that came in from the piece before,
+// partial[2 * piece + 1] for one that starts there), and the last of its blocks
+// to arrive adds them up, in the list's order.
 template <typename S, typename D, bool VEC>
-__global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* __restrict__ keys,
-                                                        const uint32_t* __restrict__ vals, int n, uint32_t vocab,
-                                                        int piece_len, int pieces, const S* __restrict__ d_out,
-                                                        int64_t d_ld, D* __restrict__ d_table, int64_t t_ld, int hidden,
-                                                        float scale, bool accumulate, float* __restrict__ partial,
-                                                        const uint8_t* __restrict__ used, int fill_rows) {
+__global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
+                                                        const uint32_t* vals, int n, uint32_t vocab,
+                                                        int piece_len, const S* d_out, int64_t d_ld,
+                                                        D* d_table, int64_t t_ld, int hidden, float scale,
+                                                        bool accumulate, float* partial, uint32_t* tickets,
+                                                        int slabs, Ids ids, Fill fill) {
     constexpr int V = VEC ? 8 : 1;
-    const int col = blockIdx.y * kCols<VEC> + threadIdx.x * V;
-    if (col >= hidden) return;
-    if (int(blockIdx.x) >= pieces) {
-        const int64_t r0 = int64_t(blockIdx.x - pieces) * fill_rows;
-        const float zero[V] = {};
-        for (int r = 0; r < fill_rows; ++r)
-            if (r0 + r < vocab && !used[r0 + r]) write_row<D, V>(d_table + (r0 + r) * t_ld + col, zero, 0.0f, false);
+    __shared__ bool finish;
+    __shared__ uint32_t skeys[kMaxPiece], svals[kMaxPiece];
+    dependent_wait();
+    // sums and fills take turns, so that the machine always has some of both
+    const int64_t sums = int64_t(gridDim.x) - fill.blocks, b = blockIdx.x;
+    const int64_t sum = b * sums / gridDim.x;
+    if ((b + 1) * sums / gridDim.x == sum) {
+        fill_rows(fill, ids, n, b - sum);
         return;
     }
-    const int i0 = blockIdx.x * piece_len, i1 = min(n, i0 + piece_len);
-    uint32_t key = keys[i0];
+    const int piece = int(sum / slabs), slab = int(sum % slabs);
+    const int col = slab * kCols<VEC> + threadIdx.x * V;
+    const bool mine = col < hidden;
+    const int i0 = piece * piece_len, i1 = min(n, i0 + piece_len);
+    if (i0 + int(threadIdx.x) < i1) {
+        skeys[threadIdx.x] = keys[i0 + threadIdx.x];
+        svals[threadIdx.x] = vals[i0 + threadIdx.x];
+    }
+    const uint32_t key_before = i0 > 0 ? keys[i0 - 1] : vocab, key_after = i1 < n ? keys[i1] : vocab;
+    __syncthreads();
+    uint32_t key = skeys[0];
     if (key >= vocab) return;                       // the ids without a gradient come last
-    bool from_before = i0 > 0 && keys[i0 - 1] == key;
     float acc[V] = {};
-    constexpr int U = 4;
-    for (int i = i0; i < i1; i += U) {
-        Pack<S, V> x[U];
-        uint32_t k[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            k[u] = i + u < i1 ? keys[i + u] : vocab;
-            if (k[u] < vocab) {
-                const S* p = d_out + int64_t(vals[i + u]) * d_ld + col;
-                if constexpr (VEC) x[u] = ld_nc<S, V>(p);
-                else x[u].v[0] = *p;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i + u >= i1) break;
-            if (k[u] != key) {                      // the run ends inside the piece
-                if (from_before) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) partial[size_t(2 * blockIdx.x) * hidden + col + j] = acc[j];
-                } else {
-                    write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
-                }
-                from_before = false;
-#pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] = 0.0f;
-                key = k[u];
-                if (key >= vocab) return;
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] += Elem<S>::widen(x[u].v[j]);
-        }
-    }
-    const bool goes_on = i1 < n && keys[i1] == key;
-    if (from_before || goes_on) {
-        float* p = partial + size_t(2 * blockIdx.x + (from_before ? 0 : 1)) * hidden + col;
-#pragma unroll
-        for (int j = 0; j < V; ++j) p[j] = acc[j];
-    } else {
-        write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
-    }
-}
 
-template <typename D>
-__global__ void __launch_bounds__(kThreads) join_kernel(const uint32_t* __restrict__ keys, int n, uint32_t vocab,
-                                                        int piece_len, const float* __restrict__ partial,
-                                                        D* __restrict__ d_table, int64_t t_ld, int hidden, float scale,
-                                                        bool accumulate) {
-    const int p = blockIdx.x, i0 = p * piece_len, i1 = min(n, i0 + piece_len);
-    const uint32_t key = keys[i1 - 1];
-    if (key >= vocab || i1 >= n || keys[i1] != key) return;     // no run goes on
-    if (i0 > 0 && keys[i0 - 1] == key && keys[i0] == key) return;   // it began in an earlier piece
-    // the run's end: doubling steps from i1, then halving
-    int lo = i1, step = 1;
-    while (lo + step < n && keys[lo + step] == key) {
-        lo += step;
-        step *= 2;
+    // Leaves this piece's part of a long run [.., ..) that starts at or before i (keys[i] == key).
+    auto part_of_run = [&](bool from_before, int i) {
+        if (mine) {
+            float* p = partial + size_t(2 * piece + (from_before ? 0 : 1)) * hidden + col;
+            if constexpr (VEC) {
+                __stcg(reinterpret_cast<float4*>(p), make_float4(acc[0], acc[1], acc[2], acc[3]));
+                __stcg(reinterpret_cast<float4*>(p) + 1, make_float4(acc[4], acc[5], acc[6], acc[7]));
+            } else {
+                __stcg(p, acc[0]);
+            }
+        }
+        // the run's ends: doubling steps, then halving
+        int lo = i, step = 1;
+        while (lo + step < n && keys[lo + step] == key) {
+            lo += step;
+            step *= 2;
+        }
+        int hi = min(n, lo + step);
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (keys[mid] == key) lo = mid; else hi = mid;
+        }
+        const int last = lo / piece_len;
+        hi = i;
+        step = 1;
+        while (hi - step >= 0 && keys[hi - step] == key) {
+            hi -= step;
+            step *= 2;
+        }
+        lo = max(-1, hi - step);
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (keys[mid] == key) hi = mid; else lo = mid;
+        }
+        const int first = hi / piece_len;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0)
+            finish = atomicAdd(&tickets[size_t(first) * slabs + slab], 1u) == uint32_t(last - first);
+        __syncthreads();
+        if (finish && mine) {
+            __threadfence();
+            const float* p = partial + size_t(2 * first + 1) * hidden + col;
+            float sum[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] = __ldcg(p + j);
+            p += hidden;                            // of piece first + 1, come in from before
+#pragma unroll 4
+            for (int q = first + 1; q <= last; ++q, p += 2 * size_t(hidden)) {
+                if constexpr (VEC) {
+                    const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
+                    const float4 b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+                    sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
+                    sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
+                } else {
+                    sum[0] += __ldcg(p);
+                }
+            }
+            write_row<D, V>(d_table + int64_t(key) * t_ld + col, sum, scale, accumulate);
+        }
+        __syncthreads();                            // `finish` is free again
+    };
+
+    // Adds rows [i, end) to acc; where the key changes, finishes the run before.
+    auto add_rows = [&](int i, int end) {
+        constexpr int U = 4;
+        for (; i < end; i += U) {
+            Pack<S, V> x[U];
+            uint32_t k[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                k[u] = i + u < end ? skeys[i + u - i0] : vocab;
+                if (k[u] < vocab && mine) {
+                    const S* p = d_out + int64_t(svals[i + u - i0]) * d_ld + col;
+                    if constexpr (VEC) x[u] = ld_nc<S, V>(p);
+                    else x[u].v[0] = *p;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i + u >= end) break;
+                if (k[u] != key) {
+                    if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+                    key = k[u];
+                    if (key >= vocab) return;
+                }
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] += Elem<S>::widen(x[u].v[j]);
+                }
+            }
+        }
+    };
+
+    int i = i0;
+    if (key_before == key) {                        // first the run that comes in from the piece before
+        while (i < i1 && skeys[i - i0] == key) ++i;
+        add_rows(i0, i);
+        part_of_run(true, i0);
+        if (i == i1) return;
+        key = skeys[i - i0];
+        if (key >= vocab) return;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = 0.0f;
     }
-    int hi = min(n, lo + step);                                 // keys[lo] == key, keys[hi] != key or hi == n
-    while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if (keys[mid] == key) lo = mid; else hi = mid;
-    }
-    const int last = lo / piece_len;
-    const int col = blockIdx.y * kThreads + threadIdx.x;
-    if (col >= hidden) return;
-    float acc[1] = {partial[size_t(2 * p + 1) * hidden + col]};
-#pragma unroll 8
-    for (int q = p + 1; q <= last; ++q) acc[0] += partial[size_t(2 * q) * hidden + col];
-    write_row<D, 1>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
+    add_rows(i, i1);
+    if (key >= vocab) return;
+    if (key_after == key) part_of_run(false, i1 - 1);
+    else if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
 }
 
 // ----------------------------------------------------------------- launches
 struct GradLayout {
     SortShape sort;
     int piece_len, pieces;
-    size_t keys, vals, counts, partial, used, total;      // byte offsets (two key and two value buffers)
+    size_t keys, vals, counts, partial, tickets, used, total;      // byte offsets (two key and two value buffers)
 };
 
 // Pieces of 32 tokens, shorter while there are too few for the machine: a
@@ -353,7 +549,7 @@ struct GradLayout {
 GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t hidden) {
     GradLayout g;
     g.sort = sort_shape(tokens, vocab);
-    g.piece_len = tokens >= 8192 ? 32 : tokens >= 2048 ? 16 : 8;
+    g.piece_len = tokens >= 8192 ? kMaxPiece : tokens >= 2048 ? 16 : 8;
     g.pieces = int((tokens + g.piece_len - 1) / g.piece_len);
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     size_t at = 0;
@@ -365,9 +561,11 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t hidden) {
     at += up(size_t(g.sort.tiles) * kBins * 4);
     g.partial = at;
     at += up(size_t(g.pieces) * 2 * size_t(hidden) * 4);
+    g.tickets = at;                 // one for each piece and block of columns, of one element at least
+    at += up(size_t(g.pieces) * size_t((hidden + kCols<false> - 1) / kCols<false>) * 4);
     g.used = at;
-    at += up(size_t(vocab));
-    g.total = at;
+    at += g.sort.tiles > 1 ? up(size_t(vocab)) : 0;
+    g.total = at > 0 ? at : 256;    // never an empty buffer, which has no address
     return g;
 }
 
@@ -378,13 +576,9 @@ int run_lookup(const void* ids, int wide, int64_t tokens, const S* table, int64_
                      host::aligned(table, 16) && host::aligned(out, 16);
     const int per = kThreads * 4 * (vec ? 8 : 1);
     const dim3 grid(unsigned(tokens), unsigned((hidden + per - 1) / per));
-    if (vec)
-        lookup_kernel<S, D, true><<<grid, kThreads, 0, st>>>(ids, wide, table, table_ld, vocab, out, out_ld,
-                                                             int(hidden), scale, dev_status);
-    else
-        lookup_kernel<S, D, false><<<grid, kThreads, 0, st>>>(ids, wide, table, table_ld, vocab, out, out_ld,
-                                                              int(hidden), scale, dev_status);
-    return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA;
+    const auto kernel = vec ? &lookup_kernel<S, D, true> : &lookup_kernel<S, D, false>;
+    return launch_dependent(kernel, grid, kThreads, 0, st, ids, wide, table, table_ld, vocab, out, out_ld, int(hidden),
+                            scale, dev_status);
 }
 
 template <typename S, typename D>
@@ -398,41 +592,59 @@ int run_grad(const Ids& ids, int64_t tokens, const S* d_out, int64_t d_ld, D* d_
                          reinterpret_cast<uint32_t*>(ws + g.vals + up(size_t(tokens) * 4))};
     auto* counts = reinterpret_cast<uint32_t*>(ws + g.counts);
     auto* partial = reinterpret_cast<float*>(ws + g.partial);
-    uint8_t* used = accumulate ? nullptr : ws + g.used;
+    auto* tickets = reinterpret_cast<uint32_t*>(ws + g.tickets);
     const int n = int(tokens);
-    if (used && cudaMemsetAsync(used, 0, size_t(ids.vocab), st) != cudaSuccess) return FP8Z_ECUDA;
-    for (int p = 0; p < g.sort.passes && n > 0; ++p) {
-        const uint32_t* kin = p ? keys[(p - 1) & 1] : nullptr;
-        const uint32_t* vin = p ? vals[(p - 1) & 1] : nullptr;
-        count_kernel<<<g.sort.tiles, kThreads, 0, st>>>(ids, kin, n, p * g.sort.digit, g.sort.digit, counts,
-                                                        p ? nullptr : used);
-        place_kernel<<<g.sort.tiles, kThreads, 0, st>>>(ids, kin, vin, n, p * g.sort.digit, g.sort.digit, counts,
-                                                        g.sort.tiles, keys[p & 1], vals[p & 1]);
-    }
-    const uint32_t* k = keys[(g.sort.passes - 1) & 1];
-    const uint32_t* v = vals[(g.sort.passes - 1) & 1];
     const bool vec = hidden % 8 == 0 && (d_ld * sizeof(S)) % 16 == 0 && (t_ld * sizeof(D)) % 16 == 0 &&
                      host::aligned(d_out, 16) && host::aligned(d_table, 16);
-    const int fill_rows = 8;
-    const int64_t fill = accumulate ? 0 : (ids.vocab + fill_rows - 1) / fill_rows;
-    const int cols = vec ? kCols<true> : kCols<false>;
-    const dim3 grid(unsigned(g.pieces + fill), unsigned((hidden + cols - 1) / cols));
-    if (grid.x > 0) {
-        if (vec)
-            runs_kernel<S, D, true><<<grid, kThreads, 0, st>>>(k, v, n, uint32_t(ids.vocab), g.piece_len, g.pieces, d_out,
-                                                               d_ld, d_table, t_ld, int(hidden), scale, accumulate,
-                                                               partial, used, fill_rows);
-        else
-            runs_kernel<S, D, false><<<grid, kThreads, 0, st>>>(k, v, n, uint32_t(ids.vocab), g.piece_len, g.pieces,
-                                                                d_out, d_ld, d_table, t_ld, int(hidden), scale,
-                                                                accumulate, partial, used, fill_rows);
+    const int cols = vec ? kCols<true> : kCols<false>, slabs = int((hidden + cols - 1) / cols);
+    const bool one = g.sort.tiles <= 1;
+    uint8_t* used = accumulate || one ? nullptr : ws + g.used;
+    const int64_t row_bytes = hidden * int64_t(sizeof(D));
+    int64_t filled = accumulate ? ids.vocab : 0;
+    auto next_fill = [&](int64_t bytes) {               // the next rows, about so many bytes of them
+        Fill f = {};
+        f.table = d_table;
+        f.used = used;
+        f.ld_bytes = t_ld * int64_t(sizeof(D));
+        f.row_bytes = row_bytes;
+        f.begin = filled;
+        f.end = filled = std::min<int64_t>(ids.vocab, filled + (bytes + row_bytes - 1) / row_bytes);
+        f.rows = int(std::min<int64_t>(kFillRows, std::max<int64_t>(1, kFillBytes / row_bytes)));
+        f.blocks = int((f.end - f.begin + f.rows - 1) / f.rows);
+        return f;
+    };
+    const int64_t all = ids.vocab * row_bytes;
+    const uint32_t *k = keys[0], *v = vals[0];
+    if (n > 0 && one) {
+        const Fill f = next_fill(kFillBesideSort);
+        if (int rc = launch_dependent(sort_tile_kernel, dim3(unsigned(1 + f.blocks)), kThreads, 0, st, ids, n,
+                                      g.sort.passes, g.sort.digit, keys[0], vals[0], f, tickets, g.pieces * slabs))
+            return rc;
+    } else if (n > 0) {
+        if (used && cudaMemsetAsync(used, 0, size_t(ids.vocab), st) != cudaSuccess) return FP8Z_ECUDA;
+        for (int p = 0; p < g.sort.passes; ++p) {
+            const uint32_t* kin = p ? keys[(p - 1) & 1] : nullptr;
+            const uint32_t* vin = p ? vals[(p - 1) & 1] : nullptr;
+            Fill f = next_fill(p ? kFillBesideSort : 0);         // the first launch finds out which rows occur
+            if (int rc = launch_dependent(count_kernel, dim3(unsigned(g.sort.tiles + f.blocks)), kThreads, 0, st, ids,
+                                          kin, n, p * g.sort.digit, g.sort.digit, counts, f, p ? nullptr : tickets,
+                                          g.pieces * slabs, p ? nullptr : used))
+                return rc;
+            f = next_fill(kFillBesideSort);
+            if (int rc = launch_dependent(place_kernel, dim3(unsigned(g.sort.tiles + f.blocks)), kThreads, 0, st, ids,
+                                          kin, vin, n, p * g.sort.digit, g.sort.digit, counts, g.sort.tiles,
+                                          keys[p & 1], vals[p & 1], f))
+                return rc;
+        }
+        k = keys[(g.sort.passes - 1) & 1];
+        v = vals[(g.sort.passes - 1) & 1];
     }
-    if (g.pieces > 1) {
-        const dim3 jgrid(unsigned(g.pieces - 1), unsigned((hidden + kThreads - 1) / kThreads));
-        join_kernel<D><<<jgrid, kThreads, 0, st>>>(k, n, uint32_t(ids.vocab), g.piece_len, partial, d_table, t_ld,
-                                                   int(hidden), scale, accumulate);
-    }
-    return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA;
+    const Fill f = next_fill(all);
+    const int64_t blocks = int64_t(g.pieces) * slabs + f.blocks;
+    if (blocks == 0) return FP8Z_OK;
+    const auto kernel = vec ? &runs_kernel<S, D, true> : &runs_kernel<S, D, false>;
+    return launch_dependent(kernel, dim3(unsigned(blocks)), kThreads, 0, st, k, v, n, uint32_t(ids.vocab), g.piece_len,
+                            d_out, d_ld, d_table, t_ld, int(hidden), scale, accumulate, partial, tickets, slabs, ids, f);
 }
 
 bool shape_ok(int64_t tokens, int64_t vocab, int64_t hidden) {

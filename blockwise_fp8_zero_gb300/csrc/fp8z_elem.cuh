@@ -34,8 +34,10 @@ struct Elem<__half> {
     static __device__ __forceinline__ __half narrow(float x) { return __float2half_rn(x); }
 };
 
-// N consecutive elements from an address aligned to min(16, N * sizeof(T)):
-// read once, through the non-coherent path.
+// N consecutive elements from a 16-byte-aligned address, through the
+// non-coherent path.  Volatile, like every load here that the compiler might
+// take for one of constant memory: a kernel may be set up before its inputs are
+// written (fp8z_launch.cuh), and no load may move before its wait.
 template <typename T, int N>
 struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
     T v[N];
@@ -47,7 +49,11 @@ __device__ __forceinline__ Pack<T, N> ld_nc(const T* p) {
     Pack<T, N> r;
     uint4* u = reinterpret_cast<uint4*>(&r);
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T) * N / 16); ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < int(sizeof(T) * N / 16); ++i)
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u[i].x), "=r"(u[i].y), "=r"(u[i].z), "=r"(u[i].w)
+                     : "l"(reinterpret_cast<const uint4*>(p) + i)
+                     : "memory");
     return r;
 }
 
@@ -66,6 +72,28 @@ __device__ __forceinline__ void st_vec(T* p, const Pack<T, N>& r) {
     const uint4* u = reinterpret_cast<const uint4*>(&r);
 #pragma unroll
     for (int i = 0; i < int(sizeof(T) * N / 16); ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+}
+
+// What is read for the last time, or written and not read again soon: loads that
+// do not stay in L1 and bring a 256-byte line pair into L2, stores that leave L2 first.
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> ld_stream(const T* p) {
+    Pack<T, N> r;
+    uint4* u = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) * N / 16); ++i)
+        asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u[i].x), "=r"(u[i].y), "=r"(u[i].z), "=r"(u[i].w)
+                     : "l"(reinterpret_cast<const uint4*>(p) + i)
+                     : "memory");
+    return r;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void st_stream(T* p, const Pack<T, N>& r) {
+    const uint4* u = reinterpret_cast<const uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) * N / 16); ++i) __stcs(reinterpret_cast<uint4*>(p) + i, u[i]);
 }
 
 inline bool dtype_ok(int32_t d) { return d == FP8Z_F32 || d == FP8Z_BF16 || d == FP8Z_F16; }

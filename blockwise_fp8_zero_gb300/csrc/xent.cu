@@ -26,6 +26,7 @@
 #include "fp8z_device.cuh"
 #include "fp8z_elem.cuh"
 #include "fp8z_host.h"
+#include "fp8z_launch.cuh"
 #include "fp8z_tcgen05.cuh"
 
 namespace fp8z {
@@ -354,7 +355,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rank = int(cluster_rank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        if (kEpi == kStats && blockIdx.x == 0) *A.ticket = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 2);
             mbar_init(empty(s), 1);
@@ -372,6 +372,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    dependent_wait();
+    if (kEpi == kStats && blockIdx.x == 0 && threadIdx.x == 0) *A.ticket = 0;
     const uint32_t tmem = *tmem_at;
     const Watchdog wd{abort_flag, A.dev_status, A.timeout_ns};
     const int tiles = A.mt * A.nt * A.splits;
@@ -500,8 +502,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------ small kernels
 // 16-bit rows copied to a stride the tensor maps can step over, zeros after the end.
-__global__ void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, int cols_pad,
-                                uint16_t* __restrict__ dst) {
+__global__ void pad_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, int cols, int cols_pad,
+                                uint16_t* dst) {
+    dependent_wait();
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
         for (int c = threadIdx.x; c < cols_pad; c += blockDim.x)
             dst[r * cols_pad + c] = c < cols ? src[r * ld + c] : uint16_t(0);
@@ -514,16 +517,17 @@ struct BlockTotal {
     int64_t kept;
 };
 
-__global__ void __launch_bounds__(1024) rows_kernel(const float2* __restrict__ part, int tiles, int n, int rows,
-                                                    const void* __restrict__ targets, int wide, int64_t ignore,
-                                                    int64_t vocab, const float* __restrict__ target_logit,
-                                                    int32_t* __restrict__ target, float* __restrict__ lse_ws,
-                                                    float* __restrict__ lse_out, float* __restrict__ loss,
-                                                    BlockTotal* __restrict__ totals, uint32_t* __restrict__ ticket,
-                                                    int mean, float scale, float* __restrict__ total,
-                                                    float* __restrict__ alpha, int32_t* dev_status) {
+__global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tiles, int n, int rows,
+                                                    const void* targets, int wide, int64_t ignore,
+                                                    int64_t vocab, const float* target_logit,
+                                                    int32_t* target, float* lse_ws,
+                                                    float* lse_out, float* loss,
+                                                    BlockTotal* totals, uint32_t* ticket,
+                                                    int mean, float scale, float* total,
+                                                    float* alpha, int32_t* dev_status) {
     __shared__ float2 sh[32][33];
     __shared__ bool last;
+    dependent_wait();
     const int r = threadIdx.x & 31, g = threadIdx.x >> 5;
     float m = -INFINITY, s = 0.0f;
     auto add = [&](float2 p) {
@@ -609,9 +613,10 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* __restrict__ p
 // The kept logits of a piece become P, in place: a warp takes a row's 256 words
 // (1 KB), reads all of it, and writes the two parts over it.
 constexpr int kProbTiles = 4;
-__global__ void __launch_bounds__(256) prob_kernel(uint8_t* __restrict__ p, int64_t row_bytes, int tiles, int words, int n,
-                                                   int v0, const int32_t* __restrict__ target,
-                                                   const float* __restrict__ lse, float p_scale, int bf16, int split_p) {
+__global__ void __launch_bounds__(256) prob_kernel(uint8_t* p, int64_t row_bytes, int tiles, int words, int n,
+                                                   int v0, const int32_t* target,
+                                                   const float* lse, float p_scale, int bf16, int split_p) {
+    dependent_wait();
     const int row = blockIdx.x, lane = threadIdx.x & 31;
     const int y = row < n ? target[row] : -1;
     const float ref = y >= 0 ? lse[row] * kLog2e : 0.0f;
@@ -643,9 +648,10 @@ __global__ void empty_total_kernel(float* total) { total[threadIdx.x] = 0.0f; }
 
 // dx = a * the sum of the K parts.
 template <typename T>
-__global__ void __launch_bounds__(256) finish_dx_kernel(const float* __restrict__ sum, int splits, int64_t part_stride,
-                                                        int64_t sum_ld, int n, int hidden, const float* __restrict__ alpha,
-                                                        T* __restrict__ dx, int64_t dx_ld) {
+__global__ void __launch_bounds__(256) finish_dx_kernel(const float* sum, int splits, int64_t part_stride,
+                                                        int64_t sum_ld, int n, int hidden, const float* alpha,
+                                                        T* dx, int64_t dx_ld) {
+    dependent_wait();
     const float a = *alpha;
     const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
     const int64_t row = blockIdx.x;
@@ -810,8 +816,7 @@ int launch_mma(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& 
     const auto k = &mma_kernel<kEpi>;
     if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), 12 + kEpi, kSmem)) return rc;
     const int64_t tiles = int64_t(A.mt) * A.nt * A.splits;
-    k<<<2 * unsigned(tiles < sms / 2 ? tiles : sms / 2), kThreads, kSmem, st>>>(ta, tb, tc, A);
-    return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA;
+    return launch_dependent(k, dim3(2 * unsigned(tiles < sms / 2 ? tiles : sms / 2)), kThreads, kSmem, st, ta, tb, tc, A);
 }
 
 int run(const void* x, const void* w, const void* targets, const fp8z_xent_args* args, float* loss, float* lse,
@@ -854,14 +859,16 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     const void *xp = x, *wp = w;
     int64_t x_ld = a.x_ld, w_ld = a.w_ld;
     if (copy_x) {
-        pad_rows_kernel<<<sms * 8, 256, 0, st>>>(static_cast<const uint16_t*>(x), a.x_ld, n, hidden, int(L.hidden_pad),
-                                                 reinterpret_cast<uint16_t*>(ws + L.x));
+        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned(sms * 8)), 256, 0, st, static_cast<const uint16_t*>(x),
+                                      a.x_ld, n, hidden, int(L.hidden_pad), reinterpret_cast<uint16_t*>(ws + L.x)))
+            return rc;
         xp = ws + L.x;
         x_ld = L.hidden_pad;
     }
     if (copy_w) {
-        pad_rows_kernel<<<sms * 8, 256, 0, st>>>(static_cast<const uint16_t*>(w), a.w_ld, vocab, hidden,
-                                                 int(L.hidden_pad), reinterpret_cast<uint16_t*>(ws + L.w));
+        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned(sms * 8)), 256, 0, st, static_cast<const uint16_t*>(w),
+                                      a.w_ld, vocab, hidden, int(L.hidden_pad), reinterpret_cast<uint16_t*>(ws + L.w)))
+            return rc;
         wp = ws + L.w;
         w_ld = L.hidden_pad;
     }
@@ -896,12 +903,12 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     if (int rc = launch_mma<kStats>(x_k, w_k, logits, A, sms, st)) return rc;
     // FP16 P is kept times 2^12: probabilities down to 2^-36 stay normal numbers or close
     const float p_scale = A.bf16 ? 1.0f : 4096.0f;
-    rows_kernel<<<(n + 31) / 32, 1024, 0, st>>>(part, A.nt, n, A.rows, targets, A.targets_wide, A.ignore, A.vocab,
-                                                target_logit, target, lse_ws, lse, loss,
-                                                reinterpret_cast<BlockTotal*>(ws + L.totals), A.ticket,
-                                                a.reduction == FP8Z_MEAN, grad ? a.grad_scale / p_scale : 1.0f, total,
-                                                grad ? alpha : nullptr, dev_status);
-    if (!grad) return done();
+    if (int rc = launch_dependent(rows_kernel, dim3(unsigned((n + 31) / 32)), 1024, 0, st, part, A.nt, n, A.rows, targets,
+                                  A.targets_wide, A.ignore, A.vocab, target_logit, target, lse_ws, lse, loss,
+                                  reinterpret_cast<BlockTotal*>(ws + L.totals), A.ticket, a.reduction == FP8Z_MEAN,
+                                  grad ? a.grad_scale / p_scale : 1.0f, total, grad ? alpha : nullptr, dev_status))
+        return rc;
+    if (!grad) return FP8Z_OK;
 
     auto* sum = reinterpret_cast<float*>(ws + L.sum);
     const bool dw_rows = host::aligned(dw, 16) && (a.dw_ld * dtype_bytes(a.dw_dtype)) % 16 == 0;
@@ -919,8 +926,9 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         const int words = int(a.vocab - v0 < L.piece ? a.vocab - v0 : L.piece), tiles = (words + kTN - 1) / kTN;
         if (v0 == last) {
             const dim3 grid(unsigned(n), unsigned((tiles + 8 * kProbTiles - 1) / (8 * kProbTiles)));
-            prob_kernel<<<grid, 256, 0, st>>>(p, L.piece * 4, tiles, words, n, v0, target, lse_ws, p_scale, A.bf16,
-                                              L.parts == 2);
+            if (int rc = launch_dependent(prob_kernel, grid, 256, 0, st, p, L.piece * 4, tiles, words, n, v0, target, lse_ws,
+                                          p_scale, A.bf16, L.parts == 2))
+                return rc;
         } else {
             MmaArgs Q = A;                              // the piece's logits again, as P
             Q.n = words;
@@ -958,12 +966,10 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     }
     const dim3 grid(unsigned(n), unsigned((hidden + 1023) / 1024));
     if (A.bf16)
-        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, n * L.hidden_pad, L.hidden_pad, n, hidden, alpha,
-                                               static_cast<__nv_bfloat16*>(dx), a.dx_ld);
-    else
-        finish_dx_kernel<<<grid, 256, 0, st>>>(sum, L.splits, n * L.hidden_pad, L.hidden_pad, n, hidden, alpha,
-                                               static_cast<__half*>(dx), a.dx_ld);
-    return done();
+        return launch_dependent(finish_dx_kernel<__nv_bfloat16>, grid, 256, 0, st, sum, L.splits, n * L.hidden_pad,
+                                L.hidden_pad, n, hidden, alpha, static_cast<__nv_bfloat16*>(dx), a.dx_ld);
+    return launch_dependent(finish_dx_kernel<__half>, grid, 256, 0, st, sum, L.splits, n * L.hidden_pad, L.hidden_pad, n,
+                            hidden, alpha, static_cast<__half*>(dx), a.dx_ld);
 }
 
 }  // namespace

@@ -45,11 +45,10 @@ plan_summary_dtype = np.dtype([
     ("real_elems", "<i8"), ("total_blocks", "<i8"), ("fold_pad_elems", "<i8"),
     ("shard_pad_elems", "<i8"), ("capacity_blocks", "<i8"), ("naive_straddled_blocks", "<i8"),
 ])
-tensor_entry_dtype = np.dtype([
-    ("src", "<u8"), ("dst", "<u8"), ("numel", "<i8"), ("first_chunk", "<i8"),
-    ("src_dtype", "<i4"), ("dst_dtype", "<i4"),
+tensor_chunk_dtype = np.dtype([
+    ("src", "<u8"), ("dst", "<u8"), ("count", "<i4"), ("src_dtype", "<i2"), ("dst_dtype", "<i2"),
 ])
-assert tensor_entry_dtype.itemsize == 40
+assert tensor_chunk_dtype.itemsize == 24
 assert param_entry_dtype.itemsize == 64 and block_desc_dtype.itemsize == 20
 
 EXPORTED = ("fp8z_plan_shards", "fp8z_adamw_requant_step", "fp8z_adamw_requant_step_rowmajor",
@@ -136,9 +135,9 @@ def lib():
         L.fp8z_transpose_rowwise.argtypes = [P, P, i64, i64, P, P, P]
         L.fp8z_dequant_rowwise.argtypes = [P, P, i64, i64, i32, P, P]
         f32 = ctypes.c_float
-        L.fp8z_encode_tensor_list.argtypes = [P, P, P, P, P, i32, P, P]
-        L.fp8z_grad_norm.argtypes = [P, i32, i64, f32, P, P, P]
-        L.fp8z_grad_clip.argtypes = [P, i32, i64, f32, f32, f32, P, P, P]
+        L.fp8z_encode_tensor_list.argtypes = [P, P, P, P, P, i32, P, i64, P]
+        L.fp8z_grad_norm.argtypes = [P, i64, f32, P, P, P]
+        L.fp8z_grad_clip.argtypes = [P, i64, f32, f32, f32, P, P, P, P]
         L.fp8z_embedding.argtypes = [P, i32, i64, P, i32, i64, i64, i64, P, i32, i64, f32, P, P]
         L.fp8z_embedding_grad_workspace.argtypes = [i64, i64, i64]
         L.fp8z_embedding_grad.argtypes = [P, i32, i64, P, i32, i64, P, i32, i64, i64, i64, f32, i64, i32,
@@ -182,11 +181,25 @@ def _dptr(t, dtype=None, name="tensor"):
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    import torch
-    cur = torch.cuda.current_device()
-    if t.device.index is not None and t.device.index != cur:
+    cur = _current_device()
+    if t.get_device() != cur:
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
     return t.data_ptr()
+
+
+# torch's public calls for the current device and stream build Python objects
+# that cost microseconds in a call that launches for two; the plain ones below
+# them are used where they exist.
+_get_device = _get_raw_stream = None
+
+
+def _current_device():
+    global _get_device
+    if _get_device is None:
+        import torch
+        torch.cuda.current_device()          # initialises CUDA once
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _get_device()
 
 
 DESC_BYTES = block_desc_dtype.itemsize       # 20
@@ -206,9 +219,13 @@ def _check_tables(cap, desc, params, nparams):
 
 
 def _stream_handle(stream):
-    import torch
+    global _get_raw_stream
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _get_raw_stream is None:
+            import torch
+            _get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _get_raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -491,27 +508,42 @@ def fp8z_dequant_rowwise(q, s, out, transpose=False, stream=None):
 
 
 # ------------------------------------- operators around the optimizer step
-def _dtype_code(t, name, allowed=(FP8Z_F32, FP8Z_BF16, FP8Z_F16)):
-    import torch
-    code = {torch.float32: FP8Z_F32, torch.bfloat16: FP8Z_BF16, torch.float16: FP8Z_F16,
-            torch.int32: FP8Z_I32, torch.int64: FP8Z_I64}.get(t.dtype)
+_FLOATS, _HALVES, _INTS = (FP8Z_F32, FP8Z_BF16, FP8Z_F16), (FP8Z_BF16, FP8Z_F16), (FP8Z_I32, FP8Z_I64)
+_dtype_codes = {}
+
+
+def _dtype_code(t, name, allowed=_FLOATS):
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float32: FP8Z_F32, torch.bfloat16: FP8Z_BF16, torch.float16: FP8Z_F16,
+                             torch.int32: FP8Z_I32, torch.int64: FP8Z_I64})
+    code = _dtype_codes.get(t.dtype)
     if code not in allowed:
         raise ValueError(f"{name} must not be {t.dtype}")
     return code
 
 
+def _ptr(t, name, code):
+    """_dptr with the element type given as a code of this module."""
+    if t is None:
+        return None
+    _dtype_code(t, name, (code,))
+    return _dptr(t, None, name)
+
+
 def _matrix(t, name):
     """(pointer, rows, cols, row stride in elements) of a 2-D CUDA tensor on the
     current device whose rows are contiguous and do not overlap."""
-    import torch
-    if t.dim() != 2 or not t.is_cuda:
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    rows, cols = shape
+    s0, s1 = t.stride()
+    ld = s0 if rows > 1 else cols
+    if (cols > 1 and s1 != 1) or ld < cols:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_current_device()}")
     return t.data_ptr(), rows, cols, ld
 
 
@@ -519,8 +551,8 @@ class TensorList:
     """The device table of a list of tensors (fp8z_encode_tensor_list), the
     number of its chunks, and the tensors it points to, which it keeps alive."""
 
-    def __init__(self, table, n, chunks, tensors):
-        self.table, self.n, self.chunks, self.tensors = table, n, chunks, tensors
+    def __init__(self, table, chunks, tensors):
+        self.table, self.chunks, self.tensors = table, chunks, tensors
 
 
 def fp8z_encode_tensor_list(srcs, dsts=None, device="cuda"):
@@ -528,7 +560,6 @@ def fp8z_encode_tensor_list(srcs, dsts=None, device="cuda"):
     any mixture) for fp8z_grad_norm and fp8z_grad_clip.  dsts: tensors of the
     same sizes that the clipped values go to (None: in place).  The table holds
     addresses: make a new one when a tensor moves."""
-    import torch
     srcs = list(srcs)
     dsts = srcs if dsts is None else list(dsts)
     if len(dsts) != len(srcs):
@@ -541,13 +572,13 @@ def fp8z_encode_tensor_list(srcs, dsts=None, device="cuda"):
         rows[:, i] = (_dptr(s, None, f"src {i}"), _dptr(d, None, f"dst {i}"), s.numel(),
                       _dtype_code(s, f"src {i}"), _dtype_code(d, f"dst {i}"))
     kinds = rows[3:].astype(np.int32)
-    out = np.zeros(max(n, 1), tensor_entry_dtype)
     chunks = ctypes.c_int64(0)
-    rc = lib().fp8z_encode_tensor_list(rows[0].ctypes.data, rows[1].ctypes.data, rows[2].ctypes.data,
-                                       kinds[0].ctypes.data, kinds[1].ctypes.data, n, out.ctypes.data,
-                                       ctypes.byref(chunks))
+    args = (rows[0].ctypes.data, rows[1].ctypes.data, rows[2].ctypes.data, kinds[0].ctypes.data, kinds[1].ctypes.data, n)
+    _check("fp8z_encode_tensor_list", lib().fp8z_encode_tensor_list(*args, None, 0, ctypes.byref(chunks)))
+    out = np.zeros(max(chunks.value, 1), tensor_chunk_dtype)
+    rc = lib().fp8z_encode_tensor_list(*args, out.ctypes.data, chunks.value, ctypes.byref(chunks))
     _check("fp8z_encode_tensor_list", rc)
-    return TensorList(table_to_device(out, device), n, int(chunks.value), (srcs, dsts))
+    return TensorList(table_to_device(out, device), int(chunks.value), (srcs, dsts))
 
 
 def fp8z_grad_norm_workspace():
@@ -556,41 +587,40 @@ def fp8z_grad_norm_workspace():
 
 
 def _norm_args(tensors, norm, workspace):
-    import torch
     if norm.numel() < 2:
         raise ValueError("norm must hold two float32 values: the norm and the coefficient")
     if workspace.numel() * workspace.element_size() < GRAD_NORM_WORKSPACE:
         raise ValueError(f"workspace must hold {GRAD_NORM_WORKSPACE} bytes")
-    return (_dptr(tensors.table, None, "table"), tensors.n, tensors.chunks, _dptr(norm, torch.float32, "norm"),
+    return (_dptr(tensors.table, None, "table"), tensors.chunks, _ptr(norm, "norm", FP8Z_F32),
             _dptr(workspace, None, "workspace"))
 
 
 def fp8z_grad_norm(tensors, norm, workspace, grad_scale=1.0, stream=None):
     """norm[0] = |grad_scale| * sqrt(sum of squares over the whole list), norm[1] = 1."""
-    table, n, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
-    _check("fp8z_grad_norm", lib().fp8z_grad_norm(table, n, chunks, grad_scale, nptr, ws, _stream_handle(stream)))
+    table, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
+    _check("fp8z_grad_norm", lib().fp8z_grad_norm(table, chunks, grad_scale, nptr, ws, _stream_handle(stream)))
 
 
-def fp8z_grad_clip(tensors, max_norm, norm, workspace, grad_scale=1.0, eps=1e-6, stream=None):
+def fp8z_grad_clip(tensors, max_norm, norm, workspace, grad_scale=1.0, eps=1e-6, dev_status=None, stream=None):
     """The norm, then dst = grad_scale * min(1, max_norm / (norm + eps)) * src for
     every tensor; norm (float32 [2], CUDA) gets the norm and the coefficient."""
-    table, n, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
-    _check("fp8z_grad_clip", lib().fp8z_grad_clip(table, n, chunks, grad_scale, max_norm, eps, nptr, ws,
-                                                  _stream_handle(stream)))
+    table, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
+    rc = lib().fp8z_grad_clip(table, chunks, grad_scale, max_norm, eps, nptr, ws,
+                              _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
+    _check("fp8z_grad_clip", rc)
 
 
 def fp8z_embedding(ids, table, out, scale=1.0, dev_status=None, stream=None):
     """out[t] = scale * table[ids[t]].  ids: int64 or int32, any shape, contiguous;
     table [vocab, hidden], out [tokens, hidden]: float32 / bfloat16 / float16,
     rows may be strided."""
-    import torch
     tp, vocab, hidden, t_ld = _matrix(table, "table")
     op, tokens, cols, o_ld = _matrix(out, "out")
     if ids.numel() != tokens or cols != hidden:
         raise ValueError(f"out must be [{ids.numel()}, {hidden}], got {list(out.shape)}")
-    rc = lib().fp8z_embedding(_dptr(ids, None, "ids"), _dtype_code(ids, "ids", (FP8Z_I32, FP8Z_I64)), tokens, tp,
+    rc = lib().fp8z_embedding(_dptr(ids, None, "ids"), _dtype_code(ids, "ids", _INTS), tokens, tp,
                               _dtype_code(table, "table"), vocab, hidden, t_ld, op, _dtype_code(out, "out"), o_ld,
-                              scale, _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
+                              scale, _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
     _check("fp8z_embedding", rc)
 
 
@@ -606,16 +636,15 @@ def fp8z_embedding_grad(ids, d_out, d_table, workspace, scale=1.0, padding_idx=-
                         dev_status=None, stream=None):
     """d_table[v] = scale * sum of d_out[t] over ids[t] == v (zeros elsewhere), or
     that sum added to d_table (accumulate).  Deterministic."""
-    import torch
     dp, tokens, hidden, d_ld = _matrix(d_out, "d_out")
     tp, vocab, cols, t_ld = _matrix(d_table, "d_table")
     if ids.numel() != tokens or cols != hidden:
         raise ValueError(f"d_out must be [{ids.numel()}, {cols}], got {list(d_out.shape)}")
-    rc = lib().fp8z_embedding_grad(_dptr(ids, None, "ids"), _dtype_code(ids, "ids", (FP8Z_I32, FP8Z_I64)), tokens, dp,
+    rc = lib().fp8z_embedding_grad(_dptr(ids, None, "ids"), _dtype_code(ids, "ids", _INTS), tokens, dp,
                                    _dtype_code(d_out, "d_out"), d_ld, tp, _dtype_code(d_table, "d_table"), vocab,
                                    hidden, t_ld, scale, int(padding_idx), int(bool(accumulate)),
                                    _dptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
-                                   _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
+                                   _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
     _check("fp8z_embedding_grad", rc)
 
 
@@ -626,7 +655,7 @@ def _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accum
     """(x pointer, w pointer, filled fp8z_xent_args)."""
     xp, tokens, hidden, x_ld = _matrix(x, "x")
     wp, vocab, cols, w_ld = _matrix(w, "w")
-    dtype = _dtype_code(x, "x", (FP8Z_BF16, FP8Z_F16))
+    dtype = _dtype_code(x, "x", _HALVES)
     if cols != hidden or w.dtype != x.dtype:
         raise ValueError(f"w must be [vocab, {hidden}] of {x.dtype}, got {list(w.shape)} of {w.dtype}")
     if reduction not in _REDUCTIONS:
@@ -636,7 +665,7 @@ def _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accum
     if targets is not None:
         if targets.numel() != tokens:
             raise ValueError(f"targets must hold {tokens} words, got {targets.numel()}")
-        a.targets_dtype = _dtype_code(targets, "targets", (FP8Z_I32, FP8Z_I64))
+        a.targets_dtype = _dtype_code(targets, "targets", _INTS)
     if dx is not None:
         _, rows, cols, a.dx_ld = _matrix(dx, "dx")
         if (rows, cols) != (tokens, hidden) or dx.dtype != x.dtype:
@@ -661,10 +690,9 @@ def fp8z_linear_xent_workspace(x, w, dw=None, piece_words=0):
 
 
 def _xent_outputs(tokens, loss, lse, total):
-    import torch
     if loss.numel() < tokens or (lse is not None and lse.numel() < tokens) or total.numel() < 2:
         raise ValueError("loss and lse must hold one value per token, total two")
-    return _dptr(loss, torch.float32, "loss"), _dptr(lse, torch.float32, "lse"), _dptr(total, torch.float32, "total")
+    return _ptr(loss, "loss", FP8Z_F32), _ptr(lse, "lse", FP8Z_F32), _ptr(total, "total", FP8Z_F32)
 
 
 def fp8z_linear_xent(x, w, targets, loss, total, workspace, ignore_index=-100, reduction="mean", lse=None,
@@ -673,12 +701,11 @@ def fp8z_linear_xent(x, w, targets, loss, total, workspace, ignore_index=-100, r
     float32 [2] (mean or sum of the kept tokens' losses, their number), lse
     optional.  x [tokens, hidden], w [vocab, hidden]: bfloat16 or float16, rows
     may be strided; targets int64 or int32."""
-    import torch
     xp, wp, a = _xent_args(x, w, targets, None, None, ignore_index, reduction, 1.0, False)
     rc = lib().fp8z_linear_xent(xp, wp, _dptr(targets, None, "targets"), ctypes.byref(a),
                                 *_xent_outputs(a.tokens, loss, lse, total), _dptr(workspace, None, "workspace"),
                                 workspace.numel() * workspace.element_size(),
-                                _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
+                                _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
     _check("fp8z_linear_xent", rc)
 
 
@@ -686,13 +713,12 @@ def fp8z_linear_xent_grad(x, w, targets, loss, total, dx, dw, workspace, ignore_
                           grad_scale=1.0, accumulate_dw=False, lse=None, dev_status=None, stream=None):
     """fp8z_linear_xent and the gradients of grad_scale * total[0]: dx of x's type,
     dw of x's type or float32 (overwritten, or added to with accumulate_dw)."""
-    import torch
     xp, wp, a = _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accumulate_dw)
     rc = lib().fp8z_linear_xent_grad(xp, wp, _dptr(targets, None, "targets"), ctypes.byref(a),
                                      *_xent_outputs(a.tokens, loss, lse, total), dx.data_ptr(), dw.data_ptr(),
                                      _dptr(workspace, None, "workspace"),
                                      workspace.numel() * workspace.element_size(),
-                                     _dptr(dev_status, torch.int32, "dev_status"), _stream_handle(stream))
+                                     _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
     _check("fp8z_linear_xent_grad", rc)
 
 

@@ -423,37 +423,39 @@ typedef enum { FP8Z_F32 = 0, FP8Z_BF16 = 1, FP8Z_F16 = 2, FP8Z_I32 = 3, FP8Z_I64
  * so.
  */
 
-/* One tensor of a list: numel contiguous elements at src, scaled into dst. */
-typedef struct {
-    const void *src;
-    void *dst;               /* src itself, or another buffer of dst_dtype          */
-    int64_t numel;
-    int64_t first_chunk;     /* written by fp8z_encode_tensor_list                   */
-    int32_t src_dtype, dst_dtype;
-} fp8z_tensor_entry;         /* 40 bytes */
-
-#define FP8Z_TENSOR_CHUNK 4096             /* elements of one chunk of a list          */
+#define FP8Z_TENSOR_CHUNK 4096             /* most elements of one chunk of a list     */
 #define FP8Z_GRAD_NORM_WORKSPACE 32768     /* bytes; zeroed by the caller once, before the
                                               first call                              */
 
+/* Up to FP8Z_TENSOR_CHUNK neighbouring elements of one tensor of a list: read at
+ * src, scaled into dst. */
+typedef struct {
+    const void *src;
+    void *dst;               /* src itself, or another buffer of dst_dtype          */
+    int32_t count;
+    int16_t src_dtype, dst_dtype;
+} fp8z_tensor_chunk;         /* 24 bytes */
+
 /*
  * fp8z_encode_tensor_list -- host only: the table fp8z_grad_norm and
- * fp8z_grad_clip read the tensors through.  srcs, numels, src_dtypes (FP8Z_F32,
- * FP8Z_BF16 or FP8Z_F16): host arrays of n; dsts and dst_dtypes: host arrays of
- * n, or both NULL for scaling in place.  out: host array of n entries, which the
- * caller copies to device memory; *chunks_out: the number of chunks, passed to
- * the calls.  A tensor may be empty.  In place (dst == src) needs equal types.
+ * fp8z_grad_clip read the tensors through, every tensor cut into chunks.  srcs,
+ * numels, src_dtypes (FP8Z_F32, FP8Z_BF16 or FP8Z_F16): host arrays of n
+ * contiguous tensors; dsts and dst_dtypes: host arrays of n, or both NULL for
+ * scaling in place.  out: host array of `capacity` chunks, which the caller
+ * copies to device memory, or NULL to ask for the number; *chunks_out: the
+ * number of chunks.  A tensor may be empty.  In place (dst == src) needs equal
+ * types.  Returns FP8Z_OK / EINVAL / EALIGN / ENOSPACE.
  */
 FP8Z_API int fp8z_encode_tensor_list(const void *const *srcs, void *const *dsts, const int64_t *numels,
                                      const int32_t *src_dtypes, const int32_t *dst_dtypes, int32_t n,
-                                     fp8z_tensor_entry *out, int64_t *chunks_out);
+                                     fp8z_tensor_chunk *out, int64_t capacity, int64_t *chunks_out);
 
 /*
  * fp8z_grad_norm -- norm[0] = |grad_scale| * sqrt(sum of g^2 over every element
  * of every src of the list), norm[1] = 1.  Squares are FP32 (an element beyond
  * 1.8e19 makes the norm infinite), sums FP64 in a fixed order: the same list
  * gives the same bits.  An empty list has norm 0.  list: device,
- * fp8z_tensor_entry[n]; norm: device f32[2]; workspace: device,
+ * fp8z_tensor_chunk[chunks]; norm: device f32[2]; workspace: device,
  * FP8Z_GRAD_NORM_WORKSPACE bytes.
  *
  * fp8z_grad_clip -- the same, then norm[1] = coef = min(1, max_norm /
@@ -461,13 +463,17 @@ FP8Z_API int fp8z_encode_tensor_list(const void *const *srcs, void *const *dsts,
  * dst = (grad_scale * coef) * g for every element, rounded once to dst's type.
  * Everything stays on the device: an infinite norm gives coef 0 and a NaN gives
  * NaN everywhere, so the caller can tell from norm[0] that a step is lost.  In
- * place with grad_scale * coef == 1, nothing is written.
+ * place with grad_scale * coef == 1, nothing is written.  A short list takes one
+ * cooperative launch whose blocks wait for one another's sums, at most as long
+ * as fp8z_set_wait_limit_ns says: FP8Z_ETIMEOUT then lands in *dev_status
+ * (device int32 or NULL), norm is NaN, dst is not complete, and the workspace
+ * has to be zeroed again.
  * Returns FP8Z_OK / EINVAL / EALIGN / EUNSUPPORTED / ECUDA.
  */
-FP8Z_API int fp8z_grad_norm(const fp8z_tensor_entry *list, int32_t n, int64_t chunks, float grad_scale, float *norm,
+FP8Z_API int fp8z_grad_norm(const fp8z_tensor_chunk *list, int64_t chunks, float grad_scale, float *norm,
                             void *workspace, void *stream);
-FP8Z_API int fp8z_grad_clip(const fp8z_tensor_entry *list, int32_t n, int64_t chunks, float grad_scale,
-                            float max_norm, float eps, float *norm, void *workspace, void *stream);
+FP8Z_API int fp8z_grad_clip(const fp8z_tensor_chunk *list, int64_t chunks, float grad_scale, float max_norm, float eps,
+                            float *norm, void *workspace, int32_t *dev_status, void *stream);
 
 /*
  * fp8z_embedding -- out[t][:] = scale * table[ids[t]][:], the product in FP32,
