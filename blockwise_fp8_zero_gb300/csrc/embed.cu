@@ -311,56 +311,40 @@ __global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t
     }
 }
 
-// One tile: all passes in one block, the list in shared memory between them.
-__global__ void __launch_bounds__(kThreads) sort_tile_kernel(Ids ids, int n, int passes, int digit,
-                                                             uint32_t* keys_out,
-                                                             uint32_t* vals_out, Fill fill,
-                                                             uint32_t* tickets, int ntickets) {
-    __shared__ SortShared sh;
-    __shared__ uint32_t list[kTile];                   // token of each place
-    __shared__ uint32_t key_at[kTile];
+// Up to kTile tokens: a token's place is the number of keys before its own, all
+// of them compared from shared memory, a warp a token.  1021 tokens: RANK_US us
+// against SORT_US for one block that sorts digit by digit.
+constexpr int kRankTokens = 32;                        // of one block
+__global__ void __launch_bounds__(kThreads) rank_kernel(Ids ids, int n, uint32_t* keys_out, uint32_t* vals_out, Fill fill,
+                                                        uint32_t* tickets, int ntickets) {
+    __shared__ uint32_t keys[kTile];
     dependent_wait();
-    if (blockIdx.x > 0) {
-        fill_rows(fill, ids, n, blockIdx.x - 1);
+    const int blocks = gridDim.x - fill.blocks;
+    if (int(blockIdx.x) >= blocks) {
+        fill_rows(fill, ids, n, blockIdx.x - blocks);
         return;
     }
-    for (int i = threadIdx.x; i < ntickets; i += kThreads) tickets[i] = 0;
-    const int nb = 1 << digit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = warp * (32 * kItems);
-    uint32_t k[kItems], v[kItems], rank[kItems];
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < ntickets; i += blocks * kThreads) tickets[i] = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) keys[i] = ids.key(i, blockIdx.x == 0);
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int T = kRankTokens / kWarps;
+    const int i0 = blockIdx.x * kRankTokens + warp * T;
+    uint32_t k[T];
+    int before[T] = {};
 #pragma unroll
-    for (int r = 0; r < kItems; ++r) {
-        const int i = t0 + r * 32 + lane;
-        k[r] = i < n ? ids.key(i, true) : 0;
-        v[r] = uint32_t(i);
+    for (int t = 0; t < T; ++t) k[t] = i0 + t < n ? keys[i0 + t] : 0;
+    for (int j = lane; j < n; j += 32) {
+        const uint32_t q = keys[j];
+#pragma unroll
+        for (int t = 0; t < T; ++t) before[t] += q < k[t] || (q == k[t] && j < i0 + t);
     }
-    for (int p = 0; p < passes; ++p) {
-        const int shift = p * digit;
-        clear_counts(sh, nb);
-        __syncthreads();
-        tile_ranks(sh, k, rank, n - t0, shift, nb);
-        __syncthreads();
-        warp_bases(sh, nb, [&](int b, uint32_t total) { sh.base[b] = total; });
-        __syncthreads();
-        digit_bases(sh, nb, [&](int b, uint32_t&, uint32_t& total) { total = sh.base[b]; });
-        __syncthreads();
-        const bool last = p == passes - 1;
 #pragma unroll
-        for (int r = 0; r < kItems; ++r) {
-            if (t0 + r * 32 + lane < n) {
-                const uint32_t d = (k[r] >> shift) & (nb - 1);
-                const uint32_t at = sh.base[d] + sh.warp_count[warp][d] + rank[r];
-                (last ? keys_out : key_at)[at] = k[r];
-                (last ? vals_out : list)[at] = v[r];
-            }
-        }
-        __syncthreads();
-        if (!last) {
-#pragma unroll
-            for (int r = 0; r < kItems; ++r) {
-                const int i = t0 + r * 32 + lane;
-                k[r] = i < n ? key_at[i] : 0;
-                v[r] = i < n ? list[i] : 0;
-            }
+    for (int t = 0; t < T; ++t) {
+        const int at = __reduce_add_sync(0xFFFFFFFFu, before[t]);
+        if (lane == 0 && i0 + t < n) {
+            keys_out[at] = k[t];
+            vals_out[at] = uint32_t(i0 + t);
         }
     }
 }
@@ -371,8 +355,25 @@ constexpr int kMaxPiece = 32;
 template <bool VEC>
 constexpr int kCols = kThreads * (VEC ? 8 : 1);
 
+// Adds to or writes V neighbouring elements.  FP32 sums are added by the memory
+// system: one addition for each element of the call, in no race with another, and
+// no thread waits for the old value.
 template <typename D, int V>
 __device__ __forceinline__ void write_row(D* p, const float (&acc)[V], float scale, bool accumulate) {
+    if constexpr (std::is_same_v<D, float>) {
+        if (accumulate) {
+            if constexpr (V > 1) {
+#pragma unroll
+                for (int i = 0; i < V; i += 4)
+                    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + i), "f"(acc[i] * scale),
+                                 "f"(acc[i + 1] * scale), "f"(acc[i + 2] * scale), "f"(acc[i + 3] * scale)
+                                 : "memory");
+            } else {
+                asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(acc[0] * scale) : "memory");
+            }
+            return;
+        }
+    }
     Pack<D, V> y;
     if (accumulate) {
         if constexpr (V > 1) y = ld_plain<D, V>(p);
@@ -617,8 +618,9 @@ int run_grad(const Ids& ids, int64_t tokens, const S* d_out, int64_t d_ld, D* d_
     const uint32_t *k = keys[0], *v = vals[0];
     if (n > 0 && one) {
         const Fill f = next_fill(kFillBesideSort);
-        if (int rc = launch_dependent(sort_tile_kernel, dim3(unsigned(1 + f.blocks)), kThreads, 0, st, ids, n,
-                                      g.sort.passes, g.sort.digit, keys[0], vals[0], f, tickets, g.pieces * slabs))
+        const int blocks = (n + kRankTokens - 1) / kRankTokens;
+        if (int rc = launch_dependent(rank_kernel, dim3(unsigned(blocks + f.blocks)), kThreads, 0, st, ids, n, keys[0],
+                                      vals[0], f, tickets, g.pieces * slabs))
             return rc;
     } else if (n > 0) {
         if (used && cudaMemsetAsync(used, 0, size_t(ids.vocab), st) != cudaSuccess) return FP8Z_ECUDA;

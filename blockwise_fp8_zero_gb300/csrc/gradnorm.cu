@@ -13,7 +13,6 @@
 #include <cuda_runtime.h>
 
 #include "fp8z.h"
-#include "fp8z_device.cuh"
 #include "fp8z_elem.cuh"
 #include "fp8z_host.h"
 #include "fp8z_launch.cuh"
@@ -27,34 +26,47 @@ constexpr int kMaxGrid = 2048;
 static_assert(kChunk % (kThreads * 8) == 0, "whole vectors per thread");
 
 struct Workspace {
-    uint32_t ticket, arrived, left, pad;
+    uint32_t ticket, pad[3];
     double partial[kMaxGrid];
 };
 static_assert(sizeof(Workspace) <= FP8Z_GRAD_NORM_WORKSPACE, "workspace size in the header");
 
 __device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// One thread's share of a chunk's squares: at most sixteen, added in FP32.
+// One thread's share of a chunk's squares: two sums of at most 17, added in FP32.
 template <typename T>
 __device__ __forceinline__ float chunk_squares(const T* g, int n) {
     constexpr int V = 16 / sizeof(T), R = kChunk / (kThreads * V);
     float a = 0.0f, b = 0.0f;
-    if (n == kChunk && aligned16(g)) {
-        Pack<T, V> x[R];
+    if (n >= V && aligned16(g)) {
+        const int done = n / V * V;                 // the last few elements of a tensor
+        uint4 x[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = ld_nc<T, V>(g + (r * kThreads + threadIdx.x) * V);
+        for (int r = 0; r < R; ++r) {
+            const int i = int(r * kThreads + threadIdx.x) * V;
+            x[r] = ld_nc_16(g + (i + V <= n ? i : 0));       // loads without branches are all under way at once
+            if (i + V > n) x[r] = make_uint4(0, 0, 0, 0);
+        }
+        if (int(threadIdx.x) < n - done) {
+            const float p = Elem<T>::widen(g[done + threadIdx.x]);
+            a = p * p;
+        }
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r) {
+            const Pack<T, V> y = *reinterpret_cast<const Pack<T, V>*>(&x[r]);
 #pragma unroll
             for (int i = 0; i < V; i += 2) {
-                const float p = Elem<T>::widen(x[r].v[i]), q = Elem<T>::widen(x[r].v[i + 1]);
+                const float p = Elem<T>::widen(y.v[i]), q = Elem<T>::widen(y.v[i + 1]);
                 a = fmaf(p, p, a);
                 b = fmaf(q, q, b);
             }
+        }
     } else {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const float p = Elem<T>::widen(g[i]);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += 2 * kThreads) {
+            const float p = Elem<T>::widen(g[i]), q = i + kThreads < n ? Elem<T>::widen(g[i + kThreads]) : 0.0f;
             a = fmaf(p, p, a);
+            b = fmaf(q, q, b);
         }
     }
     return a + b;
@@ -81,12 +93,6 @@ __device__ __forceinline__ double block_sum(double v) {
     return r;
 }
 
-__device__ __forceinline__ double sum_partials(const Workspace* ws) {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < int(gridDim.x); i += kThreads) v += __ldcg(&ws->partial[i]);
-    return block_sum(v);
-}
-
 __device__ __forceinline__ float2 norm_and_coef(double sum, float grad_scale, float max_norm, float eps) {
     const float nm = float(fabs(double(grad_scale)) * sqrt(sum));
     const float c = max_norm / (nm + eps);         // NaN stays NaN; an infinite limit never clips
@@ -95,7 +101,7 @@ __device__ __forceinline__ float2 norm_and_coef(double sum, float grad_scale, fl
 
 // Each block takes neighbouring chunks and the sum goes on in FP64 from chunk to
 // chunk: long lists lose nothing, and the FP64 pipe sees one addition per thread
-// and 16 elements.  The block that finishes last adds the blocks' sums.
+// and 32 elements.  The block that finishes last adds the blocks' sums.
 // 503 M FP32 elements: 285 us, 7.06 TB/s.
 __global__ void __launch_bounds__(kThreads) norm_kernel(const fp8z_tensor_chunk* list, int64_t chunks, float grad_scale,
                                                         float max_norm, float eps, float* norm, Workspace* ws) {
@@ -121,7 +127,9 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const fp8z_tensor_chunk*
     __syncthreads();
     if (!last) return;
     __threadfence();
-    sum = sum_partials(ws);
+    sum = 0.0;
+    for (int i = threadIdx.x; i < int(gridDim.x); i += kThreads) sum += __ldcg(&ws->partial[i]);
+    sum = block_sum(sum);
     if (threadIdx.x == 0) {
         const float2 r = norm_and_coef(sum, grad_scale, max_norm, eps);
         norm[0] = r.x;
@@ -129,23 +137,45 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const fp8z_tensor_chunk*
     }
 }
 
+// kFull: a whole chunk; the loads of a shorter one go on, to its first elements,
+// where they would pass its end, so that all of them are under way at once.
+template <bool kFull, typename S, typename D>
+__device__ __forceinline__ void scale_vectors(const S* src, D* dst, int n, float f) {
+    constexpr int V = 8, R = kChunk / (kThreads * V), W = V * sizeof(S) / 16;
+    const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+    uint4 x[R][W];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = int(r * kThreads + threadIdx.x) * V;
+#pragma unroll
+        for (int w = 0; w < W; ++w) x[r][w] = ld_stream_16(src + (kFull || i + V <= n ? i : 0), w);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = int(r * kThreads + threadIdx.x) * V;
+        const Pack<S, V> u = *reinterpret_cast<const Pack<S, V>*>(&x[r][0]);
+        Pack<D, V> y;
+#pragma unroll
+        for (int j = 0; j < V; ++j) y.v[j] = Elem<D>::narrow(Elem<S>::widen(u.v[j]) * f);
+        if (kFull || i + V <= n) st_stream8(dst + i, y, wide);
+    }
+}
+
 template <typename S, typename D>
 __device__ __forceinline__ void chunk_scale(const S* src, D* dst, int n, float f) {
-    constexpr int V = 8, R = kChunk / (kThreads * V);
-    if (n == kChunk && aligned16(src) && aligned16(dst)) {
-        Pack<S, V> x[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = ld_stream<S, V>(src + (r * kThreads + threadIdx.x) * V);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            Pack<D, V> y;
-#pragma unroll
-            for (int i = 0; i < V; ++i) y.v[i] = Elem<D>::narrow(Elem<S>::widen(x[r].v[i]) * f);
-            st_stream<D, V>(dst + (r * kThreads + threadIdx.x) * V, y);
-        }
-    } else {
-        for (int i = threadIdx.x; i < n; i += kThreads) dst[i] = Elem<D>::narrow(Elem<S>::widen(src[i]) * f);
+    constexpr int V = 8;
+    const bool aligned = aligned16(src) && aligned16(dst);
+    if (n == kChunk && aligned) {
+        scale_vectors<true>(src, dst, n, f);
+        return;
     }
+    int i = threadIdx.x;
+    if (n >= V && aligned) {
+        scale_vectors<false>(src, dst, n, f);
+        i += n / V * V;                             // the last few elements of a tensor
+    }
+#pragma unroll 8
+    for (; i < n; i += kThreads) dst[i] = Elem<D>::narrow(Elem<S>::widen(src[i]) * f);
 }
 
 template <typename S>
@@ -174,66 +204,17 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const fp8z_tensor_chunk
     scale_chunk(t, grad_scale * norm[1]);
 }
 
-// A short list: every chunk has a block of its own, all of them resident, which
-// waits until all sums are there, adds them up for itself and scales its chunk.
-__global__ void __launch_bounds__(kThreads) clip_short_kernel(const fp8z_tensor_chunk* list, float grad_scale,
-                                                              float max_norm, float eps, float* norm, Workspace* ws,
-                                                              int64_t timeout_ns, int32_t* dev_status) {
-    __shared__ float2 result;
-    __shared__ bool ok;
-    const fp8z_tensor_chunk t = list[blockIdx.x];
-    double sum = block_sum(double(squares(t)));
-    if (threadIdx.x == 0) {
-        ws->partial[blockIdx.x] = sum;
-        __threadfence();
-        atomicAdd(&ws->arrived, 1u);
-        const uint64_t t0 = global_timer_ns();
-        bool all;
-        while (!(all = *reinterpret_cast<volatile uint32_t*>(&ws->arrived) >= gridDim.x) &&
-               global_timer_ns() - t0 <= uint64_t(timeout_ns)) {
-        }
-        if (!all) report_status(dev_status, FP8Z_ETIMEOUT);
-        __threadfence();
-        ok = all;
-    }
-    __syncthreads();
-    const bool all = ok;
-    sum = sum_partials(ws);
-    if (threadIdx.x == 0) {
-        result = norm_and_coef(sum, grad_scale, max_norm, eps);
-        if (!all) result = make_float2(NAN, NAN);
-        if (blockIdx.x == 0 || !all) {
-            norm[0] = result.x;
-            norm[1] = result.y;
-        }
-        if (atomicAdd(&ws->left, 1u) == gridDim.x - 1) ws->arrived = ws->left = 0;    // everyone has seen them
-    }
-    __syncthreads();
-    if (all) scale_chunk(t, grad_scale * result.y);
-}
-
 int launch(const fp8z_tensor_chunk* list, int64_t chunks, float grad_scale, float max_norm, float eps, float* norm,
-           void* workspace, bool clip, int32_t* dev_status, void* stream) {
+           void* workspace, bool clip, void* stream) {
     if (chunks < 0 || chunks > 0x7FFFFFFF || (chunks > 0 && !list) || !norm || !workspace) return FP8Z_EINVAL;
     if (!std::isfinite(grad_scale) || !(max_norm >= 0.0f) || !(eps >= 0.0f) || !std::isfinite(eps)) return FP8Z_EINVAL;
-    if (!host::aligned(list, 8) || !host::aligned(norm, 4) || !host::aligned(workspace, 16) ||
-        !host::aligned(dev_status, 4))
+    if (!host::aligned(list, 8) || !host::aligned(norm, 4) || !host::aligned(workspace, 16))
         return FP8Z_EALIGN;
     int sms = 0;
     if (int rc = host::device_sms(&sms)) return rc;
     const auto st = static_cast<cudaStream_t>(stream);
     auto* ws = static_cast<Workspace*>(workspace);
-    // Four blocks of 256 threads fit every SM whatever the kernel's registers.  From 100 K to 2.5 M
-    // elements the one launch takes FILL_SHORT.
-    if (clip && chunks > 0 && chunks <= sms * 4 && chunks <= kMaxGrid) {
-        int64_t limit = host::wait_limit_ns();
-        void* args[] = {&list, &grad_scale, &max_norm, &eps, &norm, &ws, &limit, &dev_status};
-        return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(&clip_short_kernel), dim3(unsigned(chunks)),
-                                           dim3(kThreads), args, 0, st) == cudaSuccess
-                   ? FP8Z_OK
-                   : FP8Z_ECUDA;
-    }
-    const int64_t most = std::min<int64_t>(sms * 8, kMaxGrid);
+    const int64_t most = std::min<int64_t>(sms * 4, kMaxGrid);
     const dim3 grid(unsigned(std::min(std::max<int64_t>(chunks, 1), most)));
     if (int rc = launch_dependent(norm_kernel, grid, kThreads, 0, st, list, chunks, grad_scale, max_norm, eps, norm, ws))
         return rc;
@@ -280,11 +261,11 @@ extern "C" int fp8z_encode_tensor_list(const void* const* srcs, void* const* dst
 extern "C" int fp8z_grad_norm(const fp8z_tensor_chunk* list, int64_t chunks, float grad_scale, float* norm,
                               void* workspace, void* stream) {
     const fp8z::host::NvtxRange nvtx_range("fp8z_grad_norm");
-    return fp8z::launch(list, chunks, grad_scale, INFINITY, 0.0f, norm, workspace, false, nullptr, stream);
+    return fp8z::launch(list, chunks, grad_scale, INFINITY, 0.0f, norm, workspace, false, stream);
 }
 
 extern "C" int fp8z_grad_clip(const fp8z_tensor_chunk* list, int64_t chunks, float grad_scale, float max_norm, float eps,
-                              float* norm, void* workspace, int32_t* dev_status, void* stream) {
+                              float* norm, void* workspace, void* stream) {
     const fp8z::host::NvtxRange nvtx_range("fp8z_grad_clip");
-    return fp8z::launch(list, chunks, grad_scale, max_norm, eps, norm, workspace, true, dev_status, stream);
+    return fp8z::launch(list, chunks, grad_scale, max_norm, eps, norm, workspace, true, stream);
 }

@@ -137,7 +137,7 @@ def lib():
         f32 = ctypes.c_float
         L.fp8z_encode_tensor_list.argtypes = [P, P, P, P, P, i32, P, i64, P]
         L.fp8z_grad_norm.argtypes = [P, i64, f32, P, P, P]
-        L.fp8z_grad_clip.argtypes = [P, i64, f32, f32, f32, P, P, P, P]
+        L.fp8z_grad_clip.argtypes = [P, i64, f32, f32, f32, P, P, P]
         L.fp8z_embedding.argtypes = [P, i32, i64, P, i32, i64, i64, i64, P, i32, i64, f32, P, P]
         L.fp8z_embedding_grad_workspace.argtypes = [i64, i64, i64]
         L.fp8z_embedding_grad.argtypes = [P, i32, i64, P, i32, i64, P, i32, i64, i64, i64, f32, i64, i32,
@@ -601,13 +601,12 @@ def fp8z_grad_norm(tensors, norm, workspace, grad_scale=1.0, stream=None):
     _check("fp8z_grad_norm", lib().fp8z_grad_norm(table, chunks, grad_scale, nptr, ws, _stream_handle(stream)))
 
 
-def fp8z_grad_clip(tensors, max_norm, norm, workspace, grad_scale=1.0, eps=1e-6, dev_status=None, stream=None):
+def fp8z_grad_clip(tensors, max_norm, norm, workspace, grad_scale=1.0, eps=1e-6, stream=None):
     """The norm, then dst = grad_scale * min(1, max_norm / (norm + eps)) * src for
     every tensor; norm (float32 [2], CUDA) gets the norm and the coefficient."""
     table, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
-    rc = lib().fp8z_grad_clip(table, chunks, grad_scale, max_norm, eps, nptr, ws,
-                              _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
-    _check("fp8z_grad_clip", rc)
+    _check("fp8z_grad_clip", lib().fp8z_grad_clip(table, chunks, grad_scale, max_norm, eps, nptr, ws,
+                                                  _stream_handle(stream)))
 
 
 def fp8z_embedding(ids, table, out, scale=1.0, dev_status=None, stream=None):

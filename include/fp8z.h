@@ -423,7 +423,7 @@ typedef enum { FP8Z_F32 = 0, FP8Z_BF16 = 1, FP8Z_F16 = 2, FP8Z_I32 = 3, FP8Z_I64
  * so.
  */
 
-#define FP8Z_TENSOR_CHUNK 4096             /* most elements of one chunk of a list     */
+#define FP8Z_TENSOR_CHUNK 8192             /* most elements of one chunk of a list     */
 #define FP8Z_GRAD_NORM_WORKSPACE 32768     /* bytes; zeroed by the caller once, before the
                                               first call                              */
 
@@ -463,17 +463,13 @@ FP8Z_API int fp8z_encode_tensor_list(const void *const *srcs, void *const *dsts,
  * dst = (grad_scale * coef) * g for every element, rounded once to dst's type.
  * Everything stays on the device: an infinite norm gives coef 0 and a NaN gives
  * NaN everywhere, so the caller can tell from norm[0] that a step is lost.  In
- * place with grad_scale * coef == 1, nothing is written.  A short list takes one
- * cooperative launch whose blocks wait for one another's sums, at most as long
- * as fp8z_set_wait_limit_ns says: FP8Z_ETIMEOUT then lands in *dev_status
- * (device int32 or NULL), norm is NaN, dst is not complete, and the workspace
- * has to be zeroed again.
+ * place with grad_scale * coef == 1, nothing is written.
  * Returns FP8Z_OK / EINVAL / EALIGN / EUNSUPPORTED / ECUDA.
  */
 FP8Z_API int fp8z_grad_norm(const fp8z_tensor_chunk *list, int64_t chunks, float grad_scale, float *norm,
                             void *workspace, void *stream);
 FP8Z_API int fp8z_grad_clip(const fp8z_tensor_chunk *list, int64_t chunks, float grad_scale, float max_norm, float eps,
-                            float *norm, void *workspace, int32_t *dev_status, void *stream);
+                            float *norm, void *workspace, void *stream);
 
 /*
  * fp8z_embedding -- out[t][:] = scale * table[ids[t]][:], the product in FP32,
