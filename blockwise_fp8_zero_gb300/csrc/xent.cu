@@ -36,12 +36,14 @@ constexpr int kTM = 256, kTN = 256, kBK = 64;          // output tile of a pair 
 constexpr int kHalf = 128;                             // a block's rows of A and of the result, and columns of B
 constexpr int kStages = 6;
 constexpr int kBytesA = kHalf * kBK * 2, kBytesB = kHalf * kBK * 2, kStageBytes = kBytesA + kBytesB;
-constexpr int kThreads = 256;                          // warp 0 loads, warp 1 multiplies, warps 4-7 read the sums
+constexpr int kHalves = 1;                             // of a tile's columns, each read by four warps
+constexpr int kThreads = 128 + 128 * kHalves;           // warps 0 and 3 load A and B, 1 multiplies, from 4 on they read the sums
 constexpr int kTmemCols = 512;                         // two accumulators of 256 columns
-constexpr int kSlab = 32 * 128;                        // staged results of one warp: 32 rows of 128 bytes
-constexpr int kStaging = 4 * 2 * kSlab;
+constexpr int kCols = kTN / kHalves;                         // columns of one of those warps
+constexpr int kSlab = 32 * 128, kSlabs = 2;            // its staged results: 32 rows of 128 bytes
+constexpr int kStaging = 4 * kHalves * kSlabs * kSlab;
 constexpr int kNumBars = 2 * kStages + 5;
-constexpr int kSmem = kStages * kStageBytes + kStaging + kNumBars * 8 + 24 + 1024;
+constexpr int kSmem = kStages * kStageBytes + kStaging + kNumBars * 8 + 32 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -53,6 +55,7 @@ struct MmaArgs {
     int kb;                   // K blocks of 64
     int b_wrap;               // B's K block returns to 0 here (the two parts of P share one x)
     int b_n0, b_k0;           // where B starts, in elements
+    int b_blocks;             // B's map has its columns as blocks of 64
     int bf16;
     int64_t timeout_ns;
     int32_t* dev_status;
@@ -62,7 +65,7 @@ struct MmaArgs {
     int targets_wide;
     int64_t ignore, vocab;
     const int32_t* target;    // -1: takes no part in the loss (written by rows_kernel)
-    float2* part;             // [tile][rows] maximum and sum
+    float2* part;             // [kHalves * tile + half][rows] maximum and sum
     float* target_logit;
     const float* lse;
     int keep_from;            // words from here on leave their logits in the piece's buffer
@@ -113,15 +116,16 @@ __device__ __forceinline__ int load_target(const void* targets, int wide, int64_
     return y == ignore || y < 0 || y >= vocab ? -1 : int(y);
 }
 
-// A warp's way out: 32 rows of 128 bytes go to one of two slabs in the layout
-// of a 128-byte-swizzled tensor map, and from there to global memory as one
-// tile, clipped at the tensor's edges.  Rows of 16 bytes per thread would leave
-// half-written 32-byte sectors all over the result.
+// A warp's way out: 32 rows of 128 bytes go to a slab in the layout of a
+// 128-byte-swizzled tensor map, and from there to global memory as one tile,
+// clipped at the tensor's edges.  A row for each thread, stored by the threads,
+// wrote 262 MB of dw at 3.4 TB/s with 32 bytes a store and less with 16; this
+// way it is 262 MB in DW_FEW us.
 struct Stager {
     uint32_t slab;
     int which, lane;
     __device__ __forceinline__ uint32_t begin() {
-        if (lane == 0) bulk_wait_read<1>();          // the slab's last tile but one has been read
+        if (lane == 0) bulk_wait_read<kSlabs - 1>();          // the slab's last tile has been read
         __syncwarp();
         return slab + which * kSlab;
     }
@@ -137,7 +141,7 @@ struct Stager {
             store(slab + which * kSlab);
             bulk_commit();
         }
-        which ^= 1;
+        if (++which == kSlabs) which = 0;
     }
 };
 
@@ -147,10 +151,10 @@ __device__ __forceinline__ void stage32(Stager& sg, const uint32_t (&r)[32]) {
     for (int j = 0; j < 8; ++j) sg.put(s, j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
 }
 
-// Maximum and sum of exponentials of one row over the tile's columns.
+// Maximum and sum of exponentials of one row over half of the tile's columns.
 __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                               int row, Stager& sg) {
-    const int col0 = t.n * kTN, n_valid = min(kTN, A.n - col0);
+                                               int row, int half, Stager& sg) {
+    const int col0 = t.n * kTN + half * kCols, n_valid = min(kCols, A.n - col0);
     const int target = row < A.m ? load_target(A.targets, A.targets_wide, A.ignore, A.vocab, row) - col0 : -1;
     const bool keep = col0 >= A.keep_from;
     float mx = -INFINITY, sum = 0.0f;
@@ -189,7 +193,7 @@ __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorM
             A.target_logit[row] = x;
         }
     }
-    if (row < A.m) A.part[size_t(t.n) * A.rows + row] = make_float2(mx, sum);
+    if (row < A.m) A.part[size_t(kHalves * t.n + half) * A.rows + row] = make_float2(mx, sum);
 }
 
 // P of eight neighbouring words of one row, times p_scale: in 16 bits, and what
@@ -213,46 +217,48 @@ __device__ __forceinline__ void prob8(const uint32_t* r, float ref, int target, 
     }
 }
 
-// Rows and columns past the end become zeros: the products read whole tiles.
-// The buffer holds, for each row and tile of 256 words, 512 bytes of P and 512
-// bytes of its second part: the room of the tile's FP32 logits.
+// Words past the end become zeros: the products read whole tiles.  The buffer
+// holds, for each row and tile of 256 words, 512 bytes of P and 512 bytes of its
+// second part: the room of the tile's FP32 logits.
 __device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                              int row, Stager& sg) {
-    const int n_valid = min(kTN, A.n - t.n * kTN);
+                                              int row, int half, Stager& sg) {
+    const int n_valid = A.n - (t.n * kTN + half * kCols);
     const int y = row < A.m ? A.target[row] : -1;
-    const int target = y - (A.v0 + t.n * kTN);
+    const int target = y - (A.v0 + t.n * kTN + half * kCols);
     const float ref = y >= 0 ? A.lse[row] * kLog2e : 0.0f;
-    for (int c = 0; c < kTN; c += 64) {
+    for (int c = 0; c < kCols; c += 64) {
         uint32_t h[32], l[32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int part = 0; part < 2; ++part) {
             uint32_t r[32];
-            tmem_ld32(r, acc + c + half * 32);
+            tmem_ld32(r, acc + c + part * 32);
             tmem_wait_ld();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int at = c + half * 32 + q * 8;
+                const int at = c + part * 32 + q * 8;
                 uint32_t hq[4], lq[4];
                 prob8(r + q * 8, ref, target - at, n_valid - at, y >= 0, A.p_scale, A.bf16, hq, lq);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    h[half * 16 + q * 4 + i] = hq[i];
-                    l[half * 16 + q * 4 + i] = lq[i];
+                    h[part * 16 + q * 4 + i] = hq[i];
+                    l[part * 16 + q * 4 + i] = lq[i];
                 }
             }
         }
+        const int col = half * kCols + c;
         stage32(sg, h);
-        sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c, 2 * t.n, row, s); });
+        sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, col, 2 * t.n, row, s); });
         if (A.split_p) {
             stage32(sg, l);
-            sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c, 2 * t.n + 1, row, s); });
+            sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, col, 2 * t.n + 1, row, s); });
         }
     }
 }
 
 __device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                             int row, Stager& sg) {
-    for (int c = 0; c < kTN && t.n * kTN + c < A.n; c += 32) {
+                                             int row, int half, Stager& sg) {
+    const int col0 = t.n * kTN + half * kCols;
+    for (int c = 0; c < kCols && col0 + c < A.n; c += 32) {
         uint32_t r[32];
         tmem_ld32(r, acc + c);
         tmem_wait_ld();
@@ -262,8 +268,8 @@ __device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap
         stage32(sg, r);
         sg.end([&](uint32_t s) {
             if (row >= A.m) return;
-            if (A.accumulate) tma_add_3d(&out, t.n * kTN + c, row, t.split, s);
-            else tma_store_3d(&out, t.n * kTN + c, row, t.split, s);
+            if (A.accumulate) tma_add_3d(&out, col0 + c, row, t.split, s);
+            else tma_store_3d(&out, col0 + c, row, t.split, s);
         });
     }
 }
@@ -282,32 +288,33 @@ __device__ __forceinline__ void weight_chunk(T* p, const uint32_t (&r)[32], int 
 }
 
 __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                                int row, Stager& sg) {
+                                                int row, int half, Stager& sg) {
     const float a = *A.alpha;
     const int y = A.v0 + row;                        // of lane 0, which issues the stores
+    const int col0 = t.n * kTN + half * kCols;
     if (A.staged && A.out_dtype != FP8Z_F32) {
-        for (int c = 0; c < kTN && t.n * kTN + c < A.n; c += 64) {
+        for (int c = 0; c < kCols && col0 + c < A.n; c += 64) {
             uint32_t h[32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int part = 0; part < 2; ++part) {
                 uint32_t r[32];
-                tmem_ld32(r, acc + c + half * 32);
+                tmem_ld32(r, acc + c + part * 32);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    h[half * 16 + j] =
+                    h[part * 16 + j] =
                         pack16(__uint_as_float(r[2 * j]) * a, __uint_as_float(r[2 * j + 1]) * a, A.bf16);
             }
             stage32(sg, h);
-            sg.end([&](uint32_t s) { if (row < A.m) tma_store_2d(&out, t.n * kTN + c, y, s); });
+            sg.end([&](uint32_t s) { if (row < A.m) tma_store_2d(&out, col0 + c, y, s); });
         }
         return;
     }
-    for (int c = 0; c < kTN && t.n * kTN + c < A.n; c += 32) {
+    for (int c = 0; c < kCols && col0 + c < A.n; c += 32) {
         uint32_t r[32];
         tmem_ld32(r, acc + c);
         tmem_wait_ld();
-        const int col = t.n * kTN + c;
+        const int col = col0 + c;
         if (A.staged) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a);
@@ -330,7 +337,7 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
 // A pair of blocks takes 256 x 256 results at a time.  Each block loads 128 rows
 // of A and 128 columns of B into a ring of kStages tiles; one thread of the
 // first block issues the products of both, into one of two accumulators in each
-// block's tensor memory, while four warps of each block read the other.  The
+// block's tensor memory, while eight warps of each block read the other.  The
 // copies of both blocks count on the first block's barriers, each block arriving
 // for its own.
 template <int kEpi>
@@ -346,26 +353,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto full = [&](int s) { return bars + s * 8; };                       // first block: both blocks' copies are there
     auto empty = [&](int s) { return bars + (kStages + s) * 8; };          // the products that read them are done
     auto tfull = [&](int b) { return bars + (2 * kStages + b) * 8; };
-    auto tempty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };  // first block: all eight warps have read it
+    auto tempty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };  // first block: both blocks' warps have read it
     const uint32_t drain = bars + (2 * kStages + 4) * 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBarsAt + kNumBars * 8);
     volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(smem + kBarsAt + kNumBars * 8 + 8);
-    volatile uint32_t* issued_by = reinterpret_cast<volatile uint32_t*>(smem + kBarsAt + kNumBars * 8 + 12);   // [2]
+    volatile uint32_t* issued_by = reinterpret_cast<volatile uint32_t*>(smem + kBarsAt + kNumBars * 8 + 16);   // [4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = int(cluster_rank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full(s), 2);
+            mbar_init(full(s), 4);
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), 8);
+            mbar_init(tempty(b), 8 * kHalves);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
+    }
+    if (threadIdx.x == 32) {
+        tensormap_prefetch(&ta);
+        tensormap_prefetch(&tb);
     }
     if (warp == 2) tmem_alloc(smem_addr(const_cast<uint32_t*>(tmem_at)), kTmemCols);
     tc_fence_before();
@@ -378,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const Watchdog wd{abort_flag, A.dev_status, A.timeout_ns};
     const int tiles = A.mt * A.nt * A.splits;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {          // one thread for A and one for B: an issue takes some 100 cycles of a stage's 512
         if (lane == 0) {
             int s = 0, ph = 0;
             uint32_t issued = 0;
@@ -391,28 +402,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t sa = base + s * kStageBytes, sb = sa + kBytesA;
-                    const uint32_t bar = cluster_addr(full(s), 0);
-                    mbar_arrive_expect_tx_cluster(bar, kStageBytes);
+                    const uint32_t sa = base + s * kStageBytes, sb = sa + kBytesA, bar = cluster_addr(full(s), 0);
                     const int kw = k >= A.b_wrap ? k - A.b_wrap : k, kb = kw * kBK + A.b_k0;
-                    if constexpr (kEpi == kWeight) {         // P^T: 128 words, 64 tokens of one part
+                    if (warp == 0) {
+                        mbar_arrive_expect_tx_cluster(bar, kBytesA);
+                        if constexpr (kEpi == kWeight)           // P^T: 128 words, 64 tokens of one part
+                            tma_load_4d_pair(sa, &ta, 0, kw * kBK, m % kTN / 64, m / kTN * 2 + (k >= A.b_wrap), bar);
+                        else if constexpr (kEpi == kSum)         // P: 128 tokens, 64 words of the first part
+                            tma_load_3d_pair(sa, &ta, k * kBK % kTN, k * kBK / kTN * 2, m, bar);
+                        else
+                            tma_load_2d_pair(sa, &ta, k * kBK, m, bar);
+                    } else {
+                        mbar_arrive_expect_tx_cluster(bar, kBytesB);
+                        if constexpr (!kBMn) {
+                            tma_load_2d_pair(sb, &tb, kb, n, bar);
+                        } else if (A.b_blocks) {                 // 128 columns as two blocks of 64
+                            tma_load_3d_pair(sb, &tb, 0, kb, n / 64, bar);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < kHalf / 64; ++j) {
-                            const int word = m + j * 64;
-                            tma_load_3d_pair(sa + j * (64 * kBK * 2), &ta, word % kTN, word / kTN * 2 + (k >= A.b_wrap),
-                                             kw * kBK, bar);
+                            for (int j = 0; j < kHalf / 64; ++j)
+                                tma_load_2d_pair(sb + j * (64 * kBK * 2), &tb, n + j * 64, kb, bar);
                         }
-                    } else if constexpr (kEpi == kSum) {     // P: 128 tokens, 64 words of the first part
-                        tma_load_3d_pair(sa, &ta, k * kBK % kTN, k * kBK / kTN * 2, m, bar);
-                    } else {
-                        tma_load_2d_pair(sa, &ta, k * kBK, m, bar);
-                    }
-                    if constexpr (kBMn) {
-#pragma unroll
-                        for (int j = 0; j < kHalf / 64; ++j)
-                            tma_load_2d_pair(sb + j * (64 * kBK * 2), &tb, n + j * 64, kb, bar);
-                    } else {
-                        tma_load_2d_pair(sb, &tb, kb, n, bar);
                     }
                     ++issued;
                     if (++s == kStages) {
@@ -421,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            st_cluster_u32(cluster_addr(smem_addr(const_cast<uint32_t*>(issued_by + rank)), 0), issued);
+            st_cluster_u32(cluster_addr(smem_addr(const_cast<uint32_t*>(issued_by + 2 * rank + (warp == 3))), 0), issued);
         }
     } else if (warp == 1 && rank == 0) {
         if (lane == 0) {
@@ -460,19 +470,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_wait_drain(drain, 0, A.dev_status);
         }
     } else if (warp >= 4) {
-        const int quarter = warp - 4;
-        Stager sg{base + kStages * kStageBytes + quarter * 2 * kSlab, 0, lane};
+        const int quarter = warp & 3, half = (warp - 4) >> 2;      // rows are the warp's own quarter of the lanes
+        Stager sg{base + kStages * kStageBytes + (warp - 4) * kSlabs * kSlab, 0, lane};
         int b = 0, bph = 0;
         for (int t = pair; t < tiles; t += pairs) {
             const TileAt at = tile_at(A, t);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull(b), bph, wd))) break;
             tc_fence_after();
-            const uint32_t acc = tmem + b * kTN + (uint32_t(quarter * 32) << 16);
+            const uint32_t acc = tmem + b * kTN + half * kCols + (uint32_t(quarter * 32) << 16);
             const int row = at.m * kTM + rank * kHalf + quarter * 32 + lane;
-            if constexpr (kEpi == kStats) epilogue_stats(A, tc, at, acc, row, sg);
-            else if constexpr (kEpi == kProb) epilogue_prob(A, tc, at, acc, row, sg);
-            else if constexpr (kEpi == kSum) epilogue_sum(A, tc, at, acc, row, sg);
-            else epilogue_weight(A, tc, at, acc, row, sg);
+            if constexpr (kEpi == kStats) epilogue_stats(A, tc, at, acc, row, half, sg);
+            else if constexpr (kEpi == kProb) epilogue_prob(A, tc, at, acc, row, half, sg);
+            else if constexpr (kEpi == kSum) epilogue_sum(A, tc, at, acc, row, half, sg);
+            else epilogue_weight(A, tc, at, acc, row, half, sg);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(tempty(b), 0);
@@ -485,10 +495,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();
     // Whatever a wait gave up on, every copy lands before either block ends.  A stage for which
-    // only one of the blocks came to issue its copies lacks the other's arrival: it is made here.
+    // some of the four threads never came to issue their copies lacks their arrivals: they are made here.
     if (rank == 0 && threadIdx.x == 0) {
-        const uint32_t a = issued_by[0], b = issued_by[1], most = max(a, b);
-        for (uint32_t i = min(a, b); i < most; ++i) mbar_arrive(full(i % kStages));
+        uint32_t most = 0;
+        for (int j = 0; j < 4; ++j) most = max(most, issued_by[j]);
+        for (int j = 0; j < 4; ++j)
+            for (uint32_t i = issued_by[j]; i < most; ++i) mbar_arrive(full(i % kStages));
         for (uint32_t i = most > kStages ? most - kStages : 0; i < most; ++i)
             mbar_wait_drain(full(i % kStages), (i / kStages) & 1, A.dev_status);
     }
@@ -529,29 +541,45 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tile
     __shared__ bool last;
     dependent_wait();
     const int r = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int row = blockIdx.x * 32 + g;               // in the end a warp has a row, and lane 0 finishes it
+    int y = -1;
+    float own = 0.0f;
+    if (r == 0 && row < n) {
+        y = load_target(targets, wide, ignore, vocab, row);
+        if (y < 0) {
+            const int64_t raw = wide ? static_cast<const int64_t*>(targets)[row]
+                                     : int64_t(static_cast<const int32_t*>(targets)[row]);
+            if (raw != ignore) report_status(dev_status, FP8Z_EINVAL);
+        } else {
+            own = target_logit[row];
+        }
+    }
     float m = -INFINITY, s = 0.0f;
     auto add = [&](float2 p) {
         const float m2 = fmaxf(m, p.x), ref = m2 == -INFINITY ? 0.0f : m2;
         s = s * ex2((m - ref) * kLog2e) + p.y * ex2((p.x - ref) * kLog2e);
         m = m2;
     };
-    {
-        const int row = blockIdx.x * 32 + r;
-        if (row < n) {
-            int t = g;
-            for (; t + 96 < tiles; t += 128) {
-                float2 q[4];
+    const int col = blockIdx.x * 32 + r;               // the row of this thread's partial results
+    if (col < n) {
+        int t = g;
+        for (; t + 224 < tiles; t += 256) {
+            float2 q[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = part[size_t(t + 32 * i) * rows + row];
+            for (int i = 0; i < 8; ++i) q[i] = part[size_t(t + 32 * i) * rows + col];
+            float top = q[0].x;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) add(q[i]);
-            }
-            for (; t < tiles; t += 32) add(part[size_t(t) * rows + row]);
+            for (int i = 1; i < 8; ++i) top = fmaxf(top, q[i].x);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += q[i].y * ex2((q[i].x - ref) * kLog2e);
+            add(make_float2(top, sum));
         }
+        for (; t < tiles; t += 32) add(part[size_t(t) * rows + col]);
     }
     sh[r][g] = make_float2(m, s);
     __syncthreads();
-    const int row = blockIdx.x * 32 + g;               // from here a warp a row
     const float2 mine = sh[g][r];
     m = mine.x;
     s = mine.y;
@@ -561,16 +589,9 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tile
     __syncthreads();
     if (r == 0) {
         float out = 0.0f;
-        int y = -1;
         if (row < n) {
-            y = load_target(targets, wide, ignore, vocab, row);
-            if (y < 0) {
-                const int64_t raw = wide ? static_cast<const int64_t*>(targets)[row]
-                                         : int64_t(static_cast<const int32_t*>(targets)[row]);
-                if (raw != ignore) report_status(dev_status, FP8Z_EINVAL);
-            }
             const float lse = m + logf(s);
-            out = y >= 0 ? lse - target_logit[row] : 0.0f;
+            out = y >= 0 ? lse - own : 0.0f;
             target[row] = y;
             lse_ws[row] = lse;
             if (lse_out) lse_out[row] = lse;
@@ -579,28 +600,31 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tile
         sh[0][g] = make_float2(out, y >= 0 ? 1.0f : 0.0f);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        BlockTotal b = {0.0, 0};
-        for (int i = 0; i < 32; ++i) {
-            b.loss += double(sh[0][i].x);
-            b.kept += sh[0][i].y != 0.0f;
-        }
-        totals[blockIdx.x] = b;
-        __threadfence();
-        last = atomicAdd(ticket, 1u) == gridDim.x - 1;
-    }
-    __syncthreads();
-    if (!last || g != 0) return;
-    __threadfence();
-    BlockTotal b = {0.0, 0};
-    for (int i = r; i < int(gridDim.x); i += 32) {
-        b.loss += __ldcg(&totals[i].loss);
-        b.kept += __ldcg(reinterpret_cast<const long long*>(&totals[i].kept));
-    }
+    if (g != 0) return;
+    BlockTotal b = {double(sh[0][r].x), int64_t(sh[0][r].y)};
+    auto reduce = [&] {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        b.loss += __shfl_down_sync(0xFFFFFFFFu, b.loss, o);
-        b.kept += __shfl_down_sync(0xFFFFFFFFu, b.kept, o);
+        for (int o = 16; o > 0; o >>= 1) {
+            b.loss += __shfl_down_sync(0xFFFFFFFFu, b.loss, o);
+            b.kept += __shfl_down_sync(0xFFFFFFFFu, b.kept, o);
+        }
+    };
+    reduce();
+    if (gridDim.x > 1) {
+        if (r == 0) {
+            totals[blockIdx.x] = b;
+            __threadfence();
+            last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+        }
+        __syncwarp();
+        if (!last) return;
+        __threadfence();
+        b = {0.0, 0};
+        for (int i = r; i < int(gridDim.x); i += 32) {
+            b.loss += __ldcg(&totals[i].loss);
+            b.kept += __ldcg(reinterpret_cast<const long long*>(&totals[i].kept));
+        }
+        reduce();
     }
     if (r == 0) {
         const double by = mean ? double(b.kept > 0 ? b.kept : 1) : 1.0;
@@ -657,6 +681,7 @@ __global__ void __launch_bounds__(256) finish_dx_kernel(const float* sum, int sp
     const int64_t row = blockIdx.x;
     if (c >= hidden) return;
     float v[4] = {};
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
         const float4 q = *reinterpret_cast<const float4*>(sum + s * part_stride + row * sum_ld + c);
         v[0] += q.x;
@@ -710,15 +735,17 @@ bool map_ok(const void* p, int64_t ld, int64_t hidden) {
 }
 
 // Parts of dx's sum over the vocabulary.  Too few tiles leave SMs idle, and a
-// last wave that is not full leaves them idle too; every part costs a write and
-// a read of FP32 sums.  Times in ns: 135 for a tile's K block of 64 (the tensor
-// cores' rate at 1.9 GHz), 8 bytes of an element at 6.5 TB/s for a part.
+// last wave that is not full leaves them idle too; every part is written and read
+// again, and every wave starts and ends.  Times in ns: 270 for a tile's K block
+// of 64 (the tensor cores' rate at 1.9 GHz), 2000 for a wave, 8 bytes of an
+// element at 6.5 TB/s for a part.
 int dx_splits(int64_t tiles, int64_t k_blocks, int64_t elems) {
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= 64 && s * 4 <= k_blocks; ++s) {
         const double waves = double((tiles * s + kSms / 2 - 1) / (kSms / 2));
-        const double t = waves * double((k_blocks + s - 1) / s) * 135.0 + double(s) * double(elems) * 8.0 / 6500.0;
+        const double t = waves * double((k_blocks + s - 1) / s) * 270.0 + waves * 2000.0 +
+                         double(s) * double(elems) * 8.0 / 6500.0;
         if (s == 1 || t < least) {
             least = t;
             best = s;
@@ -747,7 +774,7 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int6
     L.target_logit = take(L.rows * 4);
     L.lse = take(L.rows * 4);
     L.alpha = take(8);
-    L.part = take(L.vocab_tiles * L.rows * 8);
+    L.part = take(L.vocab_tiles * kHalves * L.rows * 8);
     L.totals = take((L.rows / 32) * sizeof(BlockTotal));
     if (grad) {
         L.parts = a.dw_dtype == FP8Z_F32 ? 2 : 1;
@@ -775,7 +802,7 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* 
     const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(host::tensor_map_encoder());
     if (!enc) return false;
     std::memset(map, 0, sizeof(*map));
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, type, cuuint32_t(rank), const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -792,6 +819,23 @@ bool map_f32(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(ld * 4)};
     const cuuint32_t box[2] = {32, 32};
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p, dims, strides, box);
+}
+
+// B along its columns, two blocks of 64 in one copy, where its rows are whole blocks; else one block.
+bool map_columns(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, bool blocks) {
+    if (!blocks) return map_16(map, p, cols, rows, ld, kBK);
+    const cuuint64_t dims[3] = {64, cuuint64_t(rows), cuuint64_t(cols / 64)};
+    const cuuint64_t strides[2] = {cuuint64_t(ld * 2), 128};
+    const cuuint32_t box[3] = {64, kBK, kHalf / 64};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box);
+}
+
+// The piece's buffer as P^T: 64 words, tokens, the four blocks of a tile, the two parts of each tile in turn.
+bool map_p_columns(CUtensorMap* map, const void* p, int64_t piece, int64_t rows) {
+    const cuuint64_t dims[4] = {64, cuuint64_t(rows), kTN / 64, cuuint64_t(piece / kTN * 2)};
+    const cuuint64_t strides[3] = {cuuint64_t(piece * 4), 128, kTN * 2};
+    const cuuint32_t box[4] = {64, kBK, kHalf / 64, 1};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, box);
 }
 
 // The piece's buffer as P: 256 words, the two parts of each tile in turn, rows.
@@ -903,7 +947,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     if (int rc = launch_mma<kStats>(x_k, w_k, logits, A, sms, st)) return rc;
     // FP16 P is kept times 2^12: probabilities down to 2^-36 stay normal numbers or close
     const float p_scale = A.bf16 ? 1.0f : 4096.0f;
-    if (int rc = launch_dependent(rows_kernel, dim3(unsigned((n + 31) / 32)), 1024, 0, st, part, A.nt, n, A.rows, targets,
+    if (int rc = launch_dependent(rows_kernel, dim3(unsigned((n + 31) / 32)), 1024, 0, st, part, kHalves * A.nt, n, A.rows, targets,
                                   A.targets_wide, A.ignore, A.vocab, target_logit, target, lse_ws, lse, loss,
                                   reinterpret_cast<BlockTotal*>(ws + L.totals), A.ticket, a.reduction == FP8Z_MEAN,
                                   grad ? a.grad_scale / p_scale : 1.0f, total, grad ? alpha : nullptr, dev_status))
@@ -912,11 +956,11 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
 
     auto* sum = reinterpret_cast<float*>(ws + L.sum);
     const bool dw_rows = host::aligned(dw, 16) && (a.dw_ld * dtype_bytes(a.dw_dtype)) % 16 == 0;
+    const bool blocks = L.hidden_pad % 64 == 0;
     CUtensorMap p_k, w_mn, p_mn, x_mn, p_out, sum_out, dw_out = x_k;
-    if (!map_p(&p_k, p, L.piece, n, kHalf) || !map_16(&w_mn, wp, L.hidden_pad, vocab, w_ld, kBK) ||
-        !map_p(&p_mn, p, L.piece, n, kBK) || !map_16(&x_mn, xp, L.hidden_pad, n, x_ld, kBK) ||
-        !map_p(&p_out, p, L.piece, n, 32) ||
-        !map_sum(&sum_out, sum, L.hidden_pad, n, L.splits))
+    if (!map_p(&p_k, p, L.piece, n, kHalf) || !map_columns(&w_mn, wp, L.hidden_pad, vocab, w_ld, blocks) ||
+        !map_p_columns(&p_mn, p, L.piece, n) || !map_columns(&x_mn, xp, L.hidden_pad, n, x_ld, blocks) ||
+        !map_p(&p_out, p, L.piece, n, 32) || !map_sum(&sum_out, sum, L.hidden_pad, n, L.splits))
         return FP8Z_ECUDA;
     if (dw_rows && !(a.dw_dtype == FP8Z_F32 ? map_f32(&dw_out, dw, hidden, vocab, a.dw_ld)
                                             : map_16(&dw_out, dw, hidden, vocab, a.dw_ld, 32)))
@@ -947,6 +991,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         D.splits = L.splits;
         D.b_k0 = v0;
         D.accumulate = v0 != last;
+        D.b_blocks = blocks;
         if (int rc = launch_mma<kSum>(p_k, w_mn, sum_out, D, sms, st)) return rc;
         MmaArgs W = A;                                  // dw of the piece's words = P^T x
         W.m = words;
@@ -962,6 +1007,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.accumulate = a.accumulate_dw;
         W.staged = dw_rows && (a.dw_dtype == FP8Z_F32 || !a.accumulate_dw);
         W.alpha = alpha;
+        W.b_blocks = blocks;
         if (int rc = launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st)) return rc;
     }
     const dim3 grid(unsigned(n), unsigned((hidden + 1023) / 1024));
