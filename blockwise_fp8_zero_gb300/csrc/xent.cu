@@ -635,14 +635,30 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tile
 }
 
 // The kept logits of a piece become P, in place: a warp takes a row's 256 words
-// (1 KB), reads all of it, and writes the two parts over it.
+// (1 KB), reads all of it, and writes the two parts over it.  The last block of a
+// row copies the token's x for the product with P^T, with zeros in the place of a
+// token that takes no part: its P is zero, but zero times an infinity or a NaN is
+// not, and neither may reach dw.
 constexpr int kProbTiles = 4;
-__global__ void __launch_bounds__(256) prob_kernel(uint8_t* p, int64_t row_bytes, int tiles, int words, int n,
-                                                   int v0, const int32_t* target,
-                                                   const float* lse, float p_scale, int bf16, int split_p) {
+__global__ void __launch_bounds__(256) prob_kernel(uint8_t* p, int64_t row_bytes, int tiles, int words, int v0,
+                                                   const int32_t* target, const float* lse, float p_scale, int bf16,
+                                                   int split_p, const uint16_t* x, int64_t x_ld, int hidden,
+                                                   uint16_t* kept_x, int kept_ld) {
     dependent_wait();
     const int row = blockIdx.x, lane = threadIdx.x & 31;
-    const int y = row < n ? target[row] : -1;
+    const int y = target[row];
+    if (blockIdx.y == gridDim.y - 1) {
+        const uint16_t* from = x + row * x_ld;
+        uint16_t* to = kept_x + int64_t(row) * kept_ld;
+        if (((reinterpret_cast<uintptr_t>(x) | uintptr_t(x_ld * 2) | uintptr_t(hidden * 2)) & 15) == 0) {
+            for (int c = threadIdx.x * 8; c < kept_ld; c += 256 * 8)
+                *reinterpret_cast<uint4*>(to + c) =
+                    y >= 0 && c < hidden ? *reinterpret_cast<const uint4*>(from + c) : make_uint4(0, 0, 0, 0);
+        } else {
+            for (int c = threadIdx.x; c < kept_ld; c += 256) to[c] = y >= 0 && c < hidden ? from[c] : uint16_t(0);
+        }
+        return;
+    }
     const float ref = y >= 0 ? lse[row] * kLog2e : 0.0f;
     const int t0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kProbTiles;
     uint4 in[kProbTiles][2];
@@ -670,13 +686,14 @@ __global__ void __launch_bounds__(256) prob_kernel(uint8_t* p, int64_t row_bytes
 
 __global__ void empty_total_kernel(float* total) { total[threadIdx.x] = 0.0f; }
 
-// dx = a * the sum of the K parts.
+// dx = a * the sum of the K parts, zero for a token that takes no part.
 template <typename T>
 __global__ void __launch_bounds__(256) finish_dx_kernel(const float* sum, int splits, int64_t part_stride,
-                                                        int64_t sum_ld, int n, int hidden, const float* alpha,
-                                                        T* dx, int64_t dx_ld) {
+                                                        int64_t sum_ld, int hidden, const float* alpha,
+                                                        const int32_t* target, T* dx, int64_t dx_ld) {
     dependent_wait();
     const float a = *alpha;
+    const bool kept = target[blockIdx.x] >= 0;          // else zeros, whatever w holds
     const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
     const int64_t row = blockIdx.x;
     if (c >= hidden) return;
@@ -691,7 +708,7 @@ __global__ void __launch_bounds__(256) finish_dx_kernel(const float* sum, int sp
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (c + i < hidden) dx[row * dx_ld + c + i] = Elem<T>::narrow(v[i] * a);
+        if (c + i < hidden) dx[row * dx_ld + c + i] = Elem<T>::narrow(kept ? v[i] * a : 0.0f);
 }
 
 template <typename T>
@@ -702,10 +719,10 @@ __global__ void zero_rows_kernel(T* out, int64_t ld, int64_t rows, int cols) {
 
 // ------------------------------------------------------------------ launches
 struct Layout {
-    int64_t rows, hidden_pad, vocab_tiles, piece, pieces, parts;
+    int64_t rows, hidden_pad, kept_ld, vocab_tiles, piece, pieces, parts;
     int splits;
     bool copy_x, copy_w;
-    size_t x, w, target, target_logit, lse, part, totals, alpha, p, sum, total;
+    size_t x, w, kept_x, target, target_logit, lse, part, totals, alpha, p, sum, total;
 };
 
 constexpr int64_t kPieceBytes = 1LL << 30;        // of one piece, see layout()
@@ -777,6 +794,8 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int6
     L.part = take(L.vocab_tiles * kHalves * L.rows * 8);
     L.totals = take((L.rows / 32) * sizeof(BlockTotal));
     if (grad) {
+        L.kept_ld = up(a.hidden, 64);
+        L.kept_x = take(a.tokens * L.kept_ld * 2);
         L.parts = a.dw_dtype == FP8Z_F32 ? 2 : 1;
         L.splits = dx_splits((L.rows + kTM - 1) / kTM * ((L.hidden_pad + kTN - 1) / kTN), L.vocab_tiles * (kTN / kBK),
                              a.tokens * L.hidden_pad);
@@ -959,7 +978,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     const bool blocks = L.hidden_pad % 64 == 0;
     CUtensorMap p_k, w_mn, p_mn, x_mn, p_out, sum_out, dw_out = x_k;
     if (!map_p(&p_k, p, L.piece, n, kHalf) || !map_columns(&w_mn, wp, L.hidden_pad, vocab, w_ld, blocks) ||
-        !map_p_columns(&p_mn, p, L.piece, n) || !map_columns(&x_mn, xp, L.hidden_pad, n, x_ld, blocks) ||
+        !map_p_columns(&p_mn, p, L.piece, n) || !map_columns(&x_mn, ws + L.kept_x, L.kept_ld, n, L.kept_ld, true) ||
         !map_p(&p_out, p, L.piece, n, 32) || !map_sum(&sum_out, sum, L.hidden_pad, n, L.splits))
         return FP8Z_ECUDA;
     if (dw_rows && !(a.dw_dtype == FP8Z_F32 ? map_f32(&dw_out, dw, hidden, vocab, a.dw_ld)
@@ -969,9 +988,10 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         const int v0 = int(i * L.piece);
         const int words = int(a.vocab - v0 < L.piece ? a.vocab - v0 : L.piece), tiles = (words + kTN - 1) / kTN;
         if (v0 == last) {
-            const dim3 grid(unsigned(n), unsigned((tiles + 8 * kProbTiles - 1) / (8 * kProbTiles)));
-            if (int rc = launch_dependent(prob_kernel, grid, 256, 0, st, p, L.piece * 4, tiles, words, n, v0, target, lse_ws,
-                                          p_scale, A.bf16, L.parts == 2))
+            const dim3 grid(unsigned(n), unsigned((tiles + 8 * kProbTiles - 1) / (8 * kProbTiles) + 1));
+            if (int rc = launch_dependent(prob_kernel, grid, 256, 0, st, p, L.piece * 4, tiles, words, v0, target, lse_ws,
+                                          p_scale, A.bf16, L.parts == 2, static_cast<const uint16_t*>(x), a.x_ld, hidden,
+                                          reinterpret_cast<uint16_t*>(ws + L.kept_x), int(L.kept_ld)))
                 return rc;
         } else {
             MmaArgs Q = A;                              // the piece's logits again, as P
@@ -1007,15 +1027,15 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.accumulate = a.accumulate_dw;
         W.staged = dw_rows && (a.dw_dtype == FP8Z_F32 || !a.accumulate_dw);
         W.alpha = alpha;
-        W.b_blocks = blocks;
+        W.b_blocks = 1;
         if (int rc = launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st)) return rc;
     }
     const dim3 grid(unsigned(n), unsigned((hidden + 1023) / 1024));
     if (A.bf16)
         return launch_dependent(finish_dx_kernel<__nv_bfloat16>, grid, 256, 0, st, sum, L.splits, n * L.hidden_pad,
-                                L.hidden_pad, n, hidden, alpha, static_cast<__nv_bfloat16*>(dx), a.dx_ld);
-    return launch_dependent(finish_dx_kernel<__half>, grid, 256, 0, st, sum, L.splits, n * L.hidden_pad, L.hidden_pad, n,
-                            hidden, alpha, static_cast<__half*>(dx), a.dx_ld);
+                                L.hidden_pad, hidden, alpha, target, static_cast<__nv_bfloat16*>(dx), a.dx_ld);
+    return launch_dependent(finish_dx_kernel<__half>, grid, 256, 0, st, sum, L.splits, n * L.hidden_pad, L.hidden_pad, hidden,
+                            alpha, target, static_cast<__half*>(dx), a.dx_ld);
 }
 
 }  // namespace

@@ -523,7 +523,8 @@ typedef struct {
  *   (FP8Z_SUM), total[1] = number of kept tokens.
  * A target equal to ignore_index, or outside [0, vocab) (reported as
  * FP8Z_EINVAL in *dev_status), has loss 0, takes no part in the total and gives
- * no gradient.  x [tokens, hidden], w [vocab, hidden], targets [tokens],
+ * no gradient: its dx is zero and its x does not reach dw, infinities and NaN
+ * included.  x [tokens, hidden], w [vocab, hidden], targets [tokens],
  * loss f32 [tokens], lse f32 [tokens] or NULL, total f32 [2]: device.
  *
  * fp8z_linear_xent_grad -- the same, and the gradients of grad_scale * total[0]:

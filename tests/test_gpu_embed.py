@@ -151,6 +151,56 @@ def test_grad_against_differences():
         assert (f[0] - f[1]) / (2 * step) == pytest.approx(grad[i, j].item(), abs=1e-9)
 
 
+def test_grad_does_not_read_padding():
+    """What the gradient holds at padding tokens, NaN included, does not matter."""
+    ids = torch.tensor([3, 0, 5, 0, 3], device="cuda")
+    d = _rows(5, 40, BF16, 1)
+    d[1], d[3] = float("nan"), float("inf")
+    table = torch.full((8, 40), 2.0, device="cuda")
+    ws = torch.empty(fp8z.fp8z_embedding_grad_workspace(5, 8, 40), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_embedding_grad(ids, d, table, ws, padding_idx=0)
+    assert torch.equal(table[3], d[0].float() + d[4].float()) and torch.equal(table[5], d[2].float())
+    assert not table[[0, 1, 2, 4, 6, 7]].any()
+
+
+def test_offsets_past_32_bits():
+    v, h = 300001, 7168                      # 2.15e9 elements
+    table = torch.zeros(v, h, dtype=BF16, device="cuda")
+    table[-3:] = _rows(3, h, BF16, 2)
+    ids = torch.tensor([v - 1, 0, v - 3, v - 2, v - 1], device="cuda")
+    out = torch.empty(5, h, dtype=BF16, device="cuda")
+    fp8z.fp8z_embedding(ids, table, out)
+    assert torch.equal(out, table[ids])
+    del table
+    grad = torch.full((v, h), 3.0, device="cuda")
+    ws = torch.empty(fp8z.fp8z_embedding_grad_workspace(5, v, h), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_embedding_grad(ids, out, grad, ws)
+    assert torch.equal(grad[v - 1], out[0].float() + out[4].float()) and torch.equal(grad[v - 3], out[2].float())
+    assert not grad[1:v - 3].any()
+
+
+@pytest.mark.parametrize("tokens", [300, 5000])
+def test_graph_replay(tokens):
+    v, h = 900, 64
+    ids, d = _ids("zipf", tokens, v, 1), _rows(tokens, h, BF16, 2)
+    grad, out = torch.empty(v, h, device="cuda"), torch.empty(tokens, h, dtype=BF16, device="cuda")
+    ws = torch.empty(fp8z.fp8z_embedding_grad_workspace(tokens, v, h), dtype=torch.uint8, device="cuda")
+    table = _rows(v, h, BF16, 3)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            fp8z.fp8z_embedding(ids, table, out)
+            fp8z.fp8z_embedding_grad(ids, d, grad, ws)
+    ids.copy_(_ids("uniform", tokens, v, 7))
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, table[ids])
+    _check_grad(ids, d, grad, None, 1.0, -1, False)
+
+
 def test_grad_on_another_stream():
     s = torch.cuda.Stream()
     ids = _ids("zipf", 3000, 500, 4)

@@ -148,6 +148,36 @@ def test_other_stream_and_many_tensors(ws):
     _check(ts, dsts, ts, 0.5, 1.0, norm)
 
 
+def test_more_than_2_31_elements(ws):
+    n = 2 ** 31 + 4097
+    t = torch.full((n,), 0.5, dtype=F16, device="cuda")
+    t[-1] = 2.0
+    norm = torch.zeros(2, device="cuda")
+    fp8z.fp8z_grad_clip(fp8z.fp8z_encode_tensor_list([t]), 0.25 * math.sqrt(n), norm, ws)
+    want = math.sqrt(0.25 * (n - 1) + 4.0)
+    assert abs(norm[0].item() - want) <= 10 * U * want
+    assert t[-1].item() == 1.0 and t[n // 2].item() == 0.25 and t[0].item() == 0.25
+
+
+def test_graph_replay(ws):
+    ts = _tensors([5000, 77, 20000], [F32, BF16], seed=1)
+    dsts = [torch.empty(t.numel(), device="cuda") for t in ts]
+    tl, norm = fp8z.fp8z_encode_tensor_list(ts, dsts), torch.zeros(2, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            fp8z.fp8z_grad_clip(tl, 0.1, norm, ws)
+    for k in (1.0, 3.0):
+        for t in ts:
+            t.mul_(k)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        _check(ts, dsts, ts, 0.1, 1.0, norm)
+
+
 def test_refusals(ws):
     t = torch.zeros(64, device="cuda")
     norm = torch.zeros(2, device="cuda")

@@ -195,6 +195,78 @@ def test_extreme_logits_and_bad_rows():
     assert bool(dx[rest].isfinite().all()) and bool(dx[3].isnan().any())
 
 
+def test_what_ignored_tokens_hold_does_not_matter():
+    """NaN and infinities in the x of ignored tokens, and in a padded row's unused
+    end, leave every result of the others as it is."""
+    x, w, t = _inputs(150, 72, 700, BF16, pad=8)
+    loss, lse, total, dx, dw = _buffers(150, 72, 700, BF16, F32)
+    ws = _workspace(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw))
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws)
+    want = [a.clone() for a in (loss, total, dx, dw)]
+    x[t == IGNORE] = math.nan
+    x[int((t == IGNORE).nonzero()[0]), 3] = math.inf
+    x._base[:, 72:] = math.nan
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws)
+    assert all(torch.equal(a, b) for a, b in zip((loss, total, dx, dw), want))
+
+
+def test_graph_replay_and_small_pieces_agree():
+    """A captured call replayed on new inputs gives what the eager call gives, and
+    the pieces of the vocabulary do not change dw (dx adds them in another order)."""
+    x, w, t = _inputs(70, 128, 3000, BF16)
+    loss, lse, total, dx, dw = _buffers(70, 128, 3000, BF16, F32)
+    ws = _workspace(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, lse=lse)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, lse=lse)
+    x2, _, t2 = _inputs(70, 128, 3000, BF16, seed=9)
+    x.copy_(x2)
+    t.copy_(t2)
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    got = [a.clone() for a in (loss, total, dx, dw, lse)]
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, lse=lse)
+    assert all(torch.equal(a, b) for a, b in zip(got, (loss, total, dx, dw, lse)))
+    small = _workspace(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw, piece_words=512))
+    assert small.numel() < ws.numel()
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, small, lse=lse)
+    assert torch.equal(dw, got[3]) and torch.equal(loss, got[0])
+
+
+def test_offsets_past_32_bits():
+    """A vocabulary projection of more than 2^31 elements: the last words' logits
+    and gradients are where they belong.  A logit is within 450 * 2^-22 * 7168 / 40
+    = 0.02 (the bound of this file's first lines), a probability within twice that
+    in relative terms: 0.05 tells a right row from any other."""
+    n, h, v = 3, 7168, 300001
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.zeros(v, h, dtype=BF16, device="cuda")
+    w[-5:] = (torch.randn(5, h, generator=g, device="cuda") / 40).to(BF16)
+    x = torch.randn(n, h, generator=g, device="cuda").to(BF16)
+    t = torch.tensor([v - 1, v - 3, 7], device="cuda")
+    loss, lse, total, dx, dw = _buffers(n, h, v, BF16, F32)
+    ws = torch.empty(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, lse=lse)
+    l = torch.zeros(n, v, dtype=torch.float64, device="cuda")
+    l[:, -5:] = x.double() @ w[-5:].double().t()
+    want = torch.logsumexp(l, 1) - l.gather(1, t[:, None])[:, 0]
+    # 448 steps of at most 2^-22 of a sum of absolute products under 7168 / 40
+    assert bool(((loss.double() - want).abs() <= 450 * 2.0 ** -22 * 7168 / 40).all())
+    p = torch.softmax(l, 1)
+    p.scatter_add_(1, t[:, None], torch.full((n, 1), -1.0, dtype=torch.float64, device="cuda"))
+    for i in (0, 7, v - 5, v - 3, v - 1):
+        ref = p[:, i] @ x.double() / n
+        size = p[:, i].abs() @ x.double().abs() / n
+        assert bool(((dw[i].double() - ref).abs() <= size * (2.0 ** -16 + 0.05) + 1e-12).all())
+        assert float((dw[i].double() - ref).norm() / (ref.norm() + 1e-30)) < 0.05
+
+
 def test_gradient_against_differences():
     """Central differences of the loss itself.  |w| <= 1/4 and a step of 2^-4: the
     third derivative leaves (2^-4)^2 / 6 * (2 * 0.25)^3 < 1e-4, the loss's own
@@ -257,3 +329,29 @@ def test_refusals():
     assert e.value.status == fp8z.FP8Z_ENOSPACE
     with pytest.raises(fp8z.Fp8zError):
         fp8z.fp8z_linear_xent_grad(**ok, grad_scale=math.inf)
+
+
+def test_waits_that_run_out():
+    """The products' own bounded waits, cut to 1 ns: a launch reports the timeout,
+    lets its copies and products finish and returns, and the next call with the
+    limit restored is right."""
+    x, w, t = _inputs(600, 1024, 20000, BF16)
+    loss, lse, total, dx, dw = _buffers(600, 1024, 20000, BF16, F32)
+    ws = _workspace(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fp8z.fp8z_set_wait_limit_ns(1)
+    try:
+        for _ in range(5):
+            st.zero_()
+            fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, dev_status=st)
+            torch.cuda.synchronize()
+            if st.item() != 0:
+                break
+    finally:
+        fp8z.fp8z_set_wait_limit_ns(0)
+    assert st.item() == fp8z.FP8Z_ETIMEOUT
+    st.zero_()
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, lse=lse, dev_status=st)
+    assert st.item() == 0
+    _check_loss(x, w, t, loss, total, lse, "mean")
+    _check_grad(x, w, t, dx, dw, None, "mean", 1.0)
