@@ -65,10 +65,12 @@ struct MmaArgs {
     int targets_wide;
     int64_t ignore, vocab;
     const int32_t* target;    // -1: takes no part in the loss (written by rows_kernel)
-    float2* part;             // [kHalves * tile + half][rows] maximum and sum
+    float2* part;             // [tile and half of its columns, or block][rows] maximum and sum
     float* target_logit;
     const float* lse;
     int keep_from;            // words from here on leave their logits in the piece's buffer
+    uint8_t* p;               // that buffer, p_bytes a row (few_kernel)
+    int64_t p_bytes;
     uint32_t* ticket;         // of rows_kernel, set to zero here
     int split_p;              // P in two parts
     float p_scale;
@@ -522,6 +524,132 @@ __global__ void pad_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, i
             dst[r * cols_pad + c] = c < cols ? src[r * ld + c] : uint16_t(0);
 }
 
+// ------------------------------------------------------------- few tokens
+// The logits of up to 32 tokens are one pass over w at the memory's rate, and
+// a tile of 256 rows would be multiplied mostly for nothing.  Here a warp takes
+// 16 words and all of K: four lanes read 16 bytes each of a row and of the next
+// row but seven, 32 elements of K a step, as the A fragments of two m16n8k16
+// products (which lane holds which k does not matter as long as x is held the
+// same way), and the tokens are the products' columns, eight a tile.  x waits in
+// shared memory in the order of the lanes, up to 1024 elements of K at a time and
+// the next ones on their way; each step's w is loaded four steps ahead.
+// FEW_FIGURES
+constexpr int kFewTokens = 32, kFewWords = 128;        // most tokens; words of a block of eight warps
+
+// 16 bytes into shared memory in the background; zeros where `in` is false.
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void mma_16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1, bool bf16) {
+    if (bf16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int kTiles, bool kBf16>
+__global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* w, int64_t w_ld,
+                                                  int hidden, const __grid_constant__ MmaArgs A) {
+    constexpr int kSteps = 32 / kTiles;                // of 32 elements, whose x is in shared memory
+    __shared__ uint4 xs[2][kSteps][kTiles][32];        // [][step][tile][lane]: token lane / 4, elements 8 (lane % 4) on
+    __shared__ float2 warp_part[8][kTiles * 8];
+    dependent_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *A.ticket = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int word = blockIdx.x * kFewWords + warp * 16 + g;          // and word + 8
+    const uint16_t* wa = w + int64_t(min(word, A.n - 1)) * w_ld;
+    const uint16_t* wb = w + int64_t(min(word + 8, A.n - 1)) * w_ld;
+    constexpr int U = 4;
+    uint4 a[U], b[U];
+    auto load = [&](int u, int k) {
+        const bool in = k < hidden;                    // hidden is a multiple of 8
+        a[u] = in ? ld_stream_16(wa + k, 0) : make_uint4(0, 0, 0, 0);
+        b[u] = in ? ld_stream_16(wb + k, 0) : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, q * 8 + 32 * u);
+    auto fetch_x = [&](int c) {
+        for (int i = threadIdx.x; i < kSteps * kTiles * 32; i += 256) {
+            const int step = i / (kTiles * 32), token = i / 32 % kTiles * 8 + (i >> 2 & 7);
+            const int k = (c * kSteps + step) * 32 + (i & 3) * 8;
+            const bool in = token < A.m && k < hidden;
+            copy_16(smem_addr(&xs[c & 1][0][0][0] + i), in ? x + token * x_ld + k : x, in);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const int steps = (hidden + 31) / 32, chunks = (steps + kSteps - 1) / kSteps;
+    float acc[kTiles][2][4] = {};                      // two sums each, so that a product need not wait for the one before
+    fetch_x(0);
+    for (int c = 0; c < chunks; ++c) {
+        if (c + 1 < chunks) {
+            fetch_x(c + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncthreads();
+        const int here = min(kSteps, steps - c * kSteps);
+        for (int step = 0; step < here; step += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (step + u < here) {
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) {
+                        const uint4 v = xs[c & 1][step + u][t][lane];
+                        mma_16n8k16(acc[t][0], a[u].x, b[u].x, a[u].y, b[u].y, v.x, v.y, kBf16);
+                        mma_16n8k16(acc[t][1], a[u].z, b[u].z, a[u].w, b[u].w, v.z, v.w, kBf16);
+                    }
+                }
+                load(u, (c * kSteps + step + u + U) * 32 + q * 8);
+            }
+        }
+        __syncthreads();
+    }
+    // acc[t][.][i]: word (+ 8 from i = 2 on), token 8 t + 2 q + (i & 1)
+#pragma unroll
+    for (int i = 0; i < 2 * kTiles; ++i) {
+        const int t = i / 2, c = i & 1, token = t * 8 + 2 * q + c;
+        float v0 = acc[t][0][c] + acc[t][1][c], v1 = acc[t][0][2 + c] + acc[t][1][2 + c];
+        if (token < A.m) {
+            const int y = load_target(A.targets, A.targets_wide, A.ignore, A.vocab, token);
+            if (y == word) A.target_logit[token] = v0;
+            if (y == word + 8) A.target_logit[token] = v1;
+            float* keep = reinterpret_cast<float*>(A.p + token * A.p_bytes) + (word - A.keep_from);
+            if (word >= A.keep_from && word < A.n) keep[0] = v0;
+            if (word + 8 >= A.keep_from && word + 8 < A.n) keep[8] = v1;
+        }
+        if (word >= A.n) v0 = -INFINITY;
+        if (word + 8 >= A.n) v1 = -INFINITY;
+        float m = fmaxf(v0, v1);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float ref = m == -INFINITY ? 0.0f : m * kLog2e;
+        float s = ex2(fmaf(v0, kLog2e, -ref)) + ex2(fmaf(v1, kLog2e, -ref));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (g == 0) warp_part[warp][token] = make_float2(m, s);
+    }
+    __syncthreads();
+    if (int(threadIdx.x) < kTiles * 8 && int(threadIdx.x) < A.m) {
+        float m = -INFINITY, s = 0.0f;
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, warp_part[i][threadIdx.x].x);
+        const float ref = m == -INFINITY ? 0.0f : m;
+        for (int i = 0; i < 8; ++i) {
+            const float2 p = warp_part[i][threadIdx.x];
+            s += p.y * ex2((p.x - ref) * kLog2e);
+        }
+        A.part[size_t(blockIdx.x) * A.rows + threadIdx.x] = make_float2(m, s);
+    }
+}
+
 // lse and loss of 32 rows from the tiles' maxima and sums, 32 threads a row; the
 // block that finishes last adds up the blocks' sums, in order.
 struct BlockTotal {
@@ -791,7 +919,7 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int6
     L.target_logit = take(L.rows * 4);
     L.lse = take(L.rows * 4);
     L.alpha = take(8);
-    L.part = take(L.vocab_tiles * kHalves * L.rows * 8);
+    L.part = take(L.vocab_tiles * std::max(kHalves, kTN / kFewWords) * L.rows * 8);
     L.totals = take((L.rows / 32) * sizeof(BlockTotal));
     if (grad) {
         L.kept_ld = up(a.hidden, 64);
@@ -963,10 +1091,23 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.target_logit = target_logit;
     A.keep_from = last;
     A.ticket = reinterpret_cast<uint32_t*>(alpha + 1);
-    if (int rc = launch_mma<kStats>(x_k, w_k, logits, A, sms, st)) return rc;
+    A.p = p;
+    A.p_bytes = L.piece * 4;
+    int parts = kHalves * A.nt;
+    if (n <= kFewTokens) {
+        parts = (vocab + kFewWords - 1) / kFewWords;
+        const auto few = n <= 8    ? (A.bf16 ? &few_kernel<1, true> : &few_kernel<1, false>)
+                         : n <= 16 ? (A.bf16 ? &few_kernel<2, true> : &few_kernel<2, false>)
+                                   : (A.bf16 ? &few_kernel<4, true> : &few_kernel<4, false>);
+        if (int rc = launch_dependent(few, dim3(unsigned(parts)), 256, 0, st, static_cast<const uint16_t*>(xp), x_ld,
+                                      static_cast<const uint16_t*>(wp), w_ld, int(L.hidden_pad), A))
+            return rc;
+    } else if (int rc = launch_mma<kStats>(x_k, w_k, logits, A, sms, st)) {
+        return rc;
+    }
     // FP16 P is kept times 2^12: probabilities down to 2^-36 stay normal numbers or close
     const float p_scale = A.bf16 ? 1.0f : 4096.0f;
-    if (int rc = launch_dependent(rows_kernel, dim3(unsigned((n + 31) / 32)), 1024, 0, st, part, kHalves * A.nt, n, A.rows, targets,
+    if (int rc = launch_dependent(rows_kernel, dim3(unsigned((n + 31) / 32)), 1024, 0, st, part, parts, n, A.rows, targets,
                                   A.targets_wide, A.ignore, A.vocab, target_logit, target, lse_ws, lse, loss,
                                   reinterpret_cast<BlockTotal*>(ws + L.totals), A.ticket, a.reduction == FP8Z_MEAN,
                                   grad ? a.grad_scale / p_scale : 1.0f, total, grad ? alpha : nullptr, dev_status))
