@@ -34,26 +34,25 @@ namespace {
 
 constexpr int kTM = 256, kTN = 256, kBK = 64;          // output tile of a pair of blocks, K per stage
 constexpr int kHalf = 128;                             // a block's rows of A and of the result, and columns of B
-constexpr int kStages = 6;
-constexpr int kBytesA = kHalf * kBK * 2, kBytesB = kHalf * kBK * 2, kStageBytes = kBytesA + kBytesB;
+constexpr int kTileBytes = kHalf * kBK * 2;            // of one operand's tile
+constexpr int kRing = 6 * 2 * kTileBytes;              // six stages of A and B, or four of both parts of A and B
 constexpr int kHalves = 1;                             // of a tile's columns, each read by four warps
 constexpr int kThreads = 128 + 128 * kHalves;           // warps 0 and 3 load A and B, 1 multiplies, from 4 on they read the sums
 constexpr int kTmemCols = 512;                         // two accumulators of 256 columns
 constexpr int kCols = kTN / kHalves;                         // columns of one of those warps
 constexpr int kSlab = 32 * 128, kSlabs = 2;            // its staged results: 32 rows of 128 bytes
 constexpr int kStaging = 4 * kHalves * kSlabs * kSlab;
-constexpr int kNumBars = 2 * kStages + 5;
-constexpr int kSmem = kStages * kStageBytes + kStaging + kNumBars * 8 + 32 + 1024;
+constexpr int kNumBars = 2 * 6 + 5;
+constexpr int kSmem = kRing + kStaging + kNumBars * 8 + 32 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum Epilogue { kStats, kProb, kSum, kWeight };
+enum Epilogue { kStats, kProb, kSum, kWeight, kWeightSplit };      // kWeightSplit: P in two parts
 
 struct MmaArgs {
     int m, n;                 // rows and columns of the result
     int mt, nt, splits;       // tiles, and parts of the K loop
     int kb;                   // K blocks of 64
-    int b_wrap;               // B's K block returns to 0 here (the two parts of P share one x)
     int b_n0, b_k0;           // where B starts, in elements
     int b_blocks;             // B's map has its columns as blocks of 64
     int bf16;
@@ -346,11 +345,14 @@ template <int kEpi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                const __grid_constant__ CUtensorMap tc, const __grid_constant__ MmaArgs A) {
-    constexpr bool kAMn = kEpi == kWeight, kBMn = kEpi == kSum || kEpi == kWeight;   // operands along M or N
+    constexpr bool kWeights = kEpi == kWeight || kEpi == kWeightSplit;
+    constexpr bool kAMn = kWeights, kBMn = kEpi == kSum || kWeights;                 // operands along M or N
+    constexpr int kParts = kEpi == kWeightSplit ? 2 : 1;      // of A: one B serves both, a third less to load
+    constexpr int kBytesA = kParts * kTileBytes, kStageBytes = kBytesA + kTileBytes, kStages = kRing / kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_addr(smem_raw));
-    constexpr int kBarsAt = kStages * kStageBytes + kStaging;
+    constexpr int kBarsAt = kRing + kStaging;
     const uint32_t bars = base + kBarsAt;
     auto full = [&](int s) { return bars + s * 8; };                       // first block: both blocks' copies are there
     auto empty = [&](int s) { return bars + (kStages + s) * 8; };          // the products that read them are done
@@ -405,17 +407,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kBytesA, bar = cluster_addr(full(s), 0);
-                    const int kw = k >= A.b_wrap ? k - A.b_wrap : k, kb = kw * kBK + A.b_k0;
+                    const int kb = k * kBK + A.b_k0;
                     if (warp == 0) {
                         mbar_arrive_expect_tx_cluster(bar, kBytesA);
-                        if constexpr (kEpi == kWeight)           // P^T: 128 words, 64 tokens of one part
-                            tma_load_4d_pair(sa, &ta, 0, kw * kBK, m % kTN / 64, m / kTN * 2 + (k >= A.b_wrap), bar);
+                        if constexpr (kWeights)                  // P^T: 128 words, 64 tokens
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part)
+                                tma_load_4d_pair(sa + part * kTileBytes, &ta, 0, k * kBK, m % kTN / 64,
+                                                 m / kTN * 2 + part, bar);
                         else if constexpr (kEpi == kSum)         // P: 128 tokens, 64 words of the first part
                             tma_load_3d_pair(sa, &ta, k * kBK % kTN, k * kBK / kTN * 2, m, bar);
                         else
                             tma_load_2d_pair(sa, &ta, k * kBK, m, bar);
                     } else {
-                        mbar_arrive_expect_tx_cluster(bar, kBytesB);
+                        mbar_arrive_expect_tx_cluster(bar, kTileBytes);
                         if constexpr (!kBMn) {
                             tma_load_2d_pair(sb, &tb, kb, n, bar);
                         } else if (A.b_blocks) {                 // 128 columns as two blocks of 64
@@ -455,8 +460,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint64_t db = umma_desc(sb, kBMn ? 64 * kBK * 2 : 16, 1024);
 #pragma unroll
                     for (int i = 0; i < kBK / 16; ++i)      // 16 of K: 32 bytes of a row, or 16 rows of 128 bytes
-                        umma_f16(tmem + b * kTN, da + i * (kAMn ? 128 : 2), db + i * (kBMn ? 128 : 2), idesc,
-                                 k != at.k0 || i != 0);
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part)
+                            umma_f16(tmem + b * kTN, da + part * (kTileBytes / 16) + i * (kAMn ? 128 : 2),
+                                     db + i * (kBMn ? 128 : 2), idesc, k != at.k0 || i != 0 || part != 0);
                     umma_commit_pair(empty(s));
                     if (++s == kStages) {
                         s = 0;
@@ -473,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3, half = (warp - 4) >> 2;      // rows are the warp's own quarter of the lanes
-        Stager sg{base + kStages * kStageBytes + (warp - 4) * kSlabs * kSlab, 0, lane};
+        Stager sg{base + kRing + (warp - 4) * kSlabs * kSlab, 0, lane};
         int b = 0, bph = 0;
         for (int t = pair; t < tiles; t += pairs) {
             const TileAt at = tile_at(A, t);
@@ -533,7 +540,10 @@ __global__ void pad_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, i
 // same way), and the tokens are the products' columns, eight a tile.  x waits in
 // shared memory in the order of the lanes, up to 1024 elements of K at a time and
 // the next ones on their way; each step's w is loaded four steps ahead.
-// FEW_FIGURES
+// 8 tokens: 25 us over 32000 x 2048 and 276 us over 131072 x 7168 (6.8 TB/s), the
+// row statistics included; 32 tokens 33 and 314; through tiles, 33 tokens take 37
+// and 295, and eight took 40 and 340 (every pair of blocks then reads the same
+// few lines of x at the same time).
 constexpr int kFewTokens = 32, kFewWords = 128;        // most tokens; words of a block of eight warps
 
 // 16 bytes into shared memory in the background; zeros where `in` is false.
@@ -1081,7 +1091,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.mt = (n + kTM - 1) / kTM;
     A.nt = int(L.vocab_tiles);
     A.splits = 1;
-    A.kb = A.b_wrap = int((L.hidden_pad + kBK - 1) / kBK);
+    A.kb = int((L.hidden_pad + kBK - 1) / kBK);
     A.targets = targets;
     A.targets_wide = a.targets_dtype == FP8Z_I64;
     A.ignore = a.ignore_index;
@@ -1148,7 +1158,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         MmaArgs D = A;                                  // dx += P w
         D.n = int(L.hidden_pad);
         D.nt = int((L.hidden_pad + kTN - 1) / kTN);
-        D.kb = D.b_wrap = tiles * (kTN / kBK);
+        D.kb = tiles * (kTN / kBK);
         D.splits = L.splits;
         D.b_k0 = v0;
         D.accumulate = v0 != last;
@@ -1159,8 +1169,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.n = hidden;
         W.mt = (words + kTM - 1) / kTM;
         W.nt = D.nt;
-        W.b_wrap = (n + kBK - 1) / kBK;
-        W.kb = W.b_wrap * int(L.parts);
+        W.kb = (n + kBK - 1) / kBK;
         W.v0 = v0;
         W.out = dw;
         W.out_ld = a.dw_ld;
@@ -1169,7 +1178,9 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.staged = dw_rows && (a.dw_dtype == FP8Z_F32 || !a.accumulate_dw);
         W.alpha = alpha;
         W.b_blocks = 1;
-        if (int rc = launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st)) return rc;
+        if (int rc = L.parts == 2 ? launch_mma<kWeightSplit>(p_mn, x_mn, dw_out, W, sms, st)
+                                  : launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st))
+            return rc;
     }
     const dim3 grid(unsigned(n), unsigned((hidden + 1023) / 1024));
     if (A.bf16)
