@@ -311,13 +311,15 @@ __global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t
     }
 }
 
-// Up to kTile tokens: a token's place is the number of keys before its own, all
-// of them compared from shared memory, a warp a token.  1021 tokens: RANK_US us
-// against SORT_US for one block that sorts digit by digit.
+// Up to kRankMost tokens: a token's place is the number of keys before its own,
+// all of them compared from shared memory, a warp a token.  One launch instead of
+// four or six, but tokens squared comparisons: the whole gradient of 4000 tokens
+// x 1024 takes 22 us this way and about 35 by digits, of 8000 59 and 37.
 constexpr int kRankTokens = 32;                        // of one block
+constexpr int kRankMost = 4096, kRankScan = 512;       // up to kRankScan all fills look the rows up in the ids
 __global__ void __launch_bounds__(kThreads) rank_kernel(Ids ids, int n, uint32_t* keys_out, uint32_t* vals_out, Fill fill,
-                                                        uint32_t* tickets, int ntickets) {
-    __shared__ uint32_t keys[kTile];
+                                                        uint32_t* tickets, int ntickets, uint8_t* used) {
+    __shared__ uint32_t keys[kRankMost];
     dependent_wait();
     const int blocks = gridDim.x - fill.blocks;
     if (int(blockIdx.x) >= blocks) {
@@ -325,7 +327,10 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(Ids ids, int n, uint32_t
         return;
     }
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < ntickets; i += blocks * kThreads) tickets[i] = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) keys[i] = ids.key(i, blockIdx.x == 0);
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        keys[i] = ids.key(i, blockIdx.x == 0);
+        if (used && blockIdx.x == 0 && keys[i] < uint32_t(ids.vocab)) used[keys[i]] = 1;
+    }
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int T = kRankTokens / kWarps;
@@ -490,7 +495,7 @@ __global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
 
     // Adds rows [i, end) to acc; where the key changes, finishes the run before.
     auto add_rows = [&](int i, int end) {
-        constexpr int U = 4;
+        constexpr int U = 4;                          // eight rows under way take 128 registers: 381 us for 345
         for (; i < end; i += U) {
             Pack<S, V> x[U];
             uint32_t k[U];
@@ -565,7 +570,7 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t hidden) {
     g.tickets = at;                 // one for each piece and block of columns, of one element at least
     at += up(size_t(g.pieces) * size_t((hidden + kCols<false> - 1) / kCols<false>) * 4);
     g.used = at;
-    at += g.sort.tiles > 1 ? up(size_t(vocab)) : 0;
+    at += tokens > kRankScan ? up(size_t(vocab)) : 0;
     g.total = at > 0 ? at : 256;    // never an empty buffer, which has no address
     return g;
 }
@@ -598,8 +603,8 @@ int run_grad(const Ids& ids, int64_t tokens, const S* d_out, int64_t d_ld, D* d_
     const bool vec = hidden % 8 == 0 && (d_ld * sizeof(S)) % 16 == 0 && (t_ld * sizeof(D)) % 16 == 0 &&
                      host::aligned(d_out, 16) && host::aligned(d_table, 16);
     const int cols = vec ? kCols<true> : kCols<false>, slabs = int((hidden + cols - 1) / cols);
-    const bool one = g.sort.tiles <= 1;
-    uint8_t* used = accumulate || one ? nullptr : ws + g.used;
+    const bool one = n <= kRankMost;
+    uint8_t* used = accumulate || n <= kRankScan ? nullptr : ws + g.used;
     const int64_t row_bytes = hidden * int64_t(sizeof(D));
     int64_t filled = accumulate ? ids.vocab : 0;
     auto next_fill = [&](int64_t bytes) {               // the next rows, about so many bytes of them
@@ -616,14 +621,15 @@ int run_grad(const Ids& ids, int64_t tokens, const S* d_out, int64_t d_ld, D* d_
     };
     const int64_t all = ids.vocab * row_bytes;
     const uint32_t *k = keys[0], *v = vals[0];
+    if (used && cudaMemsetAsync(used, 0, size_t(ids.vocab), st) != cudaSuccess) return FP8Z_ECUDA;
     if (n > 0 && one) {
-        const Fill f = next_fill(kFillBesideSort);
+        Fill f = next_fill(kFillBesideSort);
+        f.used = nullptr;                               // not known yet: the ids tell which rows occur
         const int blocks = (n + kRankTokens - 1) / kRankTokens;
         if (int rc = launch_dependent(rank_kernel, dim3(unsigned(blocks + f.blocks)), kThreads, 0, st, ids, n, keys[0],
-                                      vals[0], f, tickets, g.pieces * slabs))
+                                      vals[0], f, tickets, g.pieces * slabs, used))
             return rc;
     } else if (n > 0) {
-        if (used && cudaMemsetAsync(used, 0, size_t(ids.vocab), st) != cudaSuccess) return FP8Z_ECUDA;
         for (int p = 0; p < g.sort.passes; ++p) {
             const uint32_t* kin = p ? keys[(p - 1) & 1] : nullptr;
             const uint32_t* vin = p ? vals[(p - 1) & 1] : nullptr;

@@ -17,6 +17,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -276,15 +277,18 @@ __device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap
 }
 
 // A dw whose rows do not all start on 16-byte boundaries, and sums of 16-bit
-// gradients (one rounding of the whole sum), are written by the threads.
+// gradients (one rounding of the whole sum): 32 columns of the warp's 32 rows
+// pass through its slab, so that the threads write along the rows.
 template <typename T>
-__device__ __forceinline__ void weight_chunk(T* p, const uint32_t (&r)[32], int n, float a, bool accumulate) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        if (j < n) {
-            const float v = __uint_as_float(r[j]) * a;
-            p[j] = Elem<T>::narrow(accumulate ? Elem<T>::widen(p[j]) + v : v);
-        }
+__device__ __forceinline__ void weight_rows(T* p, int64_t ld, int rows, int n, const Stager& sg, bool accumulate) {
+    if (sg.lane >= n) return;
+    const int chunk = sg.lane >> 2, word = (sg.lane & 3) * 4;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(sg.slab + r * 128 + ((chunk ^ (r & 7)) << 4) + word) : "memory");
+        T* at = p + r * ld + sg.lane;
+        *at = Elem<T>::narrow(accumulate ? Elem<T>::widen(*at) + v : v);
     }
 }
 
@@ -316,21 +320,25 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
         tmem_ld32(r, acc + c);
         tmem_wait_ld();
         const int col = col0 + c;
-        if (A.staged) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a);
+        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a);
+        if (A.staged) {
             stage32(sg, r);
             sg.end([&](uint32_t s) {
                 if (row >= A.m) return;
                 if (A.accumulate) tma_add_2d(&out, col, y, s);
                 else tma_store_2d(&out, col, y, s);
             });
-        } else if (row < A.m) {
-            const size_t at = size_t(A.v0 + row) * A.out_ld + col;
-            const int n = A.n - col;
-            if (A.out_dtype == FP8Z_F32) weight_chunk(static_cast<float*>(A.out) + at, r, n, a, A.accumulate);
-            else if (A.out_dtype == FP8Z_BF16) weight_chunk(static_cast<__nv_bfloat16*>(A.out) + at, r, n, a, A.accumulate);
-            else weight_chunk(static_cast<__half*>(A.out) + at, r, n, a, A.accumulate);
+        } else {
+            __syncwarp();                            // the slab's last rows have been read
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sg.put(sg.slab, j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            __syncwarp();
+            const int first = row - sg.lane, rows = min(32, A.m - first), n = A.n - col;
+            const int64_t at = int64_t(A.v0 + first) * A.out_ld + col;
+            if (A.out_dtype == FP8Z_F32) weight_rows(static_cast<float*>(A.out) + at, A.out_ld, rows, n, sg, A.accumulate);
+            else if (A.out_dtype == FP8Z_BF16) weight_rows(static_cast<__nv_bfloat16*>(A.out) + at, A.out_ld, rows, n, sg, A.accumulate);
+            else weight_rows(static_cast<__half*>(A.out) + at, A.out_ld, rows, n, sg, A.accumulate);
         }
     }
 }
@@ -522,13 +530,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ small kernels
-// 16-bit rows copied to a stride the tensor maps can step over, zeros after the end.
-__global__ void pad_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, int cols, int cols_pad,
-                                uint16_t* dst) {
+// Elements k .. k + 7 of a row of `cols` 16-bit elements that starts on any
+// 2-byte boundary, zeros from `cols` on: five aligned words, shifted together.
+__device__ __forceinline__ uint4 ld_row8(const uint16_t* row, int k, int cols) {
+    uint32_t v[4] = {};
+    if (k + 8 <= cols) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + k);
+        const bool odd = (at & 2) != 0;
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
+        uint32_t w[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = i < 4 || odd ? *reinterpret_cast<const volatile uint32_t*>(p + i) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = odd ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k + i < cols) v[i / 2] |= uint32_t(*reinterpret_cast<const volatile uint16_t*>(row + k + i)) << (i & 1) * 16;
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// 16-bit rows copied to a stride the tensor maps can step over, zeros after the
+// end: a warp a row, 16 bytes a thread.
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, int cols,
+                                                       int cols_pad, uint16_t* dst) {
     dependent_wait();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int c = threadIdx.x; c < cols_pad; c += blockDim.x)
-            dst[r * cols_pad + c] = c < cols ? src[r * ld + c] : uint16_t(0);
+    const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+#pragma unroll 4
+    for (int c = (threadIdx.x & 31) * 8; c < cols_pad; c += 256)
+        *reinterpret_cast<uint4*>(dst + r * cols_pad + c) = ld_row8(src + r * ld, c, cols);
 }
 
 // ------------------------------------------------------------- few tokens
@@ -565,7 +597,8 @@ __device__ __forceinline__ void mma_16n8k16(float (&c)[4], uint32_t a0, uint32_t
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int kTiles, bool kBf16>
+// kAligned: the rows of w start on 16-byte boundaries (x's always do here).
+template <int kTiles, bool kBf16, bool kAligned>
 __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* w, int64_t w_ld,
                                                   int hidden, const __grid_constant__ MmaArgs A) {
     constexpr int kSteps = 32 / kTiles;                // of 32 elements, whose x is in shared memory
@@ -580,9 +613,14 @@ __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_l
     constexpr int U = 4;
     uint4 a[U], b[U];
     auto load = [&](int u, int k) {
-        const bool in = k < hidden;                    // hidden is a multiple of 8
-        a[u] = in ? ld_stream_16(wa + k, 0) : make_uint4(0, 0, 0, 0);
-        b[u] = in ? ld_stream_16(wb + k, 0) : make_uint4(0, 0, 0, 0);
+        if constexpr (kAligned) {
+            const bool in = k < hidden;                // a multiple of 8 here
+            a[u] = in ? ld_stream_16(wa + k, 0) : make_uint4(0, 0, 0, 0);
+            b[u] = in ? ld_stream_16(wb + k, 0) : make_uint4(0, 0, 0, 0);
+        } else {
+            a[u] = ld_row8(wa, k, hidden);
+            b[u] = ld_row8(wb, k, hidden);
+        }
     };
 #pragma unroll
     for (int u = 0; u < U; ++u) load(u, q * 8 + 32 * u);
@@ -909,6 +947,12 @@ int dx_splits(int64_t tiles, int64_t k_blocks, int64_t elems) {
     return best;
 }
 
+// A w that no tensor map can step over: read as it is by the one pass of a few
+// tokens' loss, else copied first.
+bool reads_w_directly(const fp8z_xent_args& a, const void* w, bool grad) {
+    return !grad && a.tokens <= kFewTokens && !map_ok(w, a.w_ld, a.hidden);
+}
+
 Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int64_t have) {
     Layout L;
     std::memset(&L, 0, sizeof(L));
@@ -1034,7 +1078,8 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         return FP8Z_EALIGN;
     int sms = 0;
     if (int rc = host::device_sms(&sms)) return rc;
-    const bool copy_x = !map_ok(x, a.x_ld, a.hidden), copy_w = !map_ok(w, a.w_ld, a.hidden);
+    const bool direct = reads_w_directly(a, w, grad);
+    const bool copy_x = !map_ok(x, a.x_ld, a.hidden), copy_w = !map_ok(w, a.w_ld, a.hidden) && !direct;
     const Layout L = layout(a, grad, copy_x, copy_w, workspace_bytes);
     if (workspace_bytes < int64_t(L.total)) return FP8Z_ENOSPACE;
     const auto st = static_cast<cudaStream_t>(stream);
@@ -1060,14 +1105,14 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     const void *xp = x, *wp = w;
     int64_t x_ld = a.x_ld, w_ld = a.w_ld;
     if (copy_x) {
-        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned(sms * 8)), 256, 0, st, static_cast<const uint16_t*>(x),
+        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned((n + 7) / 8)), 256, 0, st, static_cast<const uint16_t*>(x),
                                       a.x_ld, n, hidden, int(L.hidden_pad), reinterpret_cast<uint16_t*>(ws + L.x)))
             return rc;
         xp = ws + L.x;
         x_ld = L.hidden_pad;
     }
     if (copy_w) {
-        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned(sms * 8)), 256, 0, st, static_cast<const uint16_t*>(w),
+        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned((vocab + 7) / 8)), 256, 0, st, static_cast<const uint16_t*>(w),
                                       a.w_ld, vocab, hidden, int(L.hidden_pad), reinterpret_cast<uint16_t*>(ws + L.w)))
             return rc;
         wp = ws + L.w;
@@ -1075,7 +1120,8 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     }
     uint8_t* p = ws + L.p;
     CUtensorMap x_k, w_k, logits;
-    if (!map_16(&x_k, xp, L.hidden_pad, n, x_ld, kHalf) || !map_16(&w_k, wp, L.hidden_pad, vocab, w_ld, kHalf))
+    if (!direct && (!map_16(&x_k, xp, L.hidden_pad, n, x_ld, kHalf) ||
+                    !map_16(&w_k, wp, L.hidden_pad, vocab, w_ld, kHalf)))
         return FP8Z_ECUDA;
     if (!grad) logits = w_k;                        // not used
     else if (!map_f32(&logits, p, L.piece, n, L.piece)) return FP8Z_ECUDA;
@@ -1106,11 +1152,18 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     int parts = kHalves * A.nt;
     if (n <= kFewTokens) {
         parts = (vocab + kFewWords - 1) / kFewWords;
-        const auto few = n <= 8    ? (A.bf16 ? &few_kernel<1, true> : &few_kernel<1, false>)
-                         : n <= 16 ? (A.bf16 ? &few_kernel<2, true> : &few_kernel<2, false>)
-                                   : (A.bf16 ? &few_kernel<4, true> : &few_kernel<4, false>);
-        if (int rc = launch_dependent(few, dim3(unsigned(parts)), 256, 0, st, static_cast<const uint16_t*>(xp), x_ld,
-                                      static_cast<const uint16_t*>(wp), w_ld, int(L.hidden_pad), A))
+        const auto launch_few = [&](auto kernel) {
+            return launch_dependent(kernel, dim3(unsigned(parts)), 256, 0, st, static_cast<const uint16_t*>(xp), x_ld,
+                                    static_cast<const uint16_t*>(wp), w_ld, direct ? hidden : int(L.hidden_pad), A);
+        };
+        const auto by_type = [&](auto tiles) {
+            constexpr int T = decltype(tiles)::value;
+            if (direct) return A.bf16 ? launch_few(&few_kernel<T, true, false>) : launch_few(&few_kernel<T, false, false>);
+            return A.bf16 ? launch_few(&few_kernel<T, true, true>) : launch_few(&few_kernel<T, false, true>);
+        };
+        if (int rc = n <= 8    ? by_type(std::integral_constant<int, 1>())
+                     : n <= 16 ? by_type(std::integral_constant<int, 2>())
+                               : by_type(std::integral_constant<int, 4>()))
             return rc;
     } else if (int rc = launch_mma<kStats>(x_k, w_k, logits, A, sms, st)) {
         return rc;
@@ -1197,7 +1250,8 @@ extern "C" int64_t fp8z_linear_xent_workspace(const void* x, const void* w, cons
                                               int32_t with_grad, int64_t piece_words) {
     using namespace fp8z;
     if (!args || !args_ok(*args) || (with_grad && !grad_args_ok(*args)) || piece_words < 0) return FP8Z_EINVAL;
-    const bool cx = !map_ok(x, args->x_ld, args->hidden), cw = !map_ok(w, args->w_ld, args->hidden);
+    const bool cx = !map_ok(x, args->x_ld, args->hidden);
+    const bool cw = !map_ok(w, args->w_ld, args->hidden) && !reads_w_directly(*args, w, with_grad != 0);
     Layout L = layout(*args, with_grad != 0, cx, cw, -1);
     if (with_grad && piece_words > 0) {
         const int64_t less = L.piece - up(piece_words, kTN);
