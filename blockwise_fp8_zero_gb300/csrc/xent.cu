@@ -37,12 +37,10 @@ constexpr int kTM = 256, kTN = 256, kBK = 64;          // output tile of a pair 
 constexpr int kHalf = 128;                             // a block's rows of A and of the result, and columns of B
 constexpr int kTileBytes = kHalf * kBK * 2;            // of one operand's tile
 constexpr int kRing = 6 * 2 * kTileBytes;              // six stages of A and B, or four of both parts of A and B
-constexpr int kHalves = 1;                             // of a tile's columns, each read by four warps
-constexpr int kThreads = 128 + 128 * kHalves;           // warps 0 and 3 load A and B, 1 multiplies, from 4 on they read the sums
+constexpr int kThreads = 256;                          // warps 0 and 3 load A and B, 1 multiplies, 4 to 7 read the sums
 constexpr int kTmemCols = 512;                         // two accumulators of 256 columns
-constexpr int kCols = kTN / kHalves;                         // columns of one of those warps
-constexpr int kSlab = 32 * 128, kSlabs = 2;            // its staged results: 32 rows of 128 bytes
-constexpr int kStaging = 4 * kHalves * kSlabs * kSlab;
+constexpr int kSlab = 32 * 128, kSlabs = 2;            // staged results of one of those: 32 rows of 128 bytes
+constexpr int kStaging = 4 * kSlabs * kSlab;
 constexpr int kNumBars = 2 * 6 + 5;
 constexpr int kSmem = kRing + kStaging + kNumBars * 8 + 32 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
@@ -65,7 +63,7 @@ struct MmaArgs {
     int targets_wide;
     int64_t ignore, vocab;
     const int32_t* target;    // -1: takes no part in the loss (written by rows_kernel)
-    float2* part;             // [tile and half of its columns, or block][rows] maximum and sum
+    float2* part;             // [tile, or block of few_kernel][rows] maximum and sum
     float* target_logit;
     const float* lse;
     int keep_from;            // words from here on leave their logits in the piece's buffer
@@ -122,7 +120,7 @@ __device__ __forceinline__ int load_target(const void* targets, int wide, int64_
 // 128-byte-swizzled tensor map, and from there to global memory as one tile,
 // clipped at the tensor's edges.  A row for each thread, stored by the threads,
 // wrote 262 MB of dw at 3.4 TB/s with 32 bytes a store and less with 16; this
-// way it is 262 MB in DW_FEW us.
+// way it takes 57 us.
 struct Stager {
     uint32_t slab;
     int which, lane;
@@ -153,10 +151,10 @@ __device__ __forceinline__ void stage32(Stager& sg, const uint32_t (&r)[32]) {
     for (int j = 0; j < 8; ++j) sg.put(s, j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
 }
 
-// Maximum and sum of exponentials of one row over half of the tile's columns.
+// Maximum and sum of exponentials of one row over the tile's columns.
 __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                               int row, int half, Stager& sg) {
-    const int col0 = t.n * kTN + half * kCols, n_valid = min(kCols, A.n - col0);
+                                               int row, Stager& sg) {
+    const int col0 = t.n * kTN, n_valid = min(kTN, A.n - col0);
     const int target = row < A.m ? load_target(A.targets, A.targets_wide, A.ignore, A.vocab, row) - col0 : -1;
     const bool keep = col0 >= A.keep_from;
     float mx = -INFINITY, sum = 0.0f;
@@ -195,7 +193,7 @@ __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorM
             A.target_logit[row] = x;
         }
     }
-    if (row < A.m) A.part[size_t(kHalves * t.n + half) * A.rows + row] = make_float2(mx, sum);
+    if (row < A.m) A.part[size_t(t.n) * A.rows + row] = make_float2(mx, sum);
 }
 
 // P of eight neighbouring words of one row, times p_scale: in 16 bits, and what
@@ -223,12 +221,12 @@ __device__ __forceinline__ void prob8(const uint32_t* r, float ref, int target, 
 // holds, for each row and tile of 256 words, 512 bytes of P and 512 bytes of its
 // second part: the room of the tile's FP32 logits.
 __device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                              int row, int half, Stager& sg) {
-    const int n_valid = A.n - (t.n * kTN + half * kCols);
+                                              int row, Stager& sg) {
+    const int n_valid = A.n - t.n * kTN;
     const int y = row < A.m ? A.target[row] : -1;
-    const int target = y - (A.v0 + t.n * kTN + half * kCols);
+    const int target = y - (A.v0 + t.n * kTN);
     const float ref = y >= 0 ? A.lse[row] * kLog2e : 0.0f;
-    for (int c = 0; c < kCols; c += 64) {
+    for (int c = 0; c < kTN; c += 64) {
         uint32_t h[32], l[32];
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -247,20 +245,19 @@ __device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMa
                 }
             }
         }
-        const int col = half * kCols + c;
         stage32(sg, h);
-        sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, col, 2 * t.n, row, s); });
+        sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c, 2 * t.n, row, s); });
         if (A.split_p) {
             stage32(sg, l);
-            sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, col, 2 * t.n + 1, row, s); });
+            sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c, 2 * t.n + 1, row, s); });
         }
     }
 }
 
 __device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                             int row, int half, Stager& sg) {
-    const int col0 = t.n * kTN + half * kCols;
-    for (int c = 0; c < kCols && col0 + c < A.n; c += 32) {
+                                             int row, Stager& sg) {
+    const int col0 = t.n * kTN;
+    for (int c = 0; c < kTN && col0 + c < A.n; c += 32) {
         uint32_t r[32];
         tmem_ld32(r, acc + c);
         tmem_wait_ld();
@@ -293,12 +290,12 @@ __device__ __forceinline__ void weight_rows(T* p, int64_t ld, int rows, int n, c
 }
 
 __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                                int row, int half, Stager& sg) {
+                                                int row, Stager& sg) {
     const float a = *A.alpha;
     const int y = A.v0 + row;                        // of lane 0, which issues the stores
-    const int col0 = t.n * kTN + half * kCols;
+    const int col0 = t.n * kTN;
     if (A.staged && A.out_dtype != FP8Z_F32) {
-        for (int c = 0; c < kCols && col0 + c < A.n; c += 64) {
+        for (int c = 0; c < kTN && col0 + c < A.n; c += 64) {
             uint32_t h[32];
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
@@ -315,7 +312,7 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
         }
         return;
     }
-    for (int c = 0; c < kCols && col0 + c < A.n; c += 32) {
+    for (int c = 0; c < kTN && col0 + c < A.n; c += 32) {
         uint32_t r[32];
         tmem_ld32(r, acc + c);
         tmem_wait_ld();
@@ -346,7 +343,7 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
 // A pair of blocks takes 256 x 256 results at a time.  Each block loads 128 rows
 // of A and 128 columns of B into a ring of kStages tiles; one thread of the
 // first block issues the products of both, into one of two accumulators in each
-// block's tensor memory, while eight warps of each block read the other.  The
+// block's tensor memory, while four warps of each block read the other.  The
 // copies of both blocks count on the first block's barriers, each block arriving
 // for its own.
 template <int kEpi>
@@ -380,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), 8 * kHalves);
+            mbar_init(tempty(b), 8);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -487,19 +484,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_wait_drain(drain, 0, A.dev_status);
         }
     } else if (warp >= 4) {
-        const int quarter = warp & 3, half = (warp - 4) >> 2;      // rows are the warp's own quarter of the lanes
+        const int quarter = warp - 4;              // of the lanes: 32 rows
         Stager sg{base + kRing + (warp - 4) * kSlabs * kSlab, 0, lane};
         int b = 0, bph = 0;
         for (int t = pair; t < tiles; t += pairs) {
             const TileAt at = tile_at(A, t);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull(b), bph, wd))) break;
             tc_fence_after();
-            const uint32_t acc = tmem + b * kTN + half * kCols + (uint32_t(quarter * 32) << 16);
+            const uint32_t acc = tmem + b * kTN + (uint32_t(quarter * 32) << 16);
             const int row = at.m * kTM + rank * kHalf + quarter * 32 + lane;
-            if constexpr (kEpi == kStats) epilogue_stats(A, tc, at, acc, row, half, sg);
-            else if constexpr (kEpi == kProb) epilogue_prob(A, tc, at, acc, row, half, sg);
-            else if constexpr (kEpi == kSum) epilogue_sum(A, tc, at, acc, row, half, sg);
-            else epilogue_weight(A, tc, at, acc, row, half, sg);
+            if constexpr (kEpi == kStats) epilogue_stats(A, tc, at, acc, row, sg);
+            else if constexpr (kEpi == kProb) epilogue_prob(A, tc, at, acc, row, sg);
+            else if constexpr (kEpi == kSum) epilogue_sum(A, tc, at, acc, row, sg);
+            else epilogue_weight(A, tc, at, acc, row, sg);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(tempty(b), 0);
@@ -973,7 +970,7 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int6
     L.target_logit = take(L.rows * 4);
     L.lse = take(L.rows * 4);
     L.alpha = take(8);
-    L.part = take(L.vocab_tiles * std::max(kHalves, kTN / kFewWords) * L.rows * 8);
+    L.part = take(L.vocab_tiles * (kTN / kFewWords) * L.rows * 8);
     L.totals = take((L.rows / 32) * sizeof(BlockTotal));
     if (grad) {
         L.kept_ld = up(a.hidden, 64);
@@ -1149,7 +1146,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.ticket = reinterpret_cast<uint32_t*>(alpha + 1);
     A.p = p;
     A.p_bytes = L.piece * 4;
-    int parts = kHalves * A.nt;
+    int parts = A.nt;
     if (n <= kFewTokens) {
         parts = (vocab + kFewWords - 1) / kFewWords;
         const auto launch_few = [&](auto kernel) {
