@@ -38,6 +38,12 @@ constexpr int kHalf = 128;                             // a block's rows of A an
 constexpr int kTileBytes = kHalf * kBK * 2;            // of one operand's tile
 constexpr int kRing = 6 * 2 * kTileBytes;              // six stages of A and B, or four of both parts of A and B
 constexpr int kThreads = 256;                          // warps 0 and 3 load A and B, 1 multiplies, 4 to 7 read the sums
+// The tensor cores cut a sum off where FP32 ends, toward zero, at every step of 16
+// of K.  An FP32 dw of 4096 tokens (512 steps, two parts) came out 1e-5 off
+// (2-norm) and of 16384 4e-5; so it is added up from products of at most 2048
+// tokens, which leaves 5e-6 for any number of them and costs one part in a hundred
+// (1024 tokens: 3e-6 and five).  The additions run beside the next tiles' products.
+constexpr int kSumTokens = 2048;
 constexpr int kTmemCols = 512;                         // two accumulators of 256 columns
 constexpr int kSlab = 32 * 128, kSlabs = 2;            // staged results of one of those: 32 rows of 128 bytes
 constexpr int kStaging = 4 * kSlabs * kSlab;
@@ -52,7 +58,7 @@ struct MmaArgs {
     int m, n;                 // rows and columns of the result
     int mt, nt, splits;       // tiles, and parts of the K loop
     int kb;                   // K blocks of 64
-    int b_n0, b_k0;           // where B starts, in elements
+    int a_k0, b_n0, b_k0;     // where A and B start, in elements
     int b_blocks;             // B's map has its columns as blocks of 64
     int bf16;
     int64_t timeout_ns;
@@ -418,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if constexpr (kWeights)                  // P^T: 128 words, 64 tokens
 #pragma unroll
                             for (int part = 0; part < kParts; ++part)
-                                tma_load_4d_pair(sa + part * kTileBytes, &ta, 0, k * kBK, m % kTN / 64,
+                                tma_load_4d_pair(sa + part * kTileBytes, &ta, 0, k * kBK + A.a_k0, m % kTN / 64,
                                                  m / kTN * 2 + part, bar);
                         else if constexpr (kEpi == kSum)         // P: 128 tokens, 64 words of the first part
                             tma_load_3d_pair(sa, &ta, k * kBK % kTN, k * kBK / kTN * 2, m, bar);
@@ -1219,7 +1225,6 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.n = hidden;
         W.mt = (words + kTM - 1) / kTM;
         W.nt = D.nt;
-        W.kb = (n + kBK - 1) / kBK;
         W.v0 = v0;
         W.out = dw;
         W.out_ld = a.dw_ld;
@@ -1228,9 +1233,15 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.staged = dw_rows && (a.dw_dtype == FP8Z_F32 || !a.accumulate_dw);
         W.alpha = alpha;
         W.b_blocks = 1;
-        if (int rc = L.parts == 2 ? launch_mma<kWeightSplit>(p_mn, x_mn, dw_out, W, sms, st)
-                                  : launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st))
-            return rc;
+        const int at_once = L.parts == 2 ? kSumTokens : n;
+        for (int k0 = 0; k0 < n; k0 += at_once) {
+            W.a_k0 = W.b_k0 = k0;
+            W.kb = (std::min(n - k0, at_once) + kBK - 1) / kBK;
+            if (k0 > 0) W.accumulate = 1;
+            if (int rc = L.parts == 2 ? launch_mma<kWeightSplit>(p_mn, x_mn, dw_out, W, sms, st)
+                                      : launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st))
+                return rc;
+        }
     }
     const dim3 grid(unsigned(n), unsigned((hidden + 1023) / 1024));
     if (A.bf16)
