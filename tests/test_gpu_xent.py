@@ -111,7 +111,11 @@ def _workspace(size):
     return torch.full((size,), 255, dtype=torch.uint8, device="cuda")      # NaN wherever it is read unwritten
 
 
-SHAPES = [(1, 8, 1), (1, 64, 256), (7, 100, 1000), (5, 7, 33), (128, 64, 256), (129, 72, 257), (300, 576, 5000),
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+SHAPES = [(3000, 136, 700), (40, 72, 20000), (1, 8, 1), (1, 64, 256), (7, 100, 1000), (5, 7, 33), (128, 64, 256), (129, 72, 257), (300, 576, 5000),
           (513, 2048, 3001), (64, 40, 70000), (1000, 136, 999), (2, 4104, 515)]
 
 
@@ -123,7 +127,9 @@ def test_loss(n, h, v, dtype, pad):
     for reduction, tt in (("mean", t), ("sum", t.int())):
         loss, lse, total, _, _ = _buffers(n, h, v, dtype, F32)
         ws = _workspace(fp8z.fp8z_linear_xent_workspace(x, w))
-        fp8z.fp8z_linear_xent(x, w, tt, loss, total, ws, ignore_index=IGNORE, reduction=reduction, lse=lse)
+        st = _status()
+        fp8z.fp8z_linear_xent(x, w, tt, loss, total, ws, ignore_index=IGNORE, reduction=reduction, lse=lse, dev_status=st)
+        assert st.item() == 0                                              # no wait ran out
         _check_loss(x, w, t, loss, total, lse, reduction)
 
 
@@ -137,12 +143,13 @@ def test_gradient(n, h, v, dtype, wide, pad, piece, accumulate):
     loss, lse, total, dx, dw = _buffers(n, h, v, dtype, dw_dtype, pad)
     before = dw[:, :h].clone() if accumulate else None
     ws = _workspace(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw[:, :h], piece_words=piece))
-    reduction = "sum" if pad else "mean"
+    reduction, st = "sum" if pad else "mean", _status()
 
     def call():
-        fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx[:, :h], dw[:, :h], ws, ignore_index=IGNORE,
+        fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx[:, :h], dw[:, :h], ws, ignore_index=IGNORE, dev_status=st,
                                    reduction=reduction, grad_scale=scale, accumulate_dw=accumulate, lse=lse)
     call()
+    assert st.item() == 0                                                  # no wait ran out
     _check_loss(x, w, t, loss, total, lse, reduction)
     _check_grad(x, w, t, dx[:, :h], dw[:, :h], before, reduction, scale)
     assert bool((dx[:, h:] == 7.0).all()) and bool((dw[:, h:] == 0.5).all())
