@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
     if (key >= vocab) return;                       // the ids without a gradient come last
     float acc[V] = {};
 
-    // Leaves this piece's part of a long run [.., ..) that starts at or before i (keys[i] == key).
-    auto part_of_run = [&](bool from_before, int i) {
+    // Leaves this piece's part of a run over several pieces.
+    auto part_of_run = [&](bool from_before) {
         if (mine) {
             float* p = partial + size_t(2 * piece + (from_before ? 0 : 1)) * hidden + col;
             if constexpr (VEC) {
@@ -441,30 +441,21 @@ __global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
                 __stcg(p, acc[0]);
             }
         }
-        // the run's ends: doubling steps, then halving
-        int lo = i, step = 1;
-        while (lo + step < n && keys[lo + step] == key) {
-            lo += step;
-            step *= 2;
+        // the run's first and last piece: 32 borders of pieces at a time
+        const int lane = threadIdx.x & 31;
+        int first = piece, last = piece;
+        for (int more = 32; more == 32;) {
+            const int64_t border = int64_t(last + lane + 1) * piece_len;
+            more = __ffs(~__ballot_sync(0xFFFFFFFFu, border < n && keys[border] == key)) - 1;
+            more = more < 0 ? 32 : more;
+            last += more;
         }
-        int hi = min(n, lo + step);
-        while (hi - lo > 1) {
-            const int mid = lo + (hi - lo) / 2;
-            if (keys[mid] == key) lo = mid; else hi = mid;
+        for (int more = 32; more == 32;) {
+            const int border = (first - lane) * piece_len;
+            more = __ffs(~__ballot_sync(0xFFFFFFFFu, border > 0 && keys[border - 1] == key)) - 1;
+            more = more < 0 ? 32 : more;
+            first -= more;
         }
-        const int last = lo / piece_len;
-        hi = i;
-        step = 1;
-        while (hi - step >= 0 && keys[hi - step] == key) {
-            hi -= step;
-            step *= 2;
-        }
-        lo = max(-1, hi - step);
-        while (hi - lo > 1) {
-            const int mid = lo + (hi - lo) / 2;
-            if (keys[mid] == key) hi = mid; else lo = mid;
-        }
-        const int first = hi / piece_len;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0)
@@ -530,7 +521,7 @@ __global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
     if (key_before == key) {                        // first the run that comes in from the piece before
         while (i < i1 && skeys[i - i0] == key) ++i;
         add_rows(i0, i);
-        part_of_run(true, i0);
+        part_of_run(true);
         if (i == i1) return;
         key = skeys[i - i0];
         if (key >= vocab) return;
@@ -539,7 +530,7 @@ __global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
     }
     add_rows(i, i1);
     if (key >= vocab) return;
-    if (key_after == key) part_of_run(false, i1 - 1);
+    if (key_after == key) part_of_run(false);
     else if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
 }
 
