@@ -103,7 +103,7 @@ struct Ids {
     int32_t* dev_status;
     __device__ __forceinline__ uint32_t key(int64_t i, bool report) const {
         const int64_t id = load_id(ids, wide, i);
-        if (id == padding) return uint32_t(vocab);
+        if (id == padding && padding >= 0) return uint32_t(vocab);
         if (id < 0 || id >= vocab) {
             if (report) report_status(dev_status, FP8Z_EINVAL);
             return uint32_t(vocab);
@@ -713,6 +713,9 @@ extern "C" int fp8z_embedding_grad(const void* ids, int32_t ids_dtype, int64_t t
         !host::aligned(dev_status, 4))
         return FP8Z_EALIGN;
     if (workspace_bytes < fp8z_embedding_grad_workspace(tokens, vocab, hidden)) return FP8Z_ENOSPACE;
+    // a block for each piece and slab of columns, one column a thread at the least
+    if (int64_t(grad_layout(tokens, vocab, hidden).pieces) * ((hidden + kCols<false> - 1) / kCols<false>) > (1 << 30))
+        return FP8Z_EINVAL;
     if (tokens == 0 && accumulate) return FP8Z_OK;
     int sms = 0;
     if (int rc = host::device_sms(&sms)) return rc;

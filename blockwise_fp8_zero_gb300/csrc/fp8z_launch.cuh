@@ -34,8 +34,9 @@ int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     c.attrs = attr;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(std::forward<A>(args))...) == cudaSuccess ? FP8Z_OK
-                                                                                                  : FP8Z_ECUDA;
+    if (cudaLaunchKernelEx(&c, kernel, static_cast<P>(std::forward<A>(args))...) == cudaSuccess) return FP8Z_OK;
+    cudaGetLastError();                    // reported here, not by the next call that asks
+    return FP8Z_ECUDA;
 }
 
 }  // namespace fp8z

@@ -56,15 +56,26 @@ float pow2_at_least(float x) {
     return static_cast<float>(r);
 }
 
+namespace {
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];       // 0: not asked yet, -1: not an sm_103 part
+}  // namespace
+
 int device_sms(int* sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FP8Z_ECUDA;
-    int major = 0, minor = 0, n = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return FP8Z_ECUDA;
-    if (major != 10 || minor != 3) return FP8Z_EUNSUPPORTED;
+    const bool cacheable = dev >= 0 && dev < kMaxDevices;
+    int n = cacheable ? g_sms[dev].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return FP8Z_ECUDA;
+        if (major != 10 || minor != 3) n = -1;
+        if (cacheable) g_sms[dev].store(n, std::memory_order_release);
+    }
+    if (n < 0) return FP8Z_EUNSUPPORTED;
     *sms = n;
     return FP8Z_OK;
 }
@@ -76,7 +87,6 @@ std::atomic<int64_t> g_wait_limit_ns{kDefaultTimeoutNs};
 int64_t wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 
 namespace {
-constexpr int kMaxDevices = 64;
 constexpr int kMaxSlots = 24;
 std::atomic<int> g_smem_done[kMaxSlots][kMaxDevices];
 }  // namespace

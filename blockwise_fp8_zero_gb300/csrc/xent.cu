@@ -916,6 +916,9 @@ bool args_ok(const fp8z_xent_args& a) {
     if (a.dtype != FP8Z_BF16 && a.dtype != FP8Z_F16) return false;
     if (a.targets_dtype != FP8Z_I32 && a.targets_dtype != FP8Z_I64) return false;
     if (a.x_ld < a.hidden || a.w_ld < a.hidden) return false;
+    // tiles of the products are counted in 32 bits
+    const int64_t tt = a.tokens / kTM + 1, vt = a.vocab / kTN + 1, ht = a.hidden / kTN + 1;
+    if (tt * vt > (1 << 30) || vt * ht > (1 << 30) || tt * ht > (1 << 24)) return false;
     if (a.reduction != FP8Z_MEAN && a.reduction != FP8Z_SUM) return false;
     return true;
 }

@@ -523,27 +523,39 @@ def _dtype_code(t, name, allowed=_FLOATS):
     return code
 
 
-def _ptr(t, name, code):
-    """_dptr with the element type given as a code of this module."""
+def _elsewhere(t, name, device):
+    what = "must be a CUDA tensor" if not t.is_cuda else f"is on {t.device}, but the current device is cuda:{device}"
+    raise ValueError(f"{name} {what}")
+
+
+def _flat(t, name, device, code=None):
+    """Pointer of a contiguous CUDA tensor on the current device `device` (None ->
+    NULL), of the element type `code` where one is given."""
     if t is None:
         return None
-    _dtype_code(t, name, (code,))
-    return _dptr(t, None, name)
+    if t.get_device() != device:
+        _elsewhere(t, name, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if code is not None and _dtype_codes.get(t.dtype) != code:
+        _dtype_code(t, name, (code,))
+    return t.data_ptr()
 
 
-def _matrix(t, name):
+def _matrix(t, name, device):
     """(pointer, rows, cols, row stride in elements) of a 2-D CUDA tensor on the
-    current device whose rows are contiguous and do not overlap."""
+    current device `device` whose rows are contiguous and do not overlap."""
     shape = t.shape
-    if len(shape) != 2 or not t.is_cuda:
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    if t.get_device() != device:
+        _elsewhere(t, name, device)
     rows, cols = shape
-    s0, s1 = t.stride()
-    ld = s0 if rows > 1 else cols
-    if (cols > 1 and s1 != 1) or ld < cols:
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.get_device() != _current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_current_device()}")
     return t.data_ptr(), rows, cols, ld
 
 
@@ -553,6 +565,7 @@ class TensorList:
 
     def __init__(self, table, chunks, tensors):
         self.table, self.chunks, self.tensors = table, chunks, tensors
+        self.pointer, self.device = table.data_ptr(), table.get_device()
 
 
 def fp8z_encode_tensor_list(srcs, dsts=None, device="cuda"):
@@ -564,12 +577,12 @@ def fp8z_encode_tensor_list(srcs, dsts=None, device="cuda"):
     dsts = srcs if dsts is None else list(dsts)
     if len(dsts) != len(srcs):
         raise ValueError("one dst per src")
-    n = len(srcs)
+    n, here = len(srcs), _current_device()
     rows = np.zeros((5, max(n, 1)), np.int64)
     for i, (s, d) in enumerate(zip(srcs, dsts)):
         if s.numel() != d.numel():
             raise ValueError(f"dst {i} holds {d.numel()} elements, src {s.numel()}")
-        rows[:, i] = (_dptr(s, None, f"src {i}"), _dptr(d, None, f"dst {i}"), s.numel(),
+        rows[:, i] = (_flat(s, f"src {i}", here), _flat(d, f"dst {i}", here), s.numel(),
                       _dtype_code(s, f"src {i}"), _dtype_code(d, f"dst {i}"))
     kinds = rows[3:].astype(np.int32)
     chunks = ctypes.c_int64(0)
@@ -587,39 +600,44 @@ def fp8z_grad_norm_workspace():
 
 
 def _norm_args(tensors, norm, workspace):
+    here = _current_device()
+    if tensors.device != here:
+        _elsewhere(tensors.table, "table", here)
     if norm.numel() < 2:
         raise ValueError("norm must hold two float32 values: the norm and the coefficient")
     if workspace.numel() * workspace.element_size() < GRAD_NORM_WORKSPACE:
         raise ValueError(f"workspace must hold {GRAD_NORM_WORKSPACE} bytes")
-    return (_dptr(tensors.table, None, "table"), tensors.chunks, _ptr(norm, "norm", FP8Z_F32),
-            _dptr(workspace, None, "workspace"))
+    return _flat(norm, "norm", here, FP8Z_F32), _flat(workspace, "workspace", here)
 
 
 def fp8z_grad_norm(tensors, norm, workspace, grad_scale=1.0, stream=None):
     """norm[0] = |grad_scale| * sqrt(sum of squares over the whole list), norm[1] = 1."""
-    table, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
-    _check("fp8z_grad_norm", lib().fp8z_grad_norm(table, chunks, grad_scale, nptr, ws, _stream_handle(stream)))
+    nptr, ws = _norm_args(tensors, norm, workspace)
+    rc = lib().fp8z_grad_norm(tensors.pointer, tensors.chunks, grad_scale, nptr, ws, _stream_handle(stream))
+    _check("fp8z_grad_norm", rc)
 
 
 def fp8z_grad_clip(tensors, max_norm, norm, workspace, grad_scale=1.0, eps=1e-6, stream=None):
     """The norm, then dst = grad_scale * min(1, max_norm / (norm + eps)) * src for
     every tensor; norm (float32 [2], CUDA) gets the norm and the coefficient."""
-    table, chunks, nptr, ws = _norm_args(tensors, norm, workspace)
-    _check("fp8z_grad_clip", lib().fp8z_grad_clip(table, chunks, grad_scale, max_norm, eps, nptr, ws,
-                                                  _stream_handle(stream)))
+    nptr, ws = _norm_args(tensors, norm, workspace)
+    rc = lib().fp8z_grad_clip(tensors.pointer, tensors.chunks, grad_scale, max_norm, eps, nptr, ws,
+                              _stream_handle(stream))
+    _check("fp8z_grad_clip", rc)
 
 
 def fp8z_embedding(ids, table, out, scale=1.0, dev_status=None, stream=None):
     """out[t] = scale * table[ids[t]].  ids: int64 or int32, any shape, contiguous;
     table [vocab, hidden], out [tokens, hidden]: float32 / bfloat16 / float16,
     rows may be strided."""
-    tp, vocab, hidden, t_ld = _matrix(table, "table")
-    op, tokens, cols, o_ld = _matrix(out, "out")
+    here = _current_device()
+    tp, vocab, hidden, t_ld = _matrix(table, "table", here)
+    op, tokens, cols, o_ld = _matrix(out, "out", here)
     if ids.numel() != tokens or cols != hidden:
         raise ValueError(f"out must be [{ids.numel()}, {hidden}], got {list(out.shape)}")
-    rc = lib().fp8z_embedding(_dptr(ids, None, "ids"), _dtype_code(ids, "ids", _INTS), tokens, tp,
+    rc = lib().fp8z_embedding(_flat(ids, "ids", here), _dtype_code(ids, "ids", _INTS), tokens, tp,
                               _dtype_code(table, "table"), vocab, hidden, t_ld, op, _dtype_code(out, "out"), o_ld,
-                              scale, _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
+                              scale, _flat(dev_status, "dev_status", here, FP8Z_I32), _stream_handle(stream))
     _check("fp8z_embedding", rc)
 
 
@@ -635,15 +653,16 @@ def fp8z_embedding_grad(ids, d_out, d_table, workspace, scale=1.0, padding_idx=-
                         dev_status=None, stream=None):
     """d_table[v] = scale * sum of d_out[t] over ids[t] == v (zeros elsewhere), or
     that sum added to d_table (accumulate).  Deterministic."""
-    dp, tokens, hidden, d_ld = _matrix(d_out, "d_out")
-    tp, vocab, cols, t_ld = _matrix(d_table, "d_table")
+    here = _current_device()
+    dp, tokens, hidden, d_ld = _matrix(d_out, "d_out", here)
+    tp, vocab, cols, t_ld = _matrix(d_table, "d_table", here)
     if ids.numel() != tokens or cols != hidden:
         raise ValueError(f"d_out must be [{ids.numel()}, {cols}], got {list(d_out.shape)}")
-    rc = lib().fp8z_embedding_grad(_dptr(ids, None, "ids"), _dtype_code(ids, "ids", _INTS), tokens, dp,
+    rc = lib().fp8z_embedding_grad(_flat(ids, "ids", here), _dtype_code(ids, "ids", _INTS), tokens, dp,
                                    _dtype_code(d_out, "d_out"), d_ld, tp, _dtype_code(d_table, "d_table"), vocab,
                                    hidden, t_ld, scale, int(padding_idx), int(bool(accumulate)),
-                                   _dptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
-                                   _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
+                                   _flat(workspace, "workspace", here), workspace.numel() * workspace.element_size(),
+                                   _flat(dev_status, "dev_status", here, FP8Z_I32), _stream_handle(stream))
     _check("fp8z_embedding_grad", rc)
 
 
@@ -652,8 +671,9 @@ _REDUCTIONS = {"mean": FP8Z_MEAN, "sum": FP8Z_SUM}
 
 def _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accumulate_dw):
     """(x pointer, w pointer, filled fp8z_xent_args)."""
-    xp, tokens, hidden, x_ld = _matrix(x, "x")
-    wp, vocab, cols, w_ld = _matrix(w, "w")
+    here = _current_device()
+    xp, tokens, hidden, x_ld = _matrix(x, "x", here)
+    wp, vocab, cols, w_ld = _matrix(w, "w", here)
     dtype = _dtype_code(x, "x", _HALVES)
     if cols != hidden or w.dtype != x.dtype:
         raise ValueError(f"w must be [vocab, {hidden}] of {x.dtype}, got {list(w.shape)} of {w.dtype}")
@@ -666,11 +686,11 @@ def _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accum
             raise ValueError(f"targets must hold {tokens} words, got {targets.numel()}")
         a.targets_dtype = _dtype_code(targets, "targets", _INTS)
     if dx is not None:
-        _, rows, cols, a.dx_ld = _matrix(dx, "dx")
+        _, rows, cols, a.dx_ld = _matrix(dx, "dx", here)
         if (rows, cols) != (tokens, hidden) or dx.dtype != x.dtype:
             raise ValueError(f"dx must be [{tokens}, {hidden}] of {x.dtype}, got {list(dx.shape)} of {dx.dtype}")
     if dw is not None:
-        _, rows, cols, a.dw_ld = _matrix(dw, "dw")
+        _, rows, cols, a.dw_ld = _matrix(dw, "dw", here)
         if (rows, cols) != (vocab, hidden):
             raise ValueError(f"dw must be [{vocab}, {hidden}], got {list(dw.shape)}")
         a.dw_dtype = _dtype_code(dw, "dw", (FP8Z_F32, dtype))
@@ -688,10 +708,10 @@ def fp8z_linear_xent_workspace(x, w, dw=None, piece_words=0):
     return size
 
 
-def _xent_outputs(tokens, loss, lse, total):
+def _xent_outputs(tokens, loss, lse, total, here):
     if loss.numel() < tokens or (lse is not None and lse.numel() < tokens) or total.numel() < 2:
         raise ValueError("loss and lse must hold one value per token, total two")
-    return _ptr(loss, "loss", FP8Z_F32), _ptr(lse, "lse", FP8Z_F32), _ptr(total, "total", FP8Z_F32)
+    return _flat(loss, "loss", here, FP8Z_F32), _flat(lse, "lse", here, FP8Z_F32), _flat(total, "total", here, FP8Z_F32)
 
 
 def fp8z_linear_xent(x, w, targets, loss, total, workspace, ignore_index=-100, reduction="mean", lse=None,
@@ -700,11 +720,12 @@ def fp8z_linear_xent(x, w, targets, loss, total, workspace, ignore_index=-100, r
     float32 [2] (mean or sum of the kept tokens' losses, their number), lse
     optional.  x [tokens, hidden], w [vocab, hidden]: bfloat16 or float16, rows
     may be strided; targets int64 or int32."""
+    here = _current_device()
     xp, wp, a = _xent_args(x, w, targets, None, None, ignore_index, reduction, 1.0, False)
-    rc = lib().fp8z_linear_xent(xp, wp, _dptr(targets, None, "targets"), ctypes.byref(a),
-                                *_xent_outputs(a.tokens, loss, lse, total), _dptr(workspace, None, "workspace"),
+    rc = lib().fp8z_linear_xent(xp, wp, _flat(targets, "targets", here), ctypes.byref(a),
+                                *_xent_outputs(a.tokens, loss, lse, total, here), _flat(workspace, "workspace", here),
                                 workspace.numel() * workspace.element_size(),
-                                _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
+                                _flat(dev_status, "dev_status", here, FP8Z_I32), _stream_handle(stream))
     _check("fp8z_linear_xent", rc)
 
 
@@ -712,12 +733,13 @@ def fp8z_linear_xent_grad(x, w, targets, loss, total, dx, dw, workspace, ignore_
                           grad_scale=1.0, accumulate_dw=False, lse=None, dev_status=None, stream=None):
     """fp8z_linear_xent and the gradients of grad_scale * total[0]: dx of x's type,
     dw of x's type or float32 (overwritten, or added to with accumulate_dw)."""
+    here = _current_device()
     xp, wp, a = _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accumulate_dw)
-    rc = lib().fp8z_linear_xent_grad(xp, wp, _dptr(targets, None, "targets"), ctypes.byref(a),
-                                     *_xent_outputs(a.tokens, loss, lse, total), dx.data_ptr(), dw.data_ptr(),
-                                     _dptr(workspace, None, "workspace"),
+    rc = lib().fp8z_linear_xent_grad(xp, wp, _flat(targets, "targets", here), ctypes.byref(a),
+                                     *_xent_outputs(a.tokens, loss, lse, total, here), dx.data_ptr(), dw.data_ptr(),
+                                     _flat(workspace, "workspace", here),
                                      workspace.numel() * workspace.element_size(),
-                                     _ptr(dev_status, "dev_status", FP8Z_I32), _stream_handle(stream))
+                                     _flat(dev_status, "dev_status", here, FP8Z_I32), _stream_handle(stream))
     _check("fp8z_linear_xent_grad", rc)
 
 

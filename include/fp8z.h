@@ -491,7 +491,8 @@ FP8Z_API int fp8z_embedding(const void *ids, int32_t ids_dtype, int64_t tokens, 
  * are sorted by id, and runs of equal ids are summed piece by piece: no
  * floating-point atomics, the same bits every time.  workspace: device,
  * fp8z_embedding_grad_workspace(tokens, vocab, hidden) bytes, no
- * initialisation.  tokens, vocab <= 2^30, hidden <= 2^23.
+ * initialisation.  tokens, vocab <= 2^30, hidden <= 2^23, tokens * hidden about
+ * 2^43 at most.
  */
 FP8Z_API int64_t fp8z_embedding_grad_workspace(int64_t tokens, int64_t vocab, int64_t hidden);
 FP8Z_API int fp8z_embedding_grad(const void *ids, int32_t ids_dtype, int64_t tokens, const void *d_out,
@@ -542,7 +543,8 @@ typedef struct {
  * that do not all start on 16-byte boundaries, or a hidden size that is not a
  * multiple of 8, are copied into the workspace first.  The gradient takes the
  * largest piece that fits the workspace it is given, up to the default.
- * tokens <= 2^24, hidden <= 2^20, vocab <= 2^28.
+ * tokens <= 2^24, hidden <= 2^20, vocab <= 2^28, and at most 2^30 tiles of 256 x
+ * 256 in tokens x vocab and vocab x hidden.
  */
 FP8Z_API int64_t fp8z_linear_xent_workspace(const void *x, const void *w, const fp8z_xent_args *args,
                                             int32_t with_grad, int64_t piece_words);

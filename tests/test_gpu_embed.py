@@ -151,6 +151,14 @@ def test_grad_against_differences():
         assert (f[0] - f[1]) / (2 * step) == pytest.approx(grad[i, j].item(), abs=1e-9)
 
 
+def test_without_padding_every_bad_id_is_reported():
+    ids, d = torch.tensor([-1, 2], device="cuda"), _rows(2, 8, BF16, 1)
+    table, st = torch.zeros(4, 8, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(fp8z.fp8z_embedding_grad_workspace(2, 4, 8), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_embedding_grad(ids, d, table, ws, dev_status=st)
+    assert st.item() == fp8z.FP8Z_EINVAL and torch.equal(table[2], d[1].float()) and not table[[0, 1, 3]].any()
+
+
 def test_grad_does_not_read_padding():
     """What the gradient holds at padding tokens, NaN included, does not matter."""
     ids = torch.tensor([3, 0, 5, 0, 3], device="cuda")

@@ -114,7 +114,8 @@ def test_linear_xent(L):
         b = {**base, **kw}
         return L.fp8z_linear_xent(b["x"], b["w"], b["t"], a or args(), b["loss"], b["lse"], b["total"], b["ws"], b["wsb"],
                                   b["st"], None)
-    for bad in (dict(tokens=-1), dict(tokens=2 ** 25), dict(hidden=0), dict(vocab=0), dict(vocab=2 ** 29), dict(x_ld=15),
+    for bad in (dict(tokens=-1), dict(tokens=2 ** 25), dict(hidden=0), dict(vocab=0), dict(vocab=2 ** 29), dict(tokens=2 ** 24, vocab=2 ** 28),
+                dict(hidden=2 ** 20, vocab=2 ** 28, x_ld=2 ** 20, w_ld=2 ** 20), dict(x_ld=15),
                 dict(w_ld=15), dict(dtype=F32), dict(targets_dtype=F32), dict(reduction=2)):
         assert loss(args(**bad)) == EINVAL and grad(args(**bad)) == EINVAL, bad
         assert L.fp8z_linear_xent_workspace(P, P, args(**bad), 0, 0) == EINVAL, bad
