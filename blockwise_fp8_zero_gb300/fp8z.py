@@ -699,8 +699,8 @@ def _xent_args(x, w, targets, dx, dw, ignore_index, reduction, grad_scale, accum
 
 def fp8z_linear_xent_workspace(x, w, dw=None, piece_words=0):
     """Bytes of workspace for fp8z_linear_xent(x, w, ..) or, with dw, for
-    fp8z_linear_xent_grad(x, w, .., dw=dw): P is kept for pieces of at most
-    piece_words words (0: at most 1 GiB)."""
+    fp8z_linear_xent_grad(x, w, .., dw=dw): logits and P are kept for pieces of at
+    most piece_words words (0: at most 1 GiB, or the size of an FP32 dw)."""
     xp, wp, a = _xent_args(x, w, None, None, dw, -100, "mean", 1.0, False)
     size = int(lib().fp8z_linear_xent_workspace(xp, wp, ctypes.byref(a), int(dw is not None), int(piece_words)))
     if size < 0:

@@ -534,15 +534,18 @@ typedef struct {
  *   a = grad_scale / max(1, kept tokens) (FP8Z_MEAN) or grad_scale.
  * Products run on the tensor cores in FP32; P enters them in dtype (11 or 8
  * significant bits), as two summands of dtype where dw is FP32 (16 bits or
- * more).  The logits are never stored: the gradient goes through the vocabulary
- * in pieces, computes a piece's logits again and keeps P for that piece alone.
+ * more).  Logits are kept for one piece of the vocabulary at most: the gradient
+ * goes through the vocabulary in pieces, one buffer (4 bytes a word and token)
+ * holds the last piece's FP32 logits and then the P of each piece in turn, and the
+ * logits of the pieces before the last are computed again.
  *
  * fp8z_linear_xent_workspace -- bytes of workspace (device, 256-byte aligned, no
  * initialisation) for these arguments, with pieces of at most piece_words words
- * (0: the default, at most 1 GiB of P).  x and w count by their alignment: rows
- * that do not all start on 16-byte boundaries, or a hidden size that is not a
- * multiple of 8, are copied into the workspace first.  The gradient takes the
- * largest piece that fits the workspace it is given, up to the default.
+ * (0: the default, a piece of at most 1 GiB, or of the size of an FP32 dw where
+ * that is more).  x and w count by their alignment: rows that do not all start on
+ * 16-byte boundaries, or a hidden size that is not a multiple of 8, are copied into
+ * the workspace first.  The gradient takes the largest piece that fits the workspace
+ * it is given, up to the default.
  * tokens <= 2^24, hidden <= 2^20, vocab <= 2^28, and at most 2^30 tiles of 256 x
  * 256 in tokens x vocab and vocab x hidden.
  */
