@@ -5,8 +5,9 @@
 //
 // The gradient sorts the tokens by id (stable, so equal ids keep token order),
 // cuts the sorted list into pieces of equal length, sums each run of equal ids
-// inside a piece in registers, and joins the runs that cross pieces.  Every sum runs in FP32 in token order, whatever the schedule, and a
-// word that makes up most of a batch costs no more than many rare ones.
+// inside a piece in registers, and joins the runs that cross pieces.  Every sum
+// runs in FP32 in an order that the ids alone give, whatever the schedule, and a
+// word that makes up half of a batch costs a tenth more than many rare ones.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(Ids ids, int n, uint32_t
 }
 
 // -------------------------------------------------------------------- sums
-constexpr int kMaxPiece = 32;
+constexpr int kMaxPiece = 32, kGroup = 32;
 // Columns one block takes: V per thread.
 template <bool VEC>
 constexpr int kCols = kThreads * (VEC ? 8 : 1);
@@ -396,10 +397,15 @@ __device__ __forceinline__ void write_row(D* p, const float (&acc)[V], float sca
 // One block sums the runs of one piece of the sorted list, in its columns.  A run
 // inside its piece is finished there.  A longer one leaves a partial sum for each
 // of its pieces (partial[2 * piece] for one that came in from the piece before,
-// partial[2 * piece + 1] for one that starts there), and the last of its blocks
-// to arrive adds them up, in the list's order.
+// partial[2 * piece + 1] for one that starts there), and the last of its blocks to
+// arrive adds them up.  Over more than kGroup pieces the last block of each kGroup
+// neighbours adds theirs up, and the last of these the groups' sums.  Both go in the
+// list's order, and which way is taken depends on the ids alone.  With a word that
+// is half of 65536 tokens x 1024 it takes 127 us (272 where one block adds up all of
+// a run), without 115; at three blocks an SM, which four would spill registers for
+// (16384 x 7168: 358 us for 340).
 template <typename S, typename D, bool VEC>
-__global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
+__global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
                                                         const uint32_t* vals, int n, uint32_t vocab,
                                                         int piece_len, const S* d_out, int64_t d_ld,
                                                         D* d_table, int64_t t_ld, int hidden, float scale,
@@ -456,32 +462,52 @@ __global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
             more = more < 0 ? 32 : more;
             first -= more;
         }
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0)
-            finish = atomicAdd(&tickets[size_t(first) * slabs + slab], 1u) == uint32_t(last - first);
-        __syncthreads();
-        if (finish && mine) {
+        // whether this block is the last of `others` + 1 to arrive at a ticket
+        auto arrive = [&](uint32_t* ticket, int others) {
             __threadfence();
-            const float* p = partial + size_t(2 * first + 1) * hidden + col;
-            float sum[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum[j] = __ldcg(p + j);
-            p += hidden;                            // of piece first + 1, come in from before
-#pragma unroll 4
-            for (int q = first + 1; q <= last; ++q, p += 2 * size_t(hidden)) {
-                if constexpr (VEC) {
-                    const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
-                    const float4 b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-                    sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
-                    sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
-                } else {
-                    sum[0] += __ldcg(p);
-                }
+            __syncthreads();
+            if (threadIdx.x == 0) finish = atomicAdd(ticket, 1u) == uint32_t(others);
+            __syncthreads();
+            const bool last_one = finish;
+            __syncthreads();                        // `finish` is free again
+            __threadfence();
+            return last_one;
+        };
+        auto slot = [&](int q) { return partial + size_t(2 * q + (q == first ? 1 : 0)) * hidden + col; };
+        auto add = [&](const float* p) {
+            if constexpr (VEC) {
+                const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
+                const float4 b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+                acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
+                acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
+            } else {
+                acc[0] += __ldcg(p);
             }
-            write_row<D, V>(d_table + int64_t(key) * t_ld + col, sum, scale, accumulate);
+        };
+        const int group = piece / kGroup;
+        const bool one_level = last - first < kGroup;
+        const int q0 = one_level ? first : max(first, group * kGroup);
+        const int q1 = one_level ? last : min(last, group * kGroup + kGroup - 1);
+        // (a piece may end one run and start the next: as for the sums, each has its own ticket)
+        if (!arrive(&tickets[size_t(3 * q0 + (q0 == first ? 1 : 0)) * slabs + slab], q1 - q0)) return;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+        if (mine)
+#pragma unroll 4
+            for (int q = q0; q <= q1; ++q) add(slot(q));
+        if (!one_level) {
+            if (mine)
+#pragma unroll
+                for (int j = 0; j < V; ++j) __stcg(slot(q0) + j, acc[j]);
+            const int g0 = first / kGroup, g1 = last / kGroup;
+            if (!arrive(&tickets[size_t(3 * first + 2) * slabs + slab], g1 - g0)) return;
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+            if (mine)
+#pragma unroll 4
+                for (int g = g0; g <= g1; ++g) add(slot(max(first, g * kGroup)));
         }
-        __syncthreads();                            // `finish` is free again
+        if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
     };
 
     // Adds rows [i, end) to acc; where the key changes, finishes the run before.
@@ -517,21 +543,23 @@ __global__ void __launch_bounds__(kThreads) runs_kernel(const uint32_t* keys,
         }
     };
 
-    int i = i0;
-    if (key_before == key) {                        // first the run that comes in from the piece before
-        while (i < i1 && skeys[i - i0] == key) ++i;
-        add_rows(i0, i);
-        part_of_run(true);
-        if (i == i1) return;
-        key = skeys[i - i0];
-        if (key >= vocab) return;
+    // first the run that comes in from the piece before, if one does, then the rest
+    // (one copy of the code for both: with two, 65536 x 1024 took 125 us for 115)
+    bool from_before = key_before == key;
+    for (int i = i0, end; i < i1; i = end, from_before = false) {
+        end = i1;
+        if (from_before)
+            for (end = i + 1; end < i1 && skeys[end - i0] == key;) ++end;
+        if (i > i0) {
+            key = skeys[i - i0];
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+            for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+        }
+        if (key < vocab) add_rows(i, end);
+        if (key >= vocab) return;
+        if (from_before || key_after == key) part_of_run(from_before);
+        else if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
     }
-    add_rows(i, i1);
-    if (key >= vocab) return;
-    if (key_after == key) part_of_run(false);
-    else if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
 }
 
 // ----------------------------------------------------------------- launches
@@ -558,8 +586,8 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t hidden) {
     at += up(size_t(g.sort.tiles) * kBins * 4);
     g.partial = at;
     at += up(size_t(g.pieces) * 2 * size_t(hidden) * 4);
-    g.tickets = at;                 // one for each piece and block of columns, of one element at least
-    at += up(size_t(g.pieces) * size_t((hidden + kCols<false> - 1) / kCols<false>) * 4);
+    g.tickets = at;                 // three for each piece and block of columns, of one element a thread at least
+    at += up(3 * size_t(g.pieces) * size_t((hidden + kCols<false> - 1) / kCols<false>) * 4);
     g.used = at;
     at += tokens > kRankScan ? up(size_t(vocab)) : 0;
     g.total = at > 0 ? at : 256;    // never an empty buffer, which has no address
@@ -618,7 +646,7 @@ int run_grad(const Ids& ids, int64_t tokens, const S* d_out, int64_t d_ld, D* d_
         f.used = nullptr;                               // not known yet: the ids tell which rows occur
         const int blocks = (n + kRankTokens - 1) / kRankTokens;
         if (int rc = launch_dependent(rank_kernel, dim3(unsigned(blocks + f.blocks)), kThreads, 0, st, ids, n, keys[0],
-                                      vals[0], f, tickets, g.pieces * slabs, used))
+                                      vals[0], f, tickets, 3 * g.pieces * slabs, used))
             return rc;
     } else if (n > 0) {
         for (int p = 0; p < g.sort.passes; ++p) {
@@ -627,7 +655,7 @@ int run_grad(const Ids& ids, int64_t tokens, const S* d_out, int64_t d_ld, D* d_
             Fill f = next_fill(p ? kFillBesideSort : 0);         // the first launch finds out which rows occur
             if (int rc = launch_dependent(count_kernel, dim3(unsigned(g.sort.tiles + f.blocks)), kThreads, 0, st, ids,
                                           kin, n, p * g.sort.digit, g.sort.digit, counts, f, p ? nullptr : tickets,
-                                          g.pieces * slabs, p ? nullptr : used))
+                                          3 * g.pieces * slabs, p ? nullptr : used))
                 return rc;
             f = next_fill(kFillBesideSort);
             if (int rc = launch_dependent(place_kernel, dim3(unsigned(g.sort.tiles + f.blocks)), kThreads, 0, st, ids,
@@ -714,7 +742,7 @@ extern "C" int fp8z_embedding_grad(const void* ids, int32_t ids_dtype, int64_t t
         return FP8Z_EALIGN;
     if (workspace_bytes < fp8z_embedding_grad_workspace(tokens, vocab, hidden)) return FP8Z_ENOSPACE;
     // a block for each piece and slab of columns, one column a thread at the least
-    if (int64_t(grad_layout(tokens, vocab, hidden).pieces) * ((hidden + kCols<false> - 1) / kCols<false>) > (1 << 30))
+    if (int64_t(grad_layout(tokens, vocab, hidden).pieces) * ((hidden + kCols<false> - 1) / kCols<false>) > (1 << 29))
         return FP8Z_EINVAL;
     if (tokens == 0 && accumulate) return FP8Z_OK;
     int sms = 0;

@@ -483,7 +483,7 @@ FP8Z_API int fp8z_embedding(const void *ids, int32_t ids_dtype, int64_t tokens, 
 
 /*
  * fp8z_embedding_grad -- d_table[v][:] = scale * (sum of d_out[t][:] over the
- * tokens t with ids[t] == v), in FP32 and in token order, rounded once; rows
+ * tokens t with ids[t] == v), in FP32, in an order that the ids give, rounded once; rows
  * without a token are written as zeros.  With accumulate = 1 the sum is added
  * to d_table instead and rows without a token are not touched.  Tokens whose id
  * is padding_idx give no gradient (-1: no padding), and tokens whose id is

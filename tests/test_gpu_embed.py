@@ -97,7 +97,8 @@ def _check_grad(ids, d, table, before, scale, padding, accumulate):
 
 
 @pytest.mark.parametrize("tokens,vocab,hidden", [(0, 9, 8), (1, 1, 1), (1, 300, 24), (7, 5, 9), (100, 1000, 576), (2048, 33, 64),
-                                                 (2049, 3000, 40), (5000, 1200, 72), (9001, 70000, 16), (20000, 50, 24)])
+                                                 (2049, 3000, 40), (5000, 1200, 72), (9001, 70000, 16), (20000, 50, 24),
+                                                 (40000, 700, 40)])
 @pytest.mark.parametrize("kind", ["uniform", "one", "two", "zipf"])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_grad(tokens, vocab, hidden, kind, accumulate):
