@@ -357,9 +357,11 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(Ids ids, int n, uint32_t
 
 // -------------------------------------------------------------------- sums
 constexpr int kMaxPiece = 32, kGroup = 32;
-// Columns one block takes: V per thread.
+// Columns one block takes: eight neighbours a thread, or, where rows start between
+// 16-byte boundaries, four single ones a block apart (with one, 16384 x 1001 took 55 us
+// for 47 and 5719 x 3031 67 for 46; one and 16 rows under way 60 and 88).
 template <bool VEC>
-constexpr int kCols = kThreads * (VEC ? 8 : 1);
+constexpr int kCols = kThreads * (VEC ? 8 : 4);
 
 // Adds to or writes V neighbouring elements.  FP32 sums are added by the memory
 // system: one addition for each element of the call, in no race with another, and
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
                                                         D* d_table, int64_t t_ld, int hidden, float scale,
                                                         bool accumulate, float* partial, uint32_t* tickets,
                                                         int slabs, Ids ids, Fill fill) {
-    constexpr int V = VEC ? 8 : 1;
+    constexpr int V = VEC ? 8 : 4, kStep = VEC ? 1 : kThreads;       // columns of a thread, and from one to the next
     __shared__ bool finish;
     __shared__ uint32_t skeys[kMaxPiece], svals[kMaxPiece];
     dependent_wait();
@@ -423,8 +425,21 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
         return;
     }
     const int piece = int(sum / slabs), slab = int(sum % slabs);
-    const int col = slab * kCols<VEC> + threadIdx.x * V;
+    const int col = slab * kCols<VEC> + threadIdx.x * (VEC ? V : 1);
     const bool mine = col < hidden;
+    auto has = [&](int j) { return col + j * kStep < hidden; };
+    auto write = [&](uint32_t to, const float (&v)[V]) {
+        D* p = d_table + int64_t(to) * t_ld + col;
+        if constexpr (VEC) {
+            if (mine) write_row<D, V>(p, v, scale, accumulate);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float one[1] = {v[j]};
+                if (has(j)) write_row<D, 1>(p + j * kStep, one, scale, accumulate);
+            }
+        }
+    };
     const int i0 = piece * piece_len, i1 = min(n, i0 + piece_len);
     if (i0 + int(threadIdx.x) < i1) {
         skeys[threadIdx.x] = keys[i0 + threadIdx.x];
@@ -444,7 +459,9 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
                 __stcg(reinterpret_cast<float4*>(p), make_float4(acc[0], acc[1], acc[2], acc[3]));
                 __stcg(reinterpret_cast<float4*>(p) + 1, make_float4(acc[4], acc[5], acc[6], acc[7]));
             } else {
-                __stcg(p, acc[0]);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (has(j)) __stcg(p + j * kStep, acc[j]);
             }
         }
         // the run's first and last piece: 32 borders of pieces at a time
@@ -481,7 +498,9 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
                 acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
                 acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
             } else {
-                acc[0] += __ldcg(p);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (has(j)) acc[j] += __ldcg(p + j * kStep);
             }
         };
         const int group = piece / kGroup;
@@ -498,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
         if (!one_level) {
             if (mine)
 #pragma unroll
-                for (int j = 0; j < V; ++j) __stcg(slot(q0) + j, acc[j]);
+                for (int j = 0; j < V; ++j)
+                    if (has(j)) __stcg(slot(q0) + j * kStep, acc[j]);
             const int g0 = first / kGroup, g1 = last / kGroup;
             if (!arrive(&tickets[size_t(3 * first + 2) * slabs + slab], g1 - g0)) return;
 #pragma unroll
@@ -507,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
 #pragma unroll 4
                 for (int g = g0; g <= g1; ++g) add(slot(max(first, g * kGroup)));
         }
-        if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
+        write(key, acc);
     };
 
     // Adds rows [i, end) to acc; where the key changes, finishes the run before.
@@ -522,14 +542,17 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
                 if (k[u] < vocab && mine) {
                     const S* p = d_out + int64_t(svals[i + u - i0]) * d_ld + col;
                     if constexpr (VEC) x[u] = ld_nc<S, V>(p);
-                    else x[u].v[0] = *p;
+                    else
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            if (has(j)) x[u].v[j] = p[j * kStep];
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (i + u >= end) break;
                 if (k[u] != key) {
-                    if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
+                    write(key, acc);
 #pragma unroll
                     for (int j = 0; j < V; ++j) acc[j] = 0.0f;
                     key = k[u];
@@ -537,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
                 }
                 if (mine) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] += Elem<S>::widen(x[u].v[j]);
+                    for (int j = 0; j < V; ++j)
+                        if (VEC || has(j)) acc[j] += Elem<S>::widen(x[u].v[j]);
                 }
             }
         }
@@ -558,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
         if (key < vocab) add_rows(i, end);
         if (key >= vocab) return;
         if (from_before || key_after == key) part_of_run(from_before);
-        else if (mine) write_row<D, V>(d_table + int64_t(key) * t_ld + col, acc, scale, accumulate);
+        else write(key, acc);
     }
 }
 
@@ -586,7 +610,7 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t hidden) {
     at += up(size_t(g.sort.tiles) * kBins * 4);
     g.partial = at;
     at += up(size_t(g.pieces) * 2 * size_t(hidden) * 4);
-    g.tickets = at;                 // three for each piece and block of columns, of one element a thread at least
+    g.tickets = at;                 // three for each piece and block of columns, of four elements a thread at least
     at += up(3 * size_t(g.pieces) * size_t((hidden + kCols<false> - 1) / kCols<false>) * 4);
     g.used = at;
     at += tokens > kRankScan ? up(size_t(vocab)) : 0;
@@ -741,7 +765,7 @@ extern "C" int fp8z_embedding_grad(const void* ids, int32_t ids_dtype, int64_t t
         !host::aligned(dev_status, 4))
         return FP8Z_EALIGN;
     if (workspace_bytes < fp8z_embedding_grad_workspace(tokens, vocab, hidden)) return FP8Z_ENOSPACE;
-    // a block for each piece and slab of columns, one column a thread at the least
+    // a block for each piece and slab of columns, four columns a thread at the least
     if (int64_t(grad_layout(tokens, vocab, hidden).pieces) * ((hidden + kCols<false> - 1) / kCols<false>) > (1 << 29))
         return FP8Z_EINVAL;
     if (tokens == 0 && accumulate) return FP8Z_OK;
