@@ -554,6 +554,18 @@ __device__ __forceinline__ uint4 ld_row8(const uint16_t* row, int k, int cols) {
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// The same where k may be negative, an element at a time.
+__device__ __noinline__ uint4 part_row8(const uint16_t* row, int k, int cols) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t e = k + i >= 0 && k + i < cols ? *reinterpret_cast<const volatile uint16_t*>(row + k + i) : 0;
+        v.x = __funnelshift_r(v.x, v.y, 16), v.y = __funnelshift_r(v.y, v.z, 16);
+        v.z = __funnelshift_r(v.z, v.w, 16), v.w = __funnelshift_r(v.w, e, 16);
+    }
+    return v;
+}
+
 // 16-bit rows copied to a stride the tensor maps can step over, zeros after the
 // end: a warp a row, 16 bytes a thread.
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, int cols,
@@ -564,6 +576,23 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* src, int6
 #pragma unroll 4
     for (int c = (threadIdx.x & 31) * 8; c < cols_pad; c += 256)
         *reinterpret_cast<uint4*>(dst + r * cols_pad + c) = ld_row8(src + r * ld, c, cols);
+}
+
+// x once for each way in which rows of w start between 16-byte boundaries: copy r
+// begins with as many zeros as word r's row lies behind one, and is filled up with
+// zeros to `cols_pad`.
+__global__ void __launch_bounds__(256) shift_rows_kernel(const uint16_t* src, int64_t ld, int rows, int cols,
+                                                         int cols_pad, const uint16_t* w, int64_t w_ld, uint16_t* dst) {
+    dependent_wait();
+    const int copy = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int behind = int(reinterpret_cast<uintptr_t>(w + copy * w_ld) >> 1 & 7);
+    const uint16_t* p = src + row * ld;
+    uint16_t* to = dst + (int64_t(copy) * rows + row) * cols_pad;
+    for (int c = (threadIdx.x & 31) * 8; c < cols_pad; c += 256) {
+        const int k = c - behind;
+        *reinterpret_cast<uint4*>(to + c) = k >= 0 ? ld_row8(p, k, cols) : part_row8(p, k, cols);
+    }
 }
 
 // ------------------------------------------------------------- few tokens
@@ -600,19 +629,29 @@ __device__ __forceinline__ void mma_16n8k16(float (&c)[4], uint32_t a0, uint32_t
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// kAligned: the rows of w start on 16-byte boundaries (x's always do here).
+// kAligned: the rows of w start on 16-byte boundaries (x's always do here).  Else
+// every `period`th row is as far behind one as the first: a block takes words of one
+// kind, reads their rows in whole 16 bytes from the boundary before them, the ends an
+// element at a time, and multiplies them with the copy of x that is as far behind.
+// 9 tokens over 43109 x 6354 take 110 us, 8 over 32000 x 2047 35; with five words of
+// 4 bytes for each 16, shifted together, 330 and 101.
 template <int kTiles, bool kBf16, bool kAligned>
 __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* w, int64_t w_ld,
-                                                  int hidden, const __grid_constant__ MmaArgs A) {
+                                                  int hidden, int period, const __grid_constant__ MmaArgs A) {
     constexpr int kSteps = 32 / kTiles;                // of 32 elements, whose x is in shared memory
     __shared__ uint4 xs[2][kSteps][kTiles][32];        // [][step][tile][lane]: token lane / 4, elements 8 (lane % 4) on
     __shared__ float2 warp_part[8][kTiles * 8];
     dependent_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *A.ticket = 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int word = blockIdx.x * kFewWords + warp * 16 + g;          // and word + 8
+    const int kind = kAligned ? 0 : int(blockIdx.x) % period, by = kAligned ? 1 : period;
+    const int word = (int(blockIdx.x) / by * kFewWords + warp * 16 + g) * by + kind, word2 = word + 8 * by;
     const uint16_t* wa = w + int64_t(min(word, A.n - 1)) * w_ld;
-    const uint16_t* wb = w + int64_t(min(word + 8, A.n - 1)) * w_ld;
+    const uint16_t* wb = w + int64_t(min(word2, A.n - 1)) * w_ld;
+    const int behind = kAligned ? 0 : int(reinterpret_cast<uintptr_t>(w + kind * w_ld) >> 1 & 7);
+    const int ends = kAligned ? 0 : hidden + behind;                  // of the row, from its boundary
+    const int width = kAligned ? hidden : int(x_ld);
+    if constexpr (!kAligned) x += int64_t(kind) * A.m * x_ld;
     constexpr int U = 4;
     uint4 a[U], b[U];
     auto load = [&](int u, int k) {
@@ -620,9 +659,13 @@ __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_l
             const bool in = k < hidden;                // a multiple of 8 here
             a[u] = in ? ld_stream_16(wa + k, 0) : make_uint4(0, 0, 0, 0);
             b[u] = in ? ld_stream_16(wb + k, 0) : make_uint4(0, 0, 0, 0);
+        } else if (k >= behind && k + 8 <= ends) {
+            a[u] = word < A.n ? ld_stream_16(wa + (k - behind), 0) : make_uint4(0, 0, 0, 0);
+            b[u] = word2 < A.n ? ld_stream_16(wb + (k - behind), 0) : make_uint4(0, 0, 0, 0);
         } else {
-            a[u] = ld_row8(wa, k, hidden);
-            b[u] = ld_row8(wb, k, hidden);
+            const bool in = k < ends;
+            a[u] = in && word < A.n ? part_row8(wa, k - behind, hidden) : make_uint4(0, 0, 0, 0);
+            b[u] = in && word2 < A.n ? part_row8(wb, k - behind, hidden) : make_uint4(0, 0, 0, 0);
         }
     };
 #pragma unroll
@@ -631,12 +674,12 @@ __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_l
         for (int i = threadIdx.x; i < kSteps * kTiles * 32; i += 256) {
             const int step = i / (kTiles * 32), token = i / 32 % kTiles * 8 + (i >> 2 & 7);
             const int k = (c * kSteps + step) * 32 + (i & 3) * 8;
-            const bool in = token < A.m && k < hidden;
+            const bool in = token < A.m && k < width;
             copy_16(smem_addr(&xs[c & 1][0][0][0] + i), in ? x + token * x_ld + k : x, in);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const int steps = (hidden + 31) / 32, chunks = (steps + kSteps - 1) / kSteps;
+    const int steps = (width + 31) / 32, chunks = (steps + kSteps - 1) / kSteps;
     float acc[kTiles][2][4] = {};                      // two sums each, so that a product need not wait for the one before
     fetch_x(0);
     for (int c = 0; c < chunks; ++c) {
@@ -664,7 +707,7 @@ __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_l
         }
         __syncthreads();
     }
-    // acc[t][.][i]: word (+ 8 from i = 2 on), token 8 t + 2 q + (i & 1)
+    // acc[t][.][i]: word, or word2 from i = 2 on;, token 8 t + 2 q + (i & 1)
 #pragma unroll
     for (int i = 0; i < 2 * kTiles; ++i) {
         const int t = i / 2, c = i & 1, token = t * 8 + 2 * q + c;
@@ -672,13 +715,13 @@ __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_l
         if (token < A.m) {
             const int y = load_target(A.targets, A.targets_wide, A.ignore, A.vocab, token);
             if (y == word) A.target_logit[token] = v0;
-            if (y == word + 8) A.target_logit[token] = v1;
-            float* keep = reinterpret_cast<float*>(A.p + token * A.p_bytes) + (word - A.keep_from);
-            if (word >= A.keep_from && word < A.n) keep[0] = v0;
-            if (word + 8 >= A.keep_from && word + 8 < A.n) keep[8] = v1;
+            if (y == word2) A.target_logit[token] = v1;
+            float* keep = reinterpret_cast<float*>(A.p + token * A.p_bytes);
+            if (word >= A.keep_from && word < A.n) keep[word - A.keep_from] = v0;
+            if (word2 >= A.keep_from && word2 < A.n) keep[word2 - A.keep_from] = v1;
         }
         if (word >= A.n) v0 = -INFINITY;
-        if (word + 8 >= A.n) v1 = -INFINITY;
+        if (word2 >= A.n) v1 = -INFINITY;
         float m = fmaxf(v0, v1);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -959,7 +1002,15 @@ bool reads_w_directly(const fp8z_xent_args& a, const void* w, bool grad) {
     return !grad && a.tokens <= kFewTokens && !map_ok(w, a.w_ld, a.hidden);
 }
 
-Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int64_t have) {
+// Rows of w after which their distance from a 16-byte boundary repeats, and the
+// elements of a row of x that is shifted by up to seven.
+int period_of(int64_t w_ld) { return w_ld % 2 ? 8 : w_ld % 4 ? 4 : w_ld % 8 ? 2 : 1; }
+int64_t shifted_width(int64_t hidden) { return up(hidden + 7, 8); }
+int few_blocks(int64_t vocab, int period) {
+    return period * int(((vocab + period - 1) / period + kFewWords - 1) / kFewWords);
+}
+
+Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, bool direct, int64_t have) {
     Layout L;
     std::memset(&L, 0, sizeof(L));
     L.copy_x = copy_x;
@@ -973,13 +1024,13 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, int6
         at += size_t(up(bytes, 256));
         return r;
     };
-    L.x = take(copy_x ? a.tokens * L.hidden_pad * 2 : 0);
+    L.x = take(direct ? period_of(a.w_ld) * a.tokens * shifted_width(a.hidden) * 2 : copy_x ? a.tokens * L.hidden_pad * 2 : 0);
     L.w = take(copy_w ? a.vocab * L.hidden_pad * 2 : 0);
     L.target = take(L.rows * 4);
     L.target_logit = take(L.rows * 4);
     L.lse = take(L.rows * 4);
     L.alpha = take(8);
-    L.part = take(L.vocab_tiles * (kTN / kFewWords) * L.rows * 8);
+    L.part = take(std::max<int64_t>(L.vocab_tiles, few_blocks(a.vocab, direct ? period_of(a.w_ld) : 1)) * L.rows * 8);
     L.totals = take((L.rows / 32) * sizeof(BlockTotal));
     if (grad) {
         L.kept_ld = up(a.hidden, 64);
@@ -1085,8 +1136,8 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     int sms = 0;
     if (int rc = host::device_sms(&sms)) return rc;
     const bool direct = reads_w_directly(a, w, grad);
-    const bool copy_x = !map_ok(x, a.x_ld, a.hidden), copy_w = !map_ok(w, a.w_ld, a.hidden) && !direct;
-    const Layout L = layout(a, grad, copy_x, copy_w, workspace_bytes);
+    const bool copy_x = !map_ok(x, a.x_ld, a.hidden) && !direct, copy_w = !map_ok(w, a.w_ld, a.hidden) && !direct;
+    const Layout L = layout(a, grad, copy_x, copy_w, direct, workspace_bytes);
     if (workspace_bytes < int64_t(L.total)) return FP8Z_ENOSPACE;
     const auto st = static_cast<cudaStream_t>(stream);
     auto* ws = static_cast<uint8_t*>(workspace);
@@ -1116,6 +1167,15 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
             return rc;
         xp = ws + L.x;
         x_ld = L.hidden_pad;
+    }
+    const int period = period_of(a.w_ld);
+    if (direct) {
+        x_ld = shifted_width(hidden);
+        if (int rc = launch_dependent(shift_rows_kernel, dim3(unsigned((n + 7) / 8), unsigned(period)), 256, 0, st,
+                                      static_cast<const uint16_t*>(x), a.x_ld, n, hidden, int(x_ld),
+                                      static_cast<const uint16_t*>(w), a.w_ld, reinterpret_cast<uint16_t*>(ws + L.x)))
+            return rc;
+        xp = ws + L.x;
     }
     if (copy_w) {
         if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned((vocab + 7) / 8)), 256, 0, st, static_cast<const uint16_t*>(w),
@@ -1157,10 +1217,10 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.p_bytes = L.piece * 4;
     int parts = A.nt;
     if (n <= kFewTokens) {
-        parts = (vocab + kFewWords - 1) / kFewWords;
+        parts = few_blocks(vocab, direct ? period : 1);
         const auto launch_few = [&](auto kernel) {
             return launch_dependent(kernel, dim3(unsigned(parts)), 256, 0, st, static_cast<const uint16_t*>(xp), x_ld,
-                                    static_cast<const uint16_t*>(wp), w_ld, direct ? hidden : int(L.hidden_pad), A);
+                                    static_cast<const uint16_t*>(wp), w_ld, direct ? hidden : int(L.hidden_pad), period, A);
         };
         const auto by_type = [&](auto tiles) {
             constexpr int T = decltype(tiles)::value;
@@ -1261,9 +1321,9 @@ extern "C" int64_t fp8z_linear_xent_workspace(const void* x, const void* w, cons
                                               int32_t with_grad, int64_t piece_words) {
     using namespace fp8z;
     if (!args || !args_ok(*args) || (with_grad && !grad_args_ok(*args)) || piece_words < 0) return FP8Z_EINVAL;
-    const bool cx = !map_ok(x, args->x_ld, args->hidden);
-    const bool cw = !map_ok(w, args->w_ld, args->hidden) && !reads_w_directly(*args, w, with_grad != 0);
-    Layout L = layout(*args, with_grad != 0, cx, cw, -1);
+    const bool direct = reads_w_directly(*args, w, with_grad != 0);
+    const bool cx = !map_ok(x, args->x_ld, args->hidden) && !direct, cw = !map_ok(w, args->w_ld, args->hidden) && !direct;
+    Layout L = layout(*args, with_grad != 0, cx, cw, direct, -1);
     if (with_grad && piece_words > 0) {
         const int64_t less = L.piece - up(piece_words, kTN);
         if (less > 0) return int64_t(L.total) - less * args->tokens * 4;

@@ -362,3 +362,19 @@ def test_waits_that_run_out():
     assert st.item() == 0
     _check_loss(x, w, t, loss, total, lse, "mean")
     _check_grad(x, w, t, dx, dw, None, "mean", 1.0)
+
+
+@pytest.mark.parametrize("ld,start", [(40, 0), (40, 3), (44, 1), (42, 4), (41, 5), (47, 7)])
+@pytest.mark.parametrize("n,h,v", [(1, 33, 5), (9, 40, 1025), (32, 34, 3001), (3, 1, 9), (17, 7, 300)])
+def test_rows_of_w_between_16_byte_boundaries(ld, start, n, h, v):
+    """w starts anywhere and steps by anything; what lies before, between and behind its rows is NaN."""
+    x, dense, t = _inputs(n, h, v, BF16, seed=ld + start, pad=1)
+    flat = torch.full((start + v * ld + 16,), math.nan, dtype=BF16, device="cuda")
+    w = flat[start:start + v * ld].view(v, ld)[:, :h]
+    w.copy_(dense)
+    loss, lse, total, _, _ = _buffers(n, h, v, BF16, F32)
+    ws = _workspace(fp8z.fp8z_linear_xent_workspace(x, w))
+    st = _status()
+    fp8z.fp8z_linear_xent(x, w, t, loss, total, ws, ignore_index=IGNORE, lse=lse, dev_status=st)
+    assert st.item() == 0
+    _check_loss(x, w, t, loss, total, lse, "mean")
