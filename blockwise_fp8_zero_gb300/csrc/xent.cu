@@ -84,6 +84,7 @@ struct MmaArgs {
     int64_t out_ld;
     int out_dtype, accumulate, staged;
     const float* alpha;
+    int beside;               // kWeight: runs beside the kernel before it
 };
 
 struct TileAt {
@@ -291,13 +292,13 @@ __device__ __forceinline__ void weight_rows(T* p, int64_t ld, int rows, int n, c
         float v;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(sg.slab + r * 128 + ((chunk ^ (r & 7)) << 4) + word) : "memory");
         T* at = p + r * ld + sg.lane;
-        *at = Elem<T>::narrow(accumulate ? Elem<T>::widen(*at) + v : v);
+        *at = Elem<T>::narrow(accumulate ? Elem<T>::widen(__ldcg(at)) + v : v);
     }
 }
 
 __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
                                                 int row, Stager& sg) {
-    const float a = *A.alpha;
+    const float a = __ldcg(A.alpha);                 // not from an L1 that may be older than what wrote it
     const int y = A.v0 + row;                        // of lane 0, which issues the stores
     const int col0 = t.n * kTN;
     if (A.staged && A.out_dtype != FP8Z_F32) {
@@ -398,7 +399,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    dependent_wait();
+    // dw needs nothing of dx's sum, which is launched just before it: a block may start as
+    // soon as an SM is free.  dx's kernel lets it be launched after its own wait, so what
+    // came before dx is done; dx itself is waited for at the end, for whoever comes next.
+    const bool beside = kWeights && A.beside;
+    if (!beside) dependent_wait();
     if (kEpi == kStats && blockIdx.x == 0 && threadIdx.x == 0) *A.ticket = 0;
     const uint32_t tmem = *tmem_at;
     const Watchdog wd{abort_flag, A.dev_status, A.timeout_ns};
@@ -530,6 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    if (beside) dependent_wait();
 }
 
 // ------------------------------------------------------------ small kernels
@@ -1301,6 +1307,10 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
             W.a_k0 = W.b_k0 = k0;
             W.kb = (std::min(n - k0, at_once) + kBK - 1) / kBK;
             if (k0 > 0) W.accumulate = 1;
+            // Where a pair of blocks has few tiles of dw, an early start counts: 729 tokens x 2541 x 240
+            // take 33 us for 40, 256 x 32000 x 1024 107 for 116.  Where it has many, the pairs drift apart
+            // and share less of what they load: 517 x 100666 x 6376 would take 2060 us for 2007.
+            W.beside = k0 == 0 && int64_t(W.mt) * W.nt <= 16 * (kSms / 2);
             if (int rc = L.parts == 2 ? launch_mma<kWeightSplit>(p_mn, x_mn, dw_out, W, sms, st)
                                       : launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st))
                 return rc;
