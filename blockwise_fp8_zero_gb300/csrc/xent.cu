@@ -37,16 +37,19 @@ constexpr int kTM = 256, kTN = 256, kBK = 64;          // output tile of a pair 
 constexpr int kHalf = 128;                             // a block's rows of A and of the result, and columns of B
 constexpr int kTileBytes = kHalf * kBK * 2;            // of one operand's tile
 constexpr int kRing = 6 * 2 * kTileBytes;              // six stages of A and B, or four of both parts of A and B
-constexpr int kThreads = 256;                          // warps 0 and 3 load A and B, 1 multiplies, 4 to 7 read the sums
+constexpr int kReaders = 8;                            // warps that read the sums: 32 rows and 128 columns each
+constexpr int kThreads = 128 + 32 * kReaders;          // warps 0 and 3 load A and B, 1 multiplies, the readers follow
 // The tensor cores cut a sum off where FP32 ends, toward zero, at every step of 16
-// of K.  An FP32 dw of 4096 tokens (512 steps, two parts) came out 1e-5 off
-// (2-norm) and of 16384 4e-5; so it is added up from products of at most 2048
-// tokens, which leaves 5e-6 for any number of them and costs one part in a hundred
-// (1024 tokens: 3e-6 and five).  The additions run beside the next tiles' products.
-constexpr int kSumTokens = 2048;
+// of K: logits of hidden 7168 (448 steps) came out so far off that the loss was 4e-6
+// off (FP32 products: 8e-7), an FP32 dw of 4096 tokens (512 steps, two parts) 1e-5.
+// So the sums of the logits and of an FP32 dw leave tensor memory after some blocks of
+// K and are added up, rounded, in the readers' registers: loss 7e-7 off, dw 2.3e-6,
+// of which the two parts of P make up 1.7e-6.  That takes 3 % of the loss's time (4 with
+// 16 blocks of K for the logits, 2.5 with 32 and 9e-7) and 1 to 2 of the gradient's.
+constexpr int kLogitBlocks = 24, kWeightBlocks = 8;
 constexpr int kTmemCols = 512;                         // two accumulators of 256 columns
-constexpr int kSlab = 32 * 128, kSlabs = 2;            // staged results of one of those: 32 rows of 128 bytes
-constexpr int kStaging = 4 * kSlabs * kSlab;
+constexpr int kSlab = 32 * 128;                        // staged results of a reader: 32 rows of 128 bytes
+constexpr int kStaging = kReaders * kSlab;
 constexpr int kNumBars = 2 * 6 + 5;
 constexpr int kSmem = kRing + kStaging + kNumBars * 8 + 32 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
@@ -58,7 +61,8 @@ struct MmaArgs {
     int m, n;                 // rows and columns of the result
     int mt, nt, splits;       // tiles, and parts of the K loop
     int kb;                   // K blocks of 64
-    int a_k0, b_n0, b_k0;     // where A and B start, in elements
+    int sum_blocks;           // of them, at most, in one sum in tensor memory (0: all)
+    int b_n0, b_k0;           // where B starts, in elements
     int b_blocks;             // B's map has its columns as blocks of 64
     int bf16;
     int64_t timeout_ns;
@@ -130,11 +134,11 @@ __device__ __forceinline__ int load_target(const void* targets, int wide, int64_
 // way it takes 57 us.
 struct Stager {
     uint32_t slab;
-    int which, lane;
+    int lane;
     __device__ __forceinline__ uint32_t begin() {
-        if (lane == 0) bulk_wait_read<kSlabs - 1>();          // the slab's last tile has been read
+        if (lane == 0) bulk_wait_read<0>();                   // the slab's last tile has been read
         __syncwarp();
-        return slab + which * kSlab;
+        return slab;
     }
     __device__ __forceinline__ void put(uint32_t s, int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) const {
         st_shared_v4(s + lane * 128 + ((chunk ^ (lane & 7)) << 4), a, b, c, d);
@@ -145,30 +149,34 @@ struct Stager {
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-            store(slab + which * kSlab);
+            store(slab);
             bulk_commit();
         }
-        if (++which == kSlabs) which = 0;
     }
 };
 
-__device__ __forceinline__ void stage32(Stager& sg, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void stage32(Stager& sg, const uint32_t* r) {
     const uint32_t s = sg.begin();
 #pragma unroll
     for (int j = 0; j < 8; ++j) sg.put(s, j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
 }
 
+// A reader's results: 128 columns, from c0 of the tile on, of the row of each lane.
+constexpr int kOwn = 128;
+using Sums = uint32_t[kOwn];
+
 // Maximum and sum of exponentials of one row over the tile's columns.
-__device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                               int row, Stager& sg) {
+__device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, Sums& sums,
+                                               int c0, int row, Stager& sg) {
     const int col0 = t.n * kTN, n_valid = min(kTN, A.n - col0);
     const int target = row < A.m ? load_target(A.targets, A.targets_wide, A.ignore, A.vocab, row) - col0 : -1;
     const bool keep = col0 >= A.keep_from;
     float mx = -INFINITY, sum = 0.0f;
-    for (int c = 0; c < n_valid; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(r, acc + c);
-        tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < kOwn; i += 32) {
+        const int c = c0 + i;
+        uint32_t* r = sums + i;
+        if (c >= n_valid) break;
         if (keep) {
             stage32(sg, r);
             sg.end([&](uint32_t s) {
@@ -200,7 +208,7 @@ __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorM
             A.target_logit[row] = x;
         }
     }
-    if (row < A.m) A.part[size_t(t.n) * A.rows + row] = make_float2(mx, sum);
+    if (row < A.m) A.part[size_t(t.n * 2 + c0 / kOwn) * A.rows + row] = make_float2(mx, sum);
 }
 
 // P of eight neighbouring words of one row, times p_scale: in 16 bits, and what
@@ -227,55 +235,46 @@ __device__ __forceinline__ void prob8(const uint32_t* r, float ref, int target, 
 // Words past the end become zeros: the products read whole tiles.  The buffer
 // holds, for each row and tile of 256 words, 512 bytes of P and 512 bytes of its
 // second part: the room of the tile's FP32 logits.
-__device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                              int row, Stager& sg) {
+__device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, Sums& sums,
+                                              int c0, int row, Stager& sg) {
     const int n_valid = A.n - t.n * kTN;
     const int y = row < A.m ? A.target[row] : -1;
     const int target = y - (A.v0 + t.n * kTN);
     const float ref = y >= 0 ? A.lse[row] * kLog2e : 0.0f;
-    for (int c = 0; c < kTN; c += 64) {
+#pragma unroll
+    for (int i = 0; i < kOwn; i += 64) {
         uint32_t h[32], l[32];
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            uint32_t r[32];
-            tmem_ld32(r, acc + c + part * 32);
-            tmem_wait_ld();
+        for (int q = 0; q < 8; ++q) {
+            const int at = c0 + i + q * 8;
+            uint32_t hq[4], lq[4];
+            prob8(sums + i + q * 8, ref, target - at, n_valid - at, y >= 0, A.p_scale, A.bf16, hq, lq);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int at = c + part * 32 + q * 8;
-                uint32_t hq[4], lq[4];
-                prob8(r + q * 8, ref, target - at, n_valid - at, y >= 0, A.p_scale, A.bf16, hq, lq);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[part * 16 + q * 4 + i] = hq[i];
-                    l[part * 16 + q * 4 + i] = lq[i];
-                }
+            for (int k = 0; k < 4; ++k) {
+                h[q * 4 + k] = hq[k];
+                l[q * 4 + k] = lq[k];
             }
         }
         stage32(sg, h);
-        sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c, 2 * t.n, row, s); });
+        sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c0 + i, 2 * t.n, row, s); });
         if (A.split_p) {
             stage32(sg, l);
-            sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c, 2 * t.n + 1, row, s); });
+            sg.end([&](uint32_t s) { if (row < A.m) tma_store_3d(&out, c0 + i, 2 * t.n + 1, row, s); });
         }
     }
 }
 
-__device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                             int row, Stager& sg) {
-    const int col0 = t.n * kTN;
-    for (int c = 0; c < kTN && col0 + c < A.n; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(r, acc + c);
-        tmem_wait_ld();
-        if (t.k0 == t.k1)
+__device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, Sums& sums,
+                                             int c0, int row, Stager& sg) {
+    const int col0 = t.n * kTN + c0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0;
-        stage32(sg, r);
+    for (int i = 0; i < kOwn; i += 32) {
+        if (col0 + i >= A.n) break;
+        stage32(sg, sums + i);
         sg.end([&](uint32_t s) {
             if (row >= A.m) return;
-            if (A.accumulate) tma_add_3d(&out, col0 + c, row, t.split, s);
-            else tma_store_3d(&out, col0 + c, row, t.split, s);
+            if (A.accumulate) tma_add_3d(&out, col0 + i, row, t.split, s);
+            else tma_store_3d(&out, col0 + i, row, t.split, s);
         });
     }
 }
@@ -296,34 +295,29 @@ __device__ __forceinline__ void weight_rows(T* p, int64_t ld, int rows, int n, c
     }
 }
 
-__device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, uint32_t acc,
-                                                int row, Stager& sg) {
+__device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensorMap& out, const TileAt& t, Sums& sums,
+                                                int c0, int row, Stager& sg) {
     const float a = __ldcg(A.alpha);                 // not from an L1 that may be older than what wrote it
     const int y = A.v0 + row;                        // of lane 0, which issues the stores
-    const int col0 = t.n * kTN;
+    const int col0 = t.n * kTN + c0;
     if (A.staged && A.out_dtype != FP8Z_F32) {
-        for (int c = 0; c < kTN && col0 + c < A.n; c += 64) {
+#pragma unroll
+        for (int i = 0; i < kOwn; i += 64) {
+            if (col0 + i >= A.n) break;
             uint32_t h[32];
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                uint32_t r[32];
-                tmem_ld32(r, acc + c + part * 32);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    h[part * 16 + j] =
-                        pack16(__uint_as_float(r[2 * j]) * a, __uint_as_float(r[2 * j + 1]) * a, A.bf16);
-            }
+            for (int j = 0; j < 32; ++j)
+                h[j] = pack16(__uint_as_float(sums[i + 2 * j]) * a, __uint_as_float(sums[i + 2 * j + 1]) * a, A.bf16);
             stage32(sg, h);
-            sg.end([&](uint32_t s) { if (row < A.m) tma_store_2d(&out, col0 + c, y, s); });
+            sg.end([&](uint32_t s) { if (row < A.m) tma_store_2d(&out, col0 + i, y, s); });
         }
         return;
     }
-    for (int c = 0; c < kTN && col0 + c < A.n; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(r, acc + c);
-        tmem_wait_ld();
-        const int col = col0 + c;
+#pragma unroll
+    for (int i = 0; i < kOwn; i += 32) {
+        const int col = col0 + i;
+        uint32_t* r = sums + i;
+        if (col >= A.n) break;
 #pragma unroll
         for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a);
         if (A.staged) {
@@ -347,10 +341,16 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
     }
 }
 
+// Sums of one tile's K loop in tensor memory, one after the other.
+__device__ __forceinline__ int sums_of(const MmaArgs& A, const TileAt& t) {
+    return A.sum_blocks == 0 ? 1 : max(1, (t.k1 - t.k0 + A.sum_blocks - 1) / A.sum_blocks);
+}
+__device__ __forceinline__ int sum_start(const TileAt& t, int i, int sums) { return t.k0 + (t.k1 - t.k0) * i / sums; }
+
 // A pair of blocks takes 256 x 256 results at a time.  Each block loads 128 rows
 // of A and 128 columns of B into a ring of kStages tiles; one thread of the
 // first block issues the products of both, into one of two accumulators in each
-// block's tensor memory, while four warps of each block read the other.  The
+// block's tensor memory, while eight warps of each block read the other.  The
 // copies of both blocks count on the first block's barriers, each block arriving
 // for its own.
 template <int kEpi>
@@ -359,6 +359,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap tc, const __grid_constant__ MmaArgs A) {
     constexpr bool kWeights = kEpi == kWeight || kEpi == kWeightSplit;
     constexpr bool kAMn = kWeights, kBMn = kEpi == kSum || kWeights;                 // operands along M or N
+    constexpr bool kOneSum = kEpi == kSum || kEpi == kWeight;                        // 16 bits in the end
+    constexpr bool kAddAll = kEpi == kProb || kEpi == kWeightSplit;                  // the first sum to zeros: fewer registers
     constexpr int kParts = kEpi == kWeightSplit ? 2 : 1;      // of A: one B serves both, a third less to load
     constexpr int kBytesA = kParts * kTileBytes, kStageBytes = kBytesA + kTileBytes, kStages = kRing / kStageBytes;
     extern __shared__ uint8_t smem_raw[];
@@ -384,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), 8);
+            mbar_init(tempty(b), 2 * kReaders);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -429,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if constexpr (kWeights)                  // P^T: 128 words, 64 tokens
 #pragma unroll
                             for (int part = 0; part < kParts; ++part)
-                                tma_load_4d_pair(sa + part * kTileBytes, &ta, 0, k * kBK + A.a_k0, m % kTN / 64,
+                                tma_load_4d_pair(sa + part * kTileBytes, &ta, 0, k * kBK, m % kTN / 64,
                                                  m / kTN * 2 + part, bar);
                         else if constexpr (kEpi == kSum)         // P: 128 tokens, 64 words of the first part
                             tma_load_3d_pair(sa, &ta, k * kBK % kTN, k * kBK / kTN * 2, m, bar);
@@ -463,56 +465,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const TileAt at = tile_at(A, t);
-                if (!mbar_wait_bounded(tempty(b), bph ^ 1, wd)) break;
-                tc_fence_after();
-                for (int k = at.k0; k < at.k1; ++k) {
-                    if (!mbar_wait_bounded(full(s), ph, wd)) {
+                const int sums = sums_of(A, at);
+                for (int i = 0; i < sums && ok; ++i) {
+                    const int first = sum_start(at, i, sums), end = sum_start(at, i + 1, sums);
+                    if (!mbar_wait_bounded(tempty(b), bph ^ 1, wd)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = base + s * kStageBytes, sb = sa + kBytesA;
-                    const uint64_t da = umma_desc(sa, kAMn ? 64 * kBK * 2 : 16, 1024);
-                    const uint64_t db = umma_desc(sb, kBMn ? 64 * kBK * 2 : 16, 1024);
+                    for (int k = first; k < end; ++k) {
+                        if (!mbar_wait_bounded(full(s), ph, wd)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = base + s * kStageBytes, sb = sa + kBytesA;
+                        const uint64_t da = umma_desc(sa, kAMn ? 64 * kBK * 2 : 16, 1024);
+                        const uint64_t db = umma_desc(sb, kBMn ? 64 * kBK * 2 : 16, 1024);
 #pragma unroll
-                    for (int i = 0; i < kBK / 16; ++i)      // 16 of K: 32 bytes of a row, or 16 rows of 128 bytes
+                        for (int j = 0; j < kBK / 16; ++j)  // 16 of K: 32 bytes of a row, or 16 rows of 128 bytes
 #pragma unroll
-                        for (int part = 0; part < kParts; ++part)
-                            umma_f16(tmem + b * kTN, da + part * (kTileBytes / 16) + i * (kAMn ? 128 : 2),
-                                     db + i * (kBMn ? 128 : 2), idesc, k != at.k0 || i != 0 || part != 0);
-                    umma_commit_pair(empty(s));
-                    if (++s == kStages) {
-                        s = 0;
-                        ph ^= 1;
+                            for (int part = 0; part < kParts; ++part)
+                                umma_f16(tmem + b * kTN, da + part * (kTileBytes / 16) + j * (kAMn ? 128 : 2),
+                                         db + j * (kBMn ? 128 : 2), idesc, k != first || j != 0 || part != 0);
+                        umma_commit_pair(empty(s));
+                        if (++s == kStages) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
+                    if (!ok) break;
+                    umma_commit_pair(tfull(b));
+                    if (b) bph ^= 1;
+                    b ^= 1;
                 }
-                if (!ok) break;
-                umma_commit_pair(tfull(b));
-                if (b) bph ^= 1;
-                b ^= 1;
             }
             umma_commit_pair(drain);       // and every product is done before tensor memory is freed
             mbar_wait_drain(drain, 0, A.dev_status);
         }
     } else if (warp >= 4) {
-        const int quarter = warp - 4;              // of the lanes: 32 rows
-        Stager sg{base + kRing + (warp - 4) * kSlabs * kSlab, 0, lane};
+        const int quarter = warp & 3, c0 = (warp - 4) / 4 * kOwn;    // a warp reaches its quarter of the lanes: 32 rows
+        Stager sg{base + kRing + (warp - 4) * kSlab, lane};
         int b = 0, bph = 0;
+        bool ok = true;
         for (int t = pair; t < tiles; t += pairs) {
             const TileAt at = tile_at(A, t);
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull(b), bph, wd))) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + b * kTN + (uint32_t(quarter * 32) << 16);
+            const int n_sums = sums_of(A, at);
+            Sums sums;
+            if constexpr (kAddAll)
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j) sums[j] = 0;
+            for (int i = 0; i < n_sums; ++i) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull(b), bph, wd));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + b * kTN + c0 + (uint32_t(quarter * 32) << 16);
+                if (kOneSum || (!kAddAll && i == 0)) {
+#pragma unroll
+                    for (int c = 0; c < kOwn; c += 32) tmem_ld32(reinterpret_cast<uint32_t(&)[32]>(sums[c]), acc + c);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kOwn; c += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(r, acc + c);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sums[c + j] = __float_as_uint(__uint_as_float(sums[c + j]) + __uint_as_float(r[j]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty(b), 0);
+                if (b) bph ^= 1;
+                b ^= 1;
+            }
+            if (!ok) break;
+            if (at.k0 == at.k1)                      // nothing was multiplied
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j) sums[j] = 0;
             const int row = at.m * kTM + rank * kHalf + quarter * 32 + lane;
-            if constexpr (kEpi == kStats) epilogue_stats(A, tc, at, acc, row, sg);
-            else if constexpr (kEpi == kProb) epilogue_prob(A, tc, at, acc, row, sg);
-            else if constexpr (kEpi == kSum) epilogue_sum(A, tc, at, acc, row, sg);
-            else epilogue_weight(A, tc, at, acc, row, sg);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(tempty(b), 0);
-            if (b) bph ^= 1;
-            b ^= 1;
+            if constexpr (kEpi == kStats) epilogue_stats(A, tc, at, sums, c0, row, sg);
+            else if constexpr (kEpi == kProb) epilogue_prob(A, tc, at, sums, c0, row, sg);
+            else if constexpr (kEpi == kSum) epilogue_sum(A, tc, at, sums, c0, row, sg);
+            else epilogue_weight(A, tc, at, sums, c0, row, sg);
         }
         if (lane == 0) bulk_wait_all();
     }
@@ -635,6 +672,13 @@ __device__ __forceinline__ void mma_16n8k16(float (&c)[4], uint32_t a0, uint32_t
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Blocks an SM that the registers allow.  8 tokens over 131072 x 7168: 277 us with four
+// and 300 with three; 32 over 32000 x 2048: 32 with two, 35 with three.  Odd rows:
+// 8 over 32000 x 2047 35 us with three and 40 with four, 32 over 43109 x 6354 151 and
+// 165 with two.
+template <int kTiles, bool kAligned>
+constexpr int few_blocks_sm = !kAligned || kTiles == 2 ? 3 : kTiles == 1 ? 4 : 2;
+
 // kAligned: the rows of w start on 16-byte boundaries (x's always do here).  Else
 // every `period`th row is as far behind one as the first: a block takes words of one
 // kind, reads their rows in whole 16 bytes from the boundary before them, the ends an
@@ -642,7 +686,7 @@ __device__ __forceinline__ void mma_16n8k16(float (&c)[4], uint32_t a0, uint32_t
 // 9 tokens over 43109 x 6354 take 110 us, 8 over 32000 x 2047 35; with five words of
 // 4 bytes for each 16, shifted together, 330 and 101.
 template <int kTiles, bool kBf16, bool kAligned>
-__global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* w, int64_t w_ld,
+__global__ void __launch_bounds__(256, few_blocks_sm<kTiles, kAligned>) few_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* w, int64_t w_ld,
                                                   int hidden, int period, const __grid_constant__ MmaArgs A) {
     constexpr int kSteps = 32 / kTiles;                // of 32 elements, whose x is in shared memory
     __shared__ uint4 xs[2][kSteps][kTiles][32];        // [][step][tile][lane]: token lane / 4, elements 8 (lane % 4) on
@@ -686,7 +730,7 @@ __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_l
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const int steps = (width + 31) / 32, chunks = (steps + kSteps - 1) / kSteps;
-    float acc[kTiles][2][4] = {};                      // two sums each, so that a product need not wait for the one before
+    float acc[kTiles][4] = {}, sum[kTiles][4] = {};    // of the x in shared memory, and of all before
     fetch_x(0);
     for (int c = 0; c < chunks; ++c) {
         if (c + 1 < chunks) {
@@ -704,20 +748,25 @@ __global__ void __launch_bounds__(256) few_kernel(const uint16_t* x, int64_t x_l
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {
                         const uint4 v = xs[c & 1][step + u][t][lane];
-                        mma_16n8k16(acc[t][0], a[u].x, b[u].x, a[u].y, b[u].y, v.x, v.y, kBf16);
-                        mma_16n8k16(acc[t][1], a[u].z, b[u].z, a[u].w, b[u].w, v.z, v.w, kBf16);
+                        mma_16n8k16(acc[t], a[u].x, b[u].x, a[u].y, b[u].y, v.x, v.y, kBf16);
+                        mma_16n8k16(acc[t], a[u].z, b[u].z, a[u].w, b[u].w, v.z, v.w, kBf16);
                     }
                 }
                 load(u, (c * kSteps + step + u + U) * 32 + q * 8);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4 * kTiles; ++i) {         // as above: the products' sums are cut off, these are rounded
+            sum[i / 4][i & 3] += acc[i / 4][i & 3];
+            acc[i / 4][i & 3] = 0.0f;
+        }
         __syncthreads();
     }
-    // acc[t][.][i]: word, or word2 from i = 2 on;, token 8 t + 2 q + (i & 1)
+    // sum[t][i]: word, or word2 from i = 2 on;, token 8 t + 2 q + (i & 1)
 #pragma unroll
     for (int i = 0; i < 2 * kTiles; ++i) {
         const int t = i / 2, c = i & 1, token = t * 8 + 2 * q + c;
-        float v0 = acc[t][0][c] + acc[t][1][c], v1 = acc[t][0][2 + c] + acc[t][1][2 + c];
+        float v0 = sum[t][c], v1 = sum[t][2 + c];
         if (token < A.m) {
             const int y = load_target(A.targets, A.targets_wide, A.ignore, A.vocab, token);
             if (y == word) A.target_logit[token] = v0;
@@ -1036,7 +1085,7 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, bool
     L.target_logit = take(L.rows * 4);
     L.lse = take(L.rows * 4);
     L.alpha = take(8);
-    L.part = take(std::max<int64_t>(L.vocab_tiles, few_blocks(a.vocab, direct ? period_of(a.w_ld) : 1)) * L.rows * 8);
+    L.part = take(std::max<int64_t>(L.vocab_tiles * (kTN / kOwn), few_blocks(a.vocab, direct ? period_of(a.w_ld) : 1)) * L.rows * 8);
     L.totals = take((L.rows / 32) * sizeof(BlockTotal));
     if (grad) {
         L.kept_ld = up(a.hidden, 64);
@@ -1210,6 +1259,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.nt = int(L.vocab_tiles);
     A.splits = 1;
     A.kb = int((L.hidden_pad + kBK - 1) / kBK);
+    A.sum_blocks = kLogitBlocks;
     A.targets = targets;
     A.targets_wide = a.targets_dtype == FP8Z_I64;
     A.ignore = a.ignore_index;
@@ -1221,7 +1271,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.ticket = reinterpret_cast<uint32_t*>(alpha + 1);
     A.p = p;
     A.p_bytes = L.piece * 4;
-    int parts = A.nt;
+    int parts = A.nt * (kTN / kOwn);
     if (n <= kFewTokens) {
         parts = few_blocks(vocab, direct ? period : 1);
         const auto launch_few = [&](auto kernel) {
@@ -1284,6 +1334,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         D.n = int(L.hidden_pad);
         D.nt = int((L.hidden_pad + kTN - 1) / kTN);
         D.kb = tiles * (kTN / kBK);
+        D.sum_blocks = 0;
         D.splits = L.splits;
         D.b_k0 = v0;
         D.accumulate = v0 != last;
@@ -1302,19 +1353,15 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.staged = dw_rows && (a.dw_dtype == FP8Z_F32 || !a.accumulate_dw);
         W.alpha = alpha;
         W.b_blocks = 1;
-        const int at_once = L.parts == 2 ? kSumTokens : n;
-        for (int k0 = 0; k0 < n; k0 += at_once) {
-            W.a_k0 = W.b_k0 = k0;
-            W.kb = (std::min(n - k0, at_once) + kBK - 1) / kBK;
-            if (k0 > 0) W.accumulate = 1;
-            // Where a pair of blocks has few tiles of dw, an early start counts: 729 tokens x 2541 x 240
-            // take 33 us for 40, 256 x 32000 x 1024 107 for 116.  Where it has many, the pairs drift apart
-            // and share less of what they load: 517 x 100666 x 6376 would take 2060 us for 2007.
-            W.beside = k0 == 0 && int64_t(W.mt) * W.nt <= 16 * (kSms / 2);
-            if (int rc = L.parts == 2 ? launch_mma<kWeightSplit>(p_mn, x_mn, dw_out, W, sms, st)
-                                      : launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st))
-                return rc;
-        }
+        W.kb = (n + kBK - 1) / kBK;
+        W.sum_blocks = L.parts == 2 ? kWeightBlocks : 0;
+        // Where a pair of blocks has few tiles of dw, an early start counts: 729 tokens x 2541 x 240
+        // take 33 us for 40, 256 x 32000 x 1024 107 for 116.  Where it has many, the pairs drift apart
+        // and share less of what they load: 517 x 100666 x 6376 would take 2060 us for 2007.
+        W.beside = int64_t(W.mt) * W.nt <= 16 * (kSms / 2);
+        if (int rc = L.parts == 2 ? launch_mma<kWeightSplit>(p_mn, x_mn, dw_out, W, sms, st)
+                                  : launch_mma<kWeight>(p_mn, x_mn, dw_out, W, sms, st))
+            return rc;
     }
     const dim3 grid(unsigned(n), unsigned((hidden + 1023) / 1024));
     if (A.bf16)
