@@ -609,16 +609,25 @@ __device__ __noinline__ uint4 part_row8(const uint16_t* row, int k, int cols) {
     return v;
 }
 
-// 16-bit rows copied to a stride the tensor maps can step over, zeros after the
-// end: a warp a row, 16 bytes a thread.
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, int cols,
-                                                       int cols_pad, uint16_t* dst) {
+// 16-bit rows of x, then of w, copied to a stride the tensor maps can step over,
+// zeros after the end: a warp a row, 16 bytes a thread.  Either may have no rows.
+struct PadRows {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t ld;
+    int rows;
+};
+__global__ void __launch_bounds__(256) pad_rows_kernel(const PadRows x, const PadRows w, int cols, int cols_pad) {
     dependent_wait();
-    const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (r >= rows) return;
+    int r = int(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const bool of_x = r < x.rows;
+    const PadRows& m = of_x ? x : w;
+    if (!of_x) r -= x.rows;
+    if (r >= m.rows) return;
+    const uint16_t* from = m.src + r * m.ld;
+    uint16_t* to = m.dst + int64_t(r) * cols_pad;
 #pragma unroll 4
-    for (int c = (threadIdx.x & 31) * 8; c < cols_pad; c += 256)
-        *reinterpret_cast<uint4*>(dst + r * cols_pad + c) = ld_row8(src + r * ld, c, cols);
+    for (int c = (threadIdx.x & 31) * 8; c < cols_pad; c += 256) *reinterpret_cast<uint4*>(to + c) = ld_row8(from, c, cols);
 }
 
 // x once for each way in which rows of w start between 16-byte boundaries: copy r
@@ -1217,12 +1226,20 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     }
     const void *xp = x, *wp = w;
     int64_t x_ld = a.x_ld, w_ld = a.w_ld;
-    if (copy_x) {
-        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned((n + 7) / 8)), 256, 0, st, static_cast<const uint16_t*>(x),
-                                      a.x_ld, n, hidden, int(L.hidden_pad), reinterpret_cast<uint16_t*>(ws + L.x)))
+    if (copy_x || copy_w) {
+        const PadRows px = {static_cast<const uint16_t*>(x), reinterpret_cast<uint16_t*>(ws + L.x), a.x_ld, copy_x ? n : 0};
+        const PadRows pw = {static_cast<const uint16_t*>(w), reinterpret_cast<uint16_t*>(ws + L.w), a.w_ld, copy_w ? vocab : 0};
+        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned((px.rows + pw.rows + 7) / 8)), 256, 0, st, px, pw, hidden,
+                                      int(L.hidden_pad)))
             return rc;
-        xp = ws + L.x;
-        x_ld = L.hidden_pad;
+        if (copy_x) {
+            xp = ws + L.x;
+            x_ld = L.hidden_pad;
+        }
+        if (copy_w) {
+            wp = ws + L.w;
+            w_ld = L.hidden_pad;
+        }
     }
     const int period = period_of(a.w_ld);
     if (direct) {
@@ -1232,13 +1249,6 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
                                       static_cast<const uint16_t*>(w), a.w_ld, reinterpret_cast<uint16_t*>(ws + L.x)))
             return rc;
         xp = ws + L.x;
-    }
-    if (copy_w) {
-        if (int rc = launch_dependent(pad_rows_kernel, dim3(unsigned((vocab + 7) / 8)), 256, 0, st, static_cast<const uint16_t*>(w),
-                                      a.w_ld, vocab, hidden, int(L.hidden_pad), reinterpret_cast<uint16_t*>(ws + L.w)))
-            return rc;
-        wp = ws + L.w;
-        w_ld = L.hidden_pad;
     }
     uint8_t* p = ws + L.p;
     CUtensorMap x_k, w_k, logits;
