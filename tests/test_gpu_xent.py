@@ -378,3 +378,26 @@ def test_rows_of_w_between_16_byte_boundaries(ld, start, n, h, v):
     fp8z.fp8z_linear_xent(x, w, t, loss, total, ws, ignore_index=IGNORE, lse=lse, dev_status=st)
     assert st.item() == 0
     _check_loss(x, w, t, loss, total, lse, "mean")
+
+
+@pytest.mark.parametrize("n", [1, 8, 16, 32, 40, 300])
+@pytest.mark.parametrize("h", [1536, 28672, 28679])
+def test_long_sums_are_rounded_not_cut_off(n, h):
+    """Products of one sign: a sum that the tensor cores cut off at every 16 of K is short
+    by up to 2^-23 of itself a step (a quarter of that on average, 5e-5 at 1792 steps).
+    No more than 24 blocks of 64, 96 steps, are added up that way; the sums of these are
+    rounded, h / 1024 times at most by 2^-24 (in steps of 256 for a few tokens)."""
+    g = torch.Generator(device="cuda").manual_seed(h + n)
+    x = (torch.rand(n, h, generator=g, device="cuda") + 0.5).to(BF16)
+    w = ((torch.rand(300, h, generator=g, device="cuda") + 0.5) * (20.0 / h)).to(BF16)
+    t = torch.randint(0, 300, (n,), generator=g, device="cuda")
+    loss, lse, total, _, _ = _buffers(n, h, 300, BF16, F32)
+    st = _status()
+    fp8z.fp8z_linear_xent(x, w, t, loss, total, _workspace(fp8z.fp8z_linear_xent_workspace(x, w)), lse=lse, dev_status=st)
+    assert st.item() == 0
+    l = x.double() @ w.double().t()
+    want = torch.logsumexp(l, 1)
+    off = (96 * 2.0 ** -23 + (h / 256 + 2) * 2.0 ** -24) * l.amax(1)
+    rest = 2.0 ** -22 + 2.0 ** -23 * l.amax(1) + 64 * 2.0 ** -24 + 2.0 ** -23 * want
+    assert bool(((lse.double() - want).abs() <= off + rest).all())
+    assert bool(((loss.double() - (want - l.gather(1, t[:, None])[:, 0])).abs() <= 2 * off + rest).all())
