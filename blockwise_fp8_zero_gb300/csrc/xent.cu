@@ -848,11 +848,11 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tile
     };
     const int col = blockIdx.x * 32 + r;               // the row of this thread's partial results
     if (col < n) {
-        int t = g;
-        for (; t + 224 < tiles; t += 256) {
+        for (int t = g; t < tiles; t += 256) {
             float2 q[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = part[size_t(t + 32 * i) * rows + col];
+            for (int i = 0; i < 8; ++i)
+                q[i] = t + 32 * i < tiles ? part[size_t(t + 32 * i) * rows + col] : make_float2(-INFINITY, 0.0f);
             float top = q[0].x;
 #pragma unroll
             for (int i = 1; i < 8; ++i) top = fmaxf(top, q[i].x);
@@ -862,7 +862,6 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tile
             for (int i = 0; i < 8; ++i) sum += q[i].y * ex2((q[i].x - ref) * kLog2e);
             add(make_float2(top, sum));
         }
-        for (; t < tiles; t += 32) add(part[size_t(t) * rows + col]);
     }
     sh[r][g] = make_float2(m, s);
     __syncthreads();
