@@ -29,6 +29,7 @@
 #include "fp8z_host.h"
 #include "fp8z_launch.cuh"
 #include "fp8z_tcgen05.cuh"
+#include "fp8z_tiles.h"
 
 namespace fp8z {
 namespace {
@@ -341,12 +342,6 @@ __device__ __forceinline__ void epilogue_weight(const MmaArgs& A, const CUtensor
     }
 }
 
-// Sums of one tile's K loop in tensor memory, one after the other.
-__device__ __forceinline__ int sums_of(const MmaArgs& A, const TileAt& t) {
-    return A.sum_blocks == 0 ? 1 : max(1, (t.k1 - t.k0 + A.sum_blocks - 1) / A.sum_blocks);
-}
-__device__ __forceinline__ int sum_start(const TileAt& t, int i, int sums) { return t.k0 + (t.k1 - t.k0) * i / sums; }
-
 // A pair of blocks takes 256 x 256 results at a time.  Each block loads 128 rows
 // of A and 128 columns of B into a ring of kStages tiles; one thread of the
 // first block issues the products of both, into one of two accumulators in each
@@ -465,9 +460,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const TileAt at = tile_at(A, t);
-                const int sums = sums_of(A, at);
+                const int sums = sums_of(at.k0, at.k1, A.sum_blocks);
                 for (int i = 0; i < sums && ok; ++i) {
-                    const int first = sum_start(at, i, sums), end = sum_start(at, i + 1, sums);
+                    const int first = sum_start(at.k0, at.k1, i, sums), end = sum_start(at.k0, at.k1, i + 1, sums);
                     if (!mbar_wait_bounded(tempty(b), bph ^ 1, wd)) {
                         ok = false;
                         break;
@@ -510,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int t = pair; t < tiles; t += pairs) {
             const TileAt at = tile_at(A, t);
-            const int n_sums = sums_of(A, at);
+            const int n_sums = kOneSum ? 1 : sums_of(at.k0, at.k1, A.sum_blocks);
             Sums sums;
             if constexpr (kAddAll)
 #pragma unroll
