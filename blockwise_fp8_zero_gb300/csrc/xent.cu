@@ -7,7 +7,11 @@
 //   dx = a * P w,   dw = a * P^T x,   a = grad_scale / (number of kept tokens, or 1)
 //
 // The loss needs one product whose epilogue turns each 256 columns of logits
-// into a maximum and a sum of exponentials per token.  The gradient goes through
+// into a maximum and a sum of exponentials per token.  Every exponential is taken
+// of a difference to a maximum m that is formed first, and m and the sum s go on
+// apart: the loss is log s + (m - l_y) and a probability exp(l - m) / s, so that
+// neither loses what m holds beyond their own size (a loss of 1e-15 at logits of
+// 4000 comes out as 0; from an FP32 lse it was 3e-4 off).  The gradient goes through
 // the vocabulary in pieces: P of a piece, in 16 bits, is what the two other
 // products read.  The buffer that holds one piece of P holds the logits of one
 // piece just as well, so the first pass leaves the last piece's logits there
@@ -76,7 +80,7 @@ struct MmaArgs {
     const int32_t* target;    // -1: takes no part in the loss (written by rows_kernel)
     float2* part;             // [tile, or block of few_kernel][rows] maximum and sum
     float* target_logit;
-    const float* lse;
+    const float2* row_stats;  // maximum of a row, 1 / the sum of its exponentials
     int keep_from;            // words from here on leave their logits in the piece's buffer
     uint8_t* p;               // that buffer, p_bytes a row (few_kernel)
     int64_t p_bytes;
@@ -121,6 +125,22 @@ __device__ __forceinline__ float2 unpack16(uint32_t u, int bf16) {
     if (bf16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
     const __half2 h = *reinterpret_cast<const __half2*>(&u);
     return __half22float2(h);
+}
+
+// (a - m) * log2(e) of two logits by packed instructions: two for both, as one fused
+// multiplication and addition each would be, which would round m * log2(e).
+__device__ __forceinline__ float2 exponents(uint32_t a, uint32_t b, float m) {
+    float2 e;
+    asm("{\n\t.reg .b64 L, M, K;\n\t"
+        "mov.b64 L, {%2, %3};\n\t"
+        "mov.b64 M, {%4, %4};\n\t"
+        "mov.b64 K, {%5, %5};\n\t"
+        "sub.rn.f32x2 L, L, M;\n\t"
+        "mul.rn.f32x2 L, L, K;\n\t"
+        "mov.b64 {%0, %1}, L;\n\t}"
+        : "=f"(e.x), "=f"(e.y)
+        : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(m), "f"(kLog2e));
+    return e;
 }
 
 __device__ __forceinline__ int load_target(const void* targets, int wide, int64_t ignore, int64_t vocab, int row) {
@@ -192,14 +212,15 @@ __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorM
         float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(r[j]));
-        const float m2 = fmaxf(mx, top), ref = m2 == -INFINITY ? 0.0f : m2 * kLog2e;
+        const float m2 = fmaxf(mx, top), ref = m2 == -INFINITY ? 0.0f : m2;
         float s = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-            s += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-            s2 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -ref));
+            const float2 e = exponents(r[j], r[j + 1], ref);
+            s += ex2(e.x);
+            s2 += ex2(e.y);
         }
-        sum = fmaf(sum, ex2(fmaf(mx, kLog2e, -ref)), s + s2);
+        sum = fmaf(sum, ex2((mx - ref) * kLog2e), s + s2);
         mx = m2;
         if (target >= c && target < c + 32) {
             float x = 0.0f;
@@ -213,19 +234,21 @@ __device__ __forceinline__ void epilogue_stats(const MmaArgs& A, const CUtensorM
 }
 
 // P of eight neighbouring words of one row, times p_scale: in 16 bits, and what
-// that rounding left in another 16.  ref = lse * log2(e); target: the row's word
-// relative to the first of the eight; valid: words before the vocabulary's end.
-__device__ __forceinline__ void prob8(const uint32_t* r, float ref, int target, int valid, bool kept, float p_scale,
+// that rounding left in another 16.  stats: the row's maximum and 1 / its sum;
+// target: the row's word relative to the first of the eight; valid: words before the
+// vocabulary's end.
+__device__ __forceinline__ void prob8(const uint32_t* r, float2 stats, int target, int valid, bool kept, float p_scale,
                                       int bf16, uint32_t (&h)[4], uint32_t (&l)[4]) {
+    const float f = stats.y * p_scale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        const float2 e = exponents(r[i * 2], r[i * 2 + 1], stats.x);
         float p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int j = i * 2 + k;
-            float v = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-            if (target == j) v -= 1.0f;
-            p[k] = kept && j < valid ? v * p_scale : 0.0f;
+            const float v = ex2(k ? e.y : e.x);
+            p[k] = kept && j < valid ? fmaf(v, f, target == j ? -p_scale : 0.0f) : 0.0f;
         }
         h[i] = pack16(p[0], p[1], bf16);
         const float2 w = unpack16(h[i], bf16);
@@ -241,7 +264,7 @@ __device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMa
     const int n_valid = A.n - t.n * kTN;
     const int y = row < A.m ? A.target[row] : -1;
     const int target = y - (A.v0 + t.n * kTN);
-    const float ref = y >= 0 ? A.lse[row] * kLog2e : 0.0f;
+    const float2 stats = y >= 0 ? A.row_stats[row] : make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < kOwn; i += 64) {
         uint32_t h[32], l[32];
@@ -249,7 +272,7 @@ __device__ __forceinline__ void epilogue_prob(const MmaArgs& A, const CUtensorMa
         for (int q = 0; q < 8; ++q) {
             const int at = c0 + i + q * 8;
             uint32_t hq[4], lq[4];
-            prob8(sums + i + q * 8, ref, target - at, n_valid - at, y >= 0, A.p_scale, A.bf16, hq, lq);
+            prob8(sums + i + q * 8, stats, target - at, n_valid - at, y >= 0, A.p_scale, A.bf16, hq, lq);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 h[q * 4 + k] = hq[k];
@@ -784,8 +807,8 @@ __global__ void __launch_bounds__(256, few_blocks_sm<kTiles, kAligned>) few_kern
         float m = fmaxf(v0, v1);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const float ref = m == -INFINITY ? 0.0f : m * kLog2e;
-        float s = ex2(fmaf(v0, kLog2e, -ref)) + ex2(fmaf(v1, kLog2e, -ref));
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float s = ex2((v0 - ref) * kLog2e) + ex2((v1 - ref) * kLog2e);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         if (g == 0) warp_part[warp][token] = make_float2(m, s);
@@ -813,7 +836,7 @@ struct BlockTotal {
 __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tiles, int n, int rows,
                                                     const void* targets, int wide, int64_t ignore,
                                                     int64_t vocab, const float* target_logit,
-                                                    int32_t* target, float* lse_ws,
+                                                    int32_t* target, float2* row_stats,
                                                     float* lse_out, float* loss,
                                                     BlockTotal* totals, uint32_t* ticket,
                                                     int mean, float scale, float* total,
@@ -870,11 +893,11 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tile
     if (r == 0) {
         float out = 0.0f;
         if (row < n) {
-            const float lse = m + logf(s);
-            out = y >= 0 ? lse - own : 0.0f;
+            const float log_s = logf(s);
+            out = y >= 0 ? log_s + (m - own) : 0.0f;
             target[row] = y;
-            lse_ws[row] = lse;
-            if (lse_out) lse_out[row] = lse;
+            row_stats[row] = make_float2(m, 1.0f / s);
+            if (lse_out) lse_out[row] = m + log_s;
             loss[row] = out;
         }
         sh[0][g] = make_float2(out, y >= 0 ? 1.0f : 0.0f);
@@ -920,8 +943,8 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2* part, int tile
 // token that takes no part: its P is zero, but zero times an infinity or a NaN is
 // not, and neither may reach dw.
 constexpr int kProbTiles = 4;
-__global__ void __launch_bounds__(256) prob_kernel(uint8_t* p, int64_t row_bytes, int tiles, int words, int v0,
-                                                   const int32_t* target, const float* lse, float p_scale, int bf16,
+__global__ void __launch_bounds__(256, 5) prob_kernel(uint8_t* p, int64_t row_bytes, int tiles, int words, int v0,
+                                                   const int32_t* target, const float2* row_stats, float p_scale, int bf16,
                                                    int split_p, const uint16_t* x, int64_t x_ld, int hidden,
                                                    uint16_t* kept_x, int kept_ld) {
     dependent_wait();
@@ -939,7 +962,7 @@ __global__ void __launch_bounds__(256) prob_kernel(uint8_t* p, int64_t row_bytes
         }
         return;
     }
-    const float ref = y >= 0 ? lse[row] * kLog2e : 0.0f;
+    const float2 stats = y >= 0 ? row_stats[row] : make_float2(0.0f, 0.0f);
     // the last words first: L2 still holds their logits (1024 tokens x 32000 x 1024: 232 us for 241)
     const int t0 = (int(gridDim.y - 2 - blockIdx.y) * 8 + (threadIdx.x >> 5)) * kProbTiles;
     uint4 in[kProbTiles][2];
@@ -958,7 +981,7 @@ __global__ void __launch_bounds__(256) prob_kernel(uint8_t* p, int64_t row_bytes
                                in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
         const int at = (t0 + i) * kTN + lane * 8;
         uint32_t h[4], l[4];
-        prob8(r, ref, y - v0 - at, words - at, y >= 0, p_scale, bf16, h, l);
+        prob8(r, stats, y - v0 - at, words - at, y >= 0, p_scale, bf16, h, l);
         uint4* q = reinterpret_cast<uint4*>(p + row * row_bytes + int64_t(t0 + i) * 1024);
         q[lane] = make_uint4(h[0], h[1], h[2], h[3]);
         if (split_p) q[32 + lane] = make_uint4(l[0], l[1], l[2], l[3]);
@@ -1003,7 +1026,7 @@ struct Layout {
     int64_t rows, hidden_pad, kept_ld, vocab_tiles, piece, pieces, parts;
     int splits;
     bool copy_x, copy_w;
-    size_t x, w, kept_x, target, target_logit, lse, part, totals, alpha, p, sum, total;
+    size_t x, w, kept_x, target, target_logit, row_stats, part, totals, alpha, p, sum, total;
 };
 
 constexpr int64_t kPieceBytes = 1LL << 30;        // of one piece, see layout()
@@ -1087,7 +1110,7 @@ Layout layout(const fp8z_xent_args& a, bool grad, bool copy_x, bool copy_w, bool
     L.w = take(copy_w ? a.vocab * L.hidden_pad * 2 : 0);
     L.target = take(L.rows * 4);
     L.target_logit = take(L.rows * 4);
-    L.lse = take(L.rows * 4);
+    L.row_stats = take(L.rows * 8);
     L.alpha = take(8);
     L.part = take(std::max<int64_t>(L.vocab_tiles * (kTN / kOwn), few_blocks(a.vocab, direct ? period_of(a.w_ld) : 1)) * L.rows * 8);
     L.totals = take((L.rows / 32) * sizeof(BlockTotal));
@@ -1203,7 +1226,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     const int n = int(a.tokens), hidden = int(a.hidden), vocab = int(a.vocab);
     auto* target = reinterpret_cast<int32_t*>(ws + L.target);
     auto* target_logit = reinterpret_cast<float*>(ws + L.target_logit);
-    auto* lse_ws = reinterpret_cast<float*>(ws + L.lse);
+    auto* row_stats = reinterpret_cast<float2*>(ws + L.row_stats);
     auto* alpha = reinterpret_cast<float*>(ws + L.alpha);
     auto* part = reinterpret_cast<float2*>(ws + L.part);
     const auto done = [] { return cudaGetLastError() == cudaSuccess ? FP8Z_OK : FP8Z_ECUDA; };
@@ -1298,7 +1321,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     // FP16 P is kept times 2^12: probabilities down to 2^-36 stay normal numbers or close
     const float p_scale = A.bf16 ? 1.0f : 4096.0f;
     if (int rc = launch_dependent(rows_kernel, dim3(unsigned((n + 31) / 32)), 1024, 0, st, part, parts, n, A.rows, targets,
-                                  A.targets_wide, A.ignore, A.vocab, target_logit, target, lse_ws, lse, loss,
+                                  A.targets_wide, A.ignore, A.vocab, target_logit, target, row_stats, lse, loss,
                                   reinterpret_cast<BlockTotal*>(ws + L.totals), A.ticket, a.reduction == FP8Z_MEAN,
                                   grad ? a.grad_scale / p_scale : 1.0f, total, grad ? alpha : nullptr, dev_status))
         return rc;
@@ -1320,7 +1343,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         const int words = int(a.vocab - v0 < L.piece ? a.vocab - v0 : L.piece), tiles = (words + kTN - 1) / kTN;
         if (v0 == last) {
             const dim3 grid(unsigned(n), unsigned((tiles + 8 * kProbTiles - 1) / (8 * kProbTiles) + 1));
-            if (int rc = launch_dependent(prob_kernel, grid, 256, 0, st, p, L.piece * 4, tiles, words, v0, target, lse_ws,
+            if (int rc = launch_dependent(prob_kernel, grid, 256, 0, st, p, L.piece * 4, tiles, words, v0, target, row_stats,
                                           p_scale, A.bf16, L.parts == 2, static_cast<const uint16_t*>(x), a.x_ld, hidden,
                                           reinterpret_cast<uint16_t*>(ws + L.kept_x), int(L.kept_ld)))
                 return rc;
@@ -1330,7 +1353,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
             Q.nt = tiles;
             Q.v0 = v0;
             Q.b_n0 = v0;
-            Q.lse = lse_ws;
+            Q.row_stats = row_stats;
             Q.split_p = L.parts == 2;
             Q.p_scale = p_scale;
             if (int rc = launch_mma<kProb>(x_k, w_k, p_out, Q, sms, st)) return rc;

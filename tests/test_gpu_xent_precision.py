@@ -1,0 +1,102 @@
+"""What the cross entropy keeps of small losses and probabilities, against 64 bits.
+
+The inputs have two columns for each token t, so that every logit is one that FP32
+holds exactly: x[t] is A_t and g, w[v] 1 and -k, hence l[t][v] = A_t - g k[t][v], and
+the largest logit is A_t.  With exact logits the error is the softmax's own and does
+not grow with A: l - max is exact; its product with log2(e) (within 2^-26) is within
+1.25 * 2^-24 of itself, so that an exponential of -G is within r = 2^-22 + 1.25 G 2^-24
+of itself, three times that after a partial sum's and a row's rescaling.  The sum s >= 1
+of the exponentials collects one 2^-24 for each addition on a term's way: 16 of a chain,
+2 to join chains, 4 segments, 8 + 1 tiles of a thread, 5 of a warp: under 40.  logf is
+within an ulp."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from blockwise_fp8_zero_gb300 import fp8z  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+BF16, F16 = torch.bfloat16, torch.float16
+UNIT = {BF16: 2.0 ** -8, F16: 2.0 ** -11}
+V = 1000
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from blockwise_fp8_zero_gb300 import build
+    build.build()
+    fp8z.lib()
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _exact_logits(n, kind, dtype, odd, top):
+    """(x, w, targets, A, g k as float64 [n, V]) with rows of 2 n (+ 1) columns."""
+    gen = _gen(n)
+    h = 2 * n + (1 if odd else 0)
+    a = ((torch.rand(n, generator=gen, device="cuda") * 1.98 - 0.99) * top).to(dtype)
+    t = torch.randint(0, V, (n,), generator=gen, device="cuda")
+    if kind == "confident":          # the target is above all other words by g
+        g = torch.tensor([6.0, 17.0, 40.0], device="cuda")[torch.arange(n, device="cuda") % 3]
+        k = torch.ones(n, V, device="cuda")
+        k.scatter_(1, t[:, None], 0.0)
+    else:                            # the largest logit anywhere, the target anywhere
+        g = torch.full((n,), 2.5, device="cuda")
+        k = torch.randint(1, 65, (n, V), generator=gen, device="cuda") / 8.0
+        k.scatter_(1, torch.randint(0, V, (n, 1), generator=gen, device="cuda"), 0.0)
+    x = torch.zeros(n, h, dtype=dtype, device="cuda")
+    w = torch.zeros(V, h, dtype=dtype, device="cuda")
+    i = torch.arange(n, device="cuda")
+    x[i, 2 * i], x[i, 2 * i + 1] = a, g.to(dtype)
+    w[:, 0:2 * n:2] = 1.0
+    w[:, 1:2 * n:2] = -k.t().to(dtype)
+    return x, w, t, a.double(), g.double()[:, None] * k.double()
+
+
+@pytest.mark.parametrize("n", [3, 20, 40])
+@pytest.mark.parametrize("kind", ["confident", "spread"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("odd,piece", [(False, 0), (True, 0), (False, 256)])
+@pytest.mark.parametrize("top", [1.0, 4000.0])
+def test_small_losses_of_large_logits(n, kind, dtype, odd, piece, top):
+    x, w, t, a, gk = _exact_logits(n, kind, dtype, odd, top)
+    e = torch.exp(-gk)
+    s = e.sum(1)
+    own = gk.gather(1, t[:, None])[:, 0]
+    tail = s - 1.0
+    # log1p keeps a loss of 1e-15
+    want = torch.log1p(torch.where(own == 0.0, (e.scatter(1, t[:, None], 0.0)).sum(1), tail)) + own
+    r = 3 * (2.0 ** -22 + 1.25 * float(gk.max()) * 2.0 ** -24)
+    ds = 40 * 2.0 ** -24 * s + r * tail                     # on s
+    bound = ds / s + 2.0 ** -22 * want
+    loss, lse, total = (torch.full((k,), math.nan, device="cuda") for k in (n, n, 2))
+    ws = torch.full((fp8z.fp8z_linear_xent_workspace(x, w),), 255, dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_linear_xent(x, w, t, loss, total, ws, lse=lse, reduction="sum")
+    assert bool((loss >= 0).all())
+    assert bool(((loss.double() - want).abs() <= bound).all())
+    assert bool(((lse.double() - (a + torch.log(s))).abs() <= ds / s + 2.0 ** -22 * torch.log(s) + 2.0 ** -24 * (a.abs() + 8)).all())
+
+    dx = torch.empty_like(x)
+    dw = torch.full((V, x.shape[1]), math.nan, device="cuda")
+    ws = torch.full((fp8z.fp8z_linear_xent_workspace(x, w, dw=dw, piece_words=piece),), 255, dtype=torch.uint8, device="cuda")
+    first = loss.clone()
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, reduction="sum")
+    if x.shape[1] % 8 == 0:          # else the loss of few tokens reads w where it is, in another order
+        assert torch.equal(first, loss)
+    assert bool((loss >= 0).all()) and bool(((loss.double() - want).abs() <= bound).all())
+    # dw[v][2 t] = A_t P[t][v]: one product, so P itself is seen
+    p = e / s[:, None]
+    at_target = torch.zeros_like(p).scatter_(1, t[:, None], 1.0)
+    P = torch.where(at_target.bool() & (own == 0.0)[:, None], -((s - e.gather(1, t[:, None])[:, 0]) / s)[:, None].expand_as(p), p - at_target)
+    got = dw[:, 0:2 * n:2].t().double() / torch.where(a == 0.0, torch.ones_like(a), a)[:, None]
+    err = p * (ds / s + r)[:, None] + 2.0 ** -23 * at_target               # and 1 subtracted
+    # P leaves in two parts of dtype (FP16 counts in 2^-36 at the least), the product and dw round
+    tol = err + P.abs() * (UNIT[dtype] ** 2 + 2.0 ** -22) + (2.0 ** -37 if dtype == F16 else 0.0)
+    ok = (got - P).abs() <= tol
+    assert bool(ok[a != 0.0].all())
