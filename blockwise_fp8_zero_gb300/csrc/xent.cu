@@ -66,7 +66,6 @@ struct MmaArgs {
     int m, n;                 // rows and columns of the result
     int mt, nt, splits;       // tiles, and parts of the K loop
     int kb;                   // K blocks of 64
-    int sum_blocks;           // of them, at most, in one sum in tensor memory (0: all)
     int b_n0, b_k0;           // where B starts, in elements
     int b_blocks;             // B's map has its columns as blocks of 64
     int bf16;
@@ -377,7 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap tc, const __grid_constant__ MmaArgs A) {
     constexpr bool kWeights = kEpi == kWeight || kEpi == kWeightSplit;
     constexpr bool kAMn = kWeights, kBMn = kEpi == kSum || kWeights;                 // operands along M or N
-    constexpr bool kOneSum = kEpi == kSum || kEpi == kWeight;                        // 16 bits in the end
+    constexpr int kSumBlocks = kEpi == kWeightSplit ? kWeightBlocks : kEpi == kSum || kEpi == kWeight ? 0 : kLogitBlocks;
+    constexpr bool kOneSum = kSumBlocks == 0;                                        // 16 bits in the end
     constexpr bool kAddAll = kEpi == kProb || kEpi == kWeightSplit;                  // the first sum to zeros: fewer registers
     constexpr int kParts = kEpi == kWeightSplit ? 2 : 1;      // of A: one B serves both, a third less to load
     constexpr int kBytesA = kParts * kTileBytes, kStageBytes = kBytesA + kTileBytes, kStages = kRing / kStageBytes;
@@ -483,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const TileAt at = tile_at(A, t);
-                const int sums = sums_of(at.k0, at.k1, A.sum_blocks);
+                const int sums = sums_of(at.k0, at.k1, kSumBlocks);
                 for (int i = 0; i < sums && ok; ++i) {
                     const int first = sum_start(at.k0, at.k1, i, sums), end = sum_start(at.k0, at.k1, i + 1, sums);
                     if (!mbar_wait_bounded(tempty(b), bph ^ 1, wd)) {
@@ -528,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int t = pair; t < tiles; t += pairs) {
             const TileAt at = tile_at(A, t);
-            const int n_sums = kOneSum ? 1 : sums_of(at.k0, at.k1, A.sum_blocks);
+            const int n_sums = sums_of(at.k0, at.k1, kSumBlocks);
             Sums sums;
             if constexpr (kAddAll)
 #pragma unroll
@@ -1287,7 +1287,6 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     A.nt = int(L.vocab_tiles);
     A.splits = 1;
     A.kb = int((L.hidden_pad + kBK - 1) / kBK);
-    A.sum_blocks = kLogitBlocks;
     A.targets = targets;
     A.targets_wide = a.targets_dtype == FP8Z_I64;
     A.ignore = a.ignore_index;
@@ -1362,7 +1361,6 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         D.n = int(L.hidden_pad);
         D.nt = int((L.hidden_pad + kTN - 1) / kTN);
         D.kb = tiles * (kTN / kBK);
-        D.sum_blocks = 0;
         D.splits = L.splits;
         D.b_k0 = v0;
         D.accumulate = v0 != last;
@@ -1382,7 +1380,6 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.alpha = alpha;
         W.b_blocks = 1;
         W.kb = (n + kBK - 1) / kBK;
-        W.sum_blocks = L.parts == 2 ? kWeightBlocks : 0;
         // Where a pair of blocks has few tiles of dw, an early start counts: 729 tokens x 2541 x 240
         // take 33 us for 40, 256 x 32000 x 1024 107 for 116.  Where it has many, the pairs drift apart
         // and share less of what they load: 517 x 100666 x 6376 would take 2060 us for 2007.
