@@ -51,7 +51,11 @@ constexpr int kThreads = 128 + 32 * kReaders;          // warps 0 and 3 load A a
 // K and are added up, rounded, in the readers' registers: loss 7e-7 off, dw 2.3e-6,
 // of which the two parts of P make up 1.7e-6.  That takes 3 % of the loss's time (4 with
 // 16 blocks of K for the logits, 2.5 with 32 and 9e-7) and 1 to 2 of the gradient's.
-constexpr int kLogitBlocks = 24, kWeightBlocks = 8;
+// A dx and a dw of 16 bits need less, but not nothing: 8192 steps (131072 words, or as many
+// tokens) may cut off 1e-3 of what was added up, twice FP16's rounding, and what all rows of
+// w have in common cancels in dx while its cut-off does not.  64 blocks, 256 steps, are 3e-5.
+// 16384 steps of one sign took 1.1e-3 off a 16-bit dw.  It takes 0.7 % of a gradient's time at the most.
+constexpr int kLogitBlocks = 24, kWeightBlocks = 8, kResultBlocks = 64;
 constexpr int kTmemCols = 512;                         // two accumulators of 256 columns
 constexpr int kSlab = 32 * 128;                        // staged results of a reader: 32 rows of 128 bytes
 constexpr int kStaging = kReaders * kSlab;
@@ -376,9 +380,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap tc, const __grid_constant__ MmaArgs A) {
     constexpr bool kWeights = kEpi == kWeight || kEpi == kWeightSplit;
     constexpr bool kAMn = kWeights, kBMn = kEpi == kSum || kWeights;                 // operands along M or N
-    constexpr int kSumBlocks = kEpi == kWeightSplit ? kWeightBlocks : kEpi == kSum || kEpi == kWeight ? 0 : kLogitBlocks;
-    constexpr bool kOneSum = kSumBlocks == 0;                                        // 16 bits in the end
-    constexpr bool kAddAll = kEpi == kProb || kEpi == kWeightSplit;                  // the first sum to zeros: fewer registers
+    constexpr int kSumBlocks = kEpi == kWeightSplit ? kWeightBlocks : kEpi == kSum || kEpi == kWeight ? kResultBlocks : kLogitBlocks;
+    constexpr bool kAddAll = kEpi != kStats;                  // the first sum to zeros: fewer registers
+    constexpr int kStep = kEpi == kSum || kEpi == kWeight ? 8 : 16;                  // columns added at a time: fewer registers, too
     constexpr int kParts = kEpi == kWeightSplit ? 2 : 1;      // of A: one B serves both, a third less to load
     constexpr int kBytesA = kParts * kTileBytes, kStageBytes = kBytesA + kTileBytes, kStages = kRing / kStageBytes;
     extern __shared__ uint8_t smem_raw[];
@@ -538,18 +542,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + b * kTN + c0 + (uint32_t(quarter * 32) << 16);
-                if (kOneSum || (!kAddAll && i == 0)) {
+                if (!kAddAll && i == 0) {
 #pragma unroll
                     for (int c = 0; c < kOwn; c += 32) tmem_ld32(reinterpret_cast<uint32_t(&)[32]>(sums[c]), acc + c);
                     tmem_wait_ld();
                 } else {
 #pragma unroll
-                    for (int c = 0; c < kOwn; c += 16) {
-                        uint32_t r[16];
-                        tmem_ld16(r, acc + c);
+                    for (int c = 0; c < kOwn; c += kStep) {
+                        uint32_t r[kStep];
+                        if constexpr (kStep == 16) tmem_ld16(r, acc + c);
+                        else tmem_ld8(r, acc + c);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
+                        for (int j = 0; j < kStep; ++j)
                             sums[c + j] = __float_as_uint(__uint_as_float(sums[c + j]) + __uint_as_float(r[j]));
                     }
                 }

@@ -100,3 +100,44 @@ def test_small_losses_of_large_logits(n, kind, dtype, odd, piece, top):
     tol = err + P.abs() * (UNIT[dtype] ** 2 + 2.0 ** -22) + (2.0 ** -37 if dtype == F16 else 0.0)
     ok = (got - P).abs() <= tol
     assert bool(ok[a != 0.0].all())
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_dx_of_a_large_vocabulary(n, dtype):
+    """x = 0: every logit is 0 and P = 2^-22, exact in both types.  w lies between 0.5 and
+    1.5, so that dx = mean(w) - w_y adds up to 1 before the target's row of ones, the last,
+    takes nearly all of it away: what was cut off on the way stays.  At most 64 blocks of 64
+    words, 256 steps, are added up in tensor memory, each cutting off 2^-23 of the sum; 16 sums
+    in registers, 64 parts and the last steps round by 2^-24.  P of the target is 1 less 2^-22."""
+    v, h = 1 << 22, 64
+    w = torch.empty(v, h, dtype=dtype, device="cuda").uniform_(0.5, 1.5, generator=_gen(1))
+    w[-1] = 1.0
+    x = torch.zeros(n, h, dtype=dtype, device="cuda")
+    t = torch.full((n,), v - 1, device="cuda")
+    loss, total = torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = torch.empty(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, reduction="sum")
+    want = w.double().mean(0) - 1.0
+    tol = 256 * 2.0 ** -23 + (16 + 64 + 8) * 2.0 ** -24 + 2.0 ** -22 + want.abs() * UNIT[dtype] + 2.0 ** -25
+    assert bool(((dx.double() - want).abs() <= tol).all())
+
+
+def test_16_bit_dw_of_many_tokens():
+    """w = 0: P = 2^-8 for every word that is not a target, and its row of dw is the sum of
+    x, between 0.5 and 1.5, over 2^18 tokens, times 2^-8.  The roundings to FP16 (2^-11 at the
+    most, 2^-12 in the mean square) have no sign, and over 512 columns their mean is within
+    6 * 2^-12 / sqrt(512); what sums cut off has one: 256 steps of 2^-23, and 64 sums that round."""
+    n, h, v = 1 << 18, 512, 256
+    x = torch.empty(n, h, dtype=F16, device="cuda").uniform_(0.5, 1.5, generator=_gen(2))
+    w = torch.zeros(v, h, dtype=F16, device="cuda")
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    loss, total = torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = torch.empty(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, reduction="sum")
+    want = x.double().sum(0) / 256
+    off = (dw[1:].double() - want) / want
+    assert bool((off.abs() <= 2.0 ** -11 + 256 * 2.0 ** -23 + 64 * 2.0 ** -24).all())
+    assert abs(float(off.mean())) <= 6 * 2.0 ** -12 / math.sqrt(h) + 256 * 2.0 ** -23 + 64 * 2.0 ** -24
