@@ -1322,8 +1322,9 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     } else if (int rc = launch_mma<kStats>(x_k, w_k, logits, A, sms, st)) {
         return rc;
     }
-    // FP16 P is kept times 2^12: probabilities down to 2^-36 stay normal numbers or close
-    const float p_scale = A.bf16 ? 1.0f : 4096.0f;
+    // FP16 P is kept times 2^15, at which 1 is still finite: normal numbers down to 2^-29, and
+    // the smallest that counts is 2^-39 (with two parts: 16 bits or more from 2^-23 on)
+    const float p_scale = A.bf16 ? 1.0f : 32768.0f;
     if (int rc = launch_dependent(rows_kernel, dim3(unsigned((n + 31) / 32)), 1024, 0, st, part, parts, n, A.rows, targets,
                                   A.targets_wide, A.ignore, A.vocab, target_logit, target, row_stats, lse, loss,
                                   reinterpret_cast<BlockTotal*>(ws + L.totals), A.ticket, a.reduction == FP8Z_MEAN,

@@ -532,12 +532,14 @@ typedef struct {
  *   P[t][v] = (exp(l[t][v] - lse[t]) - [v == targets[t]]) for kept tokens,
  *   dx = a * P w (of dtype),  dw = a * P^T x (of dw_dtype, or added to dw),
  *   a = grad_scale / max(1, kept tokens) (FP8Z_MEAN) or grad_scale.
- * Products run on the tensor cores in FP32; P enters them in dtype (11 or 8
- * significant bits), as two summands of dtype where dw is FP32 (16 bits or
- * more).  Logits are kept for one piece of the vocabulary at most: the gradient
- * goes through the vocabulary in pieces, one buffer (4 bytes a word and token)
- * holds the last piece's FP32 logits and then the P of each piece in turn, and the
- * logits of the pieces before the last are computed again.
+ * Products run on the tensor cores in FP32; P enters them in dtype, as two summands of
+ * dtype for dw where that is FP32.  In BF16 these are 8 significant bits, or 16; in
+ * FP16 11, or 22, of which only those of 2^-39 and above count (so 11 from
+ * probabilities of 2^-29 on, and 16 or more with two summands from 2^-23 on). Logits
+ * are kept for one piece of the vocabulary at most: the gradient goes through the
+ * vocabulary in pieces, one buffer (4 bytes a word and token) holds the last piece's
+ * FP32 logits and then the P of each piece in turn, and the logits of the pieces before
+ * the last are computed again.
  *
  * fp8z_linear_xent_workspace -- bytes of workspace (device, 256-byte aligned, no
  * initialisation) for these arguments, with pieces of at most piece_words words

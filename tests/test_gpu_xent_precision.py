@@ -141,3 +141,27 @@ def test_16_bit_dw_of_many_tokens():
     off = (dw[1:].double() - want) / want
     assert bool((off.abs() <= 2.0 ** -11 + 256 * 2.0 ** -23 + 64 * 2.0 ** -24).all())
     assert abs(float(off.mean())) <= 6 * 2.0 ** -12 / math.sqrt(h) + 256 * 2.0 ** -23 + 64 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_small_probabilities_in_fp16(n, piece):
+    """Words 14 to 24 below the largest logit: probabilities of 2^-20 to 2^-35.  An FP32 dw
+    gets them in two FP16 parts, 22 bits, of which those of 2^-39 count: half of that is lost.
+    The exponential and the sum are as in the bounds above."""
+    x, w, t, a, _ = _exact_logits(n, "spread", F16, False, 4000.0)
+    k = torch.randint(46, 77, (n, V), generator=_gen(n), device="cuda") / 8.0
+    k.scatter_(1, t[:, None], 0.0)
+    w[:, 1:2 * n:2] = -k.t().to(F16)
+    gk = 2.5 * k.double()
+    e = torch.exp(-gk)
+    s = e.sum(1)
+    loss, total = torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty(V, x.shape[1], device="cuda")
+    ws = torch.empty(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw, piece_words=piece), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, reduction="sum")
+    p = (e / s[:, None]).scatter(1, t[:, None], 0.0)
+    got = (dw[:, 0:2 * n:2].t().double() / a[:, None]).scatter(1, t[:, None], 0.0)
+    r = 3 * (2.0 ** -22 + 1.25 * 24.0 * 2.0 ** -24)
+    tol = p * (r + (40 + 2) * 2.0 ** -24 + 2 * 2.0 ** -22) + 2.0 ** -40
+    assert bool(((got - p).abs() <= tol).all())
