@@ -165,3 +165,26 @@ def test_small_probabilities_in_fp16(n, piece):
     r = 3 * (2.0 ** -22 + 1.25 * 24.0 * 2.0 ** -24)
     tol = p * (r + (40 + 2) * 2.0 ** -24 + 2 * 2.0 ** -22) + 2.0 ** -40
     assert bool(((got - p).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n", [4096, 65536 + 197])
+def test_fp32_dw_is_added_up_in_short_sums(n, dtype):
+    """As above with an FP32 dw: 8 blocks of K, 32 steps for each of P's two parts, may cut
+    off 2^-23 of their sum, and every sum rounds once when it is added, as dw does at the end.
+    One sum of all tokens would cut off 4096 steps of the larger case, 5e-4 at the most."""
+    h, v = 136, 256
+    x = torch.empty(n, h, dtype=dtype, device="cuda").uniform_(0.5, 1.5, generator=_gen(3))
+    w = torch.zeros(v, h, dtype=dtype, device="cuda")
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    loss, total = torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty(v, h, device="cuda")
+    ws = torch.empty(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, reduction="sum")
+    want = x.double().sum(0) / 256
+    sums = -(-n // 512)
+    bound = 64 * 2.0 ** -23 + (sums + 1) * 2.0 ** -24
+    assert bool(((dw[1:].double() - want).abs() <= bound * want).all())
+    # the target's row: 255 / 256 in two parts of dtype, taken away
+    want = -x.double().sum(0) * (255 / 256)
+    assert bool(((dw[0].double() - want).abs() <= (bound + UNIT[dtype] ** 2) * want.abs()).all())
