@@ -70,21 +70,27 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const void* ids, int w
 
 // ------------------------------------------------------------------- sort
 // Stable radix sort of (id, token) by digits of up to kMaxDigit bits, one
-// block per tile of kTile tokens: count the digits of each tile, then place
-// every token at (tokens of smaller digits) + (equal digits of earlier tiles)
-// + (its rank among equal digits of its own tile).  Ids that take no gradient
-// (padding, out of range) get the key `vocab`, which sorts last.
+// block per tile of kTile tokens, or per several neighbouring tiles of a list of more
+// than kMostBlocks: count the digits of each block's tokens, then place every token at
+// (tokens of smaller digits) + (equal digits of earlier blocks and tiles) + (its rank
+// among equal digits of its own tile).  Ids that take no gradient (padding, out of
+// range) get the key `vocab`, which sorts last.  Every block walks over the counts of
+// all blocks, work that would grow with the square of the tokens (2^24: 275 GB a pass),
+// so their number is bounded: 4194304 tokens x 8 take 5.07 ms for 7.33 with a block for
+// each tile (512 blocks 5.13, 128 5.14; 1048576 tokens 1.03, 1.13 and 1.00 for 1.13).
 constexpr int kItems = 8;
 constexpr int kTile = kThreads * kItems;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxDigit = 10;
 constexpr int kBins = 1 << kMaxDigit;
+constexpr int kMostBlocks = 256;
 
 struct SortShape {
     int bits;        // key bits
     int passes;
     int digit;       // bits per pass
-    int tiles;
+    int tiles;       // of one block
+    int blocks;
 };
 
 SortShape sort_shape(int64_t tokens, int64_t vocab) {
@@ -93,7 +99,9 @@ SortShape sort_shape(int64_t tokens, int64_t vocab) {
     while ((int64_t(1) << s.bits) <= vocab) ++s.bits;       // keys 0 .. vocab
     s.passes = (s.bits + kMaxDigit - 1) / kMaxDigit;
     s.digit = (s.bits + s.passes - 1) / s.passes;
-    s.tiles = int((tokens + kTile - 1) / kTile);
+    const int64_t tiles = (tokens + kTile - 1) / kTile;
+    s.tiles = tiles > kMostBlocks ? int((tiles + kMostBlocks - 1) / kMostBlocks) : 1;
+    s.blocks = int((tiles + s.tiles - 1) / s.tiles);
     return s;
 }
 
@@ -156,30 +164,32 @@ __device__ __forceinline__ void fill_rows(const Fill& f, const Ids& ids, int n, 
     }
 }
 
-// counts[tile * kBins + digit]; the first pass marks the rows that occur
-__global__ void __launch_bounds__(kThreads) count_kernel(Ids ids, const uint32_t* keys, int n, int shift,
+// counts[block * kBins + digit]; the first pass marks the rows that occur
+__global__ void __launch_bounds__(kThreads) count_kernel(Ids ids, const uint32_t* keys, int n, int tiles, int shift,
                                                          int digit, uint32_t* counts, Fill fill,
                                                          uint32_t* tickets, int ntickets, uint8_t* used) {
     __shared__ uint32_t bins[kBins];
     dependent_wait();
-    const int tiles = gridDim.x - fill.blocks;
-    if (int(blockIdx.x) >= tiles) {
-        fill_rows(fill, ids, n, blockIdx.x - tiles);
+    const int blocks = gridDim.x - fill.blocks;
+    if (int(blockIdx.x) >= blocks) {
+        fill_rows(fill, ids, n, blockIdx.x - blocks);
         return;
     }
     if (tickets)
-        for (int i = blockIdx.x * kThreads + threadIdx.x; i < ntickets; i += tiles * kThreads) tickets[i] = 0;
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < ntickets; i += blocks * kThreads) tickets[i] = 0;
     const uint32_t mask = (1u << digit) - 1;
     for (int b = threadIdx.x; b <= int(mask); b += kThreads) bins[b] = 0;
     __syncthreads();
-    const int t0 = blockIdx.x * kTile;
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int t0 = (blockIdx.x * tiles + tile) * kTile;
 #pragma unroll
-    for (int r = 0; r < kItems; ++r) {
-        const int i = t0 + r * kThreads + threadIdx.x;
-        if (i < n) {
-            const uint32_t k = keys ? keys[i] : ids.key(i, true);
-            atomicAdd(&bins[(k >> shift) & mask], 1u);
-            if (used && k < uint32_t(ids.vocab)) used[k] = 1;
+        for (int r = 0; r < kItems; ++r) {
+            const int i = t0 + r * kThreads + threadIdx.x;
+            if (i < n) {
+                const uint32_t k = keys ? keys[i] : ids.key(i, true);
+                atomicAdd(&bins[(k >> shift) & mask], 1u);
+                if (used && k < uint32_t(ids.vocab)) used[k] = 1;
+            }
         }
     }
     __syncthreads();
@@ -193,7 +203,7 @@ struct SortShared {
 };
 
 // base[b] = tokens of smaller digits anywhere + tokens of digit b in earlier
-// tiles, from the block's own sums of (earlier tiles, all tiles) for each bin.
+// blocks, from the block's own sums of (earlier blocks, all blocks) for each bin.
 template <typename F>
 __device__ __forceinline__ void digit_bases(SortShared& sh, int nb, F sums) {
     constexpr int B = kBins / kThreads;                 // neighbouring bins of one thread
@@ -245,18 +255,21 @@ __device__ __forceinline__ void tile_ranks(SortShared& sh, const uint32_t (&k)[k
     }
 }
 
-// Counts of the tile's warps become the counts of the warps before each; returns through total(b, n) the tile's.
-template <typename F>
-__device__ __forceinline__ void warp_bases(SortShared& sh, int nb, F total) {
-    for (int b = threadIdx.x; b < nb; b += kThreads) {
-        uint32_t s = 0;
+// Counts of the tile's warps become the counts of the warps before each; of_tile gets the
+// tile's for the digits of this thread, kThreads apart.
+__device__ __forceinline__ void warp_bases(SortShared& sh, int nb, uint32_t (&of_tile)[kBins / kThreads]) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const uint32_t c = sh.warp_count[w][b];
-            sh.warp_count[w][b] = uint16_t(s);
-            s += c;
-        }
-        total(b, s);
+    for (int j = 0; j < kBins / kThreads; ++j) {
+        const int b = threadIdx.x + j * kThreads;
+        uint32_t s = 0;
+        if (b < nb)
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const uint32_t c = sh.warp_count[w][b];
+                sh.warp_count[w][b] = uint16_t(s);
+                s += c;
+            }
+        of_tile[j] = s;
     }
 }
 
@@ -268,47 +281,58 @@ __device__ __forceinline__ void clear_counts(SortShared& sh, int nb) {
 }
 
 __global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t* keys,
-                                                         const uint32_t* vals, int n, int shift,
-                                                         int digit, const uint32_t* counts, int tiles,
+                                                         const uint32_t* vals, int n, int tiles, int shift,
+                                                         int digit, const uint32_t* counts, int blocks,
                                                          uint32_t* keys_out,
                                                          uint32_t* vals_out, Fill fill) {
     __shared__ SortShared sh;
     dependent_wait();
-    if (int(blockIdx.x) >= tiles) {
-        fill_rows(fill, ids, n, blockIdx.x - tiles);
+    if (int(blockIdx.x) >= blocks) {
+        fill_rows(fill, ids, n, blockIdx.x - blocks);
         return;
     }
     const int nb = 1 << digit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     clear_counts(sh, nb);
     digit_bases(sh, nb, [&](int b, uint32_t& mine, uint32_t& total) {
 #pragma unroll 4
-        for (int t = 0; t < tiles; ++t) {
+        for (int t = 0; t < blocks; ++t) {
             const uint32_t c = counts[size_t(t) * kBins + b];
             if (t < int(blockIdx.x)) mine += c;
             total += c;
         }
     });
-    const int t0 = blockIdx.x * kTile + warp * (32 * kItems);
-    uint32_t k[kItems], v[kItems], rank[kItems];
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int start = (blockIdx.x * tiles + tile) * kTile, t0 = start + warp * (32 * kItems);
+        if (start >= n) break;
+        uint32_t k[kItems], v[kItems], rank[kItems];
 #pragma unroll
-    for (int r = 0; r < kItems; ++r) {
-        const int i = t0 + r * 32 + lane;
-        const bool in = i < n;
-        k[r] = in ? (keys ? keys[i] : ids.key(i, false)) : 0;
-        v[r] = in ? (vals ? vals[i] : uint32_t(i)) : 0;
-    }
-    tile_ranks(sh, k, rank, n - t0, shift, nb);
-    __syncthreads();
-    warp_bases(sh, nb, [](int, uint32_t) {});
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kItems; ++r) {
-        if (t0 + r * 32 + lane < n) {
-            const uint32_t d = (k[r] >> shift) & (nb - 1);
-            const uint32_t at = sh.base[d] + sh.warp_count[warp][d] + rank[r];
-            keys_out[at] = k[r];
-            vals_out[at] = v[r];
+        for (int r = 0; r < kItems; ++r) {
+            const int i = t0 + r * 32 + lane;
+            const bool in = i < n;
+            k[r] = in ? (keys ? keys[i] : ids.key(i, false)) : 0;
+            v[r] = in ? (vals ? vals[i] : uint32_t(i)) : 0;
         }
+        tile_ranks(sh, k, rank, n - t0, shift, nb);
+        __syncthreads();
+        uint32_t of_tile[kBins / kThreads];            // tokens of this thread's digits
+        warp_bases(sh, nb, of_tile);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kItems; ++r) {
+            if (t0 + r * 32 + lane < n) {
+                const uint32_t d = (k[r] >> shift) & (nb - 1);
+                const uint32_t at = sh.base[d] + sh.warp_count[warp][d] + rank[r];
+                keys_out[at] = k[r];
+                vals_out[at] = v[r];
+            }
+        }
+        if (tile + 1 == tiles) break;
+        __syncthreads();                               // the bases and counts have been read
+#pragma unroll
+        for (int j = 0; j < kBins / kThreads; ++j)
+            if (int(threadIdx.x) + j * kThreads < nb) sh.base[threadIdx.x + j * kThreads] += of_tile[j];
+        clear_counts(sh, nb);
+        __syncthreads();
     }
 }
 
@@ -607,7 +631,7 @@ GradLayout grad_layout(int64_t tokens, int64_t vocab, int64_t hidden) {
     g.vals = at;
     at += 2 * up(size_t(tokens) * 4);
     g.counts = at;
-    at += up(size_t(g.sort.tiles) * kBins * 4);
+    at += up(size_t(g.sort.blocks) * kBins * 4);
     g.partial = at;
     at += up(size_t(g.pieces) * 2 * size_t(hidden) * 4);
     g.tickets = at;                 // three for each piece and block of columns, of four elements a thread at least
@@ -677,13 +701,13 @@ int run_grad(const Ids& ids, int64_t tokens, const S* d_out, int64_t d_ld, D* d_
             const uint32_t* kin = p ? keys[(p - 1) & 1] : nullptr;
             const uint32_t* vin = p ? vals[(p - 1) & 1] : nullptr;
             Fill f = next_fill(p ? kFillBesideSort : 0);         // the first launch finds out which rows occur
-            if (int rc = launch_dependent(count_kernel, dim3(unsigned(g.sort.tiles + f.blocks)), kThreads, 0, st, ids,
-                                          kin, n, p * g.sort.digit, g.sort.digit, counts, f, p ? nullptr : tickets,
+            if (int rc = launch_dependent(count_kernel, dim3(unsigned(g.sort.blocks + f.blocks)), kThreads, 0, st, ids,
+                                          kin, n, g.sort.tiles, p * g.sort.digit, g.sort.digit, counts, f, p ? nullptr : tickets,
                                           3 * g.pieces * slabs, p ? nullptr : used))
                 return rc;
             f = next_fill(kFillBesideSort);
-            if (int rc = launch_dependent(place_kernel, dim3(unsigned(g.sort.tiles + f.blocks)), kThreads, 0, st, ids,
-                                          kin, vin, n, p * g.sort.digit, g.sort.digit, counts, g.sort.tiles,
+            if (int rc = launch_dependent(place_kernel, dim3(unsigned(g.sort.blocks + f.blocks)), kThreads, 0, st, ids,
+                                          kin, vin, n, g.sort.tiles, p * g.sort.digit, g.sort.digit, counts, g.sort.blocks,
                                           keys[p & 1], vals[p & 1], f))
                 return rc;
         }
