@@ -20,6 +20,7 @@
 #include "fp8z_elem.cuh"
 #include "fp8z_host.h"
 #include "fp8z_launch.cuh"
+#include "fp8z_tiles.h"
 
 namespace fp8z {
 namespace {
@@ -488,21 +489,17 @@ __global__ void __launch_bounds__(kThreads, 3) runs_kernel(const uint32_t* keys,
                     if (has(j)) __stcg(p + j * kStep, acc[j]);
             }
         }
-        // the run's first and last piece: 32 borders of pieces at a time
+        // the run's first and last piece: the keys are sorted, so a border of pieces inside the
+        // run is one with its key on the other side
         const int lane = threadIdx.x & 31;
-        int first = piece, last = piece;
-        for (int more = 32; more == 32;) {
-            const int64_t border = int64_t(last + lane + 1) * piece_len;
-            more = __ffs(~__ballot_sync(0xFFFFFFFFu, border < n && keys[border] == key)) - 1;
-            more = more < 0 ? 32 : more;
-            last += more;
-        }
-        for (int more = 32; more == 32;) {
-            const int border = (first - lane) * piece_len;
-            more = __ffs(~__ballot_sync(0xFFFFFFFFu, border > 0 && keys[border - 1] == key)) - 1;
-            more = more < 0 ? 32 : more;
-            first -= more;
-        }
+        const int last = piece + run_length((n - 1) / piece_len - piece, [&](int from, int step, int end) {
+            const int q = from + step * lane;
+            return __popc(__ballot_sync(0xFFFFFFFFu, q < end && keys[(piece + q) * piece_len] == key));
+        });
+        const int first = piece - run_length(piece, [&](int from, int step, int end) {
+            const int q = from + step * lane;
+            return __popc(__ballot_sync(0xFFFFFFFFu, q < end && keys[(piece - q + 1) * piece_len - 1] == key));
+        });
         // whether this block is the last of `others` + 1 to arrive at a ticket
         auto arrive = [&](uint32_t* ticket, int others) {
             __threadfence();

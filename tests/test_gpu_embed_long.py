@@ -55,3 +55,20 @@ def test_equal_words_keep_the_list_s_order():
     ids = torch.randint(0, vocab, (n,), generator=g, device="cuda")
     order = torch.argsort(ids, stable=True)
     assert torch.equal(_grad(ids, d, vocab), _grad(ids[order], d[order], vocab))
+
+
+@pytest.mark.parametrize("tokens", [262144 + 7, (1 << 21) + 5])
+@pytest.mark.parametrize("words", [1, 2, 3, 40])
+def test_runs_over_thousands_of_pieces(tokens, words):
+    """Whole numbers again, a few words for the whole list, among 1000."""
+    g = torch.Generator(device="cuda").manual_seed(tokens + words)
+    ids = torch.randint(0, words, (tokens,), generator=g, device="cuda") * 17 + 3
+    d = torch.randint(-4, 5, (tokens, 24), generator=g, device="cuda").to(torch.bfloat16)
+    want = torch.zeros(1000, 24, dtype=torch.float64, device="cuda").index_add_(0, ids, d.double())
+    assert torch.equal(_grad(ids, d, 1000).double(), want)
+    # all but a few tokens one word, the others around it
+    ids = torch.full((tokens,), 500, device="cuda")
+    ids[::100003] = 499
+    ids[1::100003] = 501
+    want = torch.zeros(1000, 24, dtype=torch.float64, device="cuda").index_add_(0, ids, d.double())
+    assert torch.equal(_grad(ids, d, 1000).double(), want)
