@@ -95,7 +95,7 @@ __device__ __forceinline__ double block_sum(double v) {
 
 __device__ __forceinline__ float2 norm_and_coef(double sum, float grad_scale, float max_norm, float eps) {
     const float nm = float(fabs(double(grad_scale)) * sqrt(sum));
-    const float c = max_norm / (nm + eps);         // NaN stays NaN; an infinite limit never clips
+    const float c = max_norm / (nm + eps);         // NaN stays NaN; an infinite limit never clips, whatever the norm
     return make_float2(nm, isinf(max_norm) || c >= 1.0f ? 1.0f : c);
 }
 

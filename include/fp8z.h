@@ -451,19 +451,19 @@ FP8Z_API int fp8z_encode_tensor_list(const void *const *srcs, void *const *dsts,
                                      fp8z_tensor_chunk *out, int64_t capacity, int64_t *chunks_out);
 
 /*
- * fp8z_grad_norm -- norm[0] = |grad_scale| * sqrt(sum of g^2 over every element
- * of every src of the list), norm[1] = 1.  Squares are FP32 (an element beyond
- * 1.8e19 makes the norm infinite), sums FP64 in a fixed order: the same list
- * gives the same bits.  An empty list has norm 0.  list: device,
- * fp8z_tensor_chunk[chunks]; norm: device f32[2]; workspace: device,
- * FP8Z_GRAD_NORM_WORKSPACE bytes.
+ * fp8z_grad_norm -- norm[0] = |grad_scale| * sqrt(sum of g^2 over every element of
+ * every src of the list), norm[1] = 1.  Squares are FP32 (an element beyond 1.8e19
+ * makes the norm infinite, one below 1e-19 counts with fewer bits and one below
+ * 2.6e-23 not at all), sums FP64 in a fixed order: the same list gives the same
+ * bits.  An empty list has norm 0.  list: device, fp8z_tensor_chunk[chunks]; norm:
+ * device f32[2]; workspace: device, FP8Z_GRAD_NORM_WORKSPACE bytes.
  *
- * fp8z_grad_clip -- the same, then norm[1] = coef = min(1, max_norm /
- * (norm[0] + eps)) (1 when max_norm is infinite) and
- * dst = (grad_scale * coef) * g for every element, rounded once to dst's type.
- * Everything stays on the device: an infinite norm gives coef 0 and a NaN gives
- * NaN everywhere, so the caller can tell from norm[0] that a step is lost.  In
- * place with grad_scale * coef == 1, nothing is written.
+ * fp8z_grad_clip -- the same, then norm[1] = coef = min(1, max_norm / (norm[0] +
+ * eps)) (1 when max_norm is infinite) and dst = (grad_scale * coef) * g for every
+ * element, rounded once to dst's type. Everything stays on the device: with a finite
+ * max_norm an infinite norm gives coef 0 and a NaN gives NaN everywhere; with an
+ * infinite one coef is 1 whatever the norm. The caller can tell from norm[0] that a
+ * step is lost.  In place with grad_scale * coef == 1, nothing is written.
  * Returns FP8Z_OK / EINVAL / EALIGN / EUNSUPPORTED / ECUDA.
  */
 FP8Z_API int fp8z_grad_norm(const fp8z_tensor_chunk *list, int64_t chunks, float grad_scale, float *norm,
@@ -482,17 +482,18 @@ FP8Z_API int fp8z_embedding(const void *ids, int32_t ids_dtype, int64_t tokens, 
                             int32_t out_dtype, int64_t out_ld, float scale, int32_t *dev_status, void *stream);
 
 /*
- * fp8z_embedding_grad -- d_table[v][:] = scale * (sum of d_out[t][:] over the
- * tokens t with ids[t] == v), in FP32, in an order that the ids give, rounded once; rows
- * without a token are written as zeros.  With accumulate = 1 the sum is added
- * to d_table instead and rows without a token are not touched.  Tokens whose id
- * is padding_idx give no gradient (-1: no padding), and tokens whose id is
- * outside [0, vocab) none either, with FP8Z_EINVAL in *dev_status.  The tokens
- * are sorted by id, and runs of equal ids are summed piece by piece: no
- * floating-point atomics, the same bits every time.  workspace: device,
- * fp8z_embedding_grad_workspace(tokens, vocab, hidden) bytes, no
- * initialisation.  tokens, vocab <= 2^30, hidden <= 2^23, tokens * hidden about
- * 2^43 at most.
+ * fp8z_embedding_grad -- d_table[v][:] = scale * (sum of d_out[t][:] over the tokens
+ * t with ids[t] == v), in FP32, in an order that the ids give, rounded once; rows
+ * without a token are written as zeros.  With accumulate = 1 the sum is added to
+ * d_table instead and rows without a token are not touched; an FP32 d_table is added
+ * to by the memory system, which takes subnormal numbers (below 1.2e-38, in d_table,
+ * in the sum and in the result) for zero.  Tokens whose id is padding_idx give no
+ * gradient (-1: no padding), and tokens whose id is outside [0, vocab) none either,
+ * with FP8Z_EINVAL in *dev_status.  The tokens are sorted by id, and runs of equal
+ * ids are summed piece by piece, in the order of the list; each element of d_table
+ * is written or added to once: the same bits every time.  workspace: device,
+ * fp8z_embedding_grad_workspace(tokens, vocab, hidden) bytes, no initialisation.
+ * tokens, vocab <= 2^30, hidden <= 2^23, tokens * hidden about 2^43 at most.
  */
 FP8Z_API int64_t fp8z_embedding_grad_workspace(int64_t tokens, int64_t vocab, int64_t hidden);
 FP8Z_API int fp8z_embedding_grad(const void *ids, int32_t ids_dtype, int64_t tokens, const void *d_out,
