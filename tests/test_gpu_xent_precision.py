@@ -188,3 +188,21 @@ def test_fp32_dw_is_added_up_in_short_sums(n, dtype):
     # the target's row: 255 / 256 in two parts of dtype, taken away
     want = -x.double().sum(0) * (255 / 256)
     assert bool(((dw[0].double() - want).abs() <= (bound + UNIT[dtype] ** 2) * want.abs()).all())
+
+
+def test_more_tokens_than_2_to_23():
+    """An FP32 dw over 131074 blocks of K, in sums of 8.  w = 0, every target word 0: P is 2^-8,
+    or 2^-8 - 1, and x whole numbers of -2 to 2, so that every sum is one that FP32 holds: equal."""
+    n, h, v = (1 << 23) + 130, 64, 256
+    x = torch.randint(-2, 3, (n, h), generator=_gen(5), device="cuda", dtype=torch.int8).to(BF16)
+    w = torch.zeros(v, h, dtype=BF16, device="cuda")
+    t = torch.zeros(n, dtype=torch.int32, device="cuda")
+    loss, total = torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty(v, h, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(fp8z.fp8z_linear_xent_workspace(x, w, dw=dw), dtype=torch.uint8, device="cuda")
+    fp8z.fp8z_linear_xent_grad(x, w, t, loss, total, dx, dw, ws, reduction="sum", dev_status=status)
+    assert status.item() == 0 and not dx.any() and total[1].item() == n
+    s = torch.stack([part.double().sum(0) for part in x.split(1 << 20)]).sum(0)
+    assert torch.equal(dw[1:].double(), (s / 256).expand(v - 1, h))
+    assert torch.equal(dw[0].double(), s / 256 - s)
