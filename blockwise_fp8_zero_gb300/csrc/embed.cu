@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const void* ids, int w
 // among equal digits of its own tile).  Ids that take no gradient (padding, out of
 // range) get the key `vocab`, which sorts last.  Every block walks over the counts of
 // all blocks, work that would grow with the square of the tokens (2^24: 275 GB a pass),
-// so their number is bounded: 4194304 tokens x 8 take 5.07 ms for 7.33 with a block for
-// each tile (512 blocks 5.13, 128 5.14; 1048576 tokens 1.03, 1.13 and 1.00 for 1.13).
+// so their number is bounded: 4194304 tokens x 8 take 4.05 ms, with 512 or 128 blocks
+// 0.07 more, with 1024 0.66 and with a block for each tile 2.27.
 constexpr int kItems = 8;
 constexpr int kTile = kThreads * kItems;
 constexpr int kWarps = kThreads / 32;
@@ -293,6 +293,18 @@ __global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t
         return;
     }
     const int nb = 1 << digit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int begin = blockIdx.x * tiles * kTile, first = begin + warp * (32 * kItems) + lane;
+    uint32_t k[kItems], v[kItems];
+    auto load = [&](int tile) {                        // the first tile's come in while the counts are read
+#pragma unroll
+        for (int r = 0; r < kItems; ++r) {
+            const int i = first + tile * kTile + r * 32;
+            const bool in = i < n;
+            k[r] = in ? (keys ? keys[i] : ids.key(i, false)) : 0;
+            v[r] = in ? (vals ? vals[i] : uint32_t(i)) : 0;
+        }
+    };
+    load(0);
     clear_counts(sh, nb);
     digit_bases(sh, nb, [&](int b, uint32_t& mine, uint32_t& total) {
 #pragma unroll 4
@@ -303,16 +315,8 @@ __global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t
         }
     });
     for (int tile = 0; tile < tiles; ++tile) {
-        const int start = (blockIdx.x * tiles + tile) * kTile, t0 = start + warp * (32 * kItems);
-        if (start >= n) break;
-        uint32_t k[kItems], v[kItems], rank[kItems];
-#pragma unroll
-        for (int r = 0; r < kItems; ++r) {
-            const int i = t0 + r * 32 + lane;
-            const bool in = i < n;
-            k[r] = in ? (keys ? keys[i] : ids.key(i, false)) : 0;
-            v[r] = in ? (vals ? vals[i] : uint32_t(i)) : 0;
-        }
+        const int start = begin + tile * kTile, t0 = start + warp * (32 * kItems);
+        uint32_t rank[kItems];
         tile_ranks(sh, k, rank, n - t0, shift, nb);
         __syncthreads();
         uint32_t of_tile[kBins / kThreads];            // tokens of this thread's digits
@@ -327,7 +331,8 @@ __global__ void __launch_bounds__(kThreads) place_kernel(Ids ids, const uint32_t
                 vals_out[at] = v[r];
             }
         }
-        if (tile + 1 == tiles) break;
+        if (tile + 1 == tiles || start + kTile >= n) break;
+        load(tile + 1);
         __syncthreads();                               // the bases and counts have been read
 #pragma unroll
         for (int j = 0; j < kBins / kThreads; ++j)
