@@ -48,7 +48,7 @@ constexpr int kThreads = 128 + 32 * kReaders;          // warps 0 and 3 load A a
 // of K: logits of hidden 7168 (448 steps) came out so far off that the loss was 4e-6
 // off (FP32 products: 8e-7), an FP32 dw of 4096 tokens (512 steps, two parts) 1e-5.
 // So the sums of the logits and of an FP32 dw leave tensor memory after some blocks of
-// K and are added up, rounded, in the readers' registers: loss 7e-7 off, dw 2.3e-6,
+// K and are added up, rounded, in the readers' registers: loss 7e-7 off, dw 2.1e-6,
 // of which the two parts of P make up 1.7e-6.  That takes 3 % of the loss's time (4 with
 // 16 blocks of K for the logits, 2.5 with 32 and 9e-7) and 1 to 2 of the gradient's.
 // A dx and a dw of 16 bits need less, but not nothing: 8192 steps (131072 words, or as many
