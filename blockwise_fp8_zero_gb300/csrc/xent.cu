@@ -307,7 +307,7 @@ __device__ __forceinline__ void epilogue_sum(const MmaArgs& A, const CUtensorMap
     }
 }
 
-// A dw whose rows do not all start on 16-byte boundaries, and sums of 16-bit
+// A dw whose rows do not all start and end on 16-byte boundaries, and sums of 16-bit
 // gradients (one rounding of the whole sum): 32 columns of the warp's 32 rows
 // pass through its slab, so that the threads write along the rows.
 template <typename T>
@@ -1334,14 +1334,17 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
     if (!grad) return FP8Z_OK;
 
     auto* sum = reinterpret_cast<float*>(ws + L.sum);
-    const bool dw_rows = host::aligned(dw, 16) && (a.dw_ld * dtype_bytes(a.dw_dtype)) % 16 == 0;
+    // dw leaves in tiles where its rows start and end on 16-byte boundaries: a tile's store writes
+    // whole 16 bytes, and what lies behind a row that ends between two is not ours
+    const int64_t dw_bytes = dtype_bytes(a.dw_dtype);
+    const bool dw_tiles = host::aligned(dw, 16) && a.dw_ld * dw_bytes % 16 == 0 && a.hidden * dw_bytes % 16 == 0;
     const bool blocks = L.hidden_pad % 64 == 0;
     CUtensorMap p_k, w_mn, p_mn, x_mn, p_out, sum_out, dw_out = x_k;
     if (!map_p(&p_k, p, L.piece, n, kHalf) || !map_columns(&w_mn, wp, L.hidden_pad, vocab, w_ld, blocks) ||
         !map_p_columns(&p_mn, p, L.piece, n) || !map_columns(&x_mn, ws + L.kept_x, L.kept_ld, n, L.kept_ld, true) ||
         !map_p(&p_out, p, L.piece, n, 32) || !map_sum(&sum_out, sum, L.hidden_pad, n, L.splits))
         return FP8Z_ECUDA;
-    if (dw_rows && !(a.dw_dtype == FP8Z_F32 ? map_f32(&dw_out, dw, hidden, vocab, a.dw_ld)
+    if (dw_tiles && !(a.dw_dtype == FP8Z_F32 ? map_f32(&dw_out, dw, hidden, vocab, a.dw_ld)
                                             : map_16(&dw_out, dw, hidden, vocab, a.dw_ld, 32)))
         return FP8Z_ECUDA;
     for (int64_t i = L.pieces - 1; i >= 0; --i) {
@@ -1383,7 +1386,7 @@ int run(const void* x, const void* w, const void* targets, const fp8z_xent_args*
         W.out_ld = a.dw_ld;
         W.out_dtype = a.dw_dtype;
         W.accumulate = a.accumulate_dw;
-        W.staged = dw_rows && (a.dw_dtype == FP8Z_F32 || !a.accumulate_dw);
+        W.staged = dw_tiles && (a.dw_dtype == FP8Z_F32 || !a.accumulate_dw);
         W.alpha = alpha;
         W.b_blocks = 1;
         W.kb = (n + kBK - 1) / kBK;
