@@ -27,6 +27,7 @@ FP8Z_SCALE_EXACT, FP8Z_SCALE_POW2 = 0, 1
 FP8Z_DECAY_PRE, FP8Z_DECAY_POST = 0, 1
 FP8Z_F32, FP8Z_BF16, FP8Z_F16, FP8Z_I32, FP8Z_I64 = 0, 1, 2, 3, 4
 FP8Z_MEAN, FP8Z_SUM = 0, 1
+FP8Z_GROUP_ROWS, FP8Z_GROUP_K = 0, 1
 GRAD_NORM_WORKSPACE = 32768  # FP8Z_GRAD_NORM_WORKSPACE
 
 # numpy views of the ABI structs (include/fp8z.h)
@@ -59,6 +60,7 @@ EXPORTED = ("fp8z_plan_shards", "fp8z_adamw_requant_step", "fp8z_adamw_requant_s
             "fp8z_encode_tensor_list", "fp8z_grad_norm", "fp8z_grad_clip",
             "fp8z_embedding", "fp8z_embedding_grad", "fp8z_embedding_grad_workspace",
             "fp8z_linear_xent", "fp8z_linear_xent_grad", "fp8z_linear_xent_workspace",
+            "fp8z_matmul", "fp8z_matmul_workspace",
             "fp8z_e4m3_encode_bits",
             "fp8z_watchdog_selftest", "fp8z_set_wait_limit_ns", "fp8z_get_wait_limit_ns",
             "fp8z_status_string")
@@ -87,6 +89,20 @@ class fp8z_xent_args(ctypes.Structure):
 
 
 assert ctypes.sizeof(fp8z_xent_args) == 88
+
+
+class fp8z_matmul_args(ctypes.Structure):
+    _fields_ = [
+        ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+        ("a_ld", ctypes.c_int64), ("b_ld", ctypes.c_int64), ("out_ld", ctypes.c_int64),
+        ("a_scale_ld", ctypes.c_int64), ("b_scale_ld", ctypes.c_int64), ("b_group", ctypes.c_int64),
+        ("b_scale_group", ctypes.c_int64), ("out_group", ctypes.c_int64), ("b_scale_rows", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("groups", ctypes.c_int32),
+        ("group_by", ctypes.c_int32), ("offsets_dtype", ctypes.c_int32),
+    ]
+
+
+assert ctypes.sizeof(fp8z_matmul_args) == 112
 
 
 def hparams(lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=1,
@@ -146,6 +162,9 @@ def lib():
         L.fp8z_linear_xent_workspace.argtypes = [P, P, XA, i32, i64]
         L.fp8z_linear_xent.argtypes = [P, P, P, XA, P, P, P, P, i64, P, P]
         L.fp8z_linear_xent_grad.argtypes = [P, P, P, XA, P, P, P, P, P, P, i64, P, P]
+        MA = ctypes.POINTER(fp8z_matmul_args)
+        L.fp8z_matmul_workspace.argtypes = [P, P, MA]
+        L.fp8z_matmul.argtypes = [P, P, P, P, MA, P, P, P, i64, P, P]
         L.fp8z_e4m3_encode_bits.argtypes = [ctypes.c_uint32, i64, P, P]
         L.fp8z_watchdog_selftest.argtypes = [P, i64, P]
         L.fp8z_set_wait_limit_ns.argtypes = [i64]
@@ -158,6 +177,7 @@ def lib():
         L.fp8z_get_wait_limit_ns.restype = i64
         L.fp8z_embedding_grad_workspace.restype = i64
         L.fp8z_linear_xent_workspace.restype = i64
+        L.fp8z_matmul_workspace.restype = i64
         _lib = L
     return _lib
 
@@ -741,6 +761,97 @@ def fp8z_linear_xent_grad(x, w, targets, loss, total, dx, dw, workspace, ignore_
                                      workspace.numel() * workspace.element_size(),
                                      _flat(dev_status, "dev_status", here, FP8Z_I32), _stream_handle(stream))
     _check("fp8z_linear_xent_grad", rc)
+
+
+# ------------------------------- operators of a layer with FP8 weights
+def _bank(t, name, device):
+    """(pointer, groups, rows, cols, row stride, group stride) of a CUDA tensor [rows, cols]
+    (groups 0) or [groups, rows, cols] whose rows are contiguous and do not overlap."""
+    if t.dim() != 3:
+        return (*_matrix(t, name, device), 0)
+    if t.shape[0] == 0:
+        raise ValueError(f"{name} must have a group")
+    p, rows, cols, ld = _matrix(t[0], name, device)
+    step = t.stride(0)
+    if t.shape[0] == 1:
+        step = rows * ld
+    if rows > 0 and cols > 0 and step < (rows - 1) * ld + cols:
+        raise ValueError(f"{name}'s groups must not overlap")
+    return p, rows, cols, ld, step
+
+
+def _matmul_args(a, a_scale, b, b_scale, out, offsets, accumulate):
+    """(a pointer, a_scale pointer, b pointer, b_scale pointer, out pointer, filled fp8z_matmul_args)."""
+    here = _current_device()
+    ap, m, k, a_ld = _matrix(a, "a", here)
+    bp, n, bk, b_ld, b_group = _bank(b, "b", here)
+    op, om, on, out_ld, out_group = _bank(out, "out", here)
+    code = _dtype_code(out, "out")
+    if str(a.dtype) != "torch.uint8" or str(b.dtype) != "torch.uint8":
+        raise ValueError(f"a and b must be uint8 E4M3 codes, got {a.dtype} and {b.dtype}")
+    if bk != k or (om, on) != (m, n):
+        raise ValueError(f"a [.., {k}] and out [.., {m}, {on}] need b [.., {on}, {k}], got {list(b.shape)} and out {list(out.shape)}")
+    banks, grads = b.dim() == 3, out.dim() == 3
+    if (offsets is None) == (banks or grads) or (banks and grads):
+        raise ValueError("offsets go with a b [groups, n, k] or with an out [groups, m, n]")
+    groups = b.shape[0] if banks else out.shape[0] if grads else 0
+    args = fp8z_matmul_args(m, n, k, a_ld, b_ld, out_ld, 0, 0, b_group if banks else 0, 0, out_group if grads else 0, BLOCK,
+                            code, int(bool(accumulate)), groups, FP8Z_GROUP_K if grads else FP8Z_GROUP_ROWS, FP8Z_I32)
+    kb = -(-k // BLOCK)
+    if offsets is not None:
+        if offsets.numel() != groups + 1:
+            raise ValueError(f"offsets must hold {groups + 1} numbers, got {offsets.numel()}")
+        args.offsets_dtype = _dtype_code(offsets, "offsets", _INTS)
+    sp = tp = None
+    if a_scale is not None:
+        sp, rows, cols, args.a_scale_ld = _matrix(a_scale, "a_scale", here)
+        if (rows, cols) != (m, kb) or _dtype_code(a_scale, "a_scale", (FP8Z_F32,)) != FP8Z_F32:
+            raise ValueError(f"a_scale must be [{m}, {kb}], got {list(a_scale.shape)}")
+        tp, rows, cols, args.b_scale_ld, step = _bank(b_scale, "b_scale", here)
+        blocks = -(-n // BLOCK)
+        if b_scale.dim() != b.dim() or (banks and b_scale.shape[0] != groups) or cols != kb or rows not in (blocks, n) \
+                or _dtype_code(b_scale, "b_scale", (FP8Z_F32,)) != FP8Z_F32:
+            raise ValueError(f"b_scale must be [{blocks}, {kb}] (blocks) or [{n}, {kb}] (rows), for each group of b, "
+                             f"got {list(b_scale.shape)}")
+        args.b_scale_rows = BLOCK if rows == blocks and not (grads and rows == n) else 1
+        args.b_scale_group = step if banks else 0
+        if groups and (args.b_scale_rows == 1) != grads:
+            raise ValueError("groups of rows take b_scale in blocks, groups of columns in rows")
+    return ap, sp, bp, tp, op, args
+
+
+def fp8z_matmul_workspace(a, b, out, offsets=None):
+    """Bytes of workspace fp8z_matmul(a, .., b, .., out, offsets) needs: 0 where a and b
+    start on 16-byte boundaries and have row strides of whole 16 bytes."""
+    ap, _, bp, _, _, args = _matmul_args(a, None, b, None, out, offsets, False)
+    # the scales are not looked at: as they are without strides
+    args.a_scale_ld = args.b_scale_ld = -(-args.k // BLOCK)
+    args.b_scale_group = args.n * args.b_scale_ld
+    args.b_scale_rows = 1 if args.groups and args.group_by == FP8Z_GROUP_K else BLOCK
+    size = int(lib().fp8z_matmul_workspace(ap, bp, ctypes.byref(args)))
+    if size < 0:
+        raise Fp8zError("fp8z_matmul_workspace", size)
+    return size
+
+
+def fp8z_matmul(a, a_scale, b, b_scale, out, offsets=None, accumulate=False, workspace=None, dev_status=None, stream=None):
+    """out[i][j] = sum over blocks c of 128 columns of a_scale[i][c] * b_scale[j'][c] *
+    sum_k a[i][k] * b[j][k], or that sum added to out (accumulate, float32 only).
+
+    a, b: uint8 E4M3 codes [m, k], [n, k], rows may be strided; a_scale float32 [m,
+    ceil(k/128)]; b_scale float32 [ceil(n/128), ceil(k/128)] (a weight's 128x128 blocks) or
+    [n, ceil(k/128)] (row-wise); out [m, n] float32 / bfloat16 / float16.  Banks of experts:
+    b [groups, n, k] and b_scale [groups, ceil(n/128), ..] with the first row of each group
+    in offsets (groups + 1 numbers, int32 or int64, on the device), or out [groups, m, n]
+    with the first column of each group in offsets (multiples of 128).  workspace: see
+    fp8z_matmul_workspace."""
+    here = _current_device()
+    ap, sp, bp, tp, op, args = _matmul_args(a, a_scale, b, b_scale, out, offsets, accumulate)
+    rc = lib().fp8z_matmul(ap, sp, bp, tp, ctypes.byref(args), _flat(offsets, "offsets", here), op,
+                           _flat(workspace, "workspace", here),
+                           0 if workspace is None else workspace.numel() * workspace.element_size(),
+                           _flat(dev_status, "dev_status", here, FP8Z_I32), _stream_handle(stream))
+    _check("fp8z_matmul", rc)
 
 
 def fp8z_e4m3_encode_bits(first_bits, n, out, stream=None):

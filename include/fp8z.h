@@ -562,6 +562,69 @@ FP8Z_API int fp8z_linear_xent_grad(const void *x, const void *w, const void *tar
                                    int64_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * The entry points from here to fp8z_adamw are the operators of a layer whose
+ * weights the FP8 step keeps: the products its codes are multiplied in, the norm
+ * that writes their other operand, and the step of the parameters that are not
+ * kept in FP8 blocks.  Conventions as above.
+ */
+
+typedef enum { FP8Z_GROUP_ROWS = 0, FP8Z_GROUP_K = 1 } fp8z_group;
+
+/* Shapes and options of fp8z_matmul. */
+typedef struct {
+    int64_t m, n, k;                    /* rows of a, rows of b, length of both's rows           */
+    int64_t a_ld, b_ld, out_ld;         /* row strides in elements                               */
+    int64_t a_scale_ld, b_scale_ld;     /* row strides of the scales, in floats                  */
+    int64_t b_group, b_scale_group;     /* FP8Z_GROUP_ROWS: from one group's b (scales) to the
+                                           next, in elements (floats)                            */
+    int64_t out_group;                  /* FP8Z_GROUP_K: from one group's out to the next        */
+    int32_t b_scale_rows;               /* rows of b that share a scale: 128 (blocks) or 1       */
+    int32_t out_dtype;                  /* FP8Z_F32, FP8Z_BF16 or FP8Z_F16                       */
+    int32_t accumulate;                 /* 1: added to out (FP8Z_F32 only), 0: out is overwritten */
+    int32_t groups;                     /* 0: one product; up to 256 groups                      */
+    int32_t group_by;                   /* fp8z_group                                            */
+    int32_t offsets_dtype;              /* FP8Z_I32 or FP8Z_I64                                  */
+} fp8z_matmul_args;                     /* 112 bytes */
+
+/*
+ * fp8z_matmul -- product of two E4M3 matrices with FP32 scales:
+ *   out[i][j] (+)= sum_c a_scale[i][c] * b_scale[j / b_scale_rows][c] * S(i, j, c),
+ *   S(i, j, c) = sum of a[i][k] * b[j][k] over k in [128 c, 128 c + 128).
+ * a: device u8 [m, k] with a_scale f32 [m, ceil(k/128)], as fp8z_quantize_rowwise and
+ * fp8z_layer_norm write them; b: device u8 [n, k].  With b_scale_rows = 128, b_scale is
+ * f32 [ceil(n/128), ceil(k/128)]: the row-major weights and inverse scales of
+ * fp8z_adamw_requant_step_rowmajor (x W^T), or its column-major copy and transposed
+ * scale grid (dy W).  With b_scale_rows = 1 it is f32 [n, ceil(k/128)]: the column-wise
+ * layouts of fp8z_transpose_rowwise (dy^T x).  Codes are multiplied on the tensor cores;
+ * each S is an FP32 sum of the tensor cores (cut off, not rounded, at 32 of K), scaled
+ * and added up in FP32 with rounding, and the result is rounded once to out_dtype.  An
+ * FP32 out that is added to may be added to by the memory system, which takes
+ * subnormal numbers (below 1.2e-38) for zero.  A NaN code or scale reaches the results that it
+ * enters.  Every element has one fixed order: the same arguments give the same bits.
+ *
+ * Groups (a bank of experts): offsets is a device array of groups + 1 numbers that do
+ * not fall.
+ *   FP8Z_GROUP_ROWS: rows offsets[g] .. offsets[g + 1] of a and out belong to group g,
+ *     whose weight is b + g * b_group; other rows of out are left as they are.  The
+ *     last offset is at most m.  b_scale_rows is 128.
+ *   FP8Z_GROUP_K: columns offsets[g] .. offsets[g + 1] of a and b are group g's, whose
+ *     result is out + g * out_group (zeros, or unchanged with accumulate, where a group
+ *     is empty).  Offsets are multiples of 128, or k.  b_scale_rows is 1.
+ * Offsets that break these rules give FP8Z_EINVAL in *dev_status, and nothing is written.
+ *
+ * fp8z_matmul_workspace -- bytes of workspace (device, 256-byte aligned, no
+ * initialisation): 0 where a and b start on 16-byte boundaries and their strides are
+ * multiples of 16; other operands are copied there first.
+ * m, n, k <= 2^30, and at most 2^26 tiles of 16 x 128 in m x n (times the groups).
+ * k = 0 gives zeros; it is refused with FP8Z_GROUP_ROWS.
+ * Returns FP8Z_OK / EINVAL / EALIGN / ENOSPACE / EUNSUPPORTED / ECUDA.
+ */
+FP8Z_API int64_t fp8z_matmul_workspace(const void *a, const void *b, const fp8z_matmul_args *args);
+FP8Z_API int fp8z_matmul(const void *a, const float *a_scale, const void *b, const float *b_scale,
+                         const fp8z_matmul_args *args, const void *offsets, void *out, void *workspace,
+                         int64_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
  * fp8z_e4m3_encode_bits -- out[i] = E4M3 code (round to nearest even,
  * saturating, as in the step) of the float whose bit pattern is
  * first_bits + i, for i < n; n a multiple of 4, out device, 16-byte aligned.
