@@ -1,0 +1,579 @@
+// layernorm.cu -- layer norm, optionally into the row-wise E4M3 operand of a product, and
+// its gradient.
+//
+//   mean = sum x / n,  rstd = 1 / sqrt(sum (x - mean)^2 / n + eps),  xh = (x - mean) rstd
+//   y  = xh w + b
+//   dx = rstd (g - sum g / n - xh sum (g xh) / n),  g = dy w
+//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// A row is read once and waits in registers for its two sums; what bounds both
+// directions is memory traffic.  Rows longer than the registers hold are read again.
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "fp8z.h"
+#include "fp8z_device.cuh"
+#include "fp8z_elem.cuh"
+#include "fp8z_host.h"
+#include "fp8z_launch.cuh"
+
+namespace fp8z {
+namespace {
+
+constexpr int kVec = 8;                       // columns a thread takes together
+
+struct Norm {
+    int rows, cols;
+    const void* x;
+    int64_t x_ld;
+    const void* weight;       // nullptr: 1
+    const void* bias;         // nullptr: 0
+    int param_dtype;
+    void* y;
+    int64_t y_ld;
+    float* mean;
+    float* rstd;
+    float eps;
+    uint8_t* q;
+    float* q_scale;
+    int pow2;
+};
+
+struct NormGrad {
+    int rows, cols;
+    const void* dy;
+    const void* x;
+    int64_t dy_ld, x_ld, dx_ld;
+    const void* weight;
+    int param_dtype;
+    const float* mean;
+    const float* rstd;
+    void* dx;
+    float* part;              // [blocks][2][cols]
+};
+
+// Columns of a thread: kVec neighbours at a time where rows start on 16-byte boundaries
+// (kWide), else single ones kThreads apart, so that a warp's loads stay together.
+template <bool kWide, int kThreads>
+__device__ __forceinline__ int column(int j, int e, int tid) {
+    return kWide ? (j * kThreads + tid) * kVec + e : (j * kVec + e) * kThreads + tid;
+}
+
+template <typename T>
+__device__ __forceinline__ float load_one(const T* p) {
+    if constexpr (sizeof(T) == 4) {
+        float v;
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+        return v;
+    } else {
+        uint16_t u;
+        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(u) : "l"(p) : "memory");
+        return Elem<T>::widen(*reinterpret_cast<T*>(&u));
+    }
+}
+
+// Vector j of a thread's columns; zeros past the row's end.  kStream: read once.
+template <bool kWide, int kThreads, bool kStream, typename T>
+__device__ __forceinline__ void load8(const T* row, int j, int tid, int cols, float (&x)[kVec]) {
+    if constexpr (kWide) {
+        const int c = (j * kThreads + tid) * kVec;
+        if (c + kVec <= cols) {
+            Pack<T, kVec> u;
+            uint4* w = reinterpret_cast<uint4*>(&u);
+#pragma unroll
+            for (int i = 0; i < int(sizeof(T) / 2); ++i) w[i] = kStream ? ld_stream_16(row + c, i) : ld_nc_16(reinterpret_cast<const uint4*>(row + c) + i);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) x[e] = Elem<T>::widen(u.v[e]);
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        const int c = column<kWide, kThreads>(j, e, tid);
+        x[e] = c < cols ? load_one(row + c) : 0.0f;
+    }
+}
+
+template <bool kWide, int kThreads>
+__device__ __forceinline__ void load8_param(const void* p, int dtype, int j, int tid, int cols, float (&x)[kVec]) {
+    if (dtype == FP8Z_F32) load8<kWide, kThreads, false>(static_cast<const float*>(p), j, tid, cols, x);
+    else if (dtype == FP8Z_BF16) load8<kWide, kThreads, false>(static_cast<const __nv_bfloat16*>(p), j, tid, cols, x);
+    else load8<kWide, kThreads, false>(static_cast<const __half*>(p), j, tid, cols, x);
+}
+
+template <bool kWide, int kThreads, typename T>
+__device__ __forceinline__ void store8(T* row, int j, int tid, int cols, const float (&x)[kVec]) {
+    if constexpr (kWide) {
+        const int c = (j * kThreads + tid) * kVec;
+        if (c + kVec <= cols) {
+            Pack<T, kVec> u;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) u.v[e] = Elem<T>::narrow(x[e]);
+            st_vec(row + c, u);
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        const int c = column<kWide, kThreads>(j, e, tid);
+        if (c < cols) row[c] = Elem<T>::narrow(x[e]);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// Sums over a row's threads, the same in each, in a fixed order.  `slot` alternates, so
+// that one barrier a sum is enough.
+template <int kThreads>
+__device__ __forceinline__ float2 row_sum(float a, float b, float2* shared, int slot) {
+    constexpr int kWarps = kThreads / 32;
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if constexpr (kWarps == 1) return make_float2(a, b);
+    float2* s = shared + slot * kWarps;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const int i = threadIdx.x & 31;
+    const float2 v = i < kWarps ? s[i] : make_float2(0.0f, 0.0f);
+    return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+
+// The scale and codes of 128 columns, held by 16 lanes: the rule of fp8z_quantize_rowwise.
+__device__ __forceinline__ float tile_scale(float amax, bool pow2) {
+    if (amax == 0.0f) return 1.0f;
+    const float s = fmaxf(__fdiv_rn(amax, 448.0f), FLT_MIN);
+    if (!pow2) return s;
+    if (amax > FLT_MAX) return __uint_as_float(254u << 23);                        // 2^127
+    // the smallest power of two that is not below amax / 448, from amax = f 2^e, f in [1/2, 1):
+    // 448 = 7/8 * 2^9
+    int e;
+    const float f = frexpf(amax, &e);
+    const int k = max(e - 9 + (f > 0.875f ? 1 : 0), -126);
+    return __uint_as_float(uint32_t(k + 127) << 23);
+}
+
+template <typename T, bool kWide, int kThreads, int kVecs>
+__global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) norm_kernel(const __grid_constant__ Norm A) {
+    constexpr int kGroups = kThreads == 32 ? 8 : 1;                 // rows a block takes together
+    __shared__ float2 shared[2 * (kThreads / 32)];
+    dependent_wait();
+    const int tid = threadIdx.x % kThreads;
+    const float n = float(A.cols);
+    for (int64_t row = int64_t(blockIdx.x) * kGroups + threadIdx.x / kThreads; row < A.rows; row += int64_t(gridDim.x) * kGroups) {
+        const T* px = static_cast<const T*>(A.x) + row * A.x_ld;
+        float x[kVecs][kVec];
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) load8<kWide, kThreads, true>(px, j, tid, A.cols, x[j]);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) sum += x[j][e];
+        const float mean = row_sum<kThreads>(sum, 0.0f, shared, 0).x / n;
+        float sq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                x[j][e] = column<kWide, kThreads>(j, e, tid) < A.cols ? x[j][e] - mean : 0.0f;
+                sq = fmaf(x[j][e], x[j][e], sq);
+            }
+        const float rstd = __frcp_rn(__fsqrt_rn(row_sum<kThreads>(sq, 0.0f, shared, 1).x / n + A.eps));
+        if (tid == 0) {
+            if (A.mean) A.mean[row] = mean;
+            if (A.rstd) A.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            if (column<kWide, kThreads>(j, 0, tid & ~31) >= A.cols) break;              // the whole warp is past the end
+            float w[kVec], b[kVec];
+            if (A.weight) load8_param<kWide, kThreads>(A.weight, A.param_dtype, j, tid, A.cols, w);
+            if (A.bias) load8_param<kWide, kThreads>(A.bias, A.param_dtype, j, tid, A.cols, b);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                float v = x[j][e] * rstd;
+                if (A.weight) v *= w[e];
+                if (A.bias) v += b[e];
+                x[j][e] = v;
+            }
+            if (A.y) store8<kWide, kThreads>(static_cast<T*>(A.y) + row * A.y_ld, j, tid, A.cols, x[j]);
+            if (kWide && A.q) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) amax = fmaxf(amax, fabsf(x[j][e]));
+                const int c = (j * kThreads + tid) * kVec;
+                if (c >= A.cols) amax = 0.0f;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+                const float s = tile_scale(amax, A.pow2);
+                uint32_t q[2];
+                if (A.pow2) {
+                    const float r = 1.0f / s;                       // exact
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        q[i] = pack_e4m3x4(x[j][4 * i] * r, x[j][4 * i + 1] * r, x[j][4 * i + 2] * r, x[j][4 * i + 3] * r);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        q[i] = pack_e4m3x4(__fdiv_rn(x[j][4 * i], s), __fdiv_rn(x[j][4 * i + 1], s),
+                                           __fdiv_rn(x[j][4 * i + 2], s), __fdiv_rn(x[j][4 * i + 3], s));
+                }
+                if (c < A.cols) {
+                    *reinterpret_cast<uint2*>(A.q + row * A.cols + c) = make_uint2(q[0], q[1]);
+                    if ((threadIdx.x & 15) == 0) A.q_scale[row * (A.cols / FP8Z_BLOCK) + c / FP8Z_BLOCK] = s;
+                }
+            }
+        }
+    }
+}
+
+// Rows longer than 32768 columns: three passes, the later ones mostly from L2.
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ Norm A) {
+    __shared__ float2 shared[2 * 32];
+    dependent_wait();
+    for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+        const T* px = static_cast<const T*>(A.x) + row * A.x_ld;
+        float sum = 0.0f, sq = 0.0f;
+        for (int c = threadIdx.x; c < A.cols; c += 1024) sum += load_one(px + c);
+        const float mean = row_sum<1024>(sum, 0.0f, shared, 0).x / float(A.cols);
+        for (int c = threadIdx.x; c < A.cols; c += 1024) {
+            const float d = load_one(px + c) - mean;
+            sq = fmaf(d, d, sq);
+        }
+        const float rstd = __frcp_rn(__fsqrt_rn(row_sum<1024>(sq, 0.0f, shared, 1).x / float(A.cols) + A.eps));
+        if (threadIdx.x == 0) {
+            if (A.mean) A.mean[row] = mean;
+            if (A.rstd) A.rstd[row] = rstd;
+        }
+        const auto param = [&](const void* p, int c) {
+            return A.param_dtype == FP8Z_F32 ? load_one(static_cast<const float*>(p) + c)
+                   : A.param_dtype == FP8Z_BF16 ? load_one(static_cast<const __nv_bfloat16*>(p) + c)
+                                                : load_one(static_cast<const __half*>(p) + c);
+        };
+        // four columns a lane, so that a warp has a tile of 128
+        for (int c0 = threadIdx.x / 32 * 128; c0 < A.cols; c0 += 32 * 128) {
+            float v[4], amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i * 32 + (threadIdx.x & 31);
+                v[i] = 0.0f;
+                if (c >= A.cols) continue;
+                v[i] = (load_one(px + c) - mean) * rstd;
+                if (A.weight) v[i] *= param(A.weight, c);
+                if (A.bias) v[i] += param(A.bias, c);
+                if (A.y) static_cast<T*>(A.y)[row * A.y_ld + c] = Elem<T>::narrow(v[i]);
+                amax = fmaxf(amax, fabsf(v[i]));
+            }
+            if (!A.q) continue;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            const float s = tile_scale(amax, A.pow2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                A.q[row * A.cols + c0 + i * 32 + (threadIdx.x & 31)] = uint8_t(cvt_e4m3x2(__fdiv_rn(v[i], s), 0.0f));
+            if ((threadIdx.x & 31) == 0) A.q_scale[row * (A.cols / FP8Z_BLOCK) + c0 / FP8Z_BLOCK] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// A block walks over rows, keeps its columns' sums of dy xh and dy in registers, and
+// leaves them in `part` at the end: dy and x are read once.
+template <typename T, bool kWide, int kThreads, int kVecs>
+__global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) norm_grad_kernel(const __grid_constant__ NormGrad A) {
+    constexpr int kGroups = kThreads == 32 ? 8 : 1;
+    __shared__ float2 shared[2 * (kThreads / 32)];
+    __shared__ float joined[kGroups == 1 ? 1 : kGroups][kGroups == 1 ? 1 : 2 * 32 * kVec * kVecs];
+    dependent_wait();
+    const int tid = threadIdx.x % kThreads, group = threadIdx.x / kThreads;
+    const float n = float(A.cols);
+    float dw[kVecs][kVec], db[kVecs][kVec], w[kVecs][kVec];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            dw[j][e] = db[j][e] = 0.0f;
+            w[j][e] = 1.0f;
+        }
+        if (A.weight) load8_param<kWide, kThreads>(A.weight, A.param_dtype, j, tid, A.cols, w[j]);
+    }
+    int slot = 0;
+    for (int64_t row = int64_t(blockIdx.x) * kGroups + group; row < A.rows; row += int64_t(gridDim.x) * kGroups) {
+        const T* px = static_cast<const T*>(A.x) + row * A.x_ld;
+        const T* pd = static_cast<const T*>(A.dy) + row * A.dy_ld;
+        const float mean = load_one(A.mean + row), rstd = load_one(A.rstd + row);
+        float x[kVecs][kVec], d[kVecs][kVec], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            load8<kWide, kThreads, true>(px, j, tid, A.cols, x[j]);
+            load8<kWide, kThreads, true>(pd, j, tid, A.cols, d[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                x[j][e] = column<kWide, kThreads>(j, e, tid) < A.cols ? (x[j][e] - mean) * rstd : 0.0f;
+                dw[j][e] = fmaf(d[j][e], x[j][e], dw[j][e]);
+                db[j][e] += d[j][e];
+                d[j][e] *= w[j][e];
+                s1 += d[j][e];
+                s2 = fmaf(d[j][e], x[j][e], s2);
+            }
+        const float2 s = row_sum<kThreads>(s1, s2, shared, slot);
+        slot ^= 1;
+        const float c1 = s.x / n, c2 = s.y / n;
+        if (A.dx)
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                float v[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) v[e] = rstd * (d[j][e] - c1 - x[j][e] * c2);
+                store8<kWide, kThreads>(static_cast<T*>(A.dx) + row * A.dx_ld, j, tid, A.cols, v);
+            }
+    }
+    float* out = A.part + int64_t(blockIdx.x) * 2 * A.cols;
+    if constexpr (kGroups > 1) {
+        // the eight rows' warps join their sums, in order
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                joined[group][(j * kVec + e) * 32 + tid] = dw[j][e];
+                joined[group][(kVecs * kVec + j * kVec + e) * 32 + tid] = db[j][e];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * 32 * kVec * kVecs; i += 256) {
+            const int je = i / 32, k = je % (kVecs * kVec), c = column<kWide, kThreads>(k / kVec, k % kVec, i % 32);
+            float sum = 0.0f;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) sum += joined[g][i];
+            if (c < A.cols) out[(je >= kVecs * kVec ? A.cols : 0) + c] = sum;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const int c = column<kWide, kThreads>(j, e, tid);
+                if (c < A.cols) {
+                    out[c] = dw[j][e];
+                    out[A.cols + c] = db[j][e];
+                }
+            }
+    }
+}
+
+// Rows longer than 32768 columns: the sums of dw and db are added to in `part`.
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_grad_long_kernel(const __grid_constant__ NormGrad A) {
+    __shared__ float2 shared[2 * 32];
+    dependent_wait();
+    float* out = A.part + int64_t(blockIdx.x) * 2 * A.cols;
+    for (int c = threadIdx.x; c < 2 * A.cols; c += 1024) out[c] = 0.0f;
+    __syncthreads();
+    const auto weight = [&](int c) {
+        return !A.weight ? 1.0f
+               : A.param_dtype == FP8Z_F32 ? load_one(static_cast<const float*>(A.weight) + c)
+               : A.param_dtype == FP8Z_BF16 ? load_one(static_cast<const __nv_bfloat16*>(A.weight) + c)
+                                            : load_one(static_cast<const __half*>(A.weight) + c);
+    };
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+        const T* px = static_cast<const T*>(A.x) + row * A.x_ld;
+        const T* pd = static_cast<const T*>(A.dy) + row * A.dy_ld;
+        const float mean = load_one(A.mean + row), rstd = load_one(A.rstd + row);
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int c = threadIdx.x; c < A.cols; c += 1024) {
+            const float xh = (load_one(px + c) - mean) * rstd, d = load_one(pd + c), g = d * weight(c);
+            s1 += g;
+            s2 = fmaf(g, xh, s2);
+            out[c] = fmaf(d, xh, out[c]);
+            out[A.cols + c] += d;
+        }
+        const float2 s = row_sum<1024>(s1, s2, shared, slot);
+        slot ^= 1;
+        const float c1 = s.x / float(A.cols), c2 = s.y / float(A.cols);
+        if (A.dx)
+            for (int c = threadIdx.x; c < A.cols; c += 1024) {
+                const float xh = (load_one(px + c) - mean) * rstd, g = load_one(pd + c) * weight(c);
+                static_cast<T*>(A.dx)[row * A.dx_ld + c] = Elem<T>::narrow(rstd * (g - c1 - xh * c2));
+            }
+    }
+}
+
+// dw and db from the blocks' parts: 32 columns a block, its eight warps take every eighth part
+// and join in order.
+template <typename P>
+__global__ void __launch_bounds__(256) norm_parts_kernel(const float* part, int parts, int cols, P* dweight, P* dbias,
+                                                         int accumulate) {
+    __shared__ float joined[8][32];
+    dependent_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+    P* out = blockIdx.y ? dbias : dweight;
+    if (!out) return;
+    float sum = 0.0f;
+    if (c < cols)
+#pragma unroll 8
+        for (int i = warp; i < parts; i += 8) sum += __ldcg(part + (int64_t(i) * 2 + blockIdx.y) * cols + c);
+    joined[warp][lane] = sum;
+    __syncthreads();
+    if (warp != 0 || c >= cols) return;
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += joined[i][lane];
+    out[c] = Elem<P>::narrow(accumulate ? Elem<P>::widen(out[c]) + sum : sum);
+}
+
+// ------------------------------------------------------------------- host
+constexpr int kLongest = 32768;                        // columns a block's registers hold
+constexpr int kMaxParts = 304;                         // two blocks an SM
+
+bool vectors(const void* p, int64_t ld, int64_t rows, int dtype) {
+    return host::aligned(p, 16) && (rows <= 1 || ld * dtype_bytes(dtype) % 16 == 0);
+}
+
+template <typename T, bool kWide, int kThreads, int kVecs>
+int start(const Norm& A, int sms, cudaStream_t st) {
+    constexpr int kGroups = kThreads == 32 ? 8 : 1, kBlock = kThreads == 32 ? 256 : kThreads;
+    const int64_t blocks = (int64_t(A.rows) + kGroups - 1) / kGroups, most = int64_t(sms) * (2048 / kBlock);
+    return launch_dependent(&norm_kernel<T, kWide, kThreads, kVecs>, dim3(unsigned(std::min(blocks, most))), kBlock, 0, st, A);
+}
+
+template <typename T, bool kWide>
+int start_width(const Norm& A, int sms, cudaStream_t st) {
+    if (A.cols <= 32 * kVec) return start<T, kWide, 32, 1>(A, sms, st);
+    if (A.cols <= 32 * kVec * 4) return start<T, kWide, 32, 4>(A, sms, st);
+    // few rows: more threads a row
+    if (A.cols <= 1024 * kVec && A.rows <= 2 * sms) return start<T, kWide, 1024, 1>(A, sms, st);
+    if (A.cols <= 256 * kVec * 2) return start<T, kWide, 256, 2>(A, sms, st);
+    if (A.cols <= 256 * kVec * 4) return start<T, kWide, 256, 4>(A, sms, st);
+    return start<T, kWide, 1024, 4>(A, sms, st);
+}
+
+template <typename T>
+int start_type(const Norm& A, bool wide, int sms, cudaStream_t st) {
+    if (A.cols > kLongest)
+        return launch_dependent(&norm_long_kernel<T>, dim3(unsigned(std::min(A.rows, sms * 2))), 1024, 0, st, A);
+    return wide ? start_width<T, true>(A, sms, st) : start_width<T, false>(A, sms, st);
+}
+
+int parts_of(int64_t rows, int64_t cols, int sms) {
+    const int64_t blocks = cols <= 32 * kVec * 2 ? (rows + 7) / 8 : rows;
+    return int(std::min<int64_t>({std::max<int64_t>(blocks, 1), int64_t(sms) * (cols <= 256 * kVec ? 2 : 1), kMaxParts}));
+}
+
+template <typename T, bool kWide, int kThreads, int kVecs>
+int start_grad(const NormGrad& A, int parts, cudaStream_t st) {
+    return launch_dependent(&norm_grad_kernel<T, kWide, kThreads, kVecs>, dim3(unsigned(parts)), kThreads == 32 ? 256 : kThreads,
+                            0, st, A);
+}
+
+template <typename T, bool kWide>
+int start_grad_width(const NormGrad& A, int parts, cudaStream_t st) {
+    if (A.cols <= 32 * kVec * 2) return start_grad<T, kWide, 32, 2>(A, parts, st);
+    if (A.cols <= 256 * kVec) return start_grad<T, kWide, 256, 1>(A, parts, st);
+    if (A.cols <= 512 * kVec) return start_grad<T, kWide, 512, 1>(A, parts, st);
+    if (A.cols <= 1024 * kVec) return start_grad<T, kWide, 1024, 1>(A, parts, st);
+    return start_grad<T, kWide, 1024, 4>(A, parts, st);
+}
+
+template <typename T>
+int start_grad_type(const NormGrad& A, bool wide, int parts, cudaStream_t st) {
+    if (A.cols > kLongest) return launch_dependent(&norm_grad_long_kernel<T>, dim3(unsigned(parts)), 1024, 0, st, A);
+    return wide ? start_grad_width<T, true>(A, parts, st) : start_grad_width<T, false>(A, parts, st);
+}
+
+bool shape_ok(const fp8z_layer_norm_args& a) {
+    const int64_t most = 1LL << 30;
+    return a.rows >= 0 && a.cols >= 1 && a.rows <= most && a.cols <= (1LL << 24) && dtype_ok(a.dtype) &&
+           (a.param_dtype == FP8Z_F32 || a.param_dtype == a.dtype) && a.x_ld >= a.cols && a.x_ld <= (1LL << 38);
+}
+
+}  // namespace
+}  // namespace fp8z
+
+extern "C" int fp8z_layer_norm(const void* x, const void* weight, const void* bias, const fp8z_layer_norm_args* args, void* y,
+                               float* mean, float* rstd, uint8_t* q, float* q_scale, void* stream) {
+    using namespace fp8z;
+    const host::NvtxRange nvtx_range("fp8z_layer_norm");
+    if (!args || !shape_ok(*args)) return FP8Z_EINVAL;
+    const fp8z_layer_norm_args& a = *args;
+    if (!std::isfinite(a.eps) || a.eps < 0.0f || (a.pow2 != 0 && a.pow2 != 1)) return FP8Z_EINVAL;
+    if ((y && (a.y_ld < a.cols || a.y_ld > (1LL << 38))) || (q != nullptr) != (q_scale != nullptr)) return FP8Z_EINVAL;
+    if (q && a.cols % FP8Z_BLOCK) return FP8Z_EINVAL;
+    if (a.rows == 0) return FP8Z_OK;
+    if (!x || (!y && !q && !mean && !rstd)) return FP8Z_EINVAL;
+    const int size = dtype_bytes(a.dtype), psize = dtype_bytes(a.param_dtype);
+    if (!host::aligned(x, size) || !host::aligned(y, size) || !host::aligned(weight, psize) || !host::aligned(bias, psize) ||
+        !host::aligned(mean, 4) || !host::aligned(rstd, 4) || !host::aligned(q, 16) || !host::aligned(q_scale, 4))
+        return FP8Z_EALIGN;
+    const bool wide = vectors(x, a.x_ld, a.rows, a.dtype) && vectors(weight, 0, 1, 0) && vectors(bias, 0, 1, 0) &&
+                      (!y || vectors(y, a.y_ld, a.rows, a.dtype));
+    if (q && !wide && a.cols <= kLongest) return FP8Z_EALIGN;
+    int sms = 0;
+    if (int rc = host::device_sms(&sms)) return rc;
+    const Norm A = {int(a.rows), int(a.cols), x, a.x_ld, weight, bias, a.param_dtype, y, a.y_ld, mean, rstd, a.eps,
+                    q, q_scale, a.pow2};
+    const auto st = static_cast<cudaStream_t>(stream);
+    if (a.dtype == FP8Z_F32) return start_type<float>(A, wide, sms, st);
+    if (a.dtype == FP8Z_BF16) return start_type<__nv_bfloat16>(A, wide, sms, st);
+    return start_type<__half>(A, wide, sms, st);
+}
+
+extern "C" int64_t fp8z_layer_norm_grad_workspace(int64_t rows, int64_t cols) {
+    using namespace fp8z;
+    if (rows < 0 || rows > (1LL << 30) || cols < 1 || cols > (1LL << 24)) return FP8Z_EINVAL;
+    return std::min<int64_t>(std::max<int64_t>(rows, 1), kMaxParts) * 2 * cols * 4;
+}
+
+extern "C" int fp8z_layer_norm_grad(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+                                    const fp8z_layer_norm_args* args, void* dx, void* dweight, void* dbias, void* workspace,
+                                    int64_t workspace_bytes, void* stream) {
+    using namespace fp8z;
+    const host::NvtxRange nvtx_range("fp8z_layer_norm_grad");
+    if (!args || !shape_ok(*args)) return FP8Z_EINVAL;
+    const fp8z_layer_norm_args& a = *args;
+    const int64_t far = 1LL << 38;
+    if (a.dy_ld < a.cols || a.dy_ld > far || (dx && (a.dx_ld < a.cols || a.dx_ld > far))) return FP8Z_EINVAL;
+    if ((a.accumulate != 0 && a.accumulate != 1) || !workspace) return FP8Z_EINVAL;
+    if (a.rows > 0 && (!dy || !x || !mean || !rstd)) return FP8Z_EINVAL;
+    const int size = dtype_bytes(a.dtype), psize = dtype_bytes(a.param_dtype);
+    if (!host::aligned(dy, size) || !host::aligned(x, size) || !host::aligned(dx, size) || !host::aligned(weight, psize) ||
+        !host::aligned(dweight, psize) || !host::aligned(dbias, psize) || !host::aligned(mean, 4) || !host::aligned(rstd, 4) ||
+        !host::aligned(workspace, 16))
+        return FP8Z_EALIGN;
+    if (workspace_bytes < fp8z_layer_norm_grad_workspace(a.rows, a.cols)) return FP8Z_ENOSPACE;
+    int sms = 0;
+    if (int rc = host::device_sms(&sms)) return rc;
+    const auto st = static_cast<cudaStream_t>(stream);
+    auto* part = static_cast<float*>(workspace);
+    int parts = 0;
+    if (a.rows > 0) {
+        parts = parts_of(a.rows, a.cols, sms);
+        const bool wide = vectors(x, a.x_ld, a.rows, a.dtype) && vectors(dy, a.dy_ld, a.rows, a.dtype) && vectors(weight, 0, 1, 0) &&
+                          (!dx || vectors(dx, a.dx_ld, a.rows, a.dtype));
+        const NormGrad A = {int(a.rows), int(a.cols), dy, x, a.dy_ld, a.x_ld, a.dx_ld, weight, a.param_dtype, mean, rstd, dx, part};
+        const int rc = a.dtype == FP8Z_F32 ? start_grad_type<float>(A, wide, parts, st)
+                       : a.dtype == FP8Z_BF16 ? start_grad_type<__nv_bfloat16>(A, wide, parts, st)
+                                              : start_grad_type<__half>(A, wide, parts, st);
+        if (rc) return rc;
+    }
+    if (!dweight && !dbias) return FP8Z_OK;
+    const dim3 grid(unsigned((a.cols + 31) / 32), dbias ? 2 : 1);
+    const auto join = [&](auto* dw, auto* db) {
+        using P = std::remove_pointer_t<decltype(dw)>;
+        return launch_dependent(&norm_parts_kernel<P>, grid, 256, 0, st, part, parts, int(a.cols), dw, db, a.accumulate);
+    };
+    if (a.param_dtype == FP8Z_F32) return join(static_cast<float*>(dweight), static_cast<float*>(dbias));
+    if (a.param_dtype == FP8Z_BF16) return join(static_cast<__nv_bfloat16*>(dweight), static_cast<__nv_bfloat16*>(dbias));
+    return join(static_cast<__half*>(dweight), static_cast<__half*>(dbias));
+}

@@ -49,7 +49,15 @@ plan_summary_dtype = np.dtype([
 tensor_chunk_dtype = np.dtype([
     ("src", "<u8"), ("dst", "<u8"), ("count", "<i4"), ("src_dtype", "<i2"), ("dst_dtype", "<i2"),
 ])
-assert tensor_chunk_dtype.itemsize == 24
+adamw_tensor_dtype = np.dtype([
+    ("p", "<u8"), ("g", "<u8"), ("m", "<u8"), ("v", "<u8"), ("m_scale", "<u8"), ("v_scale", "<u8"), ("copy", "<u8"),
+    ("count", "<i8"), ("g_dtype", "<i4"), ("copy_dtype", "<i4"), ("state_bits", "<i4"), ("reserved", "<i4"),
+])
+adamw_chunk_dtype = np.dtype([
+    ("p", "<u8"), ("g", "<u8"), ("m", "<u8"), ("v", "<u8"), ("m_scale", "<u8"), ("v_scale", "<u8"), ("copy", "<u8"),
+    ("count", "<i4"), ("g_dtype", "<i2"), ("copy_dtype", "i1"), ("state_bits", "i1"),
+])
+assert tensor_chunk_dtype.itemsize == 24 and adamw_tensor_dtype.itemsize == 80 and adamw_chunk_dtype.itemsize == 64
 assert param_entry_dtype.itemsize == 64 and block_desc_dtype.itemsize == 20
 
 EXPORTED = ("fp8z_plan_shards", "fp8z_adamw_requant_step", "fp8z_adamw_requant_step_rowmajor",
@@ -60,7 +68,8 @@ EXPORTED = ("fp8z_plan_shards", "fp8z_adamw_requant_step", "fp8z_adamw_requant_s
             "fp8z_encode_tensor_list", "fp8z_grad_norm", "fp8z_grad_clip",
             "fp8z_embedding", "fp8z_embedding_grad", "fp8z_embedding_grad_workspace",
             "fp8z_linear_xent", "fp8z_linear_xent_grad", "fp8z_linear_xent_workspace",
-            "fp8z_matmul", "fp8z_matmul_workspace",
+            "fp8z_matmul", "fp8z_matmul_workspace", "fp8z_layer_norm", "fp8z_layer_norm_grad",
+            "fp8z_layer_norm_grad_workspace", "fp8z_encode_adamw_list", "fp8z_adamw",
             "fp8z_e4m3_encode_bits",
             "fp8z_watchdog_selftest", "fp8z_set_wait_limit_ns", "fp8z_get_wait_limit_ns",
             "fp8z_status_string")
@@ -103,6 +112,17 @@ class fp8z_matmul_args(ctypes.Structure):
 
 
 assert ctypes.sizeof(fp8z_matmul_args) == 112
+
+
+class fp8z_layer_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("x_ld", ctypes.c_int64), ("y_ld", ctypes.c_int64),
+        ("dy_ld", ctypes.c_int64), ("dx_ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+        ("pow2", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
+assert ctypes.sizeof(fp8z_layer_norm_args) == 72
 
 
 def hparams(lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=1,
@@ -165,6 +185,12 @@ def lib():
         MA = ctypes.POINTER(fp8z_matmul_args)
         L.fp8z_matmul_workspace.argtypes = [P, P, MA]
         L.fp8z_matmul.argtypes = [P, P, P, P, MA, P, P, P, i64, P, P]
+        NA = ctypes.POINTER(fp8z_layer_norm_args)
+        L.fp8z_layer_norm.argtypes = [P, P, P, NA, P, P, P, P, P, P]
+        L.fp8z_layer_norm_grad_workspace.argtypes = [i64, i64]
+        L.fp8z_layer_norm_grad.argtypes = [P, P, P, P, P, NA, P, P, P, P, i64, P]
+        L.fp8z_encode_adamw_list.argtypes = [P, i32, P, i64, P]
+        L.fp8z_adamw.argtypes = [P, i64, ctypes.POINTER(fp8z_adamw_hparams), P, P]
         L.fp8z_e4m3_encode_bits.argtypes = [ctypes.c_uint32, i64, P, P]
         L.fp8z_watchdog_selftest.argtypes = [P, i64, P]
         L.fp8z_set_wait_limit_ns.argtypes = [i64]
@@ -178,6 +204,7 @@ def lib():
         L.fp8z_embedding_grad_workspace.restype = i64
         L.fp8z_linear_xent_workspace.restype = i64
         L.fp8z_matmul_workspace.restype = i64
+        L.fp8z_layer_norm_grad_workspace.restype = i64
         _lib = L
     return _lib
 
@@ -621,6 +648,8 @@ def fp8z_grad_norm_workspace():
 
 def _norm_args(tensors, norm, workspace):
     here = _current_device()
+    if isinstance(tensors, AdamwList):
+        raise ValueError("tensors must be a list of fp8z_encode_tensor_list")
     if tensors.device != here:
         _elsewhere(tensors.table, "table", here)
     if norm.numel() < 2:
@@ -852,6 +881,149 @@ def fp8z_matmul(a, a_scale, b, b_scale, out, offsets=None, accumulate=False, wor
                            0 if workspace is None else workspace.numel() * workspace.element_size(),
                            _flat(dev_status, "dev_status", here, FP8Z_I32), _stream_handle(stream))
     _check("fp8z_matmul", rc)
+
+
+def _norm_vector(t, name, cols, device, code):
+    if t is not None and t.numel() != cols:
+        raise ValueError(f"{name} must hold {cols} elements, got {t.numel()}")
+    return _flat(t, name, device, code)
+
+
+def _norm_stat(t, name, rows, device):
+    if t is not None and t.numel() < rows:
+        raise ValueError(f"{name} must hold one value per row")
+    return _flat(t, name, device, FP8Z_F32)
+
+
+def _norm_row(t, name, x, device):
+    """(pointer, row stride) of a matrix like x, or (None, 0)."""
+    if t is None:
+        return None, 0
+    p, rows, cols, ld = _matrix(t, name, device)
+    if (rows, cols) != tuple(x.shape) or t.dtype != x.dtype:
+        raise ValueError(f"{name} must be {list(x.shape)} of {x.dtype}, got {list(t.shape)} of {t.dtype}")
+    return p, ld
+
+
+def _param_code(params, dtype):
+    """The one type of the weight, bias and gradients that are there: float32, or x's."""
+    codes = {_dtype_code(t, name, (FP8Z_F32, dtype)) for t, name in params if t is not None}
+    if len(codes) > 1:
+        raise ValueError("weight, bias and their gradients must be of one type")
+    return codes.pop() if codes else FP8Z_F32
+
+
+def fp8z_layer_norm(x, weight, bias, y, mean, rstd, eps=1e-5, q=None, q_scale=None, pow2=False, stream=None):
+    """y = (x - mean) * rstd * weight + bias for each row of x [rows, cols] (float32 /
+    bfloat16 / float16, rows may be strided).  weight, bias [cols] (float32, or x's type), y,
+    mean and rstd (float32 [rows]) may be None; q uint8 [rows, cols] and q_scale float32 [rows,
+    cols/128] take y as the row-wise E4M3 operand of fp8z_matmul (pow2: power-of-two scales)."""
+    here = _current_device()
+    xp, rows, cols, x_ld = _matrix(x, "x", here)
+    dtype = _dtype_code(x, "x")
+    code = _param_code(((weight, "weight"), (bias, "bias")), dtype)
+    yp, y_ld = _norm_row(y, "y", x, here)
+    if (q is None) != (q_scale is None):
+        raise ValueError("q and q_scale go together")
+    qp = sp = None
+    if q is not None:
+        if str(q.dtype) != "torch.uint8" or q.numel() != rows * cols or q_scale.numel() < rows * (cols // BLOCK):
+            raise ValueError(f"q must be uint8 [{rows}, {cols}], q_scale float32 [{rows}, {cols // BLOCK}]")
+        qp, sp = _flat(q, "q", here), _flat(q_scale, "q_scale", here, FP8Z_F32)
+    a = fp8z_layer_norm_args(rows, cols, x_ld, y_ld, 0, 0, dtype, code, int(bool(pow2)), 0, eps, 0)
+    rc = lib().fp8z_layer_norm(xp, _norm_vector(weight, "weight", cols, here, code),
+                               _norm_vector(bias, "bias", cols, here, code), ctypes.byref(a), yp,
+                               _norm_stat(mean, "mean", rows, here), _norm_stat(rstd, "rstd", rows, here), qp, sp,
+                               _stream_handle(stream))
+    _check("fp8z_layer_norm", rc)
+
+
+def fp8z_layer_norm_grad_workspace(rows, cols):
+    """Bytes of workspace fp8z_layer_norm_grad needs for these sizes."""
+    size = int(lib().fp8z_layer_norm_grad_workspace(int(rows), int(cols)))
+    if size < 0:
+        raise Fp8zError("fp8z_layer_norm_grad_workspace", size)
+    return size
+
+
+def fp8z_layer_norm_grad(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, accumulate=False, stream=None):
+    """Gradients of fp8z_layer_norm: dx of x's type; dweight and dbias of weight's type (or
+    float32), overwritten, or added to with accumulate.  weight, dx, dweight and dbias may
+    be None; mean and rstd are the forward call's."""
+    here = _current_device()
+    xp, rows, cols, x_ld = _matrix(x, "x", here)
+    dtype = _dtype_code(x, "x")
+    code = _param_code(((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")), dtype)
+    dp, dy_ld = _norm_row(dy, "dy", x, here)
+    gp, dx_ld = _norm_row(dx, "dx", x, here)
+    a = fp8z_layer_norm_args(rows, cols, x_ld, 0, dy_ld, dx_ld, dtype, code, 0, int(bool(accumulate)), 0.0, 0)
+    rc = lib().fp8z_layer_norm_grad(dp, xp, _norm_vector(weight, "weight", cols, here, code),
+                                    _norm_stat(mean, "mean", rows, here), _norm_stat(rstd, "rstd", rows, here),
+                                    ctypes.byref(a), gp, _norm_vector(dweight, "dweight", cols, here, code),
+                                    _norm_vector(dbias, "dbias", cols, here, code), _flat(workspace, "workspace", here),
+                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check("fp8z_layer_norm_grad", rc)
+
+
+class AdamwList(TensorList):
+    """The device table of fp8z_encode_adamw_list, whose chunks are of another kind."""
+
+
+def fp8z_encode_adamw_list(params, grads, exp_avgs, exp_avg_sqs, copies=None, exp_avg_scales=None,
+                           exp_avg_sq_scales=None, device="cuda"):
+    """Table for fp8z_adamw over params (contiguous float32 CUDA tensors), their gradients
+    (float32 / bfloat16 / float16) and moments: float32, or uint8 E4M3 codes with float32 scales,
+    one for every 128 elements (rounded up).  copies: bfloat16 / float16 tensors that take
+    the new values, or None for no copies.  Scales and copies may also be None for single
+    tensors.  The table holds addresses: make a new one when a tensor moves."""
+    params, grads, ms, vs = list(params), list(grads), list(exp_avgs), list(exp_avg_sqs)
+    n, here = len(params), _current_device()
+    optional = [list(t) if t is not None else [None] * n for t in (copies, exp_avg_scales, exp_avg_sq_scales)]
+    if any(len(t) != n for t in (grads, ms, vs, *optional)):
+        raise ValueError("one gradient, two moments (and one copy and scales, where given) per parameter")
+    rows = np.zeros(max(n, 1), adamw_tensor_dtype)
+    for i, (p, g, m, v, c, sm, sv) in enumerate(zip(params, grads, ms, vs, *optional)):
+        wide = str(m.dtype) != "torch.uint8"
+        for t, name in ((g, "grad"), (m, "exp_avg"), (v, "exp_avg_sq"), (c, "copy")):
+            if t is not None and t.numel() != p.numel():
+                raise ValueError(f"{name} {i} holds {t.numel()} elements, its parameter {p.numel()}")
+        if v.dtype != m.dtype:
+            raise ValueError(f"the moments of parameter {i} must be of one type")
+        if wide != (sm is None) or wide != (sv is None):
+            raise ValueError(f"parameter {i}: uint8 moments go with scales, float32 ones without")
+        if not wide and min(sm.numel(), sv.numel()) < -(-p.numel() // BLOCK):
+            raise ValueError(f"the scales of parameter {i} must hold one number for every {BLOCK} elements")
+        _dtype_code(p, f"param {i}", (FP8Z_F32,))
+        r = rows[i]
+        r["p"], r["g"] = _flat(p, f"param {i}", here, FP8Z_F32), _flat(g, f"grad {i}", here)
+        r["m"], r["v"] = (_flat(t, f"moment of param {i}", here, FP8Z_F32 if wide else None) for t in (m, v))
+        r["m_scale"], r["v_scale"] = (_flat(t, f"scale of param {i}", here, FP8Z_F32) or 0 for t in (sm, sv))
+        r["copy"] = _flat(c, f"copy {i}", here) or 0
+        r["count"], r["g_dtype"], r["state_bits"] = p.numel(), _dtype_code(g, f"grad {i}"), 32 if wide else 8
+        r["copy_dtype"] = FP8Z_BF16 if c is None else _dtype_code(c, f"copy {i}", _HALVES)
+    chunks = ctypes.c_int64(0)
+    args = (rows.ctypes.data, n)
+    _check("fp8z_encode_adamw_list", lib().fp8z_encode_adamw_list(*args, None, 0, ctypes.byref(chunks)))
+    out = np.zeros(max(chunks.value, 1), adamw_chunk_dtype)
+    rc = lib().fp8z_encode_adamw_list(*args, out.ctypes.data, chunks.value, ctypes.byref(chunks))
+    _check("fp8z_encode_adamw_list", rc)
+    return AdamwList(table_to_device(out, device), int(chunks.value), (params, grads, ms, vs, *optional))
+
+
+def fp8z_adamw(tensors, hp, grad_factor=None, stream=None):
+    """One AdamW step of every tensor of the list (fp8z_encode_adamw_list).  grad_factor: one
+    float32 on the device that multiplies every gradient (norm[1] of a clipping, 1 / a loss
+    scale), or None."""
+    here = _current_device()
+    if not isinstance(tensors, AdamwList):
+        raise ValueError("tensors must be a list of fp8z_encode_adamw_list")
+    if tensors.device != here:
+        _elsewhere(tensors.table, "table", here)
+    if grad_factor is not None and grad_factor.numel() < 1:
+        raise ValueError("grad_factor must hold one float32 value")
+    rc = lib().fp8z_adamw(tensors.pointer, tensors.chunks, ctypes.byref(hp), _flat(grad_factor, "grad_factor", here, FP8Z_F32),
+                          _stream_handle(stream))
+    _check("fp8z_adamw", rc)
 
 
 def fp8z_e4m3_encode_bits(first_bits, n, out, stream=None):

@@ -624,6 +624,101 @@ FP8Z_API int fp8z_matmul(const void *a, const float *a_scale, const void *b, con
                          const fp8z_matmul_args *args, const void *offsets, void *out, void *workspace,
                          int64_t workspace_bytes, int32_t *dev_status, void *stream);
 
+/* Shapes and options of fp8z_layer_norm and fp8z_layer_norm_grad. */
+typedef struct {
+    int64_t rows, cols;
+    int64_t x_ld, y_ld, dy_ld, dx_ld;   /* row strides in elements                        */
+    int32_t dtype;                      /* of x, y, dy and dx: FP8Z_F32, FP8Z_BF16, FP8Z_F16 */
+    int32_t param_dtype;                /* of weight, bias and their gradients: FP8Z_F32, or dtype */
+    int32_t pow2;                       /* 1: power-of-two scales in q_scale              */
+    int32_t accumulate;                 /* gradient: 1: added to dweight and dbias        */
+    float eps;                          /* >= 0                                           */
+    int32_t reserved;
+} fp8z_layer_norm_args;                 /* 72 bytes */
+
+/*
+ * fp8z_layer_norm -- for each row of x [rows, cols], in FP32:
+ *   mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) * rstd * weight + bias, rounded once to y's type.
+ * weight, bias [cols]: NULL for 1 and 0.  y [rows, cols], mean and rstd f32 [rows]: each may
+ * be NULL; the gradient needs mean and rstd.  q, q_scale (both or neither): y, before it is
+ * rounded, as the row-wise E4M3 operand of fp8z_matmul: device u8 [rows, cols] (16-byte
+ * aligned) and f32 [rows, cols/128], by the rule of fp8z_quantize_rowwise.  With q, cols is
+ * a multiple of 128, and rows of x and y, weight and bias start on 16-byte boundaries
+ * (FP8Z_EALIGN; not asked of more than 32768 columns).
+ *
+ * fp8z_layer_norm_grad -- from dy [rows, cols], x, weight, and the forward call's mean and rstd,
+ * with xh = (x - mean) * rstd and g = dy * weight, in FP32:
+ *   dx = rstd * (g - sum g / cols - xh * sum (g * xh) / cols)   (of dtype),
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy  (of param_dtype),
+ * or these sums added to dweight and dbias.  Sums over rows are FP32, in an order that the
+ * shape gives: the same bits every time.  dx, dweight and dbias may be NULL.  rows = 0 gives
+ * zero sums.  workspace: device, fp8z_layer_norm_grad_workspace(rows, cols) bytes, no
+ * initialisation.
+ * rows <= 2^30, cols <= 2^24.  Rows on 16-byte boundaries take the vector paths; rows of
+ * more than 32768 columns do not stay in registers and are read again.
+ * Returns FP8Z_OK / EINVAL / EALIGN / ENOSPACE / EUNSUPPORTED / ECUDA.
+ */
+FP8Z_API int fp8z_layer_norm(const void *x, const void *weight, const void *bias, const fp8z_layer_norm_args *args,
+                             void *y, float *mean, float *rstd, uint8_t *q, float *q_scale, void *stream);
+FP8Z_API int64_t fp8z_layer_norm_grad_workspace(int64_t rows, int64_t cols);
+FP8Z_API int fp8z_layer_norm_grad(const void *dy, const void *x, const void *weight, const float *mean,
+                                  const float *rstd, const fp8z_layer_norm_args *args, void *dx, void *dweight,
+                                  void *dbias, void *workspace, int64_t workspace_bytes, void *stream);
+
+#define FP8Z_ADAMW_CHUNK 8192              /* most elements of one chunk of a list     */
+
+/* One tensor of fp8z_adamw's list (host). */
+typedef struct {
+    float *p;                /* parameter, FP32, updated in place                    */
+    const void *g;           /* gradient                                             */
+    void *m, *v;             /* moments: FP32, or E4M3 codes                         */
+    float *m_scale, *v_scale;/* 8 bits: one scale for every 128 elements, from the first on */
+    void *copy;              /* NULL, or p's new values in 16 bits                   */
+    int64_t count;
+    int32_t g_dtype;         /* FP8Z_F32, FP8Z_BF16 or FP8Z_F16                      */
+    int32_t copy_dtype;      /* FP8Z_BF16 or FP8Z_F16                                */
+    int32_t state_bits;      /* 32 or 8                                              */
+    int32_t reserved;
+} fp8z_adamw_tensor;         /* 80 bytes */
+
+/* Up to FP8Z_ADAMW_CHUNK neighbouring elements of one tensor of a list. */
+typedef struct {
+    float *p;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    void *copy;
+    int32_t count;
+    int16_t g_dtype;
+    int8_t copy_dtype;       /* -1: no copy                                          */
+    int8_t state_bits;
+} fp8z_adamw_chunk;          /* 64 bytes */
+
+/*
+ * fp8z_encode_adamw_list -- host only: the table fp8z_adamw takes the tensors from, every
+ * tensor cut into chunks.  out: host array of `capacity` chunks, which the caller copies
+ * to device memory, or NULL to ask for the number; *chunks_out: the number of chunks.  A
+ * tensor may be empty.  Tensors do not overlap.  Returns FP8Z_OK / EINVAL / EALIGN / ENOSPACE.
+ *
+ * fp8z_adamw -- one AdamW step of every tensor of the list: the per-element arithmetic of
+ * fp8z_adamw_requant_step (hp's lr, beta1, beta2, eps, weight_decay, step and decay_mode; its
+ * quantizer fields are checked and not used), for parameters that are not kept in FP8
+ * blocks: norms, biases, embeddings.  grad_factor: device f32, multiplied into every
+ * gradient first (a clipping coefficient, 1 / a loss scale), or NULL for 1.
+ * Moments in 8 bits, for every 128 elements of a tensor (fewer at its end): m is
+ * E4M3(m' * s), v is E4M3(sqrt(v') * s), s = 448 / (the largest magnitude of the 128) (1 where all are
+ * zero, at most FLT_MAX), and the scale kept is 1 / s: a moment is code * scale, v its square.
+ * A v' that is not zero keeps at least the smallest code.  Zero codes with any finite scale are
+ * zero moments, so that buffers of zeros start a run.  An infinite or NaN moment leaves the
+ * 128 elements it is among without meaning.
+ * list: device, fp8z_adamw_chunk[chunks].  Returns FP8Z_OK / EINVAL / EALIGN / EUNSUPPORTED / ECUDA.
+ */
+FP8Z_API int fp8z_encode_adamw_list(const fp8z_adamw_tensor *tensors, int32_t n, fp8z_adamw_chunk *out,
+                                    int64_t capacity, int64_t *chunks_out);
+FP8Z_API int fp8z_adamw(const fp8z_adamw_chunk *list, int64_t chunks, const fp8z_adamw_hparams *hp,
+                        const float *grad_factor, void *stream);
+
 /*
  * fp8z_e4m3_encode_bits -- out[i] = E4M3 code (round to nearest even,
  * saturating, as in the step) of the float whose bit pattern is
