@@ -75,6 +75,16 @@ __device__ __forceinline__ float ld_scale(const float* p) {
     return v;
 }
 
+// Registers a thread of this warpgroup has from here on.
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // Two FP32 numbers in one register pair: the packed instructions do both at once.
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
     uint64_t r;
@@ -100,7 +110,13 @@ __device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
     return r;
 }
 
-// The 16 registers of a tmem_ld16 hold their values from here on.
+// The registers of a tmem_ld16 or tmem_ld32 hold their values from here on.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
@@ -108,39 +124,123 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+// tmem_ld8, tmem_ld16 and tmem_ld32 for a warp that is together already.
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[8], uint32_t taddr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[16], uint32_t taddr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[32], uint32_t taddr) { tmem_ld32(r, taddr); }
 
 __device__ __forceinline__ void ld_shared_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint64_t ld_shared_pair(uint32_t addr) {
+    uint64_t a;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(a) : "r"(addr) : "memory");
+    return a;
 }
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Column j of v: a row's scales of four blocks from k on, zeros past k1.
+template <int kN>
+__device__ __forceinline__ void load_scales(const float* row, int k, int k1, float (&v)[4][kN], int j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i][j] = k + i < k1 ? ld_scale(row + k + i) : 0.0f;
+}
+
 // A block's sums times their scales, added up: kCols columns of tensor memory from
-// `acc` on, of the row of each lane.  kRows: the columns' scales are the FP32 numbers
-// at `scales` in shared memory and `f` is the row's; otherwise `f` is both.
-template <int kCols, bool kColScales>
+// `acc` on, of the row of each lane, kStep at a time, the next ones on their way.
+// kColScales: the columns' scales are the FP32 numbers at `scales` in shared memory and
+// `f` is the row's; otherwise `f` is both.
+template <int kCols, bool kColScales, int kStep>
 __device__ __forceinline__ void add_block(uint64_t (&sums)[kCols / 2], uint32_t acc, float f, uint32_t scales) {
     const uint64_t ff = pair_of(f, f);
-    uint32_t r[2][16];
-    tmem_ld16(r[0], acc);
+    uint32_t r[2][kStep];
+    uint64_t col[kColScales ? kStep / 2 : 1];
+    tmem_load(r[0], acc);
 #pragma unroll
-    for (int c = 0; c < kCols / 16; ++c) {
+    for (int c = 0; c < kCols / kStep; ++c) {
+        if constexpr (kColScales)
+#pragma unroll
+            for (int j = 0; j < kStep / 4; ++j) ld_shared_pairs(scales + (c * kStep + j * 4) * 4, col[2 * j], col[2 * j + 1]);
         tmem_arrived(r[c & 1]);
-        if (c + 1 < kCols / 16) tmem_ld16(r[(c + 1) & 1], acc + 16 * (c + 1));
+        if (c + 1 < kCols / kStep) tmem_load(r[(c + 1) & 1], acc + kStep * (c + 1));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t* d = r[c & 1] + 4 * j;
-            uint64_t f0 = ff, f1 = ff;
-            if constexpr (kColScales) {
-                ld_shared_pairs(scales + (c * 16 + j * 4) * 4, f0, f1);
-                f0 = mul_pair(f0, ff);
-                f1 = mul_pair(f1, ff);
-            }
-            uint64_t* s = sums + c * 8 + j * 2;
-            s[0] = fma_pair(pair_of(d[0], d[1]), f0, s[0]);
-            s[1] = fma_pair(pair_of(d[2], d[3]), f1, s[1]);
+        for (int j = 0; j < kStep / 2; ++j) {
+            uint64_t x = ff;
+            if constexpr (kColScales) x = mul_pair(col[j], ff);
+            uint64_t& s = sums[c * (kStep / 2) + j];
+            s = fma_pair(pair_of(r[c & 1][2 * j], r[c & 1][2 * j + 1]), x, s);
         }
+    }
+}
+
+// 16 rows and 32 columns: lane t holds rows t / 4 and t / 4 + 8 and, of every 8 columns, the
+// two from 2 (t % 4) on.
+__device__ __forceinline__ void tmem_load_16x256b(uint32_t (&r)[16], uint32_t taddr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// The same for 128 columns that each have a scale.  A lane that has one row and all columns
+// would load 128 scales a block, 16 bytes a lane each time: 1024 cycles of the SM's loads,
+// twice what the products take.  With four rows and 32 columns a lane it is a quarter.
+// Pair (h, g, e) of `sums`: row 16 h + 8 e + t / 4, columns from 8 g + 2 (t % 4) on.  `rows`
+// and `cols`: where the scales of the lane's first row and of its first columns are.
+__device__ __forceinline__ void add_block_rows(uint64_t (&sums)[64], uint32_t acc, uint32_t rows, uint32_t cols) {
+    uint32_t r[2][16];
+    tmem_load_16x256b(r[0], acc);
+    uint64_t f[4], col[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = ld_shared_f32(rows + i * 32);
+        f[i] = pair_of(x, x);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {                      // 32 columns of 16 rows, then of the other 16
+        const int h = c & 1, q = c >> 1;
+        if (h == 0)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) col[j] = ld_shared_pair(cols + (q * 4 + j) * 32);
+        tmem_arrived(r[c & 1]);
+        if (c < 7) tmem_load_16x256b(r[(c + 1) & 1], acc + ((c + 1) >> 1) * 32 + (uint32_t((c + 1) & 1) << 20));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint64_t& s = sums[(h * 16 + q * 4 + j) * 2 + e];
+                s = fma_pair(pair_of(r[c & 1][j * 4 + e * 2], r[c & 1][j * 4 + e * 2 + 1]), mul_pair(col[j], f[h * 2 + e]), s);
+            }
     }
 }
 
@@ -150,17 +250,21 @@ constexpr int kTileBytes = kHalf * kBK;
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kReaders = 8, kOwn = 128;                // warps that read the sums: 32 rows and 128 columns each
 constexpr int kAccumulators = 2;
-constexpr int kScaleSlots = 2, kScaleBlocks = 4;       // of b's row scales: slots of four blocks of K
-constexpr int kScaleBytes = kScaleBlocks * kTN * 4;
+// The readers' sums and the loads on their way take more registers than an even share of
+// the block's 384 x 168: 128 x 64 + 256 x 216 is a little less.
+constexpr int kOtherRegs = 64, kReaderRegs = 216;
+constexpr int kScaleSlots = 2, kScaleBlocks = 4;       // of scales: slots of four blocks of K
 
 template <bool kRows>
 struct Large {
-    static constexpr int kStages = kRows ? 5 : 6;
-    static constexpr int kThreads = 64 + 32 * kReaders + (kRows ? 32 : 0);   // loads, products, readers, b's scales
+    static constexpr int kStages = 5;
+    // a block's scales: its rows' and all columns', or the products of rows' and each 128 columns' one
+    static constexpr int kScaleWords = kRows ? kHalf + kTN : 2 * kHalf, kScaleBytes = kScaleBlocks * kScaleWords * 4;
+    static constexpr int kThreads = 128 + 32 * kReaders;       // loads, products, b's scales, none; readers
     static constexpr int kStaging = kStages * kStageBytes;
     static constexpr int kScales = kStaging + kReaders * kSlab;
-    static constexpr int kBars = kScales + (kRows ? kScaleSlots * kScaleBytes : 0);
-    static constexpr int kNumBars = 2 * kStages + 2 * kAccumulators + 1 + (kRows ? 2 * kScaleSlots : 0);
+    static constexpr int kBars = kScales + kScaleSlots * kScaleBytes;
+    static constexpr int kNumBars = 2 * kStages + 2 * kAccumulators + 1 + 2 * kScaleSlots;
     static constexpr int kStarts = kBars + kNumBars * 8 + 32;
     static constexpr int kSmem = kStarts + (kMaxGroups + 1) * 4 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
@@ -208,9 +312,46 @@ struct TileWalk {
     }
 };
 
+// 32 FP32 columns, or 64 of 16 bits (k16), from column i of the warp's sums on into its slab,
+// whichever way the sums lie (add_block, or kRows: add_block_rows).
+template <bool kRows, bool k16>
+__device__ __forceinline__ void stage(Stager& sg, uint64_t (&sums)[kOwn / 2], int i, bool bf16) {
+    const auto packed = [&](uint64_t p) {
+        uint32_t a, b;
+        halves(p, a, b);
+        return pack16(__uint_as_float(a), __uint_as_float(b), bf16);
+    };
+    if constexpr (!kRows) {
+        uint32_t r[32];
+#pragma unroll
+        for (int j = 0; j < (k16 ? 32 : 16); ++j) {
+            if constexpr (k16) r[j] = packed(sums[i / 2 + j]);
+            else halves(sums[i / 2 + j], r[2 * j], r[2 * j + 1]);
+        }
+        stage32(sg, r);
+    } else {
+        const uint32_t slab = sg.begin();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = h * 16 + e * 8 + sg.lane / 4;
+#pragma unroll
+                for (int g = 0; g < (k16 ? 8 : 4); ++g) {
+                    const uint64_t p = sums[(h * 16 + i / 8 + g) * 2 + e];
+                    const int byte = (g * 8 + sg.lane % 4 * 2) * (k16 ? 2 : 4);
+                    const uint32_t to = slab + swz128(row, byte);
+                    if constexpr (k16) asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(packed(p)) : "memory");
+                    else asm volatile("st.shared.b64 [%0], %1;" ::"r"(to), "l"(p) : "memory");
+                }
+            }
+    }
+}
+
 // The tile's results of one warp: 128 columns from c0 on, of the row of each lane.  A
 // tile of 32 rows leaves at once where its rows are all this product's (or the tensor
 // ends with them) and all rows start and end on 16-byte boundaries.
+template <bool kRows>
 __device__ __forceinline__ void store_large(const Args& A, const CUtensorMap& out, const Tile& t, uint64_t (&sums)[kOwn / 2],
                                             int c0, int row, Stager& sg) {
     const int first = row - sg.lane, rows = min(32, t.row_end - first), col0 = t.n * kTN + c0;
@@ -221,14 +362,7 @@ __device__ __forceinline__ void store_large(const Args& A, const CUtensorMap& ou
 #pragma unroll
         for (int i = 0; i < kOwn; i += 64) {
             if (col0 + i >= A.n) break;
-            uint32_t h[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                uint32_t a, b;
-                halves(sums[i / 2 + j], a, b);
-                h[j] = pack16(__uint_as_float(a), __uint_as_float(b), A.out_dtype == FP8Z_BF16);
-            }
-            stage32(sg, h);
+            stage<kRows, true>(sg, sums, i, A.out_dtype == FP8Z_BF16);
             sg.end([&](uint32_t s) { tma_store_3d(&out, col0 + i, row, z, s); });
         }
         return;
@@ -237,10 +371,7 @@ __device__ __forceinline__ void store_large(const Args& A, const CUtensorMap& ou
     for (int i = 0; i < kOwn; i += 32) {
         const int col = col0 + i;
         if (col >= A.n) break;
-        uint32_t r[32];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) halves(sums[i / 2 + j], r[2 * j], r[2 * j + 1]);
-        stage32(sg, r);
+        stage<kRows, false>(sg, sums, i, false);
         if (tiles) {
             sg.end([&](uint32_t s) {
                 if (A.accumulate) tma_add_3d(&out, col, row, z, s);
@@ -277,14 +408,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
     auto tfull = [&](int b) { return bars + (2 * kStages + b) * 8; };
     auto tempty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };  // first block: both blocks' warps have read it
     const uint32_t drain = bars + (2 * kStages + 4) * 8;
-    auto sfull = [&](int i) { return bars + (2 * kStages + 5 + i) * 8; };   // b's scales
+    auto sfull = [&](int i) { return bars + (2 * kStages + 5 + i) * 8; };
     auto sempty = [&](int i) { return bars + (2 * kStages + 5 + kScaleSlots + i) * 8; };
     uint8_t* words = smem + L::kBars + L::kNumBars * 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(words);
     volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(words + 8);
     volatile uint32_t* issued_by = reinterpret_cast<volatile uint32_t*>(words + 16);   // [2]
     int* starts = reinterpret_cast<int*>(smem + L::kStarts);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int rank = int(cluster_rank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
@@ -296,11 +427,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
             mbar_init(tfull(b), 1);
             mbar_init(tempty(b), 2 * kReaders);
         }
-        if (kRows)
-            for (int i = 0; i < kScaleSlots; ++i) {
-                mbar_init(sfull(i), 1);
-                mbar_init(sempty(i), kReaders);
-            }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(sfull(i), 1);
+            mbar_init(sempty(i), kReaders);
+        }
         mbar_init(drain, 1);
         *abort_flag = 0;
         issued_by[0] = issued_by[1] = 0;
@@ -322,6 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
     TileWalk walk;
     Tile at;
 
+    if (warp < 4) fewer_registers<kOtherRegs>();
     if (!run) {
     } else if (warp == 0) {
         if (lane == 0) {
@@ -355,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
             bool ok = true;
             for (int t = pair; ok && walk.at(A, starts, t, at); t += pairs) {
                 for (int k = at.k0; k < at.k1; ++k) {
-                    if (!mbar_wait_bounded(tempty(b), bph ^ 1, wd) || !mbar_wait_bounded(full(s), ph, wd)) {
+                    if (!mbar_wait_bounded(full(s), ph, wd) || !mbar_wait_bounded(tempty(b), bph ^ 1, wd)) {
                         ok = false;
                         break;
                     }
@@ -376,70 +507,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
                 }
             }
         }
-    } else if (warp < 2 + kReaders) {
-        const int quarter = warp & 3, c0 = (warp - 2) / 4 * kOwn;    // a warp reaches its quarter of the lanes: 32 rows
-        Stager sg{base + L::kStaging + (warp - 2) * kSlab, lane};
+    } else if (warp >= 4) {
+        more_registers<kReaderRegs>();
+        const int quarter = warp & 3, c0 = (warp - 4) / 4 * kOwn;    // a warp reaches its quarter of the lanes: 32 rows
+        Stager sg{base + L::kStaging + (warp - 4) * kSlab, lane};
         int b = 0, bph = 0, slot = 0, sph = 0;
         bool ok = true;
         for (int t = pair; ok && walk.at(A, starts, t, at); t += pairs) {
             const int row = at.row + rank * kHalf + quarter * 32 + lane;
-            const float* pa = A.a_scale + min(row, A.m - 1) * A.a_scale_ld;
-            const float* pb = A.b_scale + at.group * A.b_scale_group + min((at.n * kTN + c0) / kBK, A.b_scale_last) * A.b_scale_ld;
-            float fa = 0.0f, fb = 0.0f;
-            if (at.k0 < at.k1) {
-                fa = ld_scale(pa + at.k0);
-                if (!kRows) fb = ld_scale(pb + at.k0);
-            }
             uint64_t sums[kOwn / 2];
 #pragma unroll
             for (int j = 0; j < kOwn / 2; ++j) sums[j] = 0;
             for (int k = at.k0; k < at.k1; ++k) {
-                const float f = kRows ? fa : fa * fb;
-                if (k + 1 < at.k1) {                       // the next block's, while this one is multiplied
-                    fa = ld_scale(pa + k + 1);
-                    if (!kRows) fb = ld_scale(pb + k + 1);
-                }
-                const int of = kRows ? (k - at.k0) % kScaleBlocks : 0;
-                if (kRows && of == 0) ok = mbar_wait_bounded(sfull(slot), sph, wd);
+                const int of = (k - at.k0) % kScaleBlocks;
+                if (of == 0) ok = mbar_wait_bounded(sfull(slot), sph, wd);
+                const uint32_t scales = base + L::kScales + slot * L::kScaleBytes + of * L::kScaleWords * 4;
                 ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_bounded(tfull(b), bph, wd));
                 if (!ok) break;
                 tc_fence_after();
-                add_block<kOwn, kRows>(sums, tmem + b * kTN + c0 + (uint32_t(quarter * 32) << 16), f,
-                                       base + L::kScales + slot * kScaleBytes + (of * kTN + c0) * 4);
+                const uint32_t acc = tmem + b * kTN + c0 + (uint32_t(quarter * 32) << 16);
+                if constexpr (kRows) add_block_rows(sums, acc, scales + (quarter * 32 + lane / 4) * 4, scales + (kHalf + c0 + lane % 4 * 2) * 4);
+                else add_block<kOwn, false, 16>(sums, acc, ld_shared_f32(scales + (c0 + quarter * 32 + lane) * 4), 0);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote_relaxed(tempty(b), 0);
                 if (b) bph ^= 1;
                 b ^= 1;
-                if (kRows && (of == kScaleBlocks - 1 || k + 1 == at.k1)) {
+                if (of == kScaleBlocks - 1 || k + 1 == at.k1) {
                     if (lane == 0) mbar_arrive(sempty(slot));
                     if (slot) sph ^= 1;
                     slot ^= 1;
                 }
             }
-            if (ok) store_large(A, tc, at, sums, c0, row, sg);
+            if (ok) store_large<kRows>(A, tc, at, sums, c0, row, sg);
         }
         if (lane == 0) bulk_wait_all();
-    } else {
-        // Scales of b's rows, four blocks of K at a time: 32 loads a lane are under way at once.
+    } else if (warp == 2) {
+        // Scales, four blocks of K at a time: 16 to 48 loads a lane are under way at once.
         int slot = 0, sph = 0;
         bool ok = true;
         for (int t = pair; ok && walk.at(A, starts, t, at); t += pairs) {
+            const float* pb = A.b_scale + at.group * A.b_scale_group;
             for (int k = at.k0; k < at.k1; k += kScaleBlocks) {
-                float v[kScaleBlocks][kTN / 32];
+                float v[kScaleBlocks][kHalf / 32], w[kScaleBlocks][kRows ? kTN / 32 : 2];
 #pragma unroll
-                for (int j = 0; j < kTN / 32; ++j) {
-                    const float* p = A.b_scale + min(at.n * kTN + j * 32 + lane, A.b_scale_last) * A.b_scale_ld + k;
+                for (int j = 0; j < kHalf / 32; ++j)
+                    load_scales(A.a_scale + min(at.row + rank * kHalf + j * 32 + lane, A.m - 1) * A.a_scale_ld, k, at.k1, v, j);
 #pragma unroll
-                    for (int i = 0; i < kScaleBlocks; ++i) v[i][j] = k + i < at.k1 ? ld_scale(p + i) : 0.0f;
-                }
+                for (int j = 0; j < (kRows ? kTN / 32 : 2); ++j)
+                    load_scales(pb + min(kRows ? at.n * kTN + j * 32 + lane : at.n * 2 + j, A.b_scale_last) * A.b_scale_ld, k, at.k1, w, j);
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sempty(slot), sph ^ 1, wd));
                 if (!ok) break;
-                const uint32_t to = base + L::kScales + slot * kScaleBytes + lane * 4;
+                const uint32_t to = base + L::kScales + slot * L::kScaleBytes + lane * 4;
 #pragma unroll
-                for (int j = 0; j < kTN / 32; ++j)
+                for (int i = 0; i < kScaleBlocks; ++i) {
 #pragma unroll
-                    for (int i = 0; i < kScaleBlocks; ++i) st_shared_f32(to + (i * kTN + j * 32) * 4, v[i][j]);
+                    for (int j = 0; j < kHalf / 32; ++j) {
+                        st_shared_f32(to + (i * L::kScaleWords + j * 32) * 4, kRows ? v[i][j] : v[i][j] * w[i][0]);
+                        if (!kRows) st_shared_f32(to + (i * L::kScaleWords + kHalf + j * 32) * 4, v[i][j] * w[i][1]);
+                    }
+                    if (kRows)
+#pragma unroll
+                        for (int j = 0; j < kTN / 32; ++j) st_shared_f32(to + (i * L::kScaleWords + kHalf + j * 32) * 4, w[i][j]);
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sfull(slot));
                 if (slot) sph ^= 1;
@@ -528,7 +658,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(words + 8);
     volatile uint32_t* issued_by = reinterpret_cast<volatile uint32_t*>(words + 16);
     int* starts = reinterpret_cast<int*>(smem + L::kStarts);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int part = int(blockIdx.x % unsigned(splits)), tile = int(blockIdx.x / unsigned(splits));
 
     if (threadIdx.x == 0) {
@@ -654,7 +784,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tfull(b), bph, wd));
             if (!ok) break;
             tc_fence_after();
-            add_block<kT, true>(sums, tmem + b * kT + (uint32_t(quarter * 32) << 16), f, to);
+            add_block<kT, true, 16>(sums, tmem + b * kT + (uint32_t(quarter * 32) << 16), f, to);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty(b));
