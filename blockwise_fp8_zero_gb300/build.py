@@ -27,7 +27,7 @@ CPP_SOURCES = ["host.cpp", "plan.cpp"]
 HEADERS = [os.path.join(CSRC, "fp8z_device.cuh"), os.path.join(CSRC, "fp8z_host.h"),
            os.path.join(CSRC, "fp8z_elem.cuh"), os.path.join(CSRC, "fp8z_tcgen05.cuh"),
            os.path.join(CSRC, "fp8z_launch.cuh"), os.path.join(CSRC, "fp8z_tiles.h"),
-           os.path.join(CSRC, "fp8z_stage.cuh"),
+           os.path.join(CSRC, "fp8z_stage.cuh"), os.path.join(CSRC, "fp8z_pairs.cuh"),
            os.path.join(INCLUDE, "fp8z.h")]
 
 

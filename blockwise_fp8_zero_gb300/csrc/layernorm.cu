@@ -20,6 +20,7 @@
 #include "fp8z_elem.cuh"
 #include "fp8z_host.h"
 #include "fp8z_launch.cuh"
+#include "fp8z_pairs.cuh"
 
 namespace fp8z {
 namespace {
@@ -149,8 +150,13 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2* shared, int 
 // The scale and codes of 128 columns, held by 16 lanes: the rule of fp8z_quantize_rowwise.
 __device__ __forceinline__ float tile_scale(float amax, bool pow2) {
     if (amax == 0.0f) return 1.0f;
-    const float s = fmaxf(__fdiv_rn(amax, 448.0f), FLT_MIN);
-    if (!pow2) return s;
+    if (!pow2) {
+        // the rounded quotient, corrected by the remainder as in tile_codes
+        constexpr float c = 1.0f / 448.0f;
+        const float t = amax * c;
+        if (amax > 0x1p-90f && amax < 0x1p120f) return fmaf(fmaf(-t, 448.0f, amax), c, t);
+        return fmaxf(__fdiv_rn(amax, 448.0f), FLT_MIN);
+    }
     if (amax > FLT_MAX) return __uint_as_float(254u << 23);                        // 2^127
     // the smallest power of two that is not below amax / 448, from amax = f 2^e, f in [1/2, 1):
     // 448 = 7/8 * 2^9
@@ -285,6 +291,260 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
     }
 }
 
+// ------------------------------------------------------- rows through a queue
+// 16 bytes into shared memory in the background; zeros where `in` is false.
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// kN sums over a block of kThreads, the same in each thread, in a fixed order.  In a warp
+// half of the sums change lanes at every step, so that four sums take six shuffles.
+template <int kN, int kThreads>
+__device__ __forceinline__ void block_sums(float (&v)[kN], float* shared) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int which = 0, off = 16;
+#pragma unroll
+    for (int n = kN / 2; n > 0; n /= 2, off /= 2) {
+        const bool high = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float mine = high ? v[i + n] : v[i], other = high ? v[i] : v[i + n];
+            v[i] = mine + __shfl_xor_sync(0xFFFFFFFFu, other, off);
+        }
+        if (high) which += n;
+    }
+    const int last = off;                                // lanes that hold the same sum differ below it
+#pragma unroll
+    for (; off > 0; off /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], off);
+    if ((lane & (2 * last - 1)) == 0) shared[warp * kN + which] = v[0];
+    __syncthreads();
+    // the warps' sums, 32 / kN lanes for each of the kN, in every warp alike
+    constexpr int kEach = 32 / kN;
+    float all = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; w += kEach) {
+        const int mine = w + lane % kEach;
+        if (mine < kThreads / 32) all += shared[mine * kN + lane / kEach];
+    }
+#pragma unroll
+    for (int o = kEach / 2; o > 0; o /= 2) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, all, i * kEach);
+}
+
+// A thread's own queue: its columns of the next batches of rows are on their way into
+// shared memory while it works on one, and nobody else reads them, so that no barrier
+// guards the queue.  No registers hold loads: up to 196 KB an SM are a batch in work and the
+// others on their way.
+template <typename T, int kThreads, int kVecs, int kRows, int kTensors>
+struct Queue {
+    static constexpr int kUnits = Eight<T>::kUnits;
+    static constexpr int kBatch = kTensors * kRows * kVecs * kUnits * kThreads * 16;
+    static constexpr int kQueue = 6 / (kTensors * kRows * kUnits / 2);     // batches: one in work, the others on their way
+    static constexpr int kBytes = kQueue * kBatch;
+    uint32_t base;                                       // of this thread
+    __device__ __forceinline__ uint32_t at(int slot, int tensor, int r, int j, int u) const {
+        return base + slot * kBatch + (((tensor * kRows + r) * kVecs + j) * kUnits + u) * (kThreads * 16);
+    }
+    __device__ __forceinline__ void fetch(int slot, int tensor, const T* p, int64_t ld, int64_t row0, int rows, int cols) const {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int c = (j * kThreads + int(threadIdx.x)) * kVec;
+                const bool in = row0 + r < rows && c < cols;
+                const T* from = in ? p + (row0 + r) * ld + c : p;
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) copy_16(at(slot, tensor, r, j, u), reinterpret_cast<const uint4*>(from) + u, in);
+            }
+    }
+    __device__ __forceinline__ Eight<T> load(int slot, int tensor, int r, int j) const {
+        Eight<T> x;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x.u[u].x), "=r"(x.u[u].y), "=r"(x.u[u].z), "=r"(x.u[u].w)
+                         : "r"(at(slot, tensor, r, j, u))
+                         : "memory");
+        return x;
+    }
+};
+
+// Eight results as T, 16 bytes at a time.
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const uint64_t (&v)[4]) {
+    Pack<T, kVec> y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = halves(v[i]);
+        y.v[2 * i] = Elem<T>::narrow(f.x);
+        y.v[2 * i + 1] = Elem<T>::narrow(f.y);
+    }
+    st_vec(p, y);
+}
+
+// The codes of eight columns of a tile with scale s: E4M3(v / s).  v / s is formed as v times
+// 1 / s and one correction by the remainder (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000", 1990), which is the rounded quotient wherever nothing
+// overflows or goes below 2^-126 on the way; scales where it might take the division.
+__device__ __forceinline__ uint2 tile_codes(const uint64_t (&v)[4], float s, bool pow2) {
+    float t[kVec];
+    if (pow2 || (s > 0x1p-60f && s < 0x1p100f)) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+        r = pow2 ? __frcp_rn(s) : fmaf(fmaf(-s, r, 1.0f), r, r);             // exact for a power of two
+        const uint64_t rr = pair_of(r, r), ss = pair_of(-s, -s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t q = mul_pair(v[i], rr);
+            if (!pow2) q = fma_pair(fma_pair(q, ss, v[i]), rr, q);
+            const float2 f = halves(q);
+            t[2 * i] = f.x;
+            t[2 * i + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = halves(v[i]);
+            t[2 * i] = __fdiv_rn(f.x, s);
+            t[2 * i + 1] = __fdiv_rn(f.y, s);
+        }
+    }
+    return make_uint2(pack_e4m3x4(t[0], t[1], t[2], t[3]), pack_e4m3x4(t[4], t[5], t[6], t[7]));
+}
+
+// Batches of kRows rows, one block a batch at a time: the sums of a batch share two barriers.
+template <typename T, int kThreads, int kVecs, int kRows, bool kCodes>
+__global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_queue_kernel(const __grid_constant__ Norm A) {
+    using Q = Queue<T, kThreads, kVecs, kRows, 1>;
+    constexpr int kQueue = Q::kQueue;
+    extern __shared__ uint4 smem[];
+    __shared__ float shared[2][kThreads / 32 * kRows];
+    dependent_wait();
+    const Q q{smem_addr(smem) + threadIdx.x * 16};
+    const T* x = static_cast<const T*>(A.x);
+    const int64_t batches = (int64_t(A.rows) + kRows - 1) / kRows;
+    const float n = float(A.cols);
+    uint64_t w[kVecs][4], b[kVecs][4];
+    bool in[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+        in[j] = (j * kThreads + int(threadIdx.x)) * kVec < A.cols;
+        float v[kVec], u[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] = 1.0f, u[e] = 0.0f;
+        if (A.weight) load8_param<true, kThreads>(A.weight, A.param_dtype, j, threadIdx.x, A.cols, v);
+        if (A.bias) load8_param<true, kThreads>(A.bias, A.param_dtype, j, threadIdx.x, A.cols, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[j][i] = pair_of(v[2 * i], v[2 * i + 1]), b[j][i] = pair_of(u[2 * i], u[2 * i + 1]);
+    }
+#pragma unroll
+    for (int d = 0; d < kQueue - 1; ++d) {
+        q.fetch(d, 0, x, A.x_ld, (blockIdx.x + int64_t(d) * gridDim.x) * kRows, A.rows, A.cols);
+        copy_commit();
+    }
+    int slot = 0;
+    for (int64_t batch = blockIdx.x; batch < batches; batch += gridDim.x) {
+        q.fetch(slot == 0 ? kQueue - 1 : slot - 1, 0, x, A.x_ld, (batch + int64_t(kQueue - 1) * gridDim.x) * kRows, A.rows, A.cols);
+        copy_commit();
+        copy_wait<kQueue - 1>();
+        uint64_t v[kRows][kVecs][4];
+        float mean[kRows], rstd[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            uint64_t s = 0;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const Eight<T> raw = q.load(slot, 0, r, j);      // zeros past the row's end
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[r][j][i] = raw.pair(i);
+                    s = add_pair(s, v[r][j][i]);
+                }
+            }
+            const float2 f = halves(s);
+            mean[r] = f.x + f.y;
+        }
+        block_sums<kRows, kThreads>(mean, shared[0]);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            mean[r] /= n;
+            const uint64_t m = pair_of(-mean[r], -mean[r]);
+            uint64_t s = 0;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[r][j][i] = add_pair(v[r][j][i], m);
+                    if (in[j]) s = fma_pair(v[r][j][i], v[r][j][i], s);
+                }
+            const float2 f = halves(s);
+            rstd[r] = f.x + f.y;
+        }
+        block_sums<kRows, kThreads>(rstd, shared[1]);
+        const int64_t row0 = batch * kRows;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            rstd[r] = __frcp_rn(__fsqrt_rn(rstd[r] / n + A.eps));
+            if (threadIdx.x == 0 && row0 + r < A.rows) {
+                if (A.mean) A.mean[row0 + r] = mean[r];
+                if (A.rstd) A.rstd[row0 + r] = rstd[r];
+            }
+            const uint64_t f = pair_of(rstd[r], rstd[r]);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[r][j][i] = fma_pair(mul_pair(v[r][j][i], f), w[j][i], b[j][i]);
+        }
+        if (A.y)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+                    if (in[j] && row0 + r < A.rows)
+                        store_pairs(static_cast<T*>(A.y) + (row0 + r) * A.y_ld + (j * kThreads + threadIdx.x) * kVec, v[r][j]);
+        if constexpr (kCodes) {
+            float amax[kRows][kVecs];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    amax[r][j] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = halves(v[r][j][i]);
+                        amax[r][j] = fmaxf(amax[r][j], fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                    for (int j = 0; j < kVecs; ++j) amax[r][j] = fmaxf(amax[r][j], __shfl_xor_sync(0xFFFFFFFFu, amax[r][j], o));
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    const int c = (j * kThreads + int(threadIdx.x)) * kVec;
+                    const float s = tile_scale(amax[r][j], A.pow2);
+                    const uint2 codes = tile_codes(v[r][j], s, A.pow2);
+                    if (in[j] && row0 + r < A.rows) {
+                        *reinterpret_cast<uint2*>(A.q + (row0 + r) * A.cols + c) = codes;
+                        if ((threadIdx.x & 15) == 0) A.q_scale[(row0 + r) * (A.cols / FP8Z_BLOCK) + c / FP8Z_BLOCK] = s;
+                    }
+                }
+        }
+        slot = slot + 1 == kQueue ? 0 : slot + 1;
+    }
+    copy_wait<0>();
+}
+
 // ---------------------------------------------------------------- gradient
 // A block walks over rows, keeps its columns' sums of dy xh and dy in registers, and
 // leaves them in `part` at the end: dy and x are read once.
@@ -372,6 +632,110 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) norm_grad_ker
     }
 }
 
+// The same with a queue of dy and x: both are read from shared memory again for dx, so that
+// registers hold the sums of dw and db, and the weight, only.
+template <typename T, int kThreads, int kVecs, int kRows>
+__global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_grad_queue_kernel(const __grid_constant__ NormGrad A) {
+    using Q = Queue<T, kThreads, kVecs, kRows, 2>;
+    constexpr int kQueue = Q::kQueue;
+    extern __shared__ uint4 smem[];
+    __shared__ float shared[2][kThreads / 32 * 2 * kRows];
+    dependent_wait();
+    const Q q{smem_addr(smem) + threadIdx.x * 16};
+    const T *x = static_cast<const T*>(A.x), *dy = static_cast<const T*>(A.dy);
+    const int64_t batches = (int64_t(A.rows) + kRows - 1) / kRows;
+    const float n = float(A.cols);
+    uint64_t w[kVecs][4], dw[kVecs][4], db[kVecs][4];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+        float v[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] = 1.0f;
+        if (A.weight) load8_param<true, kThreads>(A.weight, A.param_dtype, j, threadIdx.x, A.cols, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[j][i] = pair_of(v[2 * i], v[2 * i + 1]), dw[j][i] = db[j][i] = 0;
+    }
+    const auto fetch = [&](int slot, int64_t batch) {
+        q.fetch(slot, 0, x, A.x_ld, batch * kRows, A.rows, A.cols);
+        q.fetch(slot, 1, dy, A.dy_ld, batch * kRows, A.rows, A.cols);
+        copy_commit();
+    };
+    float mean[kRows], rstd[kRows];                              // of the next batch
+    const auto stats = [&](int64_t batch) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const bool in = batch * kRows + r < A.rows;
+            mean[r] = in ? load_one(A.mean + batch * kRows + r) : 0.0f;
+            rstd[r] = in ? load_one(A.rstd + batch * kRows + r) : 0.0f;
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < kQueue - 1; ++d) fetch(d, blockIdx.x + int64_t(d) * gridDim.x);
+    stats(blockIdx.x);
+    int slot = 0, turn = 0;
+    for (int64_t batch = blockIdx.x; batch < batches; batch += gridDim.x) {
+        fetch(slot == 0 ? kQueue - 1 : slot - 1, batch + int64_t(kQueue - 1) * gridDim.x);
+        copy_wait<kQueue - 1>();
+        uint64_t m[kRows], f[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) m[r] = pair_of(-mean[r], -mean[r]), f[r] = pair_of(rstd[r], rstd[r]);
+        stats(batch + gridDim.x);
+        float sums[2 * kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            uint64_t s1 = 0, s2 = 0;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const Eight<T> xv = q.load(slot, 0, r, j), dv = q.load(slot, 1, r, j);   // zeros past the row's end
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t xh = mul_pair(add_pair(xv.pair(i), m[r]), f[r]), d = dv.pair(i), g = mul_pair(d, w[j][i]);
+                    dw[j][i] = fma_pair(d, xh, dw[j][i]);
+                    db[j][i] = add_pair(db[j][i], d);
+                    s1 = add_pair(s1, g);
+                    s2 = fma_pair(g, xh, s2);
+                }
+            }
+            const float2 a = halves(s1), c = halves(s2);
+            sums[r] = a.x + a.y;
+            sums[kRows + r] = c.x + c.y;
+        }
+        block_sums<2 * kRows, kThreads>(sums, shared[turn]);
+        turn ^= 1;
+        if (A.dx)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int64_t row = batch * kRows + r;
+                if (row >= A.rows) break;
+                const float c1 = sums[r] / n, c2 = sums[kRows + r] / n;
+                const uint64_t n1 = pair_of(-c1, -c1), n2 = pair_of(-c2, -c2);
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    const int c = (j * kThreads + int(threadIdx.x)) * kVec;
+                    if (c >= A.cols) break;
+                    const Eight<T> xv = q.load(slot, 0, r, j), dv = q.load(slot, 1, r, j);
+                    uint64_t v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t xh = mul_pair(add_pair(xv.pair(i), m[r]), f[r]), g = mul_pair(dv.pair(i), w[j][i]);
+                        v[i] = mul_pair(fma_pair(xh, n2, add_pair(g, n1)), f[r]);
+                    }
+                    store_pairs(static_cast<T*>(A.dx) + row * A.dx_ld + c, v);
+                }
+            }
+        slot = slot + 1 == kQueue ? 0 : slot + 1;
+    }
+    copy_wait<0>();
+    float* out = A.part + int64_t(blockIdx.x) * 2 * A.cols;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+        const int c = (j * kThreads + int(threadIdx.x)) * kVec;
+        if (c >= A.cols) break;
+        store_pairs(out + c, dw[j]);
+        store_pairs(out + A.cols + c, db[j]);
+    }
+}
+
 // Rows longer than 32768 columns: the sums of dw and db are added to in `part`.
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const __grid_constant__ NormGrad A) {
@@ -410,12 +774,12 @@ __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const __grid_const
     }
 }
 
-// dw and db from the blocks' parts: 32 columns a block, its eight warps take every eighth part
+// dw and db from the blocks' parts: 32 columns a block, its 32 warps take every 32nd part
 // and join in order.
 template <typename P>
-__global__ void __launch_bounds__(256) norm_parts_kernel(const float* part, int parts, int cols, P* dweight, P* dbias,
-                                                         int accumulate) {
-    __shared__ float joined[8][32];
+__global__ void __launch_bounds__(1024) norm_parts_kernel(const float* part, int parts, int cols, P* dweight, P* dbias,
+                                                          int accumulate) {
+    __shared__ float joined[32][33];
     dependent_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
     P* out = blockIdx.y ? dbias : dweight;
@@ -423,19 +787,19 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(const float* part, int 
     float sum = 0.0f;
     if (c < cols)
 #pragma unroll 8
-        for (int i = warp; i < parts; i += 8) sum += __ldcg(part + (int64_t(i) * 2 + blockIdx.y) * cols + c);
+        for (int i = warp; i < parts; i += 32) sum += __ldcg(part + (int64_t(i) * 2 + blockIdx.y) * cols + c);
     joined[warp][lane] = sum;
     __syncthreads();
-    if (warp != 0 || c >= cols) return;
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += joined[i][lane];
-    out[c] = Elem<P>::narrow(accumulate ? Elem<P>::widen(out[c]) + sum : sum);
+    const int mine = blockIdx.x * 32 + warp;             // a warp joins one column
+    sum = warp_sum(joined[lane][warp]);
+    if (lane == 0 && mine < cols) out[mine] = Elem<P>::narrow(accumulate ? Elem<P>::widen(out[mine]) + sum : sum);
 }
 
 // ------------------------------------------------------------------- host
 constexpr int kLongest = 32768;                        // columns a block's registers hold
-constexpr int kMaxParts = 304;                         // two blocks an SM
+
+// Blocks, and parts of the weight's gradient, at most: what SMs hold at a time.
+int64_t most_parts(int64_t cols) { return cols <= 32 * kVec * 2 ? 304 : cols <= 1024 ? 1216 : cols <= 2048 ? 608 : 304; }
 
 bool vectors(const void* p, int64_t ld, int64_t rows, int dtype) {
     return host::aligned(p, 16) && (rows <= 1 || ld * dtype_bytes(dtype) % 16 == 0);
@@ -459,16 +823,69 @@ int start_width(const Norm& A, int sms, cudaStream_t st) {
     return start<T, kWide, 1024, 4>(A, sms, st);
 }
 
+// Rows that the queues take: whole vectors, more columns than a warp's eight rows and no more
+// than a block's registers, and enough rows to fill the SMs.
+bool queued(bool wide, int64_t rows, int64_t cols, int sms) {
+    return wide && cols % kVec == 0 && cols > 32 * kVec * 2 && cols <= 8192 && rows > 2 * sms;
+}
+
+template <typename T, int kThreads, int kVecs, bool kCodes>
+int start_queue_codes(const Norm& A, int slot, int sms, cudaStream_t st) {
+    constexpr int kRows = 2;
+    using Q = Queue<T, kThreads, kVecs, kRows, 1>;
+    const auto k = &norm_queue_kernel<T, kThreads, kVecs, kRows, kCodes>;
+    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot + 16 * kCodes, Q::kBytes)) return rc;
+    const int64_t batches = (int64_t(A.rows) + kRows - 1) / kRows, most = int64_t(sms) * (1024 / (kThreads * kVecs));
+    return launch_dependent(k, dim3(unsigned(std::min(batches, most))), kThreads, Q::kBytes, st, A);
+}
+
+template <typename T, int kThreads, int kVecs>
+int start_queue(const Norm& A, int slot, int sms, cudaStream_t st) {
+    return A.q ? start_queue_codes<T, kThreads, kVecs, true>(A, slot, sms, st) : start_queue_codes<T, kThreads, kVecs, false>(A, slot, sms, st);
+}
+
 template <typename T>
-int start_type(const Norm& A, bool wide, int sms, cudaStream_t st) {
+int start_queue(const Norm& A, int slot, int sms, cudaStream_t st) {
+    if (A.cols <= 128 * kVec) return start_queue<T, 128, 1>(A, slot, sms, st);
+    if (A.cols <= 256 * kVec) return start_queue<T, 256, 1>(A, slot + 1, sms, st);
+    if (A.cols <= 512 * kVec) return start_queue<T, 512, 1>(A, slot + 2, sms, st);
+    return start_queue<T, 512, 2>(A, slot + 3, sms, st);
+}
+
+template <typename T, int kThreads, int kVecs>
+int start_grad_queue(const NormGrad& A, int slot, int parts, cudaStream_t st) {
+    constexpr int kRows = sizeof(T) == 2 ? 2 : 1;
+    using Q = Queue<T, kThreads, kVecs, kRows, 2>;
+    const auto k = &norm_grad_queue_kernel<T, kThreads, kVecs, kRows>;
+    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot, Q::kBytes)) return rc;
+    return launch_dependent(k, dim3(unsigned(parts)), kThreads, Q::kBytes, st, A);
+}
+
+template <typename T>
+int start_grad_queue(const NormGrad& A, int slot, int parts, cudaStream_t st) {
+    if (A.cols <= 128 * kVec) return start_grad_queue<T, 128, 1>(A, slot, parts, st);
+    if (A.cols <= 256 * kVec) return start_grad_queue<T, 256, 1>(A, slot + 1, parts, st);
+    if (A.cols <= 512 * kVec) return start_grad_queue<T, 512, 1>(A, slot + 2, parts, st);
+    return start_grad_queue<T, 512, 2>(A, slot + 3, parts, st);
+}
+
+template <typename T>
+int start_type(const Norm& A, bool wide, int slot, int sms, cudaStream_t st) {
+    if (queued(wide, A.rows, A.cols, sms)) return start_queue<T>(A, slot, sms, st);
     if (A.cols > kLongest)
         return launch_dependent(&norm_long_kernel<T>, dim3(unsigned(std::min(A.rows, sms * 2))), 1024, 0, st, A);
     return wide ? start_width<T, true>(A, sms, st) : start_width<T, false>(A, sms, st);
 }
 
-int parts_of(int64_t rows, int64_t cols, int sms) {
+// Blocks of the gradient, each of which leaves a part.
+int parts_of(int64_t rows, int64_t cols, bool wide, int dtype, int sms) {
+    if (queued(wide, rows, cols, sms)) {
+        const int per = dtype == FP8Z_F32 ? 1 : 2;
+        const int64_t an_sm = cols <= 128 * kVec ? 8 : cols <= 256 * kVec ? 4 : cols <= 512 * kVec ? 2 : 1;
+        return int(std::min<int64_t>({(rows + per - 1) / per, sms * an_sm, most_parts(cols)}));
+    }
     const int64_t blocks = cols <= 32 * kVec * 2 ? (rows + 7) / 8 : rows;
-    return int(std::min<int64_t>({std::max<int64_t>(blocks, 1), int64_t(sms) * (cols <= 256 * kVec ? 2 : 1), kMaxParts}));
+    return int(std::min<int64_t>({std::max<int64_t>(blocks, 1), int64_t(sms) * (cols <= 256 * kVec ? 2 : 1), most_parts(cols)}));
 }
 
 template <typename T, bool kWide, int kThreads, int kVecs>
@@ -487,7 +904,8 @@ int start_grad_width(const NormGrad& A, int parts, cudaStream_t st) {
 }
 
 template <typename T>
-int start_grad_type(const NormGrad& A, bool wide, int parts, cudaStream_t st) {
+int start_grad_type(const NormGrad& A, bool wide, int slot, int parts, int sms, cudaStream_t st) {
+    if (queued(wide, A.rows, A.cols, sms)) return start_grad_queue<T>(A, slot, parts, st);
     if (A.cols > kLongest) return launch_dependent(&norm_grad_long_kernel<T>, dim3(unsigned(parts)), 1024, 0, st, A);
     return wide ? start_grad_width<T, true>(A, parts, st) : start_grad_width<T, false>(A, parts, st);
 }
@@ -524,15 +942,15 @@ extern "C" int fp8z_layer_norm(const void* x, const void* weight, const void* bi
     const Norm A = {int(a.rows), int(a.cols), x, a.x_ld, weight, bias, a.param_dtype, y, a.y_ld, mean, rstd, a.eps,
                     q, q_scale, a.pow2};
     const auto st = static_cast<cudaStream_t>(stream);
-    if (a.dtype == FP8Z_F32) return start_type<float>(A, wide, sms, st);
-    if (a.dtype == FP8Z_BF16) return start_type<__nv_bfloat16>(A, wide, sms, st);
-    return start_type<__half>(A, wide, sms, st);
+    if (a.dtype == FP8Z_F32) return start_type<float>(A, wide, 32, sms, st);
+    if (a.dtype == FP8Z_BF16) return start_type<__nv_bfloat16>(A, wide, 36, sms, st);
+    return start_type<__half>(A, wide, 40, sms, st);
 }
 
 extern "C" int64_t fp8z_layer_norm_grad_workspace(int64_t rows, int64_t cols) {
     using namespace fp8z;
     if (rows < 0 || rows > (1LL << 30) || cols < 1 || cols > (1LL << 24)) return FP8Z_EINVAL;
-    return std::min<int64_t>(std::max<int64_t>(rows, 1), kMaxParts) * 2 * cols * 4;
+    return std::min<int64_t>(std::max<int64_t>(rows, 1), most_parts(cols)) * 2 * cols * 4;
 }
 
 extern "C" int fp8z_layer_norm_grad(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
@@ -558,20 +976,20 @@ extern "C" int fp8z_layer_norm_grad(const void* dy, const void* x, const void* w
     auto* part = static_cast<float*>(workspace);
     int parts = 0;
     if (a.rows > 0) {
-        parts = parts_of(a.rows, a.cols, sms);
         const bool wide = vectors(x, a.x_ld, a.rows, a.dtype) && vectors(dy, a.dy_ld, a.rows, a.dtype) && vectors(weight, 0, 1, 0) &&
                           (!dx || vectors(dx, a.dx_ld, a.rows, a.dtype));
+        parts = parts_of(a.rows, a.cols, wide, a.dtype, sms);
         const NormGrad A = {int(a.rows), int(a.cols), dy, x, a.dy_ld, a.x_ld, a.dx_ld, weight, a.param_dtype, mean, rstd, dx, part};
-        const int rc = a.dtype == FP8Z_F32 ? start_grad_type<float>(A, wide, parts, st)
-                       : a.dtype == FP8Z_BF16 ? start_grad_type<__nv_bfloat16>(A, wide, parts, st)
-                                              : start_grad_type<__half>(A, wide, parts, st);
+        const int rc = a.dtype == FP8Z_F32 ? start_grad_type<float>(A, wide, 64, parts, sms, st)
+                       : a.dtype == FP8Z_BF16 ? start_grad_type<__nv_bfloat16>(A, wide, 68, parts, sms, st)
+                                              : start_grad_type<__half>(A, wide, 72, parts, sms, st);
         if (rc) return rc;
     }
     if (!dweight && !dbias) return FP8Z_OK;
     const dim3 grid(unsigned((a.cols + 31) / 32), dbias ? 2 : 1);
     const auto join = [&](auto* dw, auto* db) {
         using P = std::remove_pointer_t<decltype(dw)>;
-        return launch_dependent(&norm_parts_kernel<P>, grid, 256, 0, st, part, parts, int(a.cols), dw, db, a.accumulate);
+        return launch_dependent(&norm_parts_kernel<P>, grid, 1024, 0, st, part, parts, int(a.cols), dw, db, a.accumulate);
     };
     if (a.param_dtype == FP8Z_F32) return join(static_cast<float*>(dweight), static_cast<float*>(dbias));
     if (a.param_dtype == FP8Z_BF16) return join(static_cast<__nv_bfloat16*>(dweight), static_cast<__nv_bfloat16*>(dbias));

@@ -23,6 +23,7 @@
 #include "fp8z_elem.cuh"
 #include "fp8z_host.h"
 #include "fp8z_launch.cuh"
+#include "fp8z_pairs.cuh"
 #include "fp8z_stage.cuh"
 #include "fp8z_tcgen05.cuh"
 
@@ -83,31 +84,6 @@ __device__ __forceinline__ void fewer_registers() {
 template <int kRegs>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
-// Two FP32 numbers in one register pair: the packed instructions do both at once.
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ void halves(uint64_t p, uint32_t& a, uint32_t& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p));
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // The registers of a tmem_ld16 or tmem_ld32 hold their values from here on.
