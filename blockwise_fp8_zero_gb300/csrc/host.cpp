@@ -87,7 +87,7 @@ std::atomic<int64_t> g_wait_limit_ns{kDefaultTimeoutNs};
 int64_t wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 
 namespace {
-constexpr int kMaxSlots = 80;
+constexpr int kMaxSlots = 48;
 std::atomic<int> g_smem_done[kMaxSlots][kMaxDevices];
 }  // namespace
 

@@ -150,13 +150,7 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2* shared, int 
 // The scale and codes of 128 columns, held by 16 lanes: the rule of fp8z_quantize_rowwise.
 __device__ __forceinline__ float tile_scale(float amax, bool pow2) {
     if (amax == 0.0f) return 1.0f;
-    if (!pow2) {
-        // the rounded quotient, corrected by the remainder as in tile_codes
-        constexpr float c = 1.0f / 448.0f;
-        const float t = amax * c;
-        if (amax > 0x1p-90f && amax < 0x1p120f) return fmaf(fmaf(-t, 448.0f, amax), c, t);
-        return fmaxf(__fdiv_rn(amax, 448.0f), FLT_MIN);
-    }
+    if (!pow2) return fmaxf(__fdiv_rn(amax, 448.0f), FLT_MIN);
     if (amax > FLT_MAX) return __uint_as_float(254u << 23);                        // 2^127
     // the smallest power of two that is not below amax / 448, from amax = f 2^e, f in [1/2, 1):
     // 448 = 7/8 * 2^9
@@ -302,11 +296,11 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// kN sums over a block of kThreads, the same in each thread, in a fixed order.  In a warp
-// half of the sums change lanes at every step, so that four sums take six shuffles.
-template <int kN, int kThreads>
+// kN sums over a block of at most 16 warps, the same in each thread, in a fixed order.  In a
+// warp half of the sums change lanes at every step, so that four sums take six shuffles.
+template <int kN>
 __device__ __forceinline__ void block_sums(float (&v)[kN], float* shared) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int which = 0, off = 16;
 #pragma unroll
     for (int n = kN / 2; n > 0; n /= 2, off /= 2) {
@@ -327,9 +321,9 @@ __device__ __forceinline__ void block_sums(float (&v)[kN], float* shared) {
     constexpr int kEach = 32 / kN;
     float all = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; w += kEach) {
+    for (int w = 0; w < 16; w += kEach) {
         const int mine = w + lane % kEach;
-        if (mine < kThreads / 32) all += shared[mine * kN + lane / kEach];
+        if (mine < warps) all += shared[mine * kN + lane / kEach];
     }
 #pragma unroll
     for (int o = kEach / 2; o > 0; o /= 2) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
@@ -341,27 +335,29 @@ __device__ __forceinline__ void block_sums(float (&v)[kN], float* shared) {
 // shared memory while it works on one, and nobody else reads them, so that no barrier
 // guards the queue.  No registers hold loads: up to 196 KB an SM are a batch in work and the
 // others on their way.
-template <typename T, int kThreads, int kVecs, int kRows, int kTensors>
+template <typename T, int kVecs, int kRows, int kTensors>
 struct Queue {
-    static constexpr int kUnits = Eight<T>::kUnits;
-    static constexpr int kBatch = kTensors * kRows * kVecs * kUnits * kThreads * 16;
-    static constexpr int kQueue = 6 / (kTensors * kRows * kUnits / 2);     // batches: one in work, the others on their way
-    static constexpr int kBytes = kQueue * kBatch;
-    uint32_t base;                                       // of this thread
+    static constexpr int kUnits = Eight<T>::kUnits, kPieces = kTensors * kRows * kVecs * kUnits;
+    static constexpr int kQueue = 6 / (kTensors * kRows * kUnits / 2);
+    static constexpr int bytes(int threads) { return kQueue * kPieces * threads * 16; }
+    uint32_t base, step;                                 // of this thread; bytes from one piece to the next
     __device__ __forceinline__ uint32_t at(int slot, int tensor, int r, int j, int u) const {
-        return base + slot * kBatch + (((tensor * kRows + r) * kVecs + j) * kUnits + u) * (kThreads * 16);
+        return base + (slot * kPieces + ((tensor * kRows + r) * kVecs + j) * kUnits + u) * step;
     }
-    __device__ __forceinline__ void fetch(int slot, int tensor, const T* p, int64_t ld, int64_t row0, int rows, int cols) const {
+    __device__ __forceinline__ void fetch(int slot, int tensor, const T* p, int64_t ld, int64_t row0, int rows,
+                                          const bool (&in)[kVecs]) const {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
+        for (int r = 0; r < kRows; ++r) {
+            const bool there = row0 + r < rows;
+            const T* row = p + (there ? row0 + r : 0) * ld;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                const int c = (j * kThreads + int(threadIdx.x)) * kVec;
-                const bool in = row0 + r < rows && c < cols;
-                const T* from = in ? p + (row0 + r) * ld + c : p;
+                const bool mine = there && in[j];
+                const uint4* from = reinterpret_cast<const uint4*>(row + (mine ? (j * blockDim.x + threadIdx.x) * kVec : 0));
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u) copy_16(at(slot, tensor, r, j, u), reinterpret_cast<const uint4*>(from) + u, in);
+                for (int u = 0; u < kUnits; ++u) copy_16(at(slot, tensor, r, j, u), from + u, mine);
             }
+        }
     }
     __device__ __forceinline__ Eight<T> load(int slot, int tensor, int r, int j) const {
         Eight<T> x;
@@ -374,6 +370,23 @@ struct Queue {
         return x;
     }
 };
+
+// The columns of a thread of the queued kernels, `j` of kVecs: those from eight(j) on.
+__device__ __forceinline__ int eight(int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * kVec; }
+
+// Their weights, or `otherwise` where there are none.
+__device__ __forceinline__ void params8(const void* p, int dtype, int j, bool in, float otherwise, uint64_t (&w)[4]) {
+    float v[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v[e] = otherwise;
+    if (p && in) {
+        if (dtype == FP8Z_F32) load8<true, 0, false>(static_cast<const float*>(p) + eight(j), 0, 0, kVec, v);
+        else if (dtype == FP8Z_BF16) load8<true, 0, false>(static_cast<const __nv_bfloat16*>(p) + eight(j), 0, 0, kVec, v);
+        else load8<true, 0, false>(static_cast<const __half*>(p) + eight(j), 0, 0, kVec, v);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pair_of(v[2 * i], v[2 * i + 1]);
+}
 
 // Eight results as T, 16 bytes at a time.
 template <typename T>
@@ -388,69 +401,76 @@ __device__ __forceinline__ void store_pairs(T* p, const uint64_t (&v)[4]) {
     st_vec(p, y);
 }
 
-// The codes of eight columns of a tile with scale s: E4M3(v / s).  v / s is formed as v times
-// 1 / s and one correction by the remainder (P. Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000", 1990), which is the rounded quotient wherever nothing
-// overflows or goes below 2^-126 on the way; scales where it might take the division.
-__device__ __forceinline__ uint2 tile_codes(const uint64_t (&v)[4], float s, bool pow2) {
+// The scale of a tile with the largest magnitude `amax`, and the codes E4M3(v / s) of eight of its
+// columns, by the rule of fp8z_quantize_rowwise.  A quotient is formed as the numerator times
+// a reciprocal and one correction by the remainder (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000", 1990), which rounds it as a division would wherever
+// nothing overflows or goes below 2^-126 on the way; other tiles take the division.
+__device__ __forceinline__ uint2 tile_codes(const uint64_t (&v)[4], float amax, bool pow2, float& s) {
     float t[kVec];
-    if (pow2 || (s > 0x1p-60f && s < 0x1p100f)) {
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-        r = pow2 ? __frcp_rn(s) : fmaf(fmaf(-s, r, 1.0f), r, r);             // exact for a power of two
-        const uint64_t rr = pair_of(r, r), ss = pair_of(-s, -s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint64_t q = mul_pair(v[i], rr);
-            if (!pow2) q = fma_pair(fma_pair(q, ss, v[i]), rr, q);
-            const float2 f = halves(q);
-            t[2 * i] = f.x;
-            t[2 * i + 1] = f.y;
-        }
-    } else {
+    if (pow2 || !(amax > 0x1p-50f && amax < 0x1p100f)) {
+        s = tile_scale(amax, pow2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = halves(v[i]);
             t[2 * i] = __fdiv_rn(f.x, s);
             t[2 * i + 1] = __fdiv_rn(f.y, s);
         }
+    } else {
+        constexpr float c = 1.0f / 448.0f;
+        s = amax * c;
+        s = fmaf(fmaf(-s, 448.0f, amax), c, s);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+        r = fmaf(fmaf(-s, r, 1.0f), r, r);
+        const uint64_t rr = pair_of(r, r), ss = pair_of(-s, -s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t q = mul_pair(v[i], rr);
+            const float2 f = halves(fma_pair(fma_pair(q, ss, v[i]), rr, q));
+            t[2 * i] = f.x;
+            t[2 * i + 1] = f.y;
+        }
     }
     return make_uint2(pack_e4m3x4(t[0], t[1], t[2], t[3]), pack_e4m3x4(t[4], t[5], t[6], t[7]));
 }
 
-// Batches of kRows rows, one block a batch at a time: the sums of a batch share two barriers.
-template <typename T, int kThreads, int kVecs, int kRows, bool kCodes>
-__global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_queue_kernel(const __grid_constant__ Norm A) {
-    using Q = Queue<T, kThreads, kVecs, kRows, 1>;
+// 1 / sqrt(x) to within 2 ulp: the approximation and one Newton step; infinite for 0.
+__device__ __forceinline__ float inverse_root(float x) {
+    const float r = rsqrtf(x);
+    return x == 0.0f ? r : fmaf(r * 0.5f, fmaf(-x * r, r, 1.0f), r);
+}
+
+// Batches of two rows, one block a batch at a time: the sums of a batch share two barriers.
+// A thread has 8 or 16 neighbouring columns of every row; the block is as wide as the row.
+template <typename T, int kVecs, bool kCodes>
+__global__ void __launch_bounds__(512, 2 / kVecs) norm_queue_kernel(const __grid_constant__ Norm A) {
+    constexpr int kRows = 2;
+    using Q = Queue<T, kVecs, kRows, 1>;
     constexpr int kQueue = Q::kQueue;
     extern __shared__ uint4 smem[];
-    __shared__ float shared[2][kThreads / 32 * kRows];
+    __shared__ float shared[2][16 * kRows];
     dependent_wait();
-    const Q q{smem_addr(smem) + threadIdx.x * 16};
+    const Q q{smem_addr(smem) + threadIdx.x * 16, blockDim.x * 16};
     const T* x = static_cast<const T*>(A.x);
     const int64_t batches = (int64_t(A.rows) + kRows - 1) / kRows;
-    const float n = float(A.cols);
+    const float per = 1.0f / float(A.cols);
     uint64_t w[kVecs][4], b[kVecs][4];
     bool in[kVecs];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        in[j] = (j * kThreads + int(threadIdx.x)) * kVec < A.cols;
-        float v[kVec], u[kVec];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = 1.0f, u[e] = 0.0f;
-        if (A.weight) load8_param<true, kThreads>(A.weight, A.param_dtype, j, threadIdx.x, A.cols, v);
-        if (A.bias) load8_param<true, kThreads>(A.bias, A.param_dtype, j, threadIdx.x, A.cols, u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[j][i] = pair_of(v[2 * i], v[2 * i + 1]), b[j][i] = pair_of(u[2 * i], u[2 * i + 1]);
+        in[j] = eight(j) < A.cols;
+        params8(A.weight, A.param_dtype, j, in[j], 1.0f, w[j]);
+        params8(A.bias, A.param_dtype, j, in[j], 0.0f, b[j]);
     }
 #pragma unroll
     for (int d = 0; d < kQueue - 1; ++d) {
-        q.fetch(d, 0, x, A.x_ld, (blockIdx.x + int64_t(d) * gridDim.x) * kRows, A.rows, A.cols);
+        q.fetch(d, 0, x, A.x_ld, (blockIdx.x + int64_t(d) * gridDim.x) * kRows, A.rows, in);
         copy_commit();
     }
     int slot = 0;
     for (int64_t batch = blockIdx.x; batch < batches; batch += gridDim.x) {
-        q.fetch(slot == 0 ? kQueue - 1 : slot - 1, 0, x, A.x_ld, (batch + int64_t(kQueue - 1) * gridDim.x) * kRows, A.rows, A.cols);
+        q.fetch(slot == 0 ? kQueue - 1 : slot - 1, 0, x, A.x_ld, (batch + int64_t(kQueue - 1) * gridDim.x) * kRows, A.rows, in);
         copy_commit();
         copy_wait<kQueue - 1>();
         uint64_t v[kRows][kVecs][4];
@@ -470,10 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_queu
             const float2 f = halves(s);
             mean[r] = f.x + f.y;
         }
-        block_sums<kRows, kThreads>(mean, shared[0]);
+        block_sums<kRows>(mean, shared[0]);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            mean[r] /= n;
+            mean[r] *= per;
             const uint64_t m = pair_of(-mean[r], -mean[r]);
             uint64_t s = 0;
 #pragma unroll
@@ -486,11 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_queu
             const float2 f = halves(s);
             rstd[r] = f.x + f.y;
         }
-        block_sums<kRows, kThreads>(rstd, shared[1]);
+        block_sums<kRows>(rstd, shared[1]);
         const int64_t row0 = batch * kRows;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            rstd[r] = __frcp_rn(__fsqrt_rn(rstd[r] / n + A.eps));
+            rstd[r] = inverse_root(fmaf(rstd[r], per, A.eps));
             if (threadIdx.x == 0 && row0 + r < A.rows) {
                 if (A.mean) A.mean[row0 + r] = mean[r];
                 if (A.rstd) A.rstd[row0 + r] = rstd[r];
@@ -506,8 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_queu
             for (int r = 0; r < kRows; ++r)
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j)
-                    if (in[j] && row0 + r < A.rows)
-                        store_pairs(static_cast<T*>(A.y) + (row0 + r) * A.y_ld + (j * kThreads + threadIdx.x) * kVec, v[r][j]);
+                    if (in[j] && row0 + r < A.rows) store_pairs(static_cast<T*>(A.y) + (row0 + r) * A.y_ld + eight(j), v[r][j]);
         if constexpr (kCodes) {
             float amax[kRows][kVecs];
 #pragma unroll
@@ -531,12 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_queu
             for (int r = 0; r < kRows; ++r)
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
-                    const int c = (j * kThreads + int(threadIdx.x)) * kVec;
-                    const float s = tile_scale(amax[r][j], A.pow2);
-                    const uint2 codes = tile_codes(v[r][j], s, A.pow2);
+                    float s;
+                    const uint2 codes = tile_codes(v[r][j], amax[r][j], A.pow2, s);
                     if (in[j] && row0 + r < A.rows) {
-                        *reinterpret_cast<uint2*>(A.q + (row0 + r) * A.cols + c) = codes;
-                        if ((threadIdx.x & 15) == 0) A.q_scale[(row0 + r) * (A.cols / FP8Z_BLOCK) + c / FP8Z_BLOCK] = s;
+                        *reinterpret_cast<uint2*>(A.q + (row0 + r) * A.cols + eight(j)) = codes;
+                        if ((threadIdx.x & 15) == 0) A.q_scale[(row0 + r) * (A.cols / FP8Z_BLOCK) + eight(j) / FP8Z_BLOCK] = s;
                     }
                 }
         }
@@ -634,39 +652,39 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) norm_grad_ker
 
 // The same with a queue of dy and x: both are read from shared memory again for dx, so that
 // registers hold the sums of dw and db, and the weight, only.
-template <typename T, int kThreads, int kVecs, int kRows>
-__global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_grad_queue_kernel(const __grid_constant__ NormGrad A) {
-    using Q = Queue<T, kThreads, kVecs, kRows, 2>;
+template <typename T, int kVecs>
+__global__ void __launch_bounds__(512, 2 / kVecs) norm_grad_queue_kernel(const __grid_constant__ NormGrad A) {
+    constexpr int kRows = sizeof(T) == 2 ? 2 : 1;
+    using Q = Queue<T, kVecs, kRows, 2>;
     constexpr int kQueue = Q::kQueue;
     extern __shared__ uint4 smem[];
-    __shared__ float shared[2][kThreads / 32 * 2 * kRows];
+    __shared__ float shared[2][16 * 2 * kRows];
     dependent_wait();
-    const Q q{smem_addr(smem) + threadIdx.x * 16};
+    const Q q{smem_addr(smem) + threadIdx.x * 16, blockDim.x * 16};
     const T *x = static_cast<const T*>(A.x), *dy = static_cast<const T*>(A.dy);
     const int64_t batches = (int64_t(A.rows) + kRows - 1) / kRows;
-    const float n = float(A.cols);
+    const float per = 1.0f / float(A.cols);
     uint64_t w[kVecs][4], dw[kVecs][4], db[kVecs][4];
+    bool in[kVecs];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        float v[kVec];
+        in[j] = eight(j) < A.cols;
+        params8(A.weight, A.param_dtype, j, in[j], 1.0f, w[j]);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = 1.0f;
-        if (A.weight) load8_param<true, kThreads>(A.weight, A.param_dtype, j, threadIdx.x, A.cols, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[j][i] = pair_of(v[2 * i], v[2 * i + 1]), dw[j][i] = db[j][i] = 0;
+        for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = 0;
     }
     const auto fetch = [&](int slot, int64_t batch) {
-        q.fetch(slot, 0, x, A.x_ld, batch * kRows, A.rows, A.cols);
-        q.fetch(slot, 1, dy, A.dy_ld, batch * kRows, A.rows, A.cols);
+        q.fetch(slot, 0, x, A.x_ld, batch * kRows, A.rows, in);
+        q.fetch(slot, 1, dy, A.dy_ld, batch * kRows, A.rows, in);
         copy_commit();
     };
     float mean[kRows], rstd[kRows];                              // of the next batch
     const auto stats = [&](int64_t batch) {
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            const bool in = batch * kRows + r < A.rows;
-            mean[r] = in ? load_one(A.mean + batch * kRows + r) : 0.0f;
-            rstd[r] = in ? load_one(A.rstd + batch * kRows + r) : 0.0f;
+            const bool there = batch * kRows + r < A.rows;
+            mean[r] = there ? load_one(A.mean + batch * kRows + r) : 0.0f;
+            rstd[r] = there ? load_one(A.rstd + batch * kRows + r) : 0.0f;
         }
     };
 #pragma unroll
@@ -700,19 +718,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_grad
             sums[r] = a.x + a.y;
             sums[kRows + r] = c.x + c.y;
         }
-        block_sums<2 * kRows, kThreads>(sums, shared[turn]);
+        block_sums<2 * kRows>(sums, shared[turn]);
         turn ^= 1;
         if (A.dx)
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 const int64_t row = batch * kRows + r;
                 if (row >= A.rows) break;
-                const float c1 = sums[r] / n, c2 = sums[kRows + r] / n;
+                const float c1 = sums[r] * per, c2 = sums[kRows + r] * per;
                 const uint64_t n1 = pair_of(-c1, -c1), n2 = pair_of(-c2, -c2);
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
-                    const int c = (j * kThreads + int(threadIdx.x)) * kVec;
-                    if (c >= A.cols) break;
+                    if (!in[j]) break;
                     const Eight<T> xv = q.load(slot, 0, r, j), dv = q.load(slot, 1, r, j);
                     uint64_t v[4];
 #pragma unroll
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_grad
                         const uint64_t xh = mul_pair(add_pair(xv.pair(i), m[r]), f[r]), g = mul_pair(dv.pair(i), w[j][i]);
                         v[i] = mul_pair(fma_pair(xh, n2, add_pair(g, n1)), f[r]);
                     }
-                    store_pairs(static_cast<T*>(A.dx) + row * A.dx_ld + c, v);
+                    store_pairs(static_cast<T*>(A.dx) + row * A.dx_ld + eight(j), v);
                 }
             }
         slot = slot + 1 == kQueue ? 0 : slot + 1;
@@ -728,12 +745,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / (kThreads * kVecs)) norm_grad
     copy_wait<0>();
     float* out = A.part + int64_t(blockIdx.x) * 2 * A.cols;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        const int c = (j * kThreads + int(threadIdx.x)) * kVec;
-        if (c >= A.cols) break;
-        store_pairs(out + c, dw[j]);
-        store_pairs(out + A.cols + c, db[j]);
-    }
+    for (int j = 0; j < kVecs; ++j)
+        if (in[j]) {
+            store_pairs(out + eight(j), dw[j]);
+            store_pairs(out + A.cols + eight(j), db[j]);
+        }
 }
 
 // Rows longer than 32768 columns: the sums of dw and db are added to in `part`.
@@ -798,8 +814,8 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* part, int
 // ------------------------------------------------------------------- host
 constexpr int kLongest = 32768;                        // columns a block's registers hold
 
-// Blocks, and parts of the weight's gradient, at most: what SMs hold at a time.
-int64_t most_parts(int64_t cols) { return cols <= 32 * kVec * 2 ? 304 : cols <= 1024 ? 1216 : cols <= 2048 ? 608 : 304; }
+// Parts of the weight's gradient, one for a block, at most.
+int64_t most_parts(int64_t cols) { return cols <= 2048 ? 608 : 304; }
 
 bool vectors(const void* p, int64_t ld, int64_t rows, int dtype) {
     return host::aligned(p, 16) && (rows <= 1 || ld * dtype_bytes(dtype) % 16 == 0);
@@ -829,44 +845,38 @@ bool queued(bool wide, int64_t rows, int64_t cols, int sms) {
     return wide && cols % kVec == 0 && cols > 32 * kVec * 2 && cols <= 8192 && rows > 2 * sms;
 }
 
-template <typename T, int kThreads, int kVecs, bool kCodes>
-int start_queue_codes(const Norm& A, int slot, int sms, cudaStream_t st) {
-    constexpr int kRows = 2;
-    using Q = Queue<T, kThreads, kVecs, kRows, 1>;
-    const auto k = &norm_queue_kernel<T, kThreads, kVecs, kRows, kCodes>;
-    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot + 16 * kCodes, Q::kBytes)) return rc;
-    const int64_t batches = (int64_t(A.rows) + kRows - 1) / kRows, most = int64_t(sms) * (1024 / (kThreads * kVecs));
-    return launch_dependent(k, dim3(unsigned(std::min(batches, most))), kThreads, Q::kBytes, st, A);
-}
+// Threads of a queued row, eight columns each (16 past 4096 columns), and blocks an SM.
+int queue_threads(int64_t cols) { return int((cols + (cols > 4096 ? 511 : 255)) / (cols > 4096 ? 512 : 256) * 32); }
+int queue_blocks(int64_t cols) { return cols > 4096 ? 1 : 1024 / queue_threads(cols); }
 
-template <typename T, int kThreads, int kVecs>
+template <typename T, int kVecs, bool kCodes>
 int start_queue(const Norm& A, int slot, int sms, cudaStream_t st) {
-    return A.q ? start_queue_codes<T, kThreads, kVecs, true>(A, slot, sms, st) : start_queue_codes<T, kThreads, kVecs, false>(A, slot, sms, st);
+    using Q = Queue<T, kVecs, 2, 1>;
+    const auto k = &norm_queue_kernel<T, kVecs, kCodes>;
+    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot, Q::bytes(512))) return rc;
+    const int threads = queue_threads(A.cols);
+    const int64_t batches = (int64_t(A.rows) + 1) / 2, most = int64_t(sms) * queue_blocks(A.cols);
+    return launch_dependent(k, dim3(unsigned(std::min(batches, most))), threads, Q::bytes(threads), st, A);
 }
 
 template <typename T>
 int start_queue(const Norm& A, int slot, int sms, cudaStream_t st) {
-    if (A.cols <= 128 * kVec) return start_queue<T, 128, 1>(A, slot, sms, st);
-    if (A.cols <= 256 * kVec) return start_queue<T, 256, 1>(A, slot + 1, sms, st);
-    if (A.cols <= 512 * kVec) return start_queue<T, 512, 1>(A, slot + 2, sms, st);
-    return start_queue<T, 512, 2>(A, slot + 3, sms, st);
+    if (A.cols <= 4096) return A.q ? start_queue<T, 1, true>(A, slot, sms, st) : start_queue<T, 1, false>(A, slot + 1, sms, st);
+    return A.q ? start_queue<T, 2, true>(A, slot + 2, sms, st) : start_queue<T, 2, false>(A, slot + 3, sms, st);
 }
 
-template <typename T, int kThreads, int kVecs>
+template <typename T, int kVecs>
 int start_grad_queue(const NormGrad& A, int slot, int parts, cudaStream_t st) {
-    constexpr int kRows = sizeof(T) == 2 ? 2 : 1;
-    using Q = Queue<T, kThreads, kVecs, kRows, 2>;
-    const auto k = &norm_grad_queue_kernel<T, kThreads, kVecs, kRows>;
-    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot, Q::kBytes)) return rc;
-    return launch_dependent(k, dim3(unsigned(parts)), kThreads, Q::kBytes, st, A);
+    using Q = Queue<T, kVecs, sizeof(T) == 2 ? 2 : 1, 2>;
+    const auto k = &norm_grad_queue_kernel<T, kVecs>;
+    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot, Q::bytes(512))) return rc;
+    const int threads = queue_threads(A.cols);
+    return launch_dependent(k, dim3(unsigned(parts)), threads, Q::bytes(threads), st, A);
 }
 
 template <typename T>
 int start_grad_queue(const NormGrad& A, int slot, int parts, cudaStream_t st) {
-    if (A.cols <= 128 * kVec) return start_grad_queue<T, 128, 1>(A, slot, parts, st);
-    if (A.cols <= 256 * kVec) return start_grad_queue<T, 256, 1>(A, slot + 1, parts, st);
-    if (A.cols <= 512 * kVec) return start_grad_queue<T, 512, 1>(A, slot + 2, parts, st);
-    return start_grad_queue<T, 512, 2>(A, slot + 3, parts, st);
+    return A.cols <= 4096 ? start_grad_queue<T, 1>(A, slot, parts, st) : start_grad_queue<T, 2>(A, slot + 1, parts, st);
 }
 
 template <typename T>
@@ -881,8 +891,7 @@ int start_type(const Norm& A, bool wide, int slot, int sms, cudaStream_t st) {
 int parts_of(int64_t rows, int64_t cols, bool wide, int dtype, int sms) {
     if (queued(wide, rows, cols, sms)) {
         const int per = dtype == FP8Z_F32 ? 1 : 2;
-        const int64_t an_sm = cols <= 128 * kVec ? 8 : cols <= 256 * kVec ? 4 : cols <= 512 * kVec ? 2 : 1;
-        return int(std::min<int64_t>({(rows + per - 1) / per, sms * an_sm, most_parts(cols)}));
+        return int(std::min<int64_t>({(rows + per - 1) / per, int64_t(sms) * queue_blocks(cols), most_parts(cols)}));
     }
     const int64_t blocks = cols <= 32 * kVec * 2 ? (rows + 7) / 8 : rows;
     return int(std::min<int64_t>({std::max<int64_t>(blocks, 1), int64_t(sms) * (cols <= 256 * kVec ? 2 : 1), most_parts(cols)}));
@@ -942,9 +951,9 @@ extern "C" int fp8z_layer_norm(const void* x, const void* weight, const void* bi
     const Norm A = {int(a.rows), int(a.cols), x, a.x_ld, weight, bias, a.param_dtype, y, a.y_ld, mean, rstd, a.eps,
                     q, q_scale, a.pow2};
     const auto st = static_cast<cudaStream_t>(stream);
-    if (a.dtype == FP8Z_F32) return start_type<float>(A, wide, 32, sms, st);
-    if (a.dtype == FP8Z_BF16) return start_type<__nv_bfloat16>(A, wide, 36, sms, st);
-    return start_type<__half>(A, wide, 40, sms, st);
+    if (a.dtype == FP8Z_F32) return start_type<float>(A, wide, 27, sms, st);
+    if (a.dtype == FP8Z_BF16) return start_type<__nv_bfloat16>(A, wide, 31, sms, st);
+    return start_type<__half>(A, wide, 35, sms, st);
 }
 
 extern "C" int64_t fp8z_layer_norm_grad_workspace(int64_t rows, int64_t cols) {
@@ -980,9 +989,9 @@ extern "C" int fp8z_layer_norm_grad(const void* dy, const void* x, const void* w
                           (!dx || vectors(dx, a.dx_ld, a.rows, a.dtype));
         parts = parts_of(a.rows, a.cols, wide, a.dtype, sms);
         const NormGrad A = {int(a.rows), int(a.cols), dy, x, a.dy_ld, a.x_ld, a.dx_ld, weight, a.param_dtype, mean, rstd, dx, part};
-        const int rc = a.dtype == FP8Z_F32 ? start_grad_type<float>(A, wide, 64, parts, sms, st)
-                       : a.dtype == FP8Z_BF16 ? start_grad_type<__nv_bfloat16>(A, wide, 68, parts, sms, st)
-                                              : start_grad_type<__half>(A, wide, 72, parts, sms, st);
+        const int rc = a.dtype == FP8Z_F32 ? start_grad_type<float>(A, wide, 39, parts, sms, st)
+                       : a.dtype == FP8Z_BF16 ? start_grad_type<__nv_bfloat16>(A, wide, 41, parts, sms, st)
+                                              : start_grad_type<__half>(A, wide, 43, parts, sms, st);
         if (rc) return rc;
     }
     if (!dweight && !dbias) return FP8Z_OK;
