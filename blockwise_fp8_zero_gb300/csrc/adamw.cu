@@ -148,20 +148,11 @@ __device__ __forceinline__ void load_grad(const fp8z_adamw_chunk& t, int at, con
     else f.load(static_cast<const __half*>(t.g) + at, g);
 }
 
+// The step of a lane's four elements, and their way back.
 template <bool kVec, bool k8>
-__device__ __forceinline__ void run_step(const fp8z_adamw_chunk& t, const Step& A, float factor, int at, const Four<kVec>& f) {
-    float p[4], g[4], m[4], v[4], r[4];
-    f.load_state(t.p + at, p);
-    load_grad(t, at, f, g);
-    if constexpr (k8) {
-        decode4(f.load_codes(static_cast<const uint8_t*>(t.m) + at), t.m_scale[at / kRun], m);
-        decode4(f.load_codes(static_cast<const uint8_t*>(t.v) + at), t.v_scale[at / kRun], v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = v[j] * v[j];
-    } else {
-        f.load_state(static_cast<const float*>(t.m) + at, m);
-        f.load_state(static_cast<const float*>(t.v) + at, v);
-    }
+__device__ __forceinline__ void update(const fp8z_adamw_chunk& t, const Step& A, float factor, int at, const Four<kVec>& f,
+                                       float (&p)[4], const float (&g)[4], float (&m)[4], float (&v)[4]) {
+    float r[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         adamw1(A, __fmul_rn(g[j], factor), p[j], m[j], v[j], r[j], v[j]);
@@ -189,6 +180,24 @@ __device__ __forceinline__ void run_step(const fp8z_adamw_chunk& t, const Step& 
     }
 }
 
+// One run of a tensor's end, or of tensors that are not aligned for vectors.
+template <bool kVec, bool k8>
+__device__ __forceinline__ void run_step(const fp8z_adamw_chunk& t, const Step& A, float factor, int at, const Four<kVec>& f) {
+    float p[4], g[4], m[4], v[4];
+    f.load_state(t.p + at, p);
+    load_grad(t, at, f, g);
+    if constexpr (k8) {
+        decode4(f.load_codes(static_cast<const uint8_t*>(t.m) + at), t.m_scale[at / kRun], m);
+        decode4(f.load_codes(static_cast<const uint8_t*>(t.v) + at), t.v_scale[at / kRun], v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = v[j] * v[j];
+    } else {
+        f.load_state(static_cast<const float*>(t.m) + at, m);
+        f.load_state(static_cast<const float*>(t.v) + at, v);
+    }
+    update<kVec, k8>(t, A, factor, at, f, p, g, m, v);
+}
+
 // 16 bytes of the widest tensor a lane, for every tensor of the chunk.
 __device__ __forceinline__ bool vectors(const fp8z_adamw_chunk& t) {
     const uintptr_t g = reinterpret_cast<uintptr_t>(t.g) & (t.g_dtype == FP8Z_F32 ? 15 : 7);
@@ -196,12 +205,87 @@ __device__ __forceinline__ bool vectors(const fp8z_adamw_chunk& t) {
     return ((reinterpret_cast<uintptr_t>(t.p) & 15) | g | mv | (reinterpret_cast<uintptr_t>(t.copy) & 7)) == 0;
 }
 
-template <bool kVec, bool k8>
+// Four neighbouring elements of a whole run, as they lie in memory.
+template <typename G, bool k8>
+struct Loaded {
+    uint4 p, m4, v4;
+    uint4 g4;
+    uint2 g2;
+    uint32_t m, v;
+    float ms, vs;
+
+    __device__ __forceinline__ void load(const fp8z_adamw_chunk& t, int at, int lane) {
+        const int i = at + lane * 4;
+        p = ld_stream_16(t.p + i, 0);
+        if constexpr (sizeof(G) == 4) g4 = ld_stream_16(static_cast<const float*>(t.g) + i, 0);
+        else asm volatile("ld.global.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(g2.x), "=r"(g2.y) : "l"(static_cast<const G*>(t.g) + i) : "memory");
+        if constexpr (k8) {
+            asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(m) : "l"(static_cast<const uint8_t*>(t.m) + i) : "memory");
+            asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(static_cast<const uint8_t*>(t.v) + i) : "memory");
+            ms = t.m_scale[at / kRun];
+            vs = t.v_scale[at / kRun];
+        } else {
+            m4 = ld_stream_16(static_cast<const float*>(t.m) + i, 0);
+            v4 = ld_stream_16(static_cast<const float*>(t.v) + i, 0);
+        }
+    }
+    static __device__ __forceinline__ void floats(const uint4& u, float (&x)[4]) {
+        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+    }
+    __device__ __forceinline__ void unpack(float (&pp)[4], float (&g)[4], float (&mm)[4], float (&vv)[4]) const {
+        floats(p, pp);
+        if constexpr (sizeof(G) == 4) {
+            floats(g4, g);
+        } else {
+            const Pack<G, 4> y = *reinterpret_cast<const Pack<G, 4>*>(&g2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = Elem<G>::widen(y.v[j]);
+        }
+        if constexpr (k8) {
+            decode4(m, ms, mm);
+            decode4(v, vs, vv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) vv[j] = vv[j] * vv[j];
+        } else {
+            floats(m4, mm);
+            floats(v4, vv);
+        }
+    }
+};
+
+// A chunk: each warp takes every eighth run, several at a time, so that the loads of all of them
+// are under way together.  200 M elements with 8-bit moments: one at a time 918 us.
+template <typename G, bool k8>
 __device__ __forceinline__ void chunk_step(const fp8z_adamw_chunk& t, const Step& A, float factor) {
+    constexpr int kRuns = k8 ? 4 : 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 2
-    for (int at = warp * kRun; at < t.count; at += kWarps * kRun)
-        run_step<kVec, k8>(t, A, factor, at, Four<kVec>{lane, t.count - at});
+    int at = warp * kRun;
+    for (; at + ((kRuns - 1) * kWarps + 1) * kRun <= t.count; at += kRuns * kWarps * kRun) {
+        Loaded<G, k8> l[kRuns];
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) l[i].load(t, at + i * kWarps * kRun, lane);
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+            float p[4], g[4], m[4], v[4];
+            l[i].unpack(p, g, m, v);
+            update<true, k8>(t, A, factor, at + i * kWarps * kRun, Four<true>{lane, kRun}, p, g, m, v);
+        }
+    }
+    for (; at < t.count; at += kWarps * kRun) run_step<true, k8>(t, A, factor, at, Four<true>{lane, t.count - at});
+}
+
+template <bool k8>
+__device__ __forceinline__ void chunk_step(const fp8z_adamw_chunk& t, const Step& A, float factor) {
+    if (!vectors(t)) {
+        for (int at = threadIdx.x / 32 * kRun; at < t.count; at += kWarps * kRun)
+            run_step<false, k8>(t, A, factor, at, Four<false>{int(threadIdx.x & 31), t.count - at});
+    } else if (t.g_dtype == FP8Z_F32) {
+        chunk_step<float, k8>(t, A, factor);
+    } else if (t.g_dtype == FP8Z_BF16) {
+        chunk_step<__nv_bfloat16, k8>(t, A, factor);
+    } else {
+        chunk_step<__half, k8>(t, A, factor);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const fp8z_adamw_chunk* list, const __grid_constant__ Step A,
@@ -209,13 +293,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const fp8z_adamw_chunk*
     dependent_wait();
     const fp8z_adamw_chunk t = list[blockIdx.x];
     const float f = factor ? *factor : 1.0f;
-    if (t.state_bits == 8) {
-        if (vectors(t)) chunk_step<true, true>(t, A, f);
-        else chunk_step<false, true>(t, A, f);
-    } else {
-        if (vectors(t)) chunk_step<true, false>(t, A, f);
-        else chunk_step<false, false>(t, A, f);
-    }
+    if (t.state_bits == 8) chunk_step<true>(t, A, f);
+    else chunk_step<false>(t, A, f);
 }
 
 }  // namespace

@@ -296,9 +296,9 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// kN sums over a block of at most 16 warps, the same in each thread, in a fixed order.  In a
+// kN sums over a block, the same in each thread, in a fixed order.  In a
 // warp half of the sums change lanes at every step, so that four sums take six shuffles.
-template <int kN>
+template <int kN, int kMaxWarps>
 __device__ __forceinline__ void block_sums(float (&v)[kN], float* shared) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int which = 0, off = 16;
@@ -321,7 +321,7 @@ __device__ __forceinline__ void block_sums(float (&v)[kN], float* shared) {
     constexpr int kEach = 32 / kN;
     float all = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; w += kEach) {
+    for (int w = 0; w < kMaxWarps; w += kEach) {
         const int mine = w + lane % kEach;
         if (mine < warps) all += shared[mine * kN + lane / kEach];
     }
@@ -408,13 +408,24 @@ __device__ __forceinline__ void store_pairs(T* p, const uint64_t (&v)[4]) {
 // nothing overflows or goes below 2^-126 on the way; other tiles take the division.
 __device__ __forceinline__ uint2 tile_codes(const uint64_t (&v)[4], float amax, bool pow2, float& s) {
     float t[kVec];
-    if (pow2 || !(amax > 0x1p-50f && amax < 0x1p100f)) {
+    if (!(amax > 0x1p-50f && amax < 0x1p100f)) {
         s = tile_scale(amax, pow2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = halves(v[i]);
             t[2 * i] = __fdiv_rn(f.x, s);
             t[2 * i + 1] = __fdiv_rn(f.y, s);
+        }
+    } else if (pow2) {
+        // 448 = 7/8 * 2^9: the exponent of amax less 8, one more above 1.75 of its binade; 1 / s is exact
+        const uint32_t bits = __float_as_uint(amax), k = (bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        s = __uint_as_float(k << 23);
+        const float r = __uint_as_float((254 - k) << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = halves(mul_pair(v[i], pair_of(r, r)));
+            t[2 * i] = f.x;
+            t[2 * i + 1] = f.y;
         }
     } else {
         constexpr float c = 1.0f / 448.0f;
@@ -443,13 +454,13 @@ __device__ __forceinline__ float inverse_root(float x) {
 
 // Batches of two rows, one block a batch at a time: the sums of a batch share two barriers.
 // A thread has 8 or 16 neighbouring columns of every row; the block is as wide as the row.
-template <typename T, int kVecs, bool kCodes>
-__global__ void __launch_bounds__(512, 2 / kVecs) norm_queue_kernel(const __grid_constant__ Norm A) {
-    constexpr int kRows = 2;
+template <typename T, bool kCodes>
+__global__ void __launch_bounds__(1024) norm_queue_kernel(const __grid_constant__ Norm A) {
+    constexpr int kRows = 2, kVecs = 1;
     using Q = Queue<T, kVecs, kRows, 1>;
     constexpr int kQueue = Q::kQueue;
     extern __shared__ uint4 smem[];
-    __shared__ float shared[2][16 * kRows];
+    __shared__ float shared[2][32 * kRows];
     dependent_wait();
     const Q q{smem_addr(smem) + threadIdx.x * 16, blockDim.x * 16};
     const T* x = static_cast<const T*>(A.x);
@@ -490,7 +501,7 @@ __global__ void __launch_bounds__(512, 2 / kVecs) norm_queue_kernel(const __grid
             const float2 f = halves(s);
             mean[r] = f.x + f.y;
         }
-        block_sums<kRows>(mean, shared[0]);
+        block_sums<kRows, 32>(mean, shared[0]);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             mean[r] *= per;
@@ -506,7 +517,7 @@ __global__ void __launch_bounds__(512, 2 / kVecs) norm_queue_kernel(const __grid
             const float2 f = halves(s);
             rstd[r] = f.x + f.y;
         }
-        block_sums<kRows>(rstd, shared[1]);
+        block_sums<kRows, 32>(rstd, shared[1]);
         const int64_t row0 = batch * kRows;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
@@ -718,7 +729,7 @@ __global__ void __launch_bounds__(512, 2 / kVecs) norm_grad_queue_kernel(const _
             sums[r] = a.x + a.y;
             sums[kRows + r] = c.x + c.y;
         }
-        block_sums<2 * kRows>(sums, shared[turn]);
+        block_sums<2 * kRows, 16>(sums, shared[turn]);
         turn ^= 1;
         if (A.dx)
 #pragma unroll
@@ -845,24 +856,18 @@ bool queued(bool wide, int64_t rows, int64_t cols, int sms) {
     return wide && cols % kVec == 0 && cols > 32 * kVec * 2 && cols <= 8192 && rows > 2 * sms;
 }
 
-// Threads of a queued row, eight columns each (16 past 4096 columns), and blocks an SM.
+// Threads of a queued row of the gradient, eight columns each (16 past 4096 columns), and blocks an SM.
 int queue_threads(int64_t cols) { return int((cols + (cols > 4096 ? 511 : 255)) / (cols > 4096 ? 512 : 256) * 32); }
 int queue_blocks(int64_t cols) { return cols > 4096 ? 1 : 1024 / queue_threads(cols); }
 
-template <typename T, int kVecs, bool kCodes>
+template <typename T, bool kCodes>
 int start_queue(const Norm& A, int slot, int sms, cudaStream_t st) {
-    using Q = Queue<T, kVecs, 2, 1>;
-    const auto k = &norm_queue_kernel<T, kVecs, kCodes>;
-    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot, Q::bytes(512))) return rc;
-    const int threads = queue_threads(A.cols);
-    const int64_t batches = (int64_t(A.rows) + 1) / 2, most = int64_t(sms) * queue_blocks(A.cols);
+    using Q = Queue<T, 1, 2, 1>;
+    const auto k = &norm_queue_kernel<T, kCodes>;
+    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot, Q::bytes(1024))) return rc;
+    const int threads = int((A.cols + 255) / 256 * 32);
+    const int64_t batches = (int64_t(A.rows) + 1) / 2, most = int64_t(sms) * (1024 / threads);
     return launch_dependent(k, dim3(unsigned(std::min(batches, most))), threads, Q::bytes(threads), st, A);
-}
-
-template <typename T>
-int start_queue(const Norm& A, int slot, int sms, cudaStream_t st) {
-    if (A.cols <= 4096) return A.q ? start_queue<T, 1, true>(A, slot, sms, st) : start_queue<T, 1, false>(A, slot + 1, sms, st);
-    return A.q ? start_queue<T, 2, true>(A, slot + 2, sms, st) : start_queue<T, 2, false>(A, slot + 3, sms, st);
 }
 
 template <typename T, int kVecs>
@@ -881,7 +886,7 @@ int start_grad_queue(const NormGrad& A, int slot, int parts, cudaStream_t st) {
 
 template <typename T>
 int start_type(const Norm& A, bool wide, int slot, int sms, cudaStream_t st) {
-    if (queued(wide, A.rows, A.cols, sms)) return start_queue<T>(A, slot, sms, st);
+    if (queued(wide, A.rows, A.cols, sms)) return A.q ? start_queue<T, true>(A, slot, sms, st) : start_queue<T, false>(A, slot + 1, sms, st);
     if (A.cols > kLongest)
         return launch_dependent(&norm_long_kernel<T>, dim3(unsigned(std::min(A.rows, sms * 2))), 1024, 0, st, A);
     return wide ? start_width<T, true>(A, sms, st) : start_width<T, false>(A, sms, st);
