@@ -13,6 +13,7 @@
 // Everything is read and written once: 28 bytes an element with FP32 moments and gradients,
 // 16.1 with BF16 gradients, 8-bit moments and a BF16 copy.
 #include <cfloat>
+#include <cmath>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -50,14 +51,43 @@ __device__ __forceinline__ void adamw1(const Step& A, float g, float& p, float& 
     }
 }
 
-// The multiplier of a run whose largest magnitude is amax: 448 / amax, 1 for a run of zeros.
+// The multiplier of a run whose largest magnitude is amax: 448 times 1 / amax, 1 for a run of zeros.
 __device__ __forceinline__ float run_scale(float amax) {
-    return amax == 0.0f ? 1.0f : fminf(__fdiv_rn(448.0f, amax), FLT_MAX);
+    return amax == 0.0f ? 1.0f : fminf(__fmul_rn(448.0f, __frcp_rn(amax)), FLT_MAX);
 }
 
 // Largest of the lanes' magnitudes; as whole numbers, non-negative floats keep their order.
 __device__ __forceinline__ float warp_max(float a) {
     return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));
+}
+
+// The same with a root and a quotient that are an approximation and one correction by the remainder:
+// off by one unit about once in a million times.  At 16 bytes an element the instructions are what
+// bounds the step (200 M elements with 8-bit moments and IEEE roots and quotients: 856 us).  Values where
+// that might overflow or lose its remainder, and zero, take the IEEE operation.
+__device__ __forceinline__ float root_near(float v) {
+    float y;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(v));
+    const float r = v * y;
+    return v > 0x1p-100f && v < 0x1p120f ? fmaf(fmaf(-r, r, v), 0.5f * y, r) : __fsqrt_rn(v);
+}
+__device__ __forceinline__ float quotient_near(float m, float d) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+    const float q = m * y;
+    return d > 0x1p-100f && d < 0x1p100f && fabsf(m) < 0x1p20f * d ? fmaf(fmaf(-q, d, m), y, q) : __fdiv_rn(m, d);
+}
+__device__ __forceinline__ void adamw1_near(const Step& A, float g, float& p, float& m, float v, float& r) {
+    m = __fadd_rn(__fmul_rn(A.s.beta1, m), __fmul_rn(A.s.omb1, g));
+    r = root_near(__fadd_rn(__fmul_rn(A.s.beta2, v), __fmul_rn(A.s.omb2, __fmul_rn(g, g))));
+    const float d = __fadd_rn(__fmul_rn(r, A.s.rs_bc2), A.s.eps);
+    const float su = __fmul_rn(A.s.step_size, quotient_near(m, d));
+    if (!A.post) {
+        p = __fsub_rn(__fmul_rn(p, A.s.decay), su);
+    } else {
+        const float pu = __fsub_rn(p, su);
+        p = __fsub_rn(pu, __fmul_rn(A.s.lr_wd, pu));
+    }
 }
 
 // Four elements of a lane: neighbours from 4 * lane on where the tensors allow 16-byte
@@ -171,8 +201,8 @@ __device__ __forceinline__ void update(const fp8z_adamw_chunk& t, const Step& A,
             if (r[j] > 0.0f && (q >> 8 * j & 255) == 0) q |= 1u << 8 * j;
         f.store_codes(static_cast<uint8_t*>(t.v) + at, q);
         if (f.lane == 0) {
-            t.m_scale[at / kRun] = __fdiv_rn(1.0f, sm);
-            t.v_scale[at / kRun] = __fdiv_rn(1.0f, sv);
+            t.m_scale[at / kRun] = __frcp_rn(sm);
+            t.v_scale[at / kRun] = __frcp_rn(sv);
         }
     } else {
         f.store(static_cast<float*>(t.m) + at, m);
@@ -253,6 +283,41 @@ struct Loaded {
     }
 };
 
+// kRuns whole runs with 8-bit moments, every eighth from `at` on.  The runs' scales, two for
+// each, are formed by a few lanes for all.
+template <int kRuns, typename G>
+__device__ __forceinline__ void update8(const fp8z_adamw_chunk& t, const Step& A, float factor, int at, int lane,
+                                        const Loaded<G, true> (&l)[kRuns]) {
+    const Four<true> f{lane, kRun};
+    float m[kRuns][4], r[kRuns][4];
+    float top = 0.0f;                              // of this lane's moment of this lane's run
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+        float p[4], g[4], v[4];
+        l[i].unpack(p, g, m[i], v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) adamw1_near(A, __fmul_rn(g[j], factor), p[j], m[i][j], v[j], r[i][j]);
+        const int to = at + i * kWarps * kRun;
+        f.store(t.p + to, p);
+        if (t.copy_dtype == FP8Z_BF16) f.store(static_cast<__nv_bfloat16*>(t.copy) + to, p);
+        else if (t.copy_dtype == FP8Z_F16) f.store(static_cast<__half*>(t.copy) + to, p);
+        const float am = warp_max(absmax4(m[i])), ar = warp_max(absmax4(r[i]));
+        if (lane == 2 * i) top = am;
+        if (lane == 2 * i + 1) top = ar;
+    }
+    const float scale = run_scale(top), kept = __frcp_rn(scale);
+    if (lane < 2 * kRuns) ((lane & 1) ? t.v_scale : t.m_scale)[at / kRun + (lane >> 1) * kWarps] = kept;
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+        const float sm = __shfl_sync(0xFFFFFFFFu, scale, 2 * i), sv = __shfl_sync(0xFFFFFFFFu, scale, 2 * i + 1);
+        const int to = at + i * kWarps * kRun;
+        f.store_codes(static_cast<uint8_t*>(t.m) + to, pack_e4m3x4(m[i][0] * sm, m[i][1] * sm, m[i][2] * sm, m[i][3] * sm));
+        // a v that is not zero does not become zero: what is above 0 is coded as 2^-9, the smallest code, at least
+        const auto code = [&](int j) { return r[i][j] > 0.0f ? fmaxf(r[i][j] * sv, 0x1p-9f) : r[i][j]; };
+        f.store_codes(static_cast<uint8_t*>(t.v) + to, pack_e4m3x4(code(0), code(1), code(2), code(3)));
+    }
+}
+
 // A chunk: each warp takes every eighth run, several at a time, so that the loads of all of them
 // are under way together.  200 M elements with 8-bit moments: one at a time 918 us.
 template <typename G, bool k8>
@@ -264,11 +329,15 @@ __device__ __forceinline__ void chunk_step(const fp8z_adamw_chunk& t, const Step
         Loaded<G, k8> l[kRuns];
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) l[i].load(t, at + i * kWarps * kRun, lane);
+        if constexpr (k8) {
+            update8<kRuns>(t, A, factor, at, lane, l);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kRuns; ++i) {
-            float p[4], g[4], m[4], v[4];
-            l[i].unpack(p, g, m, v);
-            update<true, k8>(t, A, factor, at + i * kWarps * kRun, Four<true>{lane, kRun}, p, g, m, v);
+            for (int i = 0; i < kRuns; ++i) {
+                float p[4], g[4], m[4], v[4];
+                l[i].unpack(p, g, m, v);
+                update<true, false>(t, A, factor, at + i * kWarps * kRun, Four<true>{lane, kRun}, p, g, m, v);
+            }
         }
     }
     for (; at < t.count; at += kWarps * kRun) run_step<true, k8>(t, A, factor, at, Four<true>{lane, t.count - at});
@@ -295,6 +364,21 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const fp8z_adamw_chunk*
     const float f = factor ? *factor : 1.0f;
     if (t.state_bits == 8) chunk_step<true>(t, A, f);
     else chunk_step<false>(t, A, f);
+}
+
+// ------------------------------------------------------------------- host
+bool params_ok(const fp8z_adamw_params& p) {
+    const auto in = [](double x, double low, double high) { return x >= low && x < high; };       // false for NaN
+    return in(p.lr, 0.0, FLT_MAX) && in(p.beta1, 0.0, 1.0) && in(p.beta2, 0.0, 1.0) && float(p.beta1) < 1.0f &&
+           float(p.beta2) < 1.0f && in(p.eps, 0.0, FLT_MAX) && float(p.eps) > 0.0f && in(p.weight_decay, 0.0, FLT_MAX) &&
+           p.step >= 1 && (p.decay_mode == FP8Z_DECAY_PRE || p.decay_mode == FP8Z_DECAY_POST);
+}
+
+// As host::adamw_scalars, from numbers that are not rounded to 32 bits first.
+host::AdamwScalars scalars(const fp8z_adamw_params& p) {
+    const double t = double(p.step), c1 = 1.0 - std::pow(p.beta1, t), c2 = 1.0 - std::pow(p.beta2, t);
+    return {float(p.beta1), float(p.beta2), float(1.0 - p.beta1), float(1.0 - p.beta2), float(p.eps), float(p.lr / c1),
+            float(1.0 / std::sqrt(c2)), float(1.0 - p.lr * p.weight_decay), float(p.lr * p.weight_decay)};
 }
 
 }  // namespace
@@ -346,16 +430,16 @@ extern "C" int fp8z_encode_adamw_list(const fp8z_adamw_tensor* tensors, int32_t 
     return FP8Z_OK;
 }
 
-extern "C" int fp8z_adamw(const fp8z_adamw_chunk* list, int64_t chunks, const fp8z_adamw_hparams* hp,
+extern "C" int fp8z_adamw(const fp8z_adamw_chunk* list, int64_t chunks, const fp8z_adamw_params* hp,
                           const float* grad_factor, void* stream) {
     using namespace fp8z;
     const host::NvtxRange nvtx_range("fp8z_adamw");
-    if (chunks < 0 || chunks > 0x7FFFFFFF || (chunks > 0 && !list) || !hp || !host::hparams_valid(*hp)) return FP8Z_EINVAL;
+    if (chunks < 0 || chunks > 0x7FFFFFFF || (chunks > 0 && !list) || !hp || !params_ok(*hp)) return FP8Z_EINVAL;
     if (!host::aligned(list, 8) || !host::aligned(grad_factor, 4)) return FP8Z_EALIGN;
     if (chunks == 0) return FP8Z_OK;
     int sms = 0;
     if (int rc = host::device_sms(&sms)) return rc;
-    const Step A = {host::adamw_scalars(*hp), hp->decay_mode == FP8Z_DECAY_POST};
+    const Step A = {scalars(*hp), hp->decay_mode == FP8Z_DECAY_POST};
     return launch_dependent(adamw_kernel, dim3(unsigned(chunks)), kThreads, 0, static_cast<cudaStream_t>(stream), list, A,
                             grad_factor);
 }

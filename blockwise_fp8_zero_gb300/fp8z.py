@@ -128,8 +128,31 @@ assert ctypes.sizeof(fp8z_layer_norm_args) == 72
 def hparams(lr=1e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=1,
             fp8_max=448.0, min_scale=1e-6, scale_mode=FP8Z_SCALE_EXACT,
             decay_mode=FP8Z_DECAY_PRE) -> fp8z_adamw_hparams:
-    return fp8z_adamw_hparams(lr, beta1, beta2, eps, weight_decay, step, fp8_max, min_scale,
-                              scale_mode, decay_mode)
+    hp = fp8z_adamw_hparams(lr, beta1, beta2, eps, weight_decay, step, fp8_max, min_scale,
+                            scale_mode, decay_mode)
+    hp.given = {"lr": lr, "beta1": beta1, "beta2": beta2, "eps": eps, "weight_decay": weight_decay}
+    return hp
+
+
+class fp8z_adamw_params(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("decay_mode", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+assert ctypes.sizeof(fp8z_adamw_params) == 56
+
+
+def _adamw_params(hp):
+    """hparams in 64 bits: the numbers hparams() was given where the 32-bit fields still hold them."""
+    given = getattr(hp, "given", {})
+    p = fp8z_adamw_params(step=hp.step, decay_mode=hp.decay_mode)
+    for k in ("lr", "beta1", "beta2", "eps", "weight_decay"):
+        x, g = getattr(hp, k), given.get(k)
+        setattr(p, k, g if g is not None and ctypes.c_float(g).value == x else x)
+    return p
 
 
 class Fp8zError(RuntimeError):
@@ -190,7 +213,7 @@ def lib():
         L.fp8z_layer_norm_grad_workspace.argtypes = [i64, i64]
         L.fp8z_layer_norm_grad.argtypes = [P, P, P, P, P, NA, P, P, P, P, i64, P]
         L.fp8z_encode_adamw_list.argtypes = [P, i32, P, i64, P]
-        L.fp8z_adamw.argtypes = [P, i64, ctypes.POINTER(fp8z_adamw_hparams), P, P]
+        L.fp8z_adamw.argtypes = [P, i64, ctypes.POINTER(fp8z_adamw_params), P, P]
         L.fp8z_e4m3_encode_bits.argtypes = [ctypes.c_uint32, i64, P, P]
         L.fp8z_watchdog_selftest.argtypes = [P, i64, P]
         L.fp8z_set_wait_limit_ns.argtypes = [i64]
@@ -1011,7 +1034,8 @@ def fp8z_encode_adamw_list(params, grads, exp_avgs, exp_avg_sqs, copies=None, ex
 
 
 def fp8z_adamw(tensors, hp, grad_factor=None, stream=None):
-    """One AdamW step of every tensor of the list (fp8z_encode_adamw_list).  grad_factor: one
+    """One AdamW step of every tensor of the list (fp8z_encode_adamw_list).  hp: hparams();
+    the quantizer's fields have no part in it.  grad_factor: one
     float32 on the device that multiplies every gradient (norm[1] of a clipping, 1 / a loss
     scale), or None."""
     here = _current_device()
@@ -1021,7 +1045,7 @@ def fp8z_adamw(tensors, hp, grad_factor=None, stream=None):
         _elsewhere(tensors.table, "table", here)
     if grad_factor is not None and grad_factor.numel() < 1:
         raise ValueError("grad_factor must hold one float32 value")
-    rc = lib().fp8z_adamw(tensors.pointer, tensors.chunks, ctypes.byref(hp), _flat(grad_factor, "grad_factor", here, FP8Z_F32),
+    rc = lib().fp8z_adamw(tensors.pointer, tensors.chunks, ctypes.byref(_adamw_params(hp)), _flat(grad_factor, "grad_factor", here, FP8Z_F32),
                           _stream_handle(stream))
     _check("fp8z_adamw", rc)
 

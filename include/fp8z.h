@@ -695,6 +695,15 @@ typedef struct {
     int8_t state_bits;
 } fp8z_adamw_chunk;          /* 64 bytes */
 
+/* Hyper-parameters of fp8z_adamw: the fields of fp8z_adamw_hparams that it has, in 64 bits.  The
+ * scalars of a step are formed from them in 64 bits and rounded once. */
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;            /* >= 1                                                 */
+    int32_t decay_mode;      /* fp8z_decay_mode                                      */
+    int32_t reserved;
+} fp8z_adamw_params;         /* 56 bytes */
+
 /*
  * fp8z_encode_adamw_list -- host only: the table fp8z_adamw takes the tensors from, every
  * tensor cut into chunks.  out: host array of `capacity` chunks, which the caller copies
@@ -702,13 +711,13 @@ typedef struct {
  * tensor may be empty.  Tensors do not overlap.  Returns FP8Z_OK / EINVAL / EALIGN / ENOSPACE.
  *
  * fp8z_adamw -- one AdamW step of every tensor of the list: the per-element arithmetic of
- * fp8z_adamw_requant_step (hp's lr, beta1, beta2, eps, weight_decay, step and decay_mode; its
- * quantizer fields are checked and not used), for parameters that are not kept in FP8
- * blocks: norms, biases, embeddings.  grad_factor: device f32, multiplied into every
+ * fp8z_adamw_requant_step, for parameters that are not kept in FP8 blocks: norms, biases,
+ * embeddings.  grad_factor: device f32, multiplied into every
  * gradient first (a clipping coefficient, 1 / a loss scale), or NULL for 1.
  * Moments in 8 bits, for every 128 elements of a tensor (fewer at its end): m is
- * E4M3(m' * s), v is E4M3(sqrt(v') * s), s = 448 / (the largest magnitude of the 128) (1 where all are
- * zero, at most FLT_MAX), and the scale kept is 1 / s: a moment is code * scale, v its square.
+ * E4M3(m' * s), v is E4M3(sqrt(v') * s), s = 448 * (1 / the largest magnitude of the 128) (1 where all are
+ * zero, at most FLT_MAX; two roundings), and the scale kept is 1 / s: a moment is code * scale, v its square.
+ * Here the root and the quotient by it may be off by one unit (2^-23 of their value).
  * A v' that is not zero keeps at least the smallest code.  Zero codes with any finite scale are
  * zero moments, so that buffers of zeros start a run.  An infinite or NaN moment leaves the
  * 128 elements it is among without meaning.
@@ -716,7 +725,7 @@ typedef struct {
  */
 FP8Z_API int fp8z_encode_adamw_list(const fp8z_adamw_tensor *tensors, int32_t n, fp8z_adamw_chunk *out,
                                     int64_t capacity, int64_t *chunks_out);
-FP8Z_API int fp8z_adamw(const fp8z_adamw_chunk *list, int64_t chunks, const fp8z_adamw_hparams *hp,
+FP8Z_API int fp8z_adamw(const fp8z_adamw_chunk *list, int64_t chunks, const fp8z_adamw_params *hp,
                         const float *grad_factor, void *stream);
 
 /*
