@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -205,13 +206,12 @@ def lib():
         L.fp8z_linear_xent_workspace.argtypes = [P, P, XA, i32, i64]
         L.fp8z_linear_xent.argtypes = [P, P, P, XA, P, P, P, P, i64, P, P]
         L.fp8z_linear_xent_grad.argtypes = [P, P, P, XA, P, P, P, P, P, P, i64, P, P]
-        MA = ctypes.POINTER(fp8z_matmul_args)
-        L.fp8z_matmul_workspace.argtypes = [P, P, MA]
-        L.fp8z_matmul.argtypes = [P, P, P, P, MA, P, P, P, i64, P, P]
-        NA = ctypes.POINTER(fp8z_layer_norm_args)
-        L.fp8z_layer_norm.argtypes = [P, P, P, NA, P, P, P, P, P, P]
+        # the structures of these come packed, as bytes
+        L.fp8z_matmul_workspace.argtypes = [P, P, P]
+        L.fp8z_matmul.argtypes = [P, P, P, P, P, P, P, P, i64, P, P]
+        L.fp8z_layer_norm.argtypes = [P, P, P, P, P, P, P, P, P, P]
         L.fp8z_layer_norm_grad_workspace.argtypes = [i64, i64]
-        L.fp8z_layer_norm_grad.argtypes = [P, P, P, P, P, NA, P, P, P, P, i64, P]
+        L.fp8z_layer_norm_grad.argtypes = [P, P, P, P, P, P, P, P, P, P, i64, P]
         L.fp8z_encode_adamw_list.argtypes = [P, i32, P, i64, P]
         L.fp8z_adamw.argtypes = [P, i64, ctypes.POINTER(fp8z_adamw_params), P, P]
         L.fp8z_e4m3_encode_bits.argtypes = [ctypes.c_uint32, i64, P, P]
@@ -579,6 +579,7 @@ def fp8z_dequant_rowwise(q, s, out, transpose=False, stream=None):
 
 # ------------------------------------- operators around the optimizer step
 _FLOATS, _HALVES, _INTS = (FP8Z_F32, FP8Z_BF16, FP8Z_F16), (FP8Z_BF16, FP8Z_F16), (FP8Z_I32, FP8Z_I64)
+_U8 = 100                    # E4M3 codes: no number of the C ABI
 _dtype_codes = {}
 
 
@@ -586,7 +587,7 @@ def _dtype_code(t, name, allowed=_FLOATS):
     if not _dtype_codes:
         import torch
         _dtype_codes.update({torch.float32: FP8Z_F32, torch.bfloat16: FP8Z_BF16, torch.float16: FP8Z_F16,
-                             torch.int32: FP8Z_I32, torch.int64: FP8Z_I64})
+                             torch.int32: FP8Z_I32, torch.int64: FP8Z_I64, torch.uint8: _U8})
     code = _dtype_codes.get(t.dtype)
     if code not in allowed:
         raise ValueError(f"{name} must not be {t.dtype}")
@@ -816,71 +817,102 @@ def fp8z_linear_xent_grad(x, w, targets, loss, total, dx, dw, workspace, ignore_
 
 
 # ------------------------------- operators of a layer with FP8 weights
-def _bank(t, name, device):
-    """(pointer, groups, rows, cols, row stride, group stride) of a CUDA tensor [rows, cols]
-    (groups 0) or [groups, rows, cols] whose rows are contiguous and do not overlap."""
-    if t.dim() != 3:
-        return (*_matrix(t, name, device), 0)
-    if t.shape[0] == 0:
+# These run for a few microseconds where a step has few rows, so that their checks ask a tensor
+# once for what they need, and pack the C structures with struct.
+def _typed_matrix(t, name, device, codes):
+    """_matrix with the tensor's type, one of `codes`: (pointer, rows, cols, row stride, type)."""
+    code = _dtype_codes.get(t.dtype)
+    if code not in codes:
+        code = _dtype_code(t, name, codes)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    if t.get_device() != device:
+        _elsewhere(t, name, device)
+    rows, cols = shape
+    ld, step = stride
+    if rows <= 1:
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), rows, cols, ld, code
+
+
+def _bank(t, name, device, codes):
+    """_typed_matrix of a tensor [rows, cols] or [groups, rows, cols], and its group stride (0, or 3-D)."""
+    shape = t.shape
+    if len(shape) != 3:
+        return (*_typed_matrix(t, name, device, codes), 0)
+    code = _dtype_codes.get(t.dtype)
+    if code not in codes:
+        code = _dtype_code(t, name, codes)
+    if t.get_device() != device:
+        _elsewhere(t, name, device)
+    groups, rows, cols = shape
+    step, ld, one = t.stride()
+    if groups == 0:
         raise ValueError(f"{name} must have a group")
-    p, rows, cols, ld = _matrix(t[0], name, device)
-    step = t.stride(0)
-    if t.shape[0] == 1:
+    if rows <= 1:
+        ld = cols
+    if groups == 1:
         step = rows * ld
+    if (one != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous rows")
     if rows > 0 and cols > 0 and step < (rows - 1) * ld + cols:
         raise ValueError(f"{name}'s groups must not overlap")
-    return p, rows, cols, ld, step
+    return t.data_ptr(), rows, cols, ld, code, step
+
+
+_CODES, _F32 = (_U8,), (FP8Z_F32,)
+_matmul_struct = struct.Struct("<11q6i")
+assert _matmul_struct.size == ctypes.sizeof(fp8z_matmul_args)
 
 
 def _matmul_args(a, a_scale, b, b_scale, out, offsets, accumulate):
-    """(a pointer, a_scale pointer, b pointer, b_scale pointer, out pointer, filled fp8z_matmul_args)."""
+    """(a pointer, a_scale pointer, b pointer, b_scale pointer, out pointer, bytes of fp8z_matmul_args).
+    Without scales: as if they had no strides."""
     here = _current_device()
-    ap, m, k, a_ld = _matrix(a, "a", here)
-    bp, n, bk, b_ld, b_group = _bank(b, "b", here)
-    op, om, on, out_ld, out_group = _bank(out, "out", here)
-    code = _dtype_code(out, "out")
-    if str(a.dtype) != "torch.uint8" or str(b.dtype) != "torch.uint8":
-        raise ValueError(f"a and b must be uint8 E4M3 codes, got {a.dtype} and {b.dtype}")
-    if bk != k or (om, on) != (m, n):
+    ap, m, k, a_ld, _ = _typed_matrix(a, "a", here, _CODES)
+    bp, n, bk, b_ld, _, b_group = _bank(b, "b", here, _CODES)
+    op, om, on, out_ld, code, out_group = _bank(out, "out", here, _FLOATS)
+    if bk != k or om != m or on != n:
         raise ValueError(f"a [.., {k}] and out [.., {m}, {on}] need b [.., {on}, {k}], got {list(b.shape)} and out {list(out.shape)}")
-    banks, grads = b.dim() == 3, out.dim() == 3
-    if (offsets is None) == (banks or grads) or (banks and grads):
-        raise ValueError("offsets go with a b [groups, n, k] or with an out [groups, m, n]")
-    groups = b.shape[0] if banks else out.shape[0] if grads else 0
-    args = fp8z_matmul_args(m, n, k, a_ld, b_ld, out_ld, 0, 0, b_group if banks else 0, 0, out_group if grads else 0, BLOCK,
-                            code, int(bool(accumulate)), groups, FP8Z_GROUP_K if grads else FP8Z_GROUP_ROWS, FP8Z_I32)
-    kb = -(-k // BLOCK)
-    if offsets is not None:
+    groups, wide, grads = 0, FP8Z_I32, False
+    if offsets is not None or b.dim() == 3 or out.dim() == 3:
+        banks, grads = b.dim() == 3, out.dim() == 3
+        if offsets is None or banks == grads:
+            raise ValueError("offsets go with a b [groups, n, k] or with an out [groups, m, n]")
+        groups = b.shape[0] if banks else out.shape[0]
         if offsets.numel() != groups + 1:
             raise ValueError(f"offsets must hold {groups + 1} numbers, got {offsets.numel()}")
-        args.offsets_dtype = _dtype_code(offsets, "offsets", _INTS)
+        wide = _dtype_code(offsets, "offsets", _INTS)
+    kb, blocks = (k + 127) // BLOCK, (n + 127) // BLOCK
     sp = tp = None
+    a_scale_ld = b_scale_ld = kb
+    b_scale_rows, b_scale_group = (1 if grads else BLOCK), n * kb
     if a_scale is not None:
-        sp, rows, cols, args.a_scale_ld = _matrix(a_scale, "a_scale", here)
-        if (rows, cols) != (m, kb) or _dtype_code(a_scale, "a_scale", (FP8Z_F32,)) != FP8Z_F32:
+        sp, rows, cols, a_scale_ld, _ = _typed_matrix(a_scale, "a_scale", here, _F32)
+        if rows != m or cols != kb:
             raise ValueError(f"a_scale must be [{m}, {kb}], got {list(a_scale.shape)}")
-        tp, rows, cols, args.b_scale_ld, step = _bank(b_scale, "b_scale", here)
-        blocks = -(-n // BLOCK)
-        if b_scale.dim() != b.dim() or (banks and b_scale.shape[0] != groups) or cols != kb or rows not in (blocks, n) \
-                or _dtype_code(b_scale, "b_scale", (FP8Z_F32,)) != FP8Z_F32:
+        tp, rows, cols, b_scale_ld, _, b_scale_group = _bank(b_scale, "b_scale", here, _F32)
+        if b_scale.dim() != b.dim() or (groups and not grads and b_scale.shape[0] != groups) or cols != kb \
+                or (rows != blocks and rows != n):
             raise ValueError(f"b_scale must be [{blocks}, {kb}] (blocks) or [{n}, {kb}] (rows), for each group of b, "
                              f"got {list(b_scale.shape)}")
-        args.b_scale_rows = BLOCK if rows == blocks and not (grads and rows == n) else 1
-        args.b_scale_group = step if banks else 0
-        if groups and (args.b_scale_rows == 1) != grads:
+        b_scale_rows = BLOCK if rows == blocks and not (grads and rows == n) else 1
+        if groups and (b_scale_rows == 1) != grads:
             raise ValueError("groups of rows take b_scale in blocks, groups of columns in rows")
-    return ap, sp, bp, tp, op, args
+    packed = _matmul_struct.pack(m, n, k, a_ld, b_ld, out_ld, a_scale_ld, b_scale_ld, b_group, b_scale_group, out_group,
+                                 b_scale_rows, code, 1 if accumulate else 0, groups, FP8Z_GROUP_K if grads else FP8Z_GROUP_ROWS,
+                                 wide)
+    return ap, sp, bp, tp, op, packed
 
 
 def fp8z_matmul_workspace(a, b, out, offsets=None):
     """Bytes of workspace fp8z_matmul(a, .., b, .., out, offsets) needs: 0 where a and b
     start on 16-byte boundaries and have row strides of whole 16 bytes."""
     ap, _, bp, _, _, args = _matmul_args(a, None, b, None, out, offsets, False)
-    # the scales are not looked at: as they are without strides
-    args.a_scale_ld = args.b_scale_ld = -(-args.k // BLOCK)
-    args.b_scale_group = args.n * args.b_scale_ld
-    args.b_scale_rows = 1 if args.groups and args.group_by == FP8Z_GROUP_K else BLOCK
-    size = int(lib().fp8z_matmul_workspace(ap, bp, ctypes.byref(args)))
+    size = int(lib().fp8z_matmul_workspace(ap, bp, args))
     if size < 0:
         raise Fp8zError("fp8z_matmul_workspace", size)
     return size
@@ -899,41 +931,50 @@ def fp8z_matmul(a, a_scale, b, b_scale, out, offsets=None, accumulate=False, wor
     fp8z_matmul_workspace."""
     here = _current_device()
     ap, sp, bp, tp, op, args = _matmul_args(a, a_scale, b, b_scale, out, offsets, accumulate)
-    rc = lib().fp8z_matmul(ap, sp, bp, tp, ctypes.byref(args), _flat(offsets, "offsets", here), op,
-                           _flat(workspace, "workspace", here),
+    rc = lib().fp8z_matmul(ap, sp, bp, tp, args, _flat(offsets, "offsets", here), op, _flat(workspace, "workspace", here),
                            0 if workspace is None else workspace.numel() * workspace.element_size(),
                            _flat(dev_status, "dev_status", here, FP8Z_I32), _stream_handle(stream))
-    _check("fp8z_matmul", rc)
+    if rc:
+        raise Fp8zError("fp8z_matmul", rc)
+
+
+_layer_norm_struct = struct.Struct("<6q4ifi")
+assert _layer_norm_struct.size == ctypes.sizeof(fp8z_layer_norm_args)
 
 
 def _norm_vector(t, name, cols, device, code):
-    if t is not None and t.numel() != cols:
+    if t is None:
+        return None
+    if t.numel() != cols:
         raise ValueError(f"{name} must hold {cols} elements, got {t.numel()}")
     return _flat(t, name, device, code)
 
 
 def _norm_stat(t, name, rows, device):
-    if t is not None and t.numel() < rows:
+    if t is None:
+        return None
+    if t.numel() < rows:
         raise ValueError(f"{name} must hold one value per row")
     return _flat(t, name, device, FP8Z_F32)
 
 
-def _norm_row(t, name, x, device):
+def _norm_row(t, name, rows, cols, dtype, device):
     """(pointer, row stride) of a matrix like x, or (None, 0)."""
     if t is None:
         return None, 0
-    p, rows, cols, ld = _matrix(t, name, device)
-    if (rows, cols) != tuple(x.shape) or t.dtype != x.dtype:
-        raise ValueError(f"{name} must be {list(x.shape)} of {x.dtype}, got {list(t.shape)} of {t.dtype}")
+    p, r, c, ld, _ = _typed_matrix(t, name, device, (dtype,))
+    if r != rows or c != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     return p, ld
 
 
-def _param_code(params, dtype):
-    """The one type of the weight, bias and gradients that are there: float32, or x's."""
-    codes = {_dtype_code(t, name, (FP8Z_F32, dtype)) for t, name in params if t is not None}
-    if len(codes) > 1:
-        raise ValueError("weight, bias and their gradients must be of one type")
-    return codes.pop() if codes else FP8Z_F32
+def _param_code(first, second, third, dtype):
+    """The type of the weight, bias and gradients, of which the first that is there says it: float32, or x's."""
+    t = first if first is not None else second if second is not None else third
+    if t is None:
+        return FP8Z_F32
+    code = _dtype_codes.get(t.dtype)
+    return code if code == FP8Z_F32 or code == dtype else _dtype_code(t, "weight, bias and their gradients", (FP8Z_F32, dtype))
 
 
 def fp8z_layer_norm(x, weight, bias, y, mean, rstd, eps=1e-5, q=None, q_scale=None, pow2=False, stream=None):
@@ -942,23 +983,23 @@ def fp8z_layer_norm(x, weight, bias, y, mean, rstd, eps=1e-5, q=None, q_scale=No
     mean and rstd (float32 [rows]) may be None; q uint8 [rows, cols] and q_scale float32 [rows,
     cols/128] take y as the row-wise E4M3 operand of fp8z_matmul (pow2: power-of-two scales)."""
     here = _current_device()
-    xp, rows, cols, x_ld = _matrix(x, "x", here)
-    dtype = _dtype_code(x, "x")
-    code = _param_code(((weight, "weight"), (bias, "bias")), dtype)
-    yp, y_ld = _norm_row(y, "y", x, here)
-    if (q is None) != (q_scale is None):
-        raise ValueError("q and q_scale go together")
+    xp, rows, cols, x_ld, dtype = _typed_matrix(x, "x", here, _FLOATS)
+    code = _param_code(weight, bias, None, dtype)
+    yp, y_ld = _norm_row(y, "y", rows, cols, dtype, here)
     qp = sp = None
-    if q is not None:
-        if str(q.dtype) != "torch.uint8" or q.numel() != rows * cols or q_scale.numel() < rows * (cols // BLOCK):
+    if q is not None or q_scale is not None:
+        if q is None or q_scale is None:
+            raise ValueError("q and q_scale go together")
+        if q.numel() != rows * cols or q_scale.numel() < rows * (cols // BLOCK):
             raise ValueError(f"q must be uint8 [{rows}, {cols}], q_scale float32 [{rows}, {cols // BLOCK}]")
-        qp, sp = _flat(q, "q", here), _flat(q_scale, "q_scale", here, FP8Z_F32)
-    a = fp8z_layer_norm_args(rows, cols, x_ld, y_ld, 0, 0, dtype, code, int(bool(pow2)), 0, eps, 0)
+        qp, sp = _flat(q, "q", here, _U8), _flat(q_scale, "q_scale", here, FP8Z_F32)
+    args = _layer_norm_struct.pack(rows, cols, x_ld, y_ld, 0, 0, dtype, code, 1 if pow2 else 0, 0, eps, 0)
     rc = lib().fp8z_layer_norm(xp, _norm_vector(weight, "weight", cols, here, code),
-                               _norm_vector(bias, "bias", cols, here, code), ctypes.byref(a), yp,
+                               _norm_vector(bias, "bias", cols, here, code), args, yp,
                                _norm_stat(mean, "mean", rows, here), _norm_stat(rstd, "rstd", rows, here), qp, sp,
                                _stream_handle(stream))
-    _check("fp8z_layer_norm", rc)
+    if rc:
+        raise Fp8zError("fp8z_layer_norm", rc)
 
 
 def fp8z_layer_norm_grad_workspace(rows, cols):
@@ -974,18 +1015,18 @@ def fp8z_layer_norm_grad(dy, x, weight, mean, rstd, dx, dweight, dbias, workspac
     float32), overwritten, or added to with accumulate.  weight, dx, dweight and dbias may
     be None; mean and rstd are the forward call's."""
     here = _current_device()
-    xp, rows, cols, x_ld = _matrix(x, "x", here)
-    dtype = _dtype_code(x, "x")
-    code = _param_code(((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")), dtype)
-    dp, dy_ld = _norm_row(dy, "dy", x, here)
-    gp, dx_ld = _norm_row(dx, "dx", x, here)
-    a = fp8z_layer_norm_args(rows, cols, x_ld, 0, dy_ld, dx_ld, dtype, code, 0, int(bool(accumulate)), 0.0, 0)
+    xp, rows, cols, x_ld, dtype = _typed_matrix(x, "x", here, _FLOATS)
+    code = _param_code(weight, dweight, dbias, dtype)
+    dp, dy_ld = _norm_row(dy, "dy", rows, cols, dtype, here)
+    gp, dx_ld = _norm_row(dx, "dx", rows, cols, dtype, here)
+    args = _layer_norm_struct.pack(rows, cols, x_ld, 0, dy_ld, dx_ld, dtype, code, 0, 1 if accumulate else 0, 0.0, 0)
     rc = lib().fp8z_layer_norm_grad(dp, xp, _norm_vector(weight, "weight", cols, here, code),
-                                    _norm_stat(mean, "mean", rows, here), _norm_stat(rstd, "rstd", rows, here),
-                                    ctypes.byref(a), gp, _norm_vector(dweight, "dweight", cols, here, code),
+                                    _norm_stat(mean, "mean", rows, here), _norm_stat(rstd, "rstd", rows, here), args, gp,
+                                    _norm_vector(dweight, "dweight", cols, here, code),
                                     _norm_vector(dbias, "dbias", cols, here, code), _flat(workspace, "workspace", here),
                                     workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    _check("fp8z_layer_norm_grad", rc)
+    if rc:
+        raise Fp8zError("fp8z_layer_norm_grad", rc)
 
 
 class AdamwList(TensorList):
