@@ -12,6 +12,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -763,6 +764,310 @@ __global__ void __launch_bounds__(512, 2 / kVecs) norm_grad_queue_kernel(const _
         }
 }
 
+// ------------------------------------------------------ rows that start anywhere
+// Rows that do not all start on 16-byte boundaries go through a block's queue in whole 16 bytes,
+// from the boundary before a row on; a thread's eight columns are then shifted out of its own and
+// the next 16 bytes (32 of FP32), and results shifted into whole 16 bytes the other way.
+// 16384 x 2001 BF16: a column at a time 123 us, the gradient 117.
+template <typename T>
+struct Shifted {
+    static constexpr int kUnits = Eight<T>::kUnits, kBytes = 16 * kUnits;      // of a thread's columns
+    uint32_t base;                                       // of the row in shared memory
+
+    // The row's bytes from the boundary before `row` on, 16 a copy.  The bytes before a tensor's
+    // first row are not ours: its first 16 bytes come an element at a time.
+    static __device__ __forceinline__ void fetch(uint32_t to, const T* row, int cols, bool there, bool first) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+        const int shift = int(at & 15), end = there ? shift + cols * int(sizeof(T)) : 0;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int c = (u * int(blockDim.x) + int(threadIdx.x)) * 16, n = min(max(end - c, 0), 16);
+            if (first && there && c == 0) {
+                for (int b = shift; b < n; b += int(sizeof(T))) {
+                    if constexpr (sizeof(T) == 4)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + b), "f"(load_one(reinterpret_cast<const float*>(at - shift + b))) : "memory");
+                    else
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + b), "h"(*reinterpret_cast<const volatile uint16_t*>(at - shift + b)) : "memory");
+                }
+            } else {
+                const uintptr_t from = n > 0 ? at - shift + c : at & ~uintptr_t(15);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + c), "l"(from), "r"(n) : "memory");
+            }
+        }
+    }
+    // The thread's columns of a row that starts `shift` bytes behind a boundary; `left` of them are the row's.
+    __device__ __forceinline__ void load(int shift, int left, uint64_t (&v)[4]) const {
+        uint32_t w[4 * kUnits + 4];
+#pragma unroll
+        for (int u = 0; u <= kUnits; ++u)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * u]), "=r"(w[4 * u + 1]), "=r"(w[4 * u + 2]), "=r"(w[4 * u + 3])
+                         : "r"(base + threadIdx.x * kBytes + u * 16)
+                         : "memory");
+        Eight<T> x;
+        shift_down(w, shift, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = x.pair(i);
+        if (left < kVec) clear(v, left);
+    }
+    static __device__ __forceinline__ void clear(uint64_t (&v)[4], int left) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = halves(v[i]);
+            v[i] = pair_of(2 * i < left ? f.x : 0.0f, 2 * i + 1 < left ? f.y : 0.0f);
+        }
+    }
+    // The words from byte `shift` (0 to 16) on; it is the same for all threads.
+    static __device__ __forceinline__ void shift_down(const uint32_t (&w)[4 * kUnits + 4], int shift, Eight<T>& x) {
+        uint32_t* o = reinterpret_cast<uint32_t*>(&x);
+        const int bits = (shift & 2) * 8;
+        const auto from = [&](auto first) {
+            constexpr int k = decltype(first)::value;
+#pragma unroll
+            for (int i = 0; i < 4 * kUnits; ++i) o[i] = sizeof(T) == 2 && i + k < 4 * kUnits + 3 ? __funnelshift_r(w[i + k], w[i + k + 1], bits) : w[i + k];
+        };
+        switch (shift >> 2) {
+            case 0: from(std::integral_constant<int, 0>()); break;
+            case 1: from(std::integral_constant<int, 1>()); break;
+            case 2: from(std::integral_constant<int, 2>()); break;
+            case 3: from(std::integral_constant<int, 3>()); break;
+            default: from(std::integral_constant<int, 4>());
+        }
+    }
+    // The thread's results to its place, 16 bytes, from where they are shifted into `row` by store
+    // after a barrier.
+    __device__ __forceinline__ void put(const uint64_t (&v)[4], Eight<T>& own) const {
+        Pack<T, kVec> y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = halves(v[i]);
+            y.v[2 * i] = Elem<T>::narrow(f.x);
+            y.v[2 * i + 1] = Elem<T>::narrow(f.y);
+        }
+        own = *reinterpret_cast<const Eight<T>*>(&y);
+        const uint4 last = own.u[kUnits - 1];            // all that the thread after it needs
+        st_shared_16(base + threadIdx.x * 16, last);
+    }
+    // A thread writes the 16 bytes (32) that end inside its own columns; what is before them is the
+    // thread's before it.
+    __device__ __forceinline__ void store(T* row, int cols, const Eight<T>& own) const {
+        const int shift = int(reinterpret_cast<uintptr_t>(row) & 15), behind = shift / int(sizeof(T));
+        uint32_t w[4 * kUnits + 4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(base + (threadIdx.x ? threadIdx.x - 1 : 0) * 16)
+                     : "memory");
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) w[4 + 4 * u] = own.u[u].x, w[5 + 4 * u] = own.u[u].y, w[6 + 4 * u] = own.u[u].z, w[7 + 4 * u] = own.u[u].w;
+        Eight<T> out;
+        shift_down(w, 16 - shift, out);
+        const int col = int(threadIdx.x) * kVec - behind, from = threadIdx.x ? 0 : behind, until = min(kVec, cols - col);
+        if (from == 0 && until == kVec) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) reinterpret_cast<uint4*>(row + col)[u] = out.u[u];
+        } else {
+            const T* e = reinterpret_cast<const T*>(&out);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (i >= from && i < until) row[col + i] = e[i];
+        }
+    }
+    static __device__ __forceinline__ void st_shared_16(uint32_t at, const uint4& v) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    }
+};
+
+// Columns threadIdx.x * 8 on of a weight that may start anywhere.
+__device__ __forceinline__ void params_any(const void* p, int dtype, int left, float otherwise, uint64_t (&w)[4]) {
+    float v[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        const int c = int(threadIdx.x) * kVec + e;
+        v[e] = otherwise;
+        if (p && e < left)
+            v[e] = dtype == FP8Z_F32 ? load_one(static_cast<const float*>(p) + c)
+                   : dtype == FP8Z_BF16 ? load_one(static_cast<const __nv_bfloat16*>(p) + c)
+                                        : load_one(static_cast<const __half*>(p) + c);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pair_of(v[2 * i], v[2 * i + 1]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_shift_kernel(const __grid_constant__ Norm A) {
+    constexpr int kRows = 2, kQueue = 6 / Eight<T>::kUnits;
+    using S = Shifted<T>;
+    extern __shared__ uint4 smem[];
+    __shared__ float shared[2][32 * kRows];
+    dependent_wait();
+    const uint32_t base = smem_addr(smem), row_bytes = blockDim.x * S::kBytes + 16;      // a thread also reads the 16 bytes after its own
+    const T* x = static_cast<const T*>(A.x);
+    const int64_t batches = (int64_t(A.rows) + kRows - 1) / kRows;
+    const float per = 1.0f / float(A.cols);
+    const int left = A.cols - int(threadIdx.x) * kVec;
+    uint64_t w[4], b[4];
+    params_any(A.weight, A.param_dtype, left, 1.0f, w);
+    params_any(A.bias, A.param_dtype, left, 0.0f, b);
+    const auto fetch = [&](int slot, int64_t batch) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t row = batch * kRows + r;
+            const bool there = row < A.rows;
+            S::fetch(base + (slot * kRows + r) * row_bytes, x + (there ? row : 0) * A.x_ld, A.cols, there, row == 0);
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int d = 0; d < kQueue - 1; ++d) fetch(d, blockIdx.x + int64_t(d) * gridDim.x);
+    int slot = 0;
+    for (int64_t batch = blockIdx.x; batch < batches; batch += gridDim.x) {
+        copy_wait<kQueue - 2>();
+        __syncthreads();                                 // all copies of the batch are there, and all have read the one before
+        fetch(slot == 0 ? kQueue - 1 : slot - 1, batch + int64_t(kQueue - 1) * gridDim.x);
+        uint64_t v[kRows][4];
+        float mean[kRows], rstd[kRows];
+        const int64_t row0 = batch * kRows;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const T* row = x + (row0 + r < A.rows ? row0 + r : 0) * A.x_ld;
+            S{base + (slot * kRows + r) * row_bytes}.load(int(reinterpret_cast<uintptr_t>(row) & 15), left, v[r]);
+            const float2 f = halves(add_pair(add_pair(v[r][0], v[r][1]), add_pair(v[r][2], v[r][3])));
+            mean[r] = f.x + f.y;
+        }
+        block_sums<kRows, 32>(mean, shared[0]);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            mean[r] *= per;
+            uint64_t s = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[r][i] = add_pair(v[r][i], pair_of(-mean[r], -mean[r]));
+            if (left < kVec) S::clear(v[r], left);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s = fma_pair(v[r][i], v[r][i], s);
+            const float2 f = halves(s);
+            rstd[r] = f.x + f.y;
+        }
+        block_sums<kRows, 32>(rstd, shared[1]);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (row0 + r >= A.rows) break;
+            rstd[r] = inverse_root(fmaf(rstd[r], per, A.eps));
+            if (threadIdx.x == 0) {
+                if (A.mean) A.mean[row0 + r] = mean[r];
+                if (A.rstd) A.rstd[row0 + r] = rstd[r];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[r][i] = fma_pair(mul_pair(v[r][i], pair_of(rstd[r], rstd[r])), w[i], b[i]);
+        }
+        if (A.y) {
+            Eight<T> own[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) S{base + (slot * kRows + r) * row_bytes}.put(v[r], own[r]);
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (row0 + r < A.rows)
+                    S{base + (slot * kRows + r) * row_bytes}.store(static_cast<T*>(A.y) + (row0 + r) * A.y_ld, A.cols, own[r]);
+        }
+        slot = slot + 1 == kQueue ? 0 : slot + 1;
+    }
+    copy_wait<0>();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_grad_shift_kernel(const __grid_constant__ NormGrad A) {
+    constexpr int kRows = sizeof(T) == 2 ? 2 : 1, kQueue = 3;
+    using S = Shifted<T>;
+    extern __shared__ uint4 smem[];
+    __shared__ float shared[2][32 * 2 * kRows];
+    dependent_wait();
+    const uint32_t base = smem_addr(smem), row_bytes = blockDim.x * S::kBytes + 16;
+    const T *x = static_cast<const T*>(A.x), *dy = static_cast<const T*>(A.dy);
+    const int64_t batches = (int64_t(A.rows) + kRows - 1) / kRows;
+    const float per = 1.0f / float(A.cols);
+    const int left = A.cols - int(threadIdx.x) * kVec;
+    uint64_t w[4], dw[4] = {}, db[4] = {};
+    params_any(A.weight, A.param_dtype, left, 1.0f, w);
+    const auto place = [&](int slot, int tensor, int r) { return base + ((slot * 2 + tensor) * kRows + r) * row_bytes; };
+    const auto fetch = [&](int slot, int64_t batch) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t row = batch * kRows + r, at = row < A.rows ? row : 0;
+            S::fetch(place(slot, 0, r), x + at * A.x_ld, A.cols, row < A.rows, row == 0);
+            S::fetch(place(slot, 1, r), dy + at * A.dy_ld, A.cols, row < A.rows, row == 0);
+        }
+        copy_commit();
+    };
+    float mean[kRows], rstd[kRows];                      // of the next batch
+    const auto stats = [&](int64_t batch) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const bool there = batch * kRows + r < A.rows;
+            mean[r] = there ? load_one(A.mean + batch * kRows + r) : 0.0f;
+            rstd[r] = there ? load_one(A.rstd + batch * kRows + r) : 0.0f;
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < kQueue - 1; ++d) fetch(d, blockIdx.x + int64_t(d) * gridDim.x);
+    stats(blockIdx.x);
+    int slot = 0, turn = 0;
+    for (int64_t batch = blockIdx.x; batch < batches; batch += gridDim.x) {
+        copy_wait<kQueue - 2>();
+        __syncthreads();
+        fetch(slot == 0 ? kQueue - 1 : slot - 1, batch + int64_t(kQueue - 1) * gridDim.x);
+        uint64_t xh[kRows][4], g[kRows][4];
+        float sums[2 * kRows], scale[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t row = batch * kRows + r < A.rows ? batch * kRows + r : 0;
+            S{place(slot, 0, r)}.load(int(reinterpret_cast<uintptr_t>(x + row * A.x_ld) & 15), left, xh[r]);
+            S{place(slot, 1, r)}.load(int(reinterpret_cast<uintptr_t>(dy + row * A.dy_ld) & 15), left, g[r]);
+            scale[r] = rstd[r];
+            uint64_t s1 = 0, s2 = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xh[r][i] = mul_pair(add_pair(xh[r][i], pair_of(-mean[r], -mean[r])), pair_of(rstd[r], rstd[r]));
+                dw[i] = fma_pair(g[r][i], xh[r][i], dw[i]);
+                db[i] = add_pair(db[i], g[r][i]);
+                g[r][i] = mul_pair(g[r][i], w[i]);
+                s1 = add_pair(s1, g[r][i]);
+                s2 = fma_pair(g[r][i], xh[r][i], s2);
+            }
+            const float2 a = halves(s1), c = halves(s2);
+            sums[r] = a.x + a.y;
+            sums[kRows + r] = c.x + c.y;
+        }
+        stats(batch + gridDim.x);
+        block_sums<2 * kRows, 32>(sums, shared[turn]);
+        turn ^= 1;
+        if (A.dx) {
+            Eight<T> own[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float c1 = sums[r] * per, c2 = sums[kRows + r] * per;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    g[r][i] = mul_pair(fma_pair(xh[r][i], pair_of(-c2, -c2), add_pair(g[r][i], pair_of(-c1, -c1))), pair_of(scale[r], scale[r]));
+                S{place(slot, 0, r)}.put(g[r], own[r]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (batch * kRows + r < A.rows)
+                    S{place(slot, 0, r)}.store(static_cast<T*>(A.dx) + (batch * kRows + r) * A.dx_ld, A.cols, own[r]);
+        }
+        slot = slot + 1 == kQueue ? 0 : slot + 1;
+    }
+    copy_wait<0>();
+    float* out = A.part + int64_t(blockIdx.x) * 2 * A.cols + threadIdx.x * kVec;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = halves(dw[i]), c = halves(db[i]);
+        if (2 * i < left) out[2 * i] = a.x, out[A.cols + 2 * i] = c.x;
+        if (2 * i + 1 < left) out[2 * i + 1] = a.y, out[A.cols + 2 * i + 1] = c.y;
+    }
+}
+
 // Rows longer than 32768 columns: the sums of dw and db are added to in `part`.
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const __grid_constant__ NormGrad A) {
@@ -856,6 +1161,35 @@ bool queued(bool wide, int64_t rows, int64_t cols, int sms) {
     return wide && cols % kVec == 0 && cols > 32 * kVec * 2 && cols <= 8192 && rows > 2 * sms;
 }
 
+// Other rows of as many columns: threads that hold a row and what may lie before and after it in whole 16 bytes.
+template <typename T>
+int shift_threads(int64_t cols) {
+    return int((cols * int(sizeof(T)) + 29 + 16 * Eight<T>::kUnits * 32 - 1) / (16 * Eight<T>::kUnits * 32) * 32);
+}
+bool shifted(bool queue, int64_t rows, int64_t cols, int sms) {
+    return !queue && cols > 32 * kVec * 2 && cols <= 8176 && rows > 2 * sms;
+}
+
+template <typename T>
+int start_shift(const Norm& A, int slot, int sms, cudaStream_t st) {
+    constexpr int kBatches = 6 / Eight<T>::kUnits, kMost = kBatches * 2 * (1024 * Shifted<T>::kBytes + 16);
+    const auto k = &norm_shift_kernel<T>;
+    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot, kMost)) return rc;
+    const int threads = shift_threads<T>(A.cols);
+    const int64_t batches = (int64_t(A.rows) + 1) / 2, most = int64_t(sms) * (1024 / threads);
+    return launch_dependent(k, dim3(unsigned(std::min(batches, most))), threads,
+                            kBatches * 2 * (threads * Shifted<T>::kBytes + 16), st, A);
+}
+
+template <typename T>
+int start_grad_shift(const NormGrad& A, int slot, int parts, cudaStream_t st) {
+    constexpr int kRows = 3 * 2 * (sizeof(T) == 2 ? 2 : 1), kMost = kRows * (1024 * Shifted<T>::kBytes + 16);
+    const auto k = &norm_grad_shift_kernel<T>;
+    if (int rc = host::set_smem_once(reinterpret_cast<const void*>(k), slot, kMost)) return rc;
+    const int threads = shift_threads<T>(A.cols);
+    return launch_dependent(k, dim3(unsigned(parts)), threads, kRows * (threads * Shifted<T>::kBytes + 16), st, A);
+}
+
 // Threads of a queued row of the gradient, eight columns each (16 past 4096 columns), and blocks an SM.
 int queue_threads(int64_t cols) { return int((cols + (cols > 4096 ? 511 : 255)) / (cols > 4096 ? 512 : 256) * 32); }
 int queue_blocks(int64_t cols) { return cols > 4096 ? 1 : 1024 / queue_threads(cols); }
@@ -886,7 +1220,9 @@ int start_grad_queue(const NormGrad& A, int slot, int parts, cudaStream_t st) {
 
 template <typename T>
 int start_type(const Norm& A, bool wide, int slot, int sms, cudaStream_t st) {
-    if (queued(wide, A.rows, A.cols, sms)) return A.q ? start_queue<T, true>(A, slot, sms, st) : start_queue<T, false>(A, slot + 1, sms, st);
+    const bool queue = queued(wide, A.rows, A.cols, sms);
+    if (queue) return A.q ? start_queue<T, true>(A, slot, sms, st) : start_queue<T, false>(A, slot + 1, sms, st);
+    if (!A.q && shifted(queue, A.rows, A.cols, sms)) return start_shift<T>(A, slot + 2, sms, st);
     if (A.cols > kLongest)
         return launch_dependent(&norm_long_kernel<T>, dim3(unsigned(std::min(A.rows, sms * 2))), 1024, 0, st, A);
     return wide ? start_width<T, true>(A, sms, st) : start_width<T, false>(A, sms, st);
@@ -894,9 +1230,13 @@ int start_type(const Norm& A, bool wide, int slot, int sms, cudaStream_t st) {
 
 // Blocks of the gradient, each of which leaves a part.
 int parts_of(int64_t rows, int64_t cols, bool wide, int dtype, int sms) {
-    if (queued(wide, rows, cols, sms)) {
+    const bool queue = queued(wide, rows, cols, sms);
+    if (queue || shifted(queue, rows, cols, sms)) {
         const int per = dtype == FP8Z_F32 ? 1 : 2;
-        return int(std::min<int64_t>({(rows + per - 1) / per, int64_t(sms) * queue_blocks(cols), most_parts(cols)}));
+        const int blocks = queue ? queue_blocks(cols) : 1024 / (dtype == FP8Z_F32 ? shift_threads<float>(cols) : shift_threads<__half>(cols));
+        // a part is written and read again: at least four batches a block, once every SM has one
+        const int64_t batches = (rows + per - 1) / per;
+        return int(std::min<int64_t>({batches, std::max<int64_t>(batches / 4, sms), int64_t(sms) * blocks, most_parts(cols)}));
     }
     const int64_t blocks = cols <= 32 * kVec * 2 ? (rows + 7) / 8 : rows;
     return int(std::min<int64_t>({std::max<int64_t>(blocks, 1), int64_t(sms) * (cols <= 256 * kVec ? 2 : 1), most_parts(cols)}));
@@ -919,7 +1259,9 @@ int start_grad_width(const NormGrad& A, int parts, cudaStream_t st) {
 
 template <typename T>
 int start_grad_type(const NormGrad& A, bool wide, int slot, int parts, int sms, cudaStream_t st) {
-    if (queued(wide, A.rows, A.cols, sms)) return start_grad_queue<T>(A, slot, parts, st);
+    const bool queue = queued(wide, A.rows, A.cols, sms);
+    if (queue) return start_grad_queue<T>(A, slot, parts, st);
+    if (shifted(queue, A.rows, A.cols, sms)) return start_grad_shift<T>(A, slot + 2, parts, st);
     if (A.cols > kLongest) return launch_dependent(&norm_grad_long_kernel<T>, dim3(unsigned(parts)), 1024, 0, st, A);
     return wide ? start_grad_width<T, true>(A, parts, st) : start_grad_width<T, false>(A, parts, st);
 }
@@ -995,8 +1337,8 @@ extern "C" int fp8z_layer_norm_grad(const void* dy, const void* x, const void* w
         parts = parts_of(a.rows, a.cols, wide, a.dtype, sms);
         const NormGrad A = {int(a.rows), int(a.cols), dy, x, a.dy_ld, a.x_ld, a.dx_ld, weight, a.param_dtype, mean, rstd, dx, part};
         const int rc = a.dtype == FP8Z_F32 ? start_grad_type<float>(A, wide, 39, parts, sms, st)
-                       : a.dtype == FP8Z_BF16 ? start_grad_type<__nv_bfloat16>(A, wide, 41, parts, sms, st)
-                                              : start_grad_type<__half>(A, wide, 43, parts, sms, st);
+                       : a.dtype == FP8Z_BF16 ? start_grad_type<__nv_bfloat16>(A, wide, 42, parts, sms, st)
+                                              : start_grad_type<__half>(A, wide, 45, parts, sms, st);
         if (rc) return rc;
     }
     if (!dweight && !dbias) return FP8Z_OK;
