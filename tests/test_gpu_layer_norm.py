@@ -100,14 +100,14 @@ def run_forward(rows, cols, dtype, pdtype, weight=True, bias=True, y=True, q=Fal
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (1, 256), (9, 255), (2, 1000), (33, 1024), (5, 1025), (400, 2001),
                                        (8, 4097), (700, 4096), (8, 7168), (310, 7168), (310, 7167), (4, 8193), (306, 12000),
-                                       (2, 32768), (3, 32769), (2, 70001)])
+                                       (700, 513), (701, 2001), (650, 8176), (650, 8177), (641, 4099), (2, 32768), (3, 32769), (2, 70001)])
 def test_forward(rows, cols):
     for i, (dt, pt) in enumerate(((BF16, F32), (F16, F16), (F32, F32), (BF16, BF16))):
         run_forward(rows, cols, dt, pt, weight=i != 2 or cols % 2 == 0, bias=i % 2 == 0, seed=i)
 
 
 @pytest.mark.parametrize("pad,lead", [(8, 8), (1, 0), (3, 5), (0, 1)])
-@pytest.mark.parametrize("rows,cols", [(5, 200), (3, 1000), (400, 4104), (4, 9000)])
+@pytest.mark.parametrize("rows,cols", [(5, 200), (3, 1000), (400, 4104), (4, 9000), (700, 1003)])
 def test_forward_strides(rows, cols, pad, lead):
     run_forward(rows, cols, BF16, F32, pad=pad, lead=lead)
     run_forward(rows, cols, F32, F32, pad=pad, lead=lead)
@@ -194,14 +194,15 @@ def run_gradient(rows, cols, dtype, pdtype, weight=True, bias=True, accumulate=F
 
 @pytest.mark.parametrize("rows,cols", [(0, 64), (1, 1), (3, 7), (100, 256), (9, 512), (2600, 500), (5, 513), (1021, 2001), (700, 2048),
                                        (8, 4097), (700, 4096), (310, 7168), (310, 7167), (4, 8193), (306, 12000), (2, 32768),
-                                       (3, 32769), (160, 40000)])
+                                       (3, 32769), (160, 40000),
+                                       (4001, 513), (3700, 2001), (3650, 8175), (4100, 519), (4100, 1000)])
 def test_gradient(rows, cols):
     for i, (dt, pt) in enumerate(((BF16, F32), (F16, F16), (F32, F32), (BF16, BF16))):
         run_gradient(rows, cols, dt, pt, weight=i != 2 or cols % 2 == 0, bias=i % 2 == 0, accumulate=i in (0, 3), seed=i, dx=i != 3)
 
 
 @pytest.mark.parametrize("pad,lead", [(8, 8), (1, 0), (3, 5), (0, 1)])
-@pytest.mark.parametrize("rows,cols", [(5, 200), (3, 1000), (400, 4104), (4, 9000)])
+@pytest.mark.parametrize("rows,cols", [(5, 200), (3, 1000), (400, 4104), (4, 9000), (3700, 1003)])
 def test_gradient_strides(rows, cols, pad, lead):
     run_gradient(rows, cols, BF16, F32, pad=pad, lead=lead)
     run_gradient(rows, cols, F32, F32, pad=pad, lead=lead, accumulate=True)
