@@ -76,6 +76,15 @@ __device__ __forceinline__ float ld_scale(const float* p) {
     return v;
 }
 
+// True in one lane of a warp that is together, by the instruction from which the compiler knows that
+// there is one: what needs uniform registers (products, commits, tiled copies) then takes its
+// operands straight, where behind a comparison of lane numbers it goes through a loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // Registers a thread of this warpgroup has from here on.
 template <int kRegs>
 __device__ __forceinline__ void fewer_registers() {
@@ -431,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
     if (warp < 4) fewer_registers<kOtherRegs>();
     if (!run) {
     } else if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int s = 0, ph = 0;
             uint32_t issued = 0;
             bool ok = true;
@@ -456,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
             st_cluster_u32(cluster_addr(smem_addr(const_cast<uint32_t*>(issued_by + rank)), 0), issued);
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elect_one()) {
             constexpr uint32_t idesc = umma_idesc_e4m3(kTM, kTN);
             int s = 0, ph = 0, b = 0, bph = 0;
             bool ok = true;
@@ -690,7 +699,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 
     if (!run) {
     } else if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int s = 0, ph = 0;
             uint32_t issued = 0;
             for (int k = k0; k < k1; ++k) {
@@ -708,7 +717,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
             *issued_by = issued;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc = umma_idesc_e4m3(kRowsB, kT);
             int s = 0, ph = 0, b = 0, bph = 0;
             for (int k = k0; k < k1; ++k) {
