@@ -152,13 +152,6 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
     return v;
 }
 
-// Column j of v: a row's scales of four blocks from k on, zeros past k1.
-template <int kN>
-__device__ __forceinline__ void load_scales(const float* row, int k, int k1, float (&v)[4][kN], int j) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i][j] = k + i < k1 ? ld_scale(row + k + i) : 0.0f;
-}
-
 // A block's sums times their scales, added up: kCols columns of tensor memory from
 // `acc` on, of the row of each lane, kStep at a time, the next ones on their way.
 // kColScales: the columns' scales are the FP32 numbers at `scales` in shared memory and
@@ -528,33 +521,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
         }
         if (lane == 0) bulk_wait_all();
     } else if (warp == 2) {
-        // Scales, four blocks of K at a time: 16 to 48 loads a lane are under way at once.
+        // Scales, two blocks of K at a time: 12 to 24 loads a lane are under way at once.
+        constexpr int kB = kRows ? kTN / 32 : 2;       // of b that a lane brings
         int slot = 0, sph = 0;
         bool ok = true;
         for (int t = pair; ok && walk.at(A, starts, t, at); t += pairs) {
+            const float* pa = A.a_scale + int64_t(at.row + rank * kHalf + lane) * A.a_scale_ld;
             const float* pb = A.b_scale + at.group * A.b_scale_group;
-            for (int k = at.k0; k < at.k1; k += kScaleBlocks) {
-                float v[kScaleBlocks][kHalf / 32], w[kScaleBlocks][kRows ? kTN / 32 : 2];
+            const int rows = A.m - (at.row + rank * kHalf + lane), b0 = kRows ? at.n * kTN + lane : at.n * 2;
+            for (int k = at.k0; ok && k < at.k1; k += kScaleBlocks) {
+#pragma unroll 1
+                for (int i = 0; i < kScaleBlocks; i += 2) {
+                    float v[2][kHalf / 32], w[2][kB];
 #pragma unroll
-                for (int j = 0; j < kHalf / 32; ++j)
-                    load_scales(A.a_scale + min(at.row + rank * kHalf + j * 32 + lane, A.m - 1) * A.a_scale_ld, k, at.k1, v, j);
+                    for (int h = 0; h < 2; ++h) {
+                        const bool in = k + i + h < at.k1;
 #pragma unroll
-                for (int j = 0; j < (kRows ? kTN / 32 : 2); ++j)
-                    load_scales(pb + min(kRows ? at.n * kTN + j * 32 + lane : at.n * 2 + j, A.b_scale_last) * A.b_scale_ld, k, at.k1, w, j);
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sempty(slot), sph ^ 1, wd));
-                if (!ok) break;
-                const uint32_t to = base + L::kScales + slot * L::kScaleBytes + lane * 4;
+                        for (int j = 0; j < kHalf / 32; ++j) v[h][j] = in && j * 32 < rows ? ld_scale(pa + j * 32 * A.a_scale_ld + k + i + h) : 0.0f;
 #pragma unroll
-                for (int i = 0; i < kScaleBlocks; ++i) {
-#pragma unroll
-                    for (int j = 0; j < kHalf / 32; ++j) {
-                        st_shared_f32(to + (i * L::kScaleWords + j * 32) * 4, kRows ? v[i][j] : v[i][j] * w[i][0]);
-                        if (!kRows) st_shared_f32(to + (i * L::kScaleWords + kHalf + j * 32) * 4, v[i][j] * w[i][1]);
+                        for (int j = 0; j < kB; ++j)
+                            w[h][j] = in ? ld_scale(pb + min(b0 + j * (kRows ? 32 : 1), A.b_scale_last) * A.b_scale_ld + k + i + h) : 0.0f;
                     }
-                    if (kRows)
+                    if (i == 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sempty(slot), sph ^ 1, wd));
+                    if (!ok) break;
+                    const uint32_t to = base + L::kScales + slot * L::kScaleBytes + i * L::kScaleWords * 4 + lane * 4;
 #pragma unroll
-                        for (int j = 0; j < kTN / 32; ++j) st_shared_f32(to + (i * L::kScaleWords + kHalf + j * 32) * 4, w[i][j]);
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int j = 0; j < kHalf / 32; ++j) {
+                            st_shared_f32(to + (h * L::kScaleWords + j * 32) * 4, kRows ? v[h][j] : v[h][j] * w[h][0]);
+                            if (!kRows) st_shared_f32(to + (h * L::kScaleWords + kHalf + j * 32) * 4, v[h][j] * w[h][1]);
+                        }
+                        if (kRows)
+#pragma unroll
+                            for (int j = 0; j < kB; ++j) st_shared_f32(to + (h * L::kScaleWords + kHalf + j * 32) * 4, w[h][j]);
+                    }
                 }
+                if (!ok) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sfull(slot));
                 if (slot) sph ^= 1;
@@ -599,7 +602,7 @@ constexpr int kMaxSplits = 8;
 template <int kT>
 struct Small {
     static constexpr int kTileA = kT * kBK, kTileB = kRowsB * kBK, kStageBytes = kTileA + kTileB;
-    static constexpr int kStages = kT <= 32 ? 5 : kT == 64 ? 4 : 3;            // two blocks an SM
+    static constexpr int kStages = kT <= 32 ? 5 : 4;                           // two blocks an SM
     static constexpr int kAcc = kT >= 32 ? 256 / kT : 8;                       // accumulators
     static constexpr int kTmem = kAcc * kT;
     static constexpr int kScales = kStages * kStageBytes;                      // two blocks' scales for each reader
@@ -945,26 +948,27 @@ Plan plan(const void* a, const void* b, const fp8z_matmul_args& g) {
 struct Choice {
     int rows, splits;
 };
+// By time: a block of K takes a pair 0.5 us (0.85 where every column has a scale), and a small block
+// 0.45 us, or 0.6 where two share an SM; a launch takes 4 us, a large tile's results 1.5, joining the
+// parts of K 1.5; nothing is quicker than its bytes.  Measured: 512 x 2048 x 7168 33 us by pairs and 25
+// with tiles of 64 rows and K in two, 1000 x 2048 x 2048 14.6 and 15.4, 4096 x 2048 x 2048 25 and 66.
 Choice choose(const fp8z_matmul_args& g, int sms) {
     if (g.groups > 0 && g.group_by == FP8Z_GROUP_K) return {0, 1};
     const int64_t kb = (g.k + kBK - 1) / kBK, groups = std::max<int64_t>(g.groups, 1);
     const int64_t each = (g.m + groups - 1) / groups;         // rows of a product, on average
-    const auto tiles = [&](int64_t rows_a, int64_t rows_b) {
-        return (g.groups > 0 ? (each + rows_a - 1) / rows_a * groups : (g.m + rows_a - 1) / rows_a) * ((g.n + rows_b - 1) / rows_b);
-    };
-    const int64_t pairs = sms / 2, slots = sms * 2;
-    const int64_t large = ((tiles(kTM, kTN) + pairs - 1) / pairs) * (kb * 560 + 3000) + 4000;
+    const auto tiles = [&](int64_t rows_a, int64_t rows_b) { return (each + rows_a - 1) / rows_a * groups * ((g.n + rows_b - 1) / rows_b); };
+    const auto waves = [](int64_t t, int64_t at_once) { return double((t + at_once - 1) / at_once); };
+    const double block = g.b_scale_rows == 1 ? 0.85 : 0.5, bytes = 5.0 + double(std::min<int64_t>(groups, std::max<int64_t>(g.m, 1))) * double(g.n) * double(g.k) / 6.5e6;
     Choice best = {0, 1};
-    int64_t least = large;
-    for (int rows = 16; rows <= 128; rows *= 2) {
+    double least = std::max(bytes, 4.0 + waves(tiles(kTM, kTN), sms / 2) * (double(kb) * block + 1.5));
+    for (int rows = 16; rows <= 64; rows *= 2) {
         if (rows > 16 && rows / 2 >= each) break;
         const int64_t t = tiles(rows, kRowsB);
-        const int64_t block = 300 + 6 * rows;                  // a block of K, with two blocks on the SM
         for (int splits = 1; splits <= kMaxSplits && splits <= kb; ++splits) {
-            const int64_t cost = ((t * splits + slots - 1) / slots) * ((kb + splits - 1) / splits) * block * 2 +
-                                 2500 + (splits > 1 ? 1500 + 10 * rows : 10 * rows);
-            if (cost < least) {
-                least = cost;
+            const double cost = 4.0 + waves(t * splits, 2 * sms) * double((kb + splits - 1) / splits) * (t * splits > sms ? 0.6 : 0.45) + (splits > 1 ? 1.5 : 0.0);
+            // the fewer parts and rows among equals
+            if (std::max(cost, bytes) < least - 0.01) {
+                least = std::max(cost, bytes);
                 best = {rows, splits};
             }
         }
@@ -1085,8 +1089,7 @@ int run(const void* a, const float* a_scale, const void* b, const float* b_scale
     switch (c.rows) {
         case 16: return launch_small<16>(ta, tb, A, rows_scaled, c.splits, blocks, 19, st);
         case 32: return launch_small<32>(ta, tb, A, rows_scaled, c.splits, blocks, 21, st);
-        case 64: return launch_small<64>(ta, tb, A, rows_scaled, c.splits, blocks, 23, st);
-        default: return launch_small<128>(ta, tb, A, rows_scaled, c.splits, blocks, 25, st);
+        default: return launch_small<64>(ta, tb, A, rows_scaled, c.splits, blocks, 23, st);
     }
 }
 
