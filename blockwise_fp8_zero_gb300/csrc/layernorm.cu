@@ -447,10 +447,11 @@ __device__ __forceinline__ uint2 tile_codes(const uint64_t (&v)[4], float amax, 
     return make_uint2(pack_e4m3x4(t[0], t[1], t[2], t[3]), pack_e4m3x4(t[4], t[5], t[6], t[7]));
 }
 
-// 1 / sqrt(x) to within 2 ulp: the approximation and one Newton step; infinite for 0.
+// 1 / sqrt(x) to within 2 ulp: the approximation and one Newton step; infinite for 0, and 0 for a
+// sum of squares that has overflowed.
 __device__ __forceinline__ float inverse_root(float x) {
     const float r = rsqrtf(x);
-    return x == 0.0f ? r : fmaf(r * 0.5f, fmaf(-x * r, r, 1.0f), r);
+    return x == 0.0f || x > FLT_MAX ? r : fmaf(r * 0.5f, fmaf(-x * r, r, 1.0f), r);
 }
 
 // Batches of two rows, one block a batch at a time: the sums of a batch share two barriers.

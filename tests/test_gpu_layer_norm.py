@@ -242,3 +242,14 @@ def test_same_bits_every_time():
         got = [t.clone() for t in (dw, db, dx)]
         assert first is None or all(torch.equal(a, b) for a, b in zip(first, got))
         first = got
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 1024), (700, 1024), (701, 2001), (2, 40000)])
+def test_squares_that_overflow(rows, cols):
+    """Values of 1e25: their squares are infinite in FP32, rstd is 0 and y the bias, whichever way the rows go."""
+    g = gen(9)
+    x = (torch.randn(rows, cols, generator=g, device="cuda").sign() * 1e25).to(BF16)
+    b = rand(g, (cols,), F32)
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    fp8z.fp8z_layer_norm(x, None, b, y, mean, rstd)
+    assert (rstd == 0).all() and torch.equal(y, b.to(BF16).expand(rows, cols))
