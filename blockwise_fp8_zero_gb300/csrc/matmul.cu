@@ -886,10 +886,10 @@ bool bytes_map(CUtensorMap* map, int rank, const void* p, int64_t cols, int64_t 
 }
 
 bool out_map(CUtensorMap* map, const fp8z_matmul_args& a, void* p) {
-    const bool by_k = a.group_by == FP8Z_GROUP_K && a.groups > 0;
+    const bool bank = a.group_by == FP8Z_GROUP_K && a.groups > 1;
     const int64_t size = dtype_bytes(a.out_dtype);
-    const cuuint64_t dims[3] = {cuuint64_t(a.n), cuuint64_t(a.m), cuuint64_t(by_k ? a.groups : 1)};
-    const cuuint64_t strides[2] = {cuuint64_t(a.out_ld * size), cuuint64_t((by_k ? a.out_group : a.out_ld * a.m) * size)};
+    const cuuint64_t dims[3] = {cuuint64_t(a.n), cuuint64_t(a.m), cuuint64_t(bank ? a.groups : 1)};
+    const cuuint64_t strides[2] = {cuuint64_t(a.out_ld * size), cuuint64_t((bank ? a.out_group : a.out_ld * a.m) * size)};
     const cuuint32_t box[3] = {cuuint32_t(128 / size), 32, 1};
     const auto type = a.out_dtype == FP8Z_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     return make_map(map, type, 3, p, dims, strides, box);
@@ -919,7 +919,8 @@ bool args_ok(const fp8z_matmul_args& a) {
     if (a.groups > 1 && a.group_by == FP8Z_GROUP_K && (a.out_group < a.out_ld * (a.m - 1) + a.n || a.out_group > most))
         return false;
     // tiles are counted in 32 bits
-    return ((a.m + 15) / 16 + a.groups) * ((a.n + 127) / 128) * std::max<int64_t>(a.groups, 1) <= (1LL << 26);
+    const int64_t products = a.groups > 0 && a.group_by == FP8Z_GROUP_K ? a.groups : 1;
+    return ((a.m + 15) / 16 + a.groups) * ((a.n + 127) / 128) * products <= (1LL << 26);
 }
 
 // A tensor map steps over rows of whole 16 bytes.
@@ -1077,7 +1078,7 @@ int run(const void* a, const float* a_scale, const void* b, const float* b_scale
         const int64_t size = dtype_bytes(g.out_dtype);
         // a tile's store writes whole 16 bytes, and what lies behind a row that ends between two is not ours
         A.staged = host::aligned(out, 16) && g.out_ld * size % 16 == 0 && g.n * size % 16 == 0 &&
-                   (!by_k || g.out_group * size % 16 == 0);
+                   (!by_k || g.groups == 1 || g.out_group * size % 16 == 0);
         if (!A.staged) tc = ta;                        // not used
         else if (!out_map(&tc, g, out)) return FP8Z_ECUDA;
         const int64_t tiles = by_rows ? (g.m / kTM + g.groups) * A.nt : int64_t(A.mt) * A.nt * A.groups;

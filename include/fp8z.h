@@ -615,8 +615,9 @@ typedef struct {
  * fp8z_matmul_workspace -- bytes of workspace (device, 256-byte aligned, no
  * initialisation): 0 where a and b start on 16-byte boundaries and their strides are
  * multiples of 16; other operands are copied there first.
- * m, n, k <= 2^30, and at most 2^26 tiles of 16 x 128 in m x n (times the groups).
- * k = 0 gives zeros; it is refused with FP8Z_GROUP_ROWS.
+ * m, n, k <= 2^30, and at most 2^26 tiles of 16 x 128 in m x n (all results together; one
+ * row of tiles more for every group).
+ * k = 0 gives zeros, and offsets are not read; it is refused with FP8Z_GROUP_ROWS.
  * Returns FP8Z_OK / EINVAL / EALIGN / ENOSPACE / EUNSUPPORTED / ECUDA.
  */
 FP8Z_API int64_t fp8z_matmul_workspace(const void *a, const void *b, const fp8z_matmul_args *args);

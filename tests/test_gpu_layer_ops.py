@@ -237,3 +237,22 @@ def test_binding_refusals():
                  lambda: fp8z.fp8z_encode_adamw_list([w.half()], [w], [w], [w])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_one_group_of_columns_has_no_group_stride():
+    """Through the C ABI: out_group of a single group is not used, 0 among its values."""
+    import ctypes
+    g = torch.Generator(device="cuda").manual_seed(8)
+    m, n, k = 300, 520, 640
+    a, b = codes(g, m, k), codes(g, n, k)
+    sa, sb = torch.ones(m, 5, device="cuda"), torch.ones(n, 5, device="cuda")
+    off = torch.tensor([0, k], dtype=torch.int32, device="cuda")
+    want, out = torch.empty(m, n, device="cuda"), torch.empty(m, n, device="cuda")
+    fp8z.fp8z_matmul(a, sa, b, sb, want[None], offsets=off)
+    for step in (0, 3, -16, 2 ** 50):
+        out.zero_()
+        args = fp8z.fp8z_matmul_args(m=m, n=n, k=k, a_ld=k, b_ld=k, out_ld=n, a_scale_ld=5, b_scale_ld=5, out_group=step, b_scale_rows=1,
+                                     out_dtype=fp8z.FP8Z_F32, groups=1, group_by=fp8z.FP8Z_GROUP_K, offsets_dtype=fp8z.FP8Z_I32)
+        rc = fp8z.lib().fp8z_matmul(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), ctypes.byref(args), off.data_ptr(),
+                                    out.data_ptr(), None, 0, None, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and torch.equal(out, want), step

@@ -173,3 +173,15 @@ def test_binding_refuses_host_tensors():
         pytest.skip("the binding asks for the current device first")
     with pytest.raises(ValueError):
         fp8z.fp8z_layer_norm(torch.zeros(2, 8), None, None, None, None, None)
+
+
+def test_matmul_tiles_of_all_groups(L):
+    """Rows of a bank are counted once, results of groups of columns for each group: at most 2^26 tiles."""
+    def size(**kw):
+        a = dict(m=2 ** 18, n=7168, k=2048, a_ld=2048, b_ld=2048, out_ld=7168, a_scale_ld=16, b_scale_ld=16, b_group=7168 * 2048,
+                 b_scale_group=56 * 16, out_group=2 ** 18 * 7168, b_scale_rows=128, out_dtype=F32, accumulate=0, groups=256,
+                 group_by=ROWS, offsets_dtype=I32)
+        a.update(kw)
+        return L.fp8z_matmul_workspace(P, P, ctypes.byref(fp8z.fp8z_matmul_args(**a)))
+    assert size() == 0 and size(m=2 ** 24) == 0 and size(m=2 ** 25) == EINVAL
+    assert size(group_by=K, b_scale_rows=1) == EINVAL and size(group_by=K, b_scale_rows=1, m=2 ** 14, out_group=2 ** 14 * 7168) == 0
