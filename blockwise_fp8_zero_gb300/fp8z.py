@@ -1065,6 +1065,14 @@ def fp8z_encode_adamw_list(params, grads, exp_avgs, exp_avg_sqs, copies=None, ex
         r["copy"] = _flat(c, f"copy {i}", here) or 0
         r["count"], r["g_dtype"], r["state_bits"] = p.numel(), _dtype_code(g, f"grad {i}"), 32 if wide else 8
         r["copy_dtype"] = FP8Z_BF16 if c is None else _dtype_code(c, f"copy {i}", _HALVES)
+    count, moment = rows["count"][:n], rows["count"][:n] * (rows["state_bits"][:n] // 8)
+    scales = -(-count // BLOCK) * 4
+    start = np.concatenate([rows[k][:n] for k in ("p", "m", "v", "copy", "m_scale", "v_scale")])
+    length = np.concatenate([count * 4, moment, moment, count * 2, scales, scales]) * (start != 0)
+    order = np.argsort(start[length > 0])
+    start, length = start[length > 0][order], length[length > 0][order]
+    if (start[:-1] + length[:-1].astype(np.uint64) > start[1:]).any():
+        raise ValueError("parameters, moments, scales and copies must not overlap")
     chunks = ctypes.c_int64(0)
     args = (rows.ctypes.data, n)
     _check("fp8z_encode_adamw_list", lib().fp8z_encode_adamw_list(*args, None, 0, ctypes.byref(chunks)))

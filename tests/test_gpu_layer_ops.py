@@ -256,3 +256,18 @@ def test_one_group_of_columns_has_no_group_stride():
         rc = fp8z.lib().fp8z_matmul(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), ctypes.byref(args), off.data_ptr(),
                                     out.data_ptr(), None, 0, None, torch.cuda.current_stream().cuda_stream)
         assert rc == 0 and torch.equal(out, want), step
+
+
+def test_adamw_list_refuses_what_overlaps():
+    """The same parameter twice, moments that share memory, a copy inside a parameter: a step would race."""
+    z = lambda n=300, d=torch.float32: torch.zeros(n, dtype=d, device="cuda")
+    p, q, buf = z(), z(), z(600)
+    for args, kw in ((([p, p], [z(), z()], [z(), z()], [z(), z()]), {}), (([p], [z()], [q], [q]), {}),
+                     (([p], [z()], [buf[:300]], [buf[299:599]]), {}), (([p], [z()], [z()], [p]), {}),
+                     (([p, q], [z(), z()], [z(), z()], [z(), z()]), dict(copies=[buf.bfloat16()[:300], q.view(torch.bfloat16)[300:]])),
+                     (([p], [z()], [z(d=torch.uint8)], [z(d=torch.uint8)]), dict(exp_avg_scales=[buf[:3]], exp_avg_sq_scales=[buf[2:5]]))):
+        with pytest.raises(ValueError):
+            fp8z.fp8z_encode_adamw_list(*args, **kw)
+    # neighbours, empty tensors and shared gradients are fine
+    assert fp8z.fp8z_encode_adamw_list([buf[:300], buf[300:], z(0)], [p, p, z(0)], [z(), z(), z(0)], [z(), z(), z(0)]).chunks == 2
+    assert fp8z.fp8z_encode_adamw_list([], [], [], []).chunks == 0
