@@ -11,7 +11,8 @@
 // the update divides by, and half the range of exponents).
 //
 // Everything is read and written once: 28 bytes an element with FP32 moments and gradients,
-// 16.1 with BF16 gradients, 8-bit moments and a BF16 copy.
+// 16.1 with BF16 gradients, 8-bit moments and a BF16 copy.  200 M elements: 806 to 856 us with
+// FP32 moments (0.97 of a copy's rate), 619 with 8-bit ones (5.2 TB/s; instructions bound it).
 #include <cfloat>
 #include <cmath>
 #include <cstdint>

@@ -59,9 +59,9 @@ __device__ __forceinline__ void stage32(Stager& sg, const uint32_t* r) {
     for (int j = 0; j < 8; ++j) sg.put(s, j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
 }
 
-// A dw whose rows do not all start and end on 16-byte boundaries, and sums of 16-bit
-// gradients (one rounding of the whole sum): 32 columns of the warp's 32 rows
-// pass through its slab, so that the threads write along the rows.
+// Results whose rows do not all start and end on 16-byte boundaries, or are not all a product's,
+// and sums of 16-bit gradients (one rounding of the whole sum): 32 columns of the
+// warp's rows pass through its slab, so that the threads write along the rows.
 template <typename T>
 __device__ __forceinline__ void weight_rows(T* p, int64_t ld, int rows, int n, const Stager& sg, bool accumulate) {
     if (sg.lane >= n) return;

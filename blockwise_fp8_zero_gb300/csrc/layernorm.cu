@@ -6,8 +6,8 @@
 //   dx = rstd (g - sum g / n - xh sum (g xh) / n),  g = dy w
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 //
-// A row is read once and waits in registers for its two sums; what bounds both
-// directions is memory traffic.  Rows longer than the registers hold are read again.
+// A row is read once and waits in registers for its two sums, many rows together (queues,
+// below) where there are many.  Rows longer than the registers hold are read again.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -455,7 +455,9 @@ __device__ __forceinline__ float inverse_root(float x) {
 }
 
 // Batches of two rows, one block a batch at a time: the sums of a batch share two barriers.
-// A thread has 8 or 16 neighbouring columns of every row; the block is as wide as the row.
+// A thread has eight neighbouring columns of every row; the block is as wide as the row.
+// 16384 x 7168 BF16 into E4M3: 120 to 125 us at a floor of 52; instructions bound it (two
+// passes over registers, largest magnitudes, a corrected quotient and a conversion an element).
 template <typename T, bool kCodes>
 __global__ void __launch_bounds__(1024) norm_queue_kernel(const __grid_constant__ Norm A) {
     constexpr int kRows = 2, kVecs = 1;
@@ -664,7 +666,8 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) norm_grad_ker
 }
 
 // The same with a queue of dy and x: both are read from shared memory again for dx, so that
-// registers hold the sums of dw and db, and the weight, only.
+// registers hold the sums of dw and db, and the weight, only.  16384 x 7168 BF16: 107 to 112 us with
+// the join of the parts, 6.3 TB/s: memory traffic.
 template <typename T, int kVecs>
 __global__ void __launch_bounds__(512, 2 / kVecs) norm_grad_queue_kernel(const __grid_constant__ NormGrad A) {
     constexpr int kRows = sizeof(T) == 2 ? 2 : 1;

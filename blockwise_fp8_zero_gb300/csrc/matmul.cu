@@ -371,6 +371,13 @@ __device__ __forceinline__ void store_large(const Args& A, const CUtensorMap& ou
 // and 128 of b into a ring of stages; one thread of the first block issues the products
 // of both, each block of K into the other of two accumulators, while eight warps of
 // each block read the one before, scale it and add it up.
+//
+// 4096 x 18432 x 7168: 448 to 475 us, 2.3 to 2.4 PFLOP/s.  The copies alone (64 KB a pair and block
+// of K from L2) take 343; the rest is the way of an accumulator to its readers and back with
+// two of them, all that tensor memory holds at 256 columns.  Stages (3 to 5) do not matter;
+// sixteen readers of 64 columns take 512 us, halves of 128 columns with four accumulators 619.
+// With a scale for every column, 2048 x 7168 x 8192 added to FP32 takes 171 us (1.4 PFLOP/s):
+// the readers' second scale is one packed product more for every sum.
 template <bool kRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThreads, 1)
     large_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -595,6 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
 // Where that leaves SMs without work, the blocks of a cluster share a tile: each takes
 // a part of K, and then adds up the parts of some of a's rows, which it reads from the
 // others' shared memory in a fixed order.
+// 8 x 18432 x 7168: 25 us, of which the weights' 132 MB are 19.5 at the copy's rate.
 constexpr int kRowsB = 128;
 constexpr int kSmallThreads = 192;             // loads, products, four readers
 constexpr int kMaxSplits = 8;
