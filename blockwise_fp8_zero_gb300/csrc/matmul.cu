@@ -277,7 +277,8 @@ struct TileWalk {
             if (group >= A.groups) return false;
             t -= group * A.mt * A.nt;
             if (A.by == kByK) {
-                out.k0 = starts[group] / kBK;
+                // both up: a group that starts at a ragged end of K is empty
+                out.k0 = (starts[group] + kBK - 1) / kBK;
                 out.k1 = (starts[group + 1] + kBK - 1) / kBK;
             }
         }

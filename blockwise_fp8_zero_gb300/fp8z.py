@@ -927,7 +927,7 @@ def fp8z_matmul(a, a_scale, b, b_scale, out, offsets=None, accumulate=False, wor
     [n, ceil(k/128)] (row-wise); out [m, n] float32 / bfloat16 / float16.  Banks of experts:
     b [groups, n, k] and b_scale [groups, ceil(n/128), ..] with the first row of each group
     in offsets (groups + 1 numbers, int32 or int64, on the device), or out [groups, m, n]
-    with the first column of each group in offsets (multiples of 128).  workspace: see
+    with the first column of each group in offsets (multiples of 128, or k).  workspace: see
     fp8z_matmul_workspace."""
     here = _current_device()
     ap, sp, bp, tp, op, args = _matmul_args(a, a_scale, b, b_scale, out, offsets, accumulate)
