@@ -492,6 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
                     b ^= 1;
                 }
             }
+            umma_commit_pair(drain);       // of this thread's products: another's commit would say nothing of them
         }
     } else if (warp >= 4) {
         more_registers<kReaderRegs>();
@@ -573,23 +574,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Large<kRows>::kThrea
             }
         }
     }
-    if (warp == 1 && lane == 0 && rank == 0) {
-        umma_commit_pair(drain);           // every product is done before tensor memory is freed
-        mbar_wait_drain(drain, 0, A.dev_status);
-    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     // Whatever a wait gave up on, every copy lands before either block ends.  A stage for which
     // one of the two threads never came to issue its copies lacks its arrival: it is made here.
     if (rank == 0 && threadIdx.x == 0) {
+        if (run) mbar_wait_drain(drain, 0, A.dev_status);      // every product is done before tensor memory is freed
         const uint32_t most = max(issued_by[0], issued_by[1]);
         for (int j = 0; j < 2; ++j)
             for (uint32_t i = issued_by[j]; i < most; ++i) mbar_arrive(full(i % kStages));
         for (uint32_t i = most > kStages ? most - kStages : 0; i < most; ++i)
             mbar_wait_drain(full(i % kStages), (i / kStages) & 1, A.dev_status);
     }
-    if (rank == 1 && threadIdx.x == 0) mbar_wait_drain(drain, 0, A.dev_status);    // the last arrival from the first block
+    if (run && rank == 1 && threadIdx.x == 0) mbar_wait_drain(drain, 0, A.dev_status);    // the last arrival from the first block
     cluster_sync();                        // neither block ends, nor frees, while the other may still reach it
     if (warp == 1) {
         tc_fence_after();
@@ -750,6 +748,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
                     bph ^= 1;
                 }
             }
+            umma_commit_one(drain);        // of this thread's products: another's commit would say nothing of them
         }
     } else {
         const int quarter = warp & 3, col = n0 + quarter * 32 + lane;
@@ -810,10 +809,6 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
             }
         }
     }
-    if (warp == 1 && lane == 0) {
-        umma_commit_one(drain);            // every product is done before tensor memory is freed
-        mbar_wait_drain(drain, 0, A.dev_status);
-    }
     if (splits > 1) {
         cluster_sync();
         if (run && warp >= 2) {
@@ -842,6 +837,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     }
     if (splits > 1) cluster_sync();        // the others may still read this block's sums
     if (warp == 1) {
+        if (run) mbar_wait_drain(drain, 0, A.dev_status);      // every product is done before tensor memory is freed
         tc_fence_after();
         tmem_dealloc_one(tmem, L::kTmem);
     }
