@@ -6,8 +6,11 @@
 //   p' = p decay - step_size m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
 //
 // lpnh.cn "Model-Optimizer" article, §4.3, with each operation rounded on its own and in
-// the order of the FP8 step, so that a parameter moves the same way in either.  In 8 bits
-// a moment is E4M3 with one FP32 scale for every 128 elements, v as its square root (what
+// the order of the FP8 step, so that the same scalars move a parameter the same way in either.  They are
+// formed from 64-bit hyper-parameters here, from 32-bit ones there: the same where FP32 holds those
+// numbers, else 1 - beta is up to 2^-25 beta apart.
+//
+// In 8 bits a moment is E4M3 with one FP32 scale for every 128 elements, v as its square root (what
 // the update divides by, and half the range of exponents).
 //
 // Everything is read and written once: 28 bytes an element with FP32 moments and gradients,

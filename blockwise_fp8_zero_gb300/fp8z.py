@@ -1084,8 +1084,9 @@ def fp8z_encode_adamw_list(params, grads, exp_avgs, exp_avg_sqs, copies=None, ex
 
 def fp8z_adamw(tensors, hp, grad_factor=None, stream=None):
     """One AdamW step of every tensor of the list (fp8z_encode_adamw_list).  hp: hparams();
-    the quantizer's fields have no part in it.  grad_factor: one
-    float32 on the device that multiplies every gradient (norm[1] of a clipping, 1 / a loss
+    the quantizer's fields have no part in it.  The numbers hparams() was given are taken in 64
+    bits, where the FP8 step takes its 32-bit fields: pass numbers that float32 holds (numpy.float32(0.95))
+    for the same bits from both.  grad_factor: one float32 on the device that multiplies every gradient (norm[1] of a clipping, 1 / a loss
     scale), or None."""
     here = _current_device()
     if not isinstance(tensors, AdamwList):

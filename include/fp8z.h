@@ -697,7 +697,9 @@ typedef struct {
 } fp8z_adamw_chunk;          /* 64 bytes */
 
 /* Hyper-parameters of fp8z_adamw: the fields of fp8z_adamw_hparams that it has, in 64 bits.  The
- * scalars of a step are formed from them in 64 bits and rounded once. */
+ * scalars of a step are formed from them in 64 bits and rounded once.  fp8z_adamw_requant_step forms them
+ * from 32-bit fields: the same scalars, and so the same bits, where FP32 holds the numbers; else
+ * 1 - beta and 1 - beta^step differ (by 2.4e-7 of themselves at 0.9 and 0.95, by 1.3e-5 at 0.999). */
 typedef struct {
     double lr, beta1, beta2, eps, weight_decay;
     int64_t step;            /* >= 1                                                 */
