@@ -11,7 +11,9 @@
 // numbers, else 1 - beta is up to 2^-25 beta apart.
 //
 // In 8 bits a moment is E4M3 with one FP32 scale for every 128 elements, v as its square root (what
-// the update divides by, and half the range of exponents).
+// the update divides by, and half the range of exponents).  Codes are the nearest: a root that a step moves by
+// less than half a code stays, so that one among larger ones follows its gradients only within the factors
+// that fp8z.h gives (1.9 at beta2 = 0.95, 11.4 at 0.999).
 //
 // Everything is read and written once: 28 bytes an element with FP32 moments and gradients,
 // 16.1 with BF16 gradients, 8-bit moments and a BF16 copy.  200 M elements: 806 to 856 us with

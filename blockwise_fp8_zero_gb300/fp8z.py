@@ -1037,7 +1037,9 @@ def fp8z_encode_adamw_list(params, grads, exp_avgs, exp_avg_sqs, copies=None, ex
                            exp_avg_sq_scales=None, device="cuda"):
     """Table for fp8z_adamw over params (contiguous float32 CUDA tensors), their gradients
     (float32 / bfloat16 / float16) and moments: float32, or uint8 E4M3 codes with float32 scales,
-    one for every 128 elements (rounded up).  copies: bfloat16 / float16 tensors that take
+    one for every 128 elements (rounded up): three
+    fraction bits, which follow a gradient's size within a factor of 1.9 at beta2 = 0.95 and of 11.4 at 0.999
+    (fp8z.h), so that float32 moments are the choice where beta2 is near 1.  copies: bfloat16 / float16 tensors that take
     the new values, or None for no copies.  Scales and copies may also be None for single
     tensors.  The table holds addresses: make a new one when a tensor moves."""
     params, grads, ms, vs = list(params), list(grads), list(exp_avgs), list(exp_avg_sqs)

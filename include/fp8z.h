@@ -724,6 +724,15 @@ typedef struct {
  * A v' that is not zero keeps at least the smallest code.  Zero codes with any finite scale are
  * zero moments, so that buffers of zeros start a run.  An infinite or NaN moment leaves the
  * 128 elements it is among without meaning.
+ * Three fraction bits, rounded to nearest: a moment that a step moves by less than half a code, 1/32 to 1/16 of it,
+ * stays as it is, however many such steps there are.  While the largest of the 128 keeps their scale, a root
+ * sqrt(v) (above 1/28672 of that largest one) therefore
+ *   does not fall where beta2 > 0.9385: v does not fade with its gradients;
+ *   is at least 1/K of the root that FP32 moments hold, K^2 = 1 + 33 / (256 (1 - beta2)) (K = 1.9 at beta2 = 0.95, 11.4 at
+ *   0.999): gradients that grow by less than K may leave v behind, and the update is up to K times FP32's;
+ *   is at most 17/16 of the largest |g| so far, or its start.
+ * With beta1 = 0.9, m stays while g is within 0.3 to 0.6 of m's size around it.  Where all 128 grow or fade together their
+ * scale carries them.  With beta2 near 1 that is little to rely on: take FP32 moments.
  * list: device, fp8z_adamw_chunk[chunks].  Returns FP8Z_OK / EINVAL / EALIGN / EUNSUPPORTED / ECUDA.
  */
 FP8Z_API int fp8z_encode_adamw_list(const fp8z_adamw_tensor *tensors, int32_t n, fp8z_adamw_chunk *out,
