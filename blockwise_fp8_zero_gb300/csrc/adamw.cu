@@ -43,20 +43,6 @@ struct Step {
     int post;                                    // FP8Z_DECAY_POST
 };
 
-__device__ __forceinline__ void adamw1(const Step& A, float g, float& p, float& m, float v, float& r, float& v1) {
-    m = __fadd_rn(__fmul_rn(A.s.beta1, m), __fmul_rn(A.s.omb1, g));
-    v1 = __fadd_rn(__fmul_rn(A.s.beta2, v), __fmul_rn(A.s.omb2, __fmul_rn(g, g)));
-    r = __fsqrt_rn(v1);
-    const float d = __fadd_rn(__fmul_rn(r, A.s.rs_bc2), A.s.eps);
-    const float su = __fmul_rn(A.s.step_size, __fdiv_rn(m, d));
-    if (!A.post) {
-        p = __fsub_rn(__fmul_rn(p, A.s.decay), su);
-    } else {
-        const float pu = __fsub_rn(p, su);
-        p = __fsub_rn(pu, __fmul_rn(A.s.lr_wd, pu));
-    }
-}
-
 // The multiplier of a run whose largest magnitude is amax: 448 times 1 / amax, 1 for a run of zeros.
 __device__ __forceinline__ float run_scale(float amax) {
     return amax == 0.0f ? 1.0f : fminf(__fmul_rn(448.0f, __frcp_rn(amax)), FLT_MAX);
@@ -67,10 +53,12 @@ __device__ __forceinline__ float warp_max(float a) {
     return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));
 }
 
-// The same with a root and a quotient that are an approximation and one correction by the remainder:
-// off by one unit about once in a million times.  At 16 bytes an element the instructions are what
-// bounds the step (200 M elements with 8-bit moments and IEEE roots and quotients: 856 us).  Values where
-// that might overflow or lose its remainder, and zero, take the IEEE operation.
+// Root and quotient as an approximation and one correction by its remainder (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000", 1990).  The root is rounded as __fsqrt_rn rounds it
+// (all fractions of two binades compared), the quotient is a unit off in a few of 2^32 pairs: the
+// reciprocal behind it is itself an approximation.  At 16 bytes an element the instructions are what bounds
+// the step (200 M elements with 8-bit moments and IEEE roots and quotients: 856 us).  Values where that might
+// overflow or lose its remainder, and zero, take the IEEE operation.
 __device__ __forceinline__ float root_near(float v) {
     float y;
     asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(v));
@@ -83,17 +71,28 @@ __device__ __forceinline__ float quotient_near(float m, float d) {
     const float q = m * y;
     return d > 0x1p-100f && d < 0x1p100f && fabsf(m) < 0x1p20f * d ? fmaf(fmaf(-q, d, m), y, q) : __fdiv_rn(m, d);
 }
-__device__ __forceinline__ void adamw1_near(const Step& A, float g, float& p, float& m, float v, float& r) {
+
+// One element; r = sqrt(v').  k8: with 8-bit moments, wherever they lie, the near operations.
+template <bool k8>
+__device__ __forceinline__ void adamw1(const Step& A, float g, float& p, float& m, float& v, float& r) {
     m = __fadd_rn(__fmul_rn(A.s.beta1, m), __fmul_rn(A.s.omb1, g));
-    r = root_near(__fadd_rn(__fmul_rn(A.s.beta2, v), __fmul_rn(A.s.omb2, __fmul_rn(g, g))));
+    v = __fadd_rn(__fmul_rn(A.s.beta2, v), __fmul_rn(A.s.omb2, __fmul_rn(g, g)));
+    r = k8 ? root_near(v) : __fsqrt_rn(v);
     const float d = __fadd_rn(__fmul_rn(r, A.s.rs_bc2), A.s.eps);
-    const float su = __fmul_rn(A.s.step_size, quotient_near(m, d));
+    const float su = __fmul_rn(A.s.step_size, k8 ? quotient_near(m, d) : __fdiv_rn(m, d));
     if (!A.post) {
         p = __fsub_rn(__fmul_rn(p, A.s.decay), su);
     } else {
         const float pu = __fsub_rn(p, su);
         p = __fsub_rn(pu, __fmul_rn(A.s.lr_wd, pu));
     }
+}
+
+// E4M3 of four roots times their run's scale.  A v that is not zero does not become zero (m / sqrt(0) would be a
+// step without bound): what is above 0 is coded as 2^-9, the smallest code, at least.
+__device__ __forceinline__ uint32_t root_codes(const float (&r)[4], float s) {
+    const auto code = [&](int j) { return r[j] > 0.0f ? fmaxf(r[j] * s, 0x1p-9f) : r[j]; };
+    return pack_e4m3x4(code(0), code(1), code(2), code(3));
 }
 
 // Four elements of a lane: neighbours from 4 * lane on where the tensors allow 16-byte
@@ -191,7 +190,7 @@ __device__ __forceinline__ void update(const fp8z_adamw_chunk& t, const Step& A,
     float r[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        adamw1(A, __fmul_rn(g[j], factor), p[j], m[j], v[j], r[j], v[j]);
+        adamw1<k8>(A, __fmul_rn(g[j], factor), p[j], m[j], v[j], r[j]);
         if (f.at(j) >= f.n) m[j] = r[j] = 0.0f;
     }
     f.store(t.p + at, p);
@@ -200,12 +199,7 @@ __device__ __forceinline__ void update(const fp8z_adamw_chunk& t, const Step& A,
     if constexpr (k8) {
         const float sm = run_scale(warp_max(absmax4(m))), sv = run_scale(warp_max(absmax4(r)));
         f.store_codes(static_cast<uint8_t*>(t.m) + at, pack_e4m3x4(m[0] * sm, m[1] * sm, m[2] * sm, m[3] * sm));
-        uint32_t q = pack_e4m3x4(r[0] * sv, r[1] * sv, r[2] * sv, r[3] * sv);
-        // a v that is not zero does not become zero: m / sqrt(0) would be a step without bound
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (r[j] > 0.0f && (q >> 8 * j & 255) == 0) q |= 1u << 8 * j;
-        f.store_codes(static_cast<uint8_t*>(t.v) + at, q);
+        f.store_codes(static_cast<uint8_t*>(t.v) + at, root_codes(r, sv));
         if (f.lane == 0) {
             t.m_scale[at / kRun] = __frcp_rn(sm);
             t.v_scale[at / kRun] = __frcp_rn(sv);
@@ -302,7 +296,7 @@ __device__ __forceinline__ void update8(const fp8z_adamw_chunk& t, const Step& A
         float p[4], g[4], v[4];
         l[i].unpack(p, g, m[i], v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) adamw1_near(A, __fmul_rn(g[j], factor), p[j], m[i][j], v[j], r[i][j]);
+        for (int j = 0; j < 4; ++j) adamw1<true>(A, __fmul_rn(g[j], factor), p[j], m[i][j], v[j], r[i][j]);
         const int to = at + i * kWarps * kRun;
         f.store(t.p + to, p);
         if (t.copy_dtype == FP8Z_BF16) f.store(static_cast<__nv_bfloat16*>(t.copy) + to, p);
@@ -318,9 +312,7 @@ __device__ __forceinline__ void update8(const fp8z_adamw_chunk& t, const Step& A
         const float sm = __shfl_sync(0xFFFFFFFFu, scale, 2 * i), sv = __shfl_sync(0xFFFFFFFFu, scale, 2 * i + 1);
         const int to = at + i * kWarps * kRun;
         f.store_codes(static_cast<uint8_t*>(t.m) + to, pack_e4m3x4(m[i][0] * sm, m[i][1] * sm, m[i][2] * sm, m[i][3] * sm));
-        // a v that is not zero does not become zero: what is above 0 is coded as 2^-9, the smallest code, at least
-        const auto code = [&](int j) { return r[i][j] > 0.0f ? fmaxf(r[i][j] * sv, 0x1p-9f) : r[i][j]; };
-        f.store_codes(static_cast<uint8_t*>(t.v) + to, pack_e4m3x4(code(0), code(1), code(2), code(3)));
+        f.store_codes(static_cast<uint8_t*>(t.v) + to, root_codes(r[i], sv));
     }
 }
 

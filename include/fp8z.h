@@ -720,7 +720,7 @@ typedef struct {
  * Moments in 8 bits, for every 128 elements of a tensor (fewer at its end): m is
  * E4M3(m' * s), v is E4M3(sqrt(v') * s), s = 448 * (1 / the largest magnitude of the 128) (1 where all are
  * zero, at most FLT_MAX; two roundings), and the scale kept is 1 / s: a moment is code * scale, v its square.
- * Here the root and the quotient by it may be off by one unit (2^-23 of their value).
+ * Here the quotient by the root may be off by one unit (2^-23 of its value), the same wherever the element lies.
  * A v' that is not zero keeps at least the smallest code.  Zero codes with any finite scale are
  * zero moments, so that buffers of zeros start a run.  An infinite or NaN moment leaves the
  * 128 elements it is among without meaning.
