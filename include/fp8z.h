@@ -596,8 +596,10 @@ typedef struct {
  * fp8z_adamw_requant_step_rowmajor (x W^T), or its column-major copy and transposed
  * scale grid (dy W).  With b_scale_rows = 1 it is f32 [n, ceil(k/128)]: the column-wise
  * layouts of fp8z_transpose_rowwise (dy^T x).  Codes are multiplied on the tensor cores;
- * each S is an FP32 sum of the tensor cores (cut off, not rounded, at 32 of K), scaled
- * and added up in FP32 with rounding, and the result is rounded once to out_dtype.  An
+ * each S is an FP32 sum of the tensor cores (cut off, not rounded, at 32 of K), multiplied
+ * by the product of its two scales and added up in FP32 with rounding, and the result is rounded once to out_dtype.
+ * The scales' own product is rounded to FP32: below 2^-126 it keeps fewer bits (off by up to 2^-150, times S), and where it
+ * passes the largest FP32 number the results are infinite, or NaN where S is 0.  An
  * FP32 out that is added to may be added to by the memory system, which takes
  * subnormal numbers (below 1.2e-38) for zero.  A NaN code or scale reaches the results that it
  * enters.  Every element has one fixed order: the same arguments give the same bits.
