@@ -373,7 +373,7 @@ __device__ __forceinline__ void store_large(const Args& A, const CUtensorMap& ou
 // of both, each block of K into the other of two accumulators, while eight warps of
 // each block read the one before, scale it and add it up.
 //
-// 4096 x 18432 x 7168: 448 to 475 us, 2.3 to 2.4 PFLOP/s.  The copies alone (64 KB a pair and block
+// 4096 x 18432 x 7168: 448 to 485 us by the box, 2.2 to 2.4 PFLOP/s.  The copies alone (64 KB a pair and block
 // of K from L2) take 343; the rest is the way of an accumulator to its readers and back with
 // two of them, all that tensor memory holds at 256 columns.  Stages (3 to 5) do not matter;
 // sixteen readers of 64 columns take 512 us, halves of 128 columns with four accumulators 619.
